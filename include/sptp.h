@@ -352,14 +352,152 @@ int sptp_down_proj_e4m3(const void* qs, const float* ss, const void* qW2, const 
                         int M, int d, int F, int P, void* out,
                         void* workspace, size_t ws_bytes, void* cuda_stream);
 
+/* ---- Between the QKV projection and the output projection -------------------
+ * sptp_attn_qkv_forward leaves every shard's q, k and v rows, sptp_down_proj
+ * takes every shard's attention output; the calls below are the sub-layer
+ * between them: rotary positions, a paged key-value cache, and the attention
+ * of one new token per sequence over it.  The pages name the attention
+ * sub-layer ([A] "Potential Solution") and leave its inside open.
+ *
+ * A shard's row of qkv_out holds its Hq query heads, then its Hkv key heads,
+ * then its Hkv value heads, D elements each (N/P = (Hq + 2 Hkv) D): Hq and Hkv
+ * count one shard's heads.  Query head h reads key/value head h / (Hq/Hkv).
+ *
+ * The cache: k_cache and v_cache [P][num_pages][Hkv][page_size][D], allocated
+ * by the caller.  page_table [B][max_pages] (int32) names the pages of each
+ * sequence, the same in every shard's pool: key j of sequence b is row
+ * j % page_size of page page_table[b][j / page_size].  Only entries that a
+ * call reaches are read.
+ *   kv_type  SPTP_KV_SAME: elements of `dtype`; k_scale and v_scale unused.
+ *            SPTP_KV_E4M3 (dtype SPTP_BF16): E4M3 codes, and k_scale, v_scale
+ *            [P][num_pages][Hkv][page_size] fp32: a head's row of D elements
+ *            quantised as by sptp_quantize_rows_e4m3.
+ *   Shape rules of all of them: 1 <= P <= 8; D % 8 == 0 (E4M3: % 16),
+ *   8 <= D <= 256; Hq % Hkv == 0; page_size % 16 == 0;
+ *   max_pages * page_size < 2^31; P * num_pages * Hkv * page_size < 2^31.
+ *   int32 arrays are 4-byte aligned, `turns` 8-byte, all others 16-byte.
+ */
+
+/* Element type of a key-value cache. */
+typedef enum sptp_kv_type_e SPTP_ENUM_INT { SPTP_KV_SAME = 0, SPTP_KV_E4M3 = 1 } sptp_kv_type;
+
+/*
+ * sptp_rope_scaling -- how the frequencies f_i = theta^(-2i/rot) are changed
+ * for contexts `factor` times as long as the model was trained on.
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     f_i of the base theta * factor^(rot/(rot-2))
+ *   PARTS   c f_i + (1 - c) f_i / factor, c = clamp((r_i - alpha)/(beta - alpha), 0, 1)
+ *           with r_i = orig_len * f_i / (2 pi), the turns that the pair makes
+ *           over the original length: fast pairs are kept, slow ones scaled.
+ */
+typedef enum sptp_rope_scaling_e SPTP_ENUM_INT {
+    SPTP_ROPE_NONE = 0,
+    SPTP_ROPE_LINEAR = 1,
+    SPTP_ROPE_NTK = 2,
+    SPTP_ROPE_PARTS = 3
+} sptp_rope_scaling;
+
+/*
+ * sptp_rope_turns -- the frequency table of the rotation, made once per model
+ * on the HOST (no CUDA call): turns[i] = round(2^64 f_i / (2 pi)), i < rot/2,
+ * in HOST memory; the caller copies it to the device.  A frequency in turns
+ * per position, as a 64-bit binary fraction, makes position * turns (mod
+ * 2^64) the angle without rounding, however far the position.
+ *   rot % 16 == 0, 16 <= rot <= 256; theta > 1; factor >= 1 (ignored for
+ *   NONE); PARTS: orig_len > 0 and beta > alpha (ignored for the others).
+ *   SPTP_ERR_SHAPE otherwise, SPTP_ERR_UNIMPLEMENTED for another scaling.
+ */
+int sptp_rope_turns(int rot, double theta, sptp_rope_scaling scaling, double factor, double orig_len,
+                    double alpha, double beta, unsigned long long* turns);
+
+/*
+ * sptp_rope -- rotary positions of the first Hr of H heads of every row:
+ *     (a, b) -> gain * (a cos t - b sin t, a sin t + b cos t),
+ *     t = 2 pi * positions[m] * turns[i] / 2^64
+ *   for the pairs i < rot/2 of a head's first rot elements: elements (i,
+ *   i + rot/2), or (2i, 2i + 1) if `interleaved`.  The other elements and
+ *   heads are copied.  transpose != 0 applies the transposed matrix (t -> -t,
+ *   the same gain): the gradient of the rotation with respect to x.
+ *   x, out    [P][M][H][D]; out may be exactly x (then only rotated elements
+ *             are written) and must not overlap it otherwise.
+ *   positions [M] int32, any value, the same for every shard.
+ *   turns     DEVICE [rot/2], from sptp_rope_turns.  rot % 16 == 0,
+ *             16 <= rot <= D; 1 <= Hr <= H; P * H < 2^24.
+ *   gain      finite: the attention factor of a scaled context (0.1 ln(factor)
+ *             + 1 is usual with PARTS), or 1.
+ * Numerics: angles to 2^-25 of a turn, products in fp32, rounded once.
+ */
+int sptp_rope(const void* x, const int* positions, const unsigned long long* turns,
+              int P, int M, int H, int Hr, int D, int rot, int interleaved, int transpose, float gain,
+              sptp_dtype dtype, void* out, void* cuda_stream);
+
+/*
+ * sptp_rope_append_kv -- the QKV rows of M new tokens, of any mix of
+ * sequences: q rotated to q_out, k rotated and stored in the cache, v stored
+ * in the cache.
+ *   qkv       [P][M][(Hq + 2 Hkv) D], sptp_attn_qkv_forward's qkv_out
+ *   positions [M] int32: a token's position, for the rotation and its slot
+ *   seq_ids   [M] int32: its row of page_table; < 0 marks a padding row:
+ *             nothing is stored for it, its row of q_out is left as it was
+ *   rot       as in sptp_rope, or 0: no rotation, turns unused
+ *   q_out     [P][M][Hq][D].  q_out and the cache must not overlap an input,
+ *             the workspace or each other.
+ * A token whose sequence is >= B, whose position is outside [0, max_pages *
+ * page_size) or whose page is outside [0, num_pages) is recorded as
+ * SPTP_ERR_SHAPE in the workspace status words; its k and v are not stored
+ * (its q is).  Of two tokens with one sequence and position, it is not
+ * defined which is stored.  workspace: at least SPTP_WS_HEADER_BYTES,
+ * 256-byte aligned.  E4M3: k is rounded to bf16, then quantised; non-finite
+ * rows are outside the contract.
+ */
+int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_ids, const int* page_table,
+                        const unsigned long long* turns, int P, int M, int Hq, int Hkv, int D, int rot,
+                        int interleaved, float gain, int B, int max_pages, int num_pages, int page_size,
+                        sptp_dtype dtype, sptp_kv_type kv_type, void* q_out, void* k_cache, void* v_cache,
+                        float* k_scale, float* v_scale, void* workspace, size_t ws_bytes, void* cuda_stream);
+
+/* Workspace bytes needed by sptp_paged_attn_decode (0 on bad args). */
+size_t sptp_paged_attn_workspace_size(int P, int B, int Hq, int Hkv, int D);
+
+/*
+ * sptp_paged_attn_decode -- attention of one token per sequence over its
+ * cached keys and values:
+ *     s_j = scale * q . k_j,  lse = ln sum_j e^s_j,  out = sum_j e^(s_j - lse) v_j
+ *   over j < seq_lens[b], and j >= seq_lens[b] - window if window > 0.
+ *   q         [P][B][Hq][D] (sptp_rope_append_kv's q_out for one token each)
+ *   seq_lens  [B] int32: keys in the cache, the new token's included.  0
+ *             gives a row of zeros and lse -inf.
+ *   out       [P][B][Hq D], the row-parallel operand of sptp_down_proj
+ *   lse       [P][B][Hq] fp32, or NULL
+ *   out and lse must not overlap an input, the workspace or each other.
+ * The work is split over the length as well, evenly over the SMs whatever the
+ * lengths, and the parts of a row are joined in a fixed order: equal inputs
+ * give equal bits.  A row's result does not depend on what the cache holds
+ * behind its length or before its window.
+ * A length outside [0, max_pages * page_size] is cut to it, a page outside
+ * [0, num_pages) counts as zero keys and values; both are recorded as
+ * SPTP_ERR_SHAPE in the workspace status words.  workspace: at least
+ * sptp_paged_attn_workspace_size(...), 256-byte aligned.
+ * Numerics: scores, softmax statistics and sums in fp32; with a bf16 or E4M3
+ * cache the weights e^(s_j - m) are rounded to bf16 for their product with v
+ * (tensor cores), as v is; out is rounded once.
+ */
+int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* page_table, const int* seq_lens, int P, int B,
+                           int Hq, int Hkv, int D, int max_pages, int num_pages, int page_size, int window,
+                           float scale, sptp_dtype dtype, sptp_kv_type kv_type, void* out, float* lse,
+                           void* workspace, size_t ws_bytes, void* cuda_stream);
+
 /*
  * sptp_read_device_status -- synchronises `cuda_stream` and returns the
  * status the kernels recorded in the workspace header since the last call
  * that reset it (every entry point above resets it when it starts):
  * SPTP_OK; SPTP_ERR_TIMEOUT if a bounded device-side wait ran out (the
  * kernels then stop early and their outputs are undefined); or
- * SPTP_ERR_SHAPE if sptp_permute_ffn_neurons met an index outside [0, F).  No counterpart
- * on the pages: this is the library's own failure detection.
+ * SPTP_ERR_SHAPE if sptp_permute_ffn_neurons met an index outside [0, F), or
+ * a call on a paged cache an index, a page or a length outside its range.  No
+ * counterpart on the pages: this is the library's own failure detection.
  */
 int sptp_read_device_status(const void* workspace, void* cuda_stream);
 

@@ -22,6 +22,8 @@ __all__ = [
     "quantize_ffn_weights_e4m3", "sptp_ffn_fp8_workspace_size", "sptp_ffn_forward_fp8",
     "sptp_gateup_swiglu_e4m3", "sptp_down_proj_e4m3", "sptp_prologue_e4m3", "VARIANTS", "STATUS",
     "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest", "CHECKED_LIB_PATH", "set_library",
+    "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
+    "sptp_paged_attn_decode", "paged_kv_cache", "ROPE_SCALINGS",
 ]
 
 SPTP_BF16 = 0
@@ -33,6 +35,11 @@ VARIANTS = {"auto": 0, "pair": 1, "chain": 2, "fused": 3, "layers": 4}
 # sptp_status codes
 STATUS = {"ok": 0, "null": -1, "shape": -2, "dtype": -3, "workspace": -4, "cuda": -5, "timeout": -6,
           "unimplemented": -7, "alias": -8, "too_large": -9, "device": -10, "bounds": -11}
+# sptp_rope_scaling: how the rotary frequencies change for longer contexts
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+# sptp_kv_type
+SPTP_KV_SAME = 0
+SPTP_KV_E4M3 = 1
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsptp.so")
 
 EXPORTED_SYMBOLS = (
@@ -43,12 +50,14 @@ EXPORTED_SYMBOLS = (
     "sptp_quantize_rows_e4m3", "sptp_ffn_fp8_workspace_size", "sptp_ffn_forward_fp8", "sptp_gateup_swiglu_e4m3",
     "sptp_down_proj_e4m3", "sptp_prologue_e4m3", "sptp_ffn_forward_ex", "dtp_ffn_stack_forward_ex",
     "sptp_attn_qkv_forward_ex", "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest",
+    "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
+    "sptp_paged_attn_decode",
 )
 
 _lib = None
 
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_ulonglong
-_LL = ctypes.c_longlong
+_LL, _D = ctypes.c_longlong, ctypes.c_double
 _SIGS = {
     "sptp_ffn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
     "sptp_ffn_forward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _Z, _P]),
@@ -76,6 +85,11 @@ _SIGS = {
     "sptp_attn_qkv_forward_ex": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _Z, _P, _I]),
     "sptp_noalloc_read_device_status": (_I, [_P]),
     "sptp_noalloc_wait_selftest": (_I, [_U64, _I, _P]),
+    "sptp_rope_turns": (_I, [_I, _D, _I, _D, _D, _D, _D, _P]),
+    "sptp_rope": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
+    "sptp_rope_append_kv": (_I, [_P] * 5 + [_I] * 7 + [_F] + [_I] * 6 + [_P] * 6 + [_Z, _P]),
+    "sptp_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "sptp_paged_attn_decode": (_I, [_P] * 7 + [_I] * 9 + [_F, _I, _I, _P, _P, _P, _Z, _P]),
 }
 
 
@@ -541,3 +555,134 @@ def sptp_down_proj_e4m3(qs, ss, qW2, sW2, P, out=None, workspace=None, stream=No
                                      _ptr(workspace), _nbytes(workspace), _stream(stream))
     _check("sptp_down_proj_e4m3", code)
     return out
+
+
+# ------------------------------------------------------------------ rotary positions, paged key-value cache
+
+def sptp_rope_turns(rot, theta=10000.0, scaling="none", factor=1.0, orig_len=0, alpha=1.0, beta=32.0, device=None):
+    """The rotation's frequency table, made once per model: int64 [rot/2] on
+    `device` (the current CUDA device if None), turns per position as 64-bit
+    binary fractions.  scaling: "none", "linear", "ntk" or "parts"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}; one of {sorted(ROPE_SCALINGS)}")
+    turns = torch.empty(max(int(rot) // 2, 0), dtype=torch.int64)
+    code = lib().sptp_rope_turns(int(rot), float(theta), ROPE_SCALINGS[scaling], float(factor), float(orig_len),
+                                 float(alpha), float(beta), turns.data_ptr())
+    _check("sptp_rope_turns", code)
+    return turns.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def sptp_rope(x, positions, turns, Hr=None, interleaved=False, transpose=False, gain=1.0, out=None, stream=None):
+    """Rotary positions of the first Hr (default: all) heads of x [P,M,H,D];
+    positions int32 [M]; turns from sptp_rope_turns.  transpose: the gradient.
+    out may be x (in place).  Returns out."""
+    P, M, H, D = x.shape
+    rot = 2 * turns.shape[0]
+    dt = _dtype_code(x)
+    _expect("positions", positions, (M,), torch.int32)
+    _expect("turns", turns, (rot // 2,), torch.int64)
+    _expect("out", out, (P, M, H, D), x.dtype, optional=True)
+    _same_device(x, positions, turns, out)
+    if out is None:
+        out = torch.empty_like(x)
+    code = lib().sptp_rope(_ptr(x), _ptr(positions), _ptr(turns), P, M, H, H if Hr is None else Hr, D, rot,
+                           int(interleaved), int(transpose), float(gain), dt, _ptr(out), _stream(stream))
+    _check("sptp_rope", code)
+    return out
+
+
+def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=False, device="cuda"):
+    """An empty paged key-value cache (k, v, k_scale, v_scale): k and v
+    [P,num_pages,Hkv,page_size,D] of `dtype`, or with e4m3 uint8 codes with
+    fp32 scales [P,num_pages,Hkv,page_size] (None otherwise)."""
+    shape = (P, num_pages, Hkv, page_size, D)
+    k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else dtype, device=device) for _ in range(2))
+    if not e4m3:
+        return k, v, None, None
+    return k, v, torch.zeros(shape[:-1], device=device), torch.zeros(shape[:-1], device=device)
+
+
+def _check_cache(cache, P, D, dtype):
+    """Sizes (num_pages, Hkv, page_size, kv_type) of a cache of activations of `dtype`."""
+    k, v, ks, vs = cache
+    if k.dim() != 5:
+        raise ValueError(f"cache: {k.dim()} dimensions, expected [P,num_pages,Hkv,page_size,D]")
+    _, num_pages, Hkv, page_size, _ = k.shape
+    e4m3 = k.dtype == torch.uint8
+    if e4m3 and dtype != torch.bfloat16:
+        raise TypeError("an E4M3 cache takes bf16 activations")
+    kvt = torch.uint8 if e4m3 else dtype
+    _expect("k_cache", k, (P, num_pages, Hkv, page_size, D), kvt)
+    _expect("v_cache", v, (P, num_pages, Hkv, page_size, D), kvt)
+    if e4m3:
+        _expect("k_scale", ks, (P, num_pages, Hkv, page_size), torch.float32)
+        _expect("v_scale", vs, (P, num_pages, Hkv, page_size), torch.float32)
+    elif ks is not None or vs is not None:
+        raise ValueError("scales belong to an E4M3 cache")
+    return num_pages, Hkv, page_size, SPTP_KV_E4M3 if e4m3 else SPTP_KV_SAME
+
+
+def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, interleaved=False, gain=1.0, q_out=None,
+                        workspace=None, stream=None):
+    """Rotates the q and k heads of qkv [P,M,(Hq+2Hkv)D] and stores k and v in
+    `cache` (see paged_kv_cache).  positions, seq_ids int32 [M] (seq_ids < 0:
+    padding); page_table int32 [B,max_pages]; turns None: no rotation.
+    Returns q_out [P,M,Hq,D]."""
+    P, M, N = qkv.shape
+    D = cache[0].shape[-1]
+    dt = _dtype_code(qkv)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, qkv.dtype)
+    _expect("qkv", qkv, (P, M, (Hq + 2 * Hkv) * D), qkv.dtype)
+    _expect("positions", positions, (M,), torch.int32)
+    _expect("seq_ids", seq_ids, (M,), torch.int32)
+    B, max_pages = page_table.shape
+    _expect("page_table", page_table, (B, max_pages), torch.int32)
+    rot = 0 if turns is None else 2 * turns.shape[0]
+    _expect("turns", turns, (rot // 2,), torch.int64, optional=True)
+    _expect("q_out", q_out, (P, M, Hq, D), qkv.dtype, optional=True)
+    _same_device(qkv, positions, seq_ids, page_table, turns, *cache, q_out, workspace)
+    if q_out is None:
+        q_out = torch.empty((P, M, Hq, D), dtype=qkv.dtype, device=qkv.device)
+    if workspace is None:
+        workspace = _workspace(SPTP_WS_HEADER_BYTES, qkv.device)
+    k, v, ks, vs = cache
+    code = lib().sptp_rope_append_kv(
+        _ptr(qkv), _ptr(positions), _ptr(seq_ids), _ptr(page_table), _ptr(turns), P, M, Hq, Hkv, D, rot,
+        int(interleaved), float(gain), B, max_pages, num_pages, page_size, dt, kv_type, _ptr(q_out), _ptr(k), _ptr(v),
+        _ptr(ks), _ptr(vs), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check("sptp_rope_append_kv", code)
+    return q_out
+
+
+def sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D) -> int:
+    return int(lib().sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D))
+
+
+def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, workspace=None,
+                           stream=None, write_lse=True):
+    """Attention of one token per sequence over a paged cache: q [P,B,Hq,D],
+    page_table int32 [B,max_pages], seq_lens int32 [B] (0: an empty row);
+    scale defaults to D^-1/2; window 0: the whole sequence.  Returns
+    (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None)."""
+    P, B, Hq, D = q.shape
+    dt = _dtype_code(q)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, q.dtype)
+    max_pages = page_table.shape[-1]
+    _expect("page_table", page_table, (B, max_pages), torch.int32)
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("out", out, (P, B, Hq * D), q.dtype, optional=True)
+    _expect("lse", lse, (P, B, Hq), torch.float32, optional=True)
+    _same_device(q, *cache, page_table, seq_lens, out, lse, workspace)
+    if out is None:
+        out = torch.empty((P, B, Hq * D), dtype=q.dtype, device=q.device)
+    if lse is None and write_lse:
+        lse = torch.empty((P, B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _workspace(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), q.device)
+    k, v, ks, vs = cache
+    code = lib().sptp_paged_attn_decode(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(page_table), _ptr(seq_lens), P, B, Hq, Hkv, D, max_pages,
+        num_pages, page_size, int(window), D ** -0.5 if scale is None else float(scale), dt, kv_type, _ptr(out),
+        _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check("sptp_paged_attn_decode", code)
+    return out, lse

@@ -16,34 +16,7 @@
 
 using namespace sptp;
 
-namespace {
-
-constexpr int kMaxD = 16384;
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-
-bool dtype_ok(int dtype) { return dtype == SPTP_BF16 || dtype == SPTP_FP32; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
-    if (a == nullptr || b == nullptr || an == 0 || bn == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + bn && b0 < a0 + an;
-}
-
-// Sizes common to both entry points.
-int check_common(int M, int d, int F, int P, int dtype) {
-    if (!dtype_ok(dtype)) return SPTP_ERR_DTYPE;
-    if (M < 0 || d < 8 || d % 8 != 0 || d > kMaxD) return SPTP_ERR_SHAPE;
-    if (P < 1 || P > kMaxGroups) return SPTP_ERR_SHAPE;
-    if (F <= 0 || F % P != 0 || (F / P) % 8 != 0) return SPTP_ERR_SHAPE;
-    if (static_cast<long long>(M) * F >= (1ll << 40)) return SPTP_ERR_SHAPE;
-    return SPTP_OK;
-}
-
+namespace sptp {
 
 // Per-device SM count and compute capability, queried once per device.
 int device_info(DevInfo* out) {
@@ -67,11 +40,22 @@ int device_info(DevInfo* out) {
     return SPTP_OK;
 }
 
-DeviceStatus* ws_status(void* ws) { return reinterpret_cast<DeviceStatus*>(ws); }
+}  // namespace sptp
 
-int reset_status(void* ws, cudaStream_t s) {
-    return cudaMemsetAsync(ws, 0, sizeof(DeviceStatus), s) == cudaSuccess ? SPTP_OK : SPTP_ERR_CUDA;
+namespace {
+
+constexpr int kMaxD = 16384;
+
+// Sizes common to both entry points.
+int check_common(int M, int d, int F, int P, int dtype) {
+    if (!dtype_ok(dtype)) return SPTP_ERR_DTYPE;
+    if (M < 0 || d < 8 || d % 8 != 0 || d > kMaxD) return SPTP_ERR_SHAPE;
+    if (P < 1 || P > kMaxGroups) return SPTP_ERR_SHAPE;
+    if (F <= 0 || F % P != 0 || (F / P) % 8 != 0) return SPTP_ERR_SHAPE;
+    if (static_cast<long long>(M) * F >= (1ll << 40)) return SPTP_ERR_SHAPE;
+    return SPTP_OK;
 }
+
 
 // Readiness counters of the fused Delayed-TP stack: per module, rows normed
 // and down halves stored per 256-row block; gate/up halves per (shard, block).

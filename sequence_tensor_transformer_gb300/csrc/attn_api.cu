@@ -1,0 +1,268 @@
+// C ABI of the attention sub-layer between the QKV projection and the output
+// projection: the frequency table of the rotary positions (host), the
+// rotation, its append to a paged key-value cache and the attention of one
+// token per sequence over that cache.  Argument checks and launches; the
+// kernels are in rope.cu and paged_attn.cu.
+#include <cmath>
+#include <cstring>
+
+#include "launch.h"
+#include "sptp.h"
+#include "sptp_internal.h"
+
+using namespace sptp;
+
+namespace {
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// One buffer of a call: its bytes, and the alignment its pointer needs.
+struct Buf {
+    const void* p;
+    size_t bytes;
+    size_t align;
+};
+
+int check_aligned(const Buf* b, int n) {
+    for (int i = 0; i < n; ++i)
+        if (b[i].p != nullptr && !aligned_to(b[i].p, b[i].align)) return SPTP_ERR_SHAPE;
+    return SPTP_OK;
+}
+
+// No output on top of an input or of another output.
+int check_alias(const Buf* outs, int n_out, const Buf* ins, int n_in) {
+    for (int o = 0; o < n_out; ++o) {
+        for (int i = 0; i < n_in; ++i)
+            if (overlaps(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes)) return SPTP_ERR_ALIAS;
+        for (int j = o + 1; j < n_out; ++j)
+            if (overlaps(outs[o].p, outs[o].bytes, outs[j].p, outs[j].bytes)) return SPTP_ERR_ALIAS;
+    }
+    return SPTP_OK;
+}
+
+int check_heads(int P, int Hq, int Hkv, int D) {
+    if (P < 1 || P > kMaxGroups || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return SPTP_ERR_SHAPE;
+    if (D < 8 || D > 256 || D % 8 != 0) return SPTP_ERR_SHAPE;
+    if (static_cast<long long>(P) * (Hq + 2ll * Hkv) >= (1ll << 24)) return SPTP_ERR_SHAPE;
+    return SPTP_OK;
+}
+
+int check_cache(int P, int Hkv, int D, int B, int max_pages, int num_pages, int page_size, int dtype, int kv_type) {
+    if (!dtype_ok(dtype) || (kv_type != SPTP_KV_SAME && kv_type != SPTP_KV_E4M3)) return SPTP_ERR_DTYPE;
+    if (kv_type == SPTP_KV_E4M3 && dtype != SPTP_BF16) return SPTP_ERR_DTYPE;
+    if (kv_type == SPTP_KV_E4M3 && D % 16 != 0) return SPTP_ERR_SHAPE;
+    if (B < 0 || max_pages < 1 || num_pages < 1 || page_size < 16 || page_size % 16 != 0) return SPTP_ERR_SHAPE;
+    if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return SPTP_ERR_SHAPE;
+    // rows of the pool, exactly: each product is below 2^31 before the next
+    long long rows = static_cast<long long>(num_pages) * page_size;
+    if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
+    rows *= P;
+    if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
+    rows *= Hkv;
+    return rows < (1ll << 31) ? SPTP_OK : SPTP_ERR_SHAPE;
+}
+
+// Elements of an activation tensor, M rows; -1 if it is beyond any GPU.
+long long elems(long long P, long long M, long long heads, long long D) {
+    const long long row = P * heads * D;  // < 2^32
+    return M <= (1ll << 42) / row ? M * row : -1;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sptp_rope_turns(int rot, double theta, sptp_rope_scaling scaling, double factor, double orig_len, double alpha,
+                    double beta, unsigned long long* turns) {
+    if (!turns) return SPTP_ERR_NULL;
+    if (scaling < SPTP_ROPE_NONE || scaling > SPTP_ROPE_PARTS) return SPTP_ERR_UNIMPLEMENTED;
+    if (rot < 16 || rot > 256 || rot % 16 != 0 || !(theta > 1.0) || !std::isfinite(theta)) return SPTP_ERR_SHAPE;
+    if (scaling == SPTP_ROPE_NONE) factor = 1.0;
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return SPTP_ERR_SHAPE;
+    if (scaling == SPTP_ROPE_PARTS && (!(orig_len > 0.0) || !std::isfinite(orig_len) || !std::isfinite(alpha) ||
+                                       !std::isfinite(beta) || !(beta > alpha)))
+        return SPTP_ERR_SHAPE;
+    if (scaling == SPTP_ROPE_NTK) theta *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+    if (!std::isfinite(theta)) return SPTP_ERR_SHAPE;
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot);
+        if (scaling == SPTP_ROPE_LINEAR) f /= factor;
+        if (scaling == SPTP_ROPE_PARTS) {
+            const double c = std::fmin(1.0, std::fmax(0.0, (orig_len * f / two_pi - alpha) / (beta - alpha)));
+            f = c * f + (1.0 - c) * (f / factor);
+        }
+        // f <= 1, so f / 2 pi is below 1/6 of a turn
+        turns[i] = static_cast<unsigned long long>(std::nearbyint(std::ldexp(f / two_pi, 64)));
+    }
+    return SPTP_OK;
+}
+
+int sptp_rope(const void* x, const int* positions, const unsigned long long* turns, int P, int M, int H, int Hr,
+              int D, int rot, int interleaved, int transpose, float gain, sptp_dtype dtype, void* out,
+              void* cuda_stream) {
+    if (!turns || (M != 0 && (!x || !positions || !out))) return SPTP_ERR_NULL;
+    if (!dtype_ok(dtype)) return SPTP_ERR_DTYPE;
+    if (P < 1 || P > kMaxGroups || M < 0 || H < 1 || Hr < 1 || Hr > H || D < 8 || D > 256 || D % 8 != 0)
+        return SPTP_ERR_SHAPE;
+    if (static_cast<long long>(P) * H >= (1ll << 24) || rot < 16 || rot > D || rot % 16 != 0 || !std::isfinite(gain))
+        return SPTP_ERR_SHAPE;
+    const long long n = elems(P, M, H, D);
+    if (n < 0) return SPTP_ERR_SHAPE;
+    const size_t xb = static_cast<size_t>(n) * esize(dtype);
+    const Buf ins[] = {{x, xb, 16}, {positions, static_cast<size_t>(M) * 4, 4}, {turns, static_cast<size_t>(rot) * 4, 8}};
+    const Buf outs[] = {{out, xb, 16}};
+    int rc = check_aligned(ins, 3);
+    if (rc == SPTP_OK) rc = check_aligned(outs, 1);
+    if (rc != SPTP_OK) return rc;
+    const int skip = out == x ? 1 : 0;
+    if ((rc = check_alias(outs, 1, ins + skip, 3 - skip)) != SPTP_OK) return rc;
+    if (M == 0) return SPTP_OK;
+    DevInfo di;
+    if ((rc = device_info(&di)) != SPTP_OK) return rc;
+    RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x;
+    p.positions = positions;
+    p.turns = turns;
+    p.P = P;
+    p.M = M;
+    p.H = H;
+    p.Hr = Hr;
+    p.D = D;
+    p.rot = rot;
+    p.interleaved = interleaved;
+    p.transpose = transpose;
+    p.gain = gain;
+    p.out = out;
+    return cuda_status(launch_rope(p, dtype == SPTP_BF16, di.sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_ids, const int* page_table,
+                        const unsigned long long* turns, int P, int M, int Hq, int Hkv, int D, int rot,
+                        int interleaved, float gain, int B, int max_pages, int num_pages, int page_size,
+                        sptp_dtype dtype, sptp_kv_type kv_type, void* q_out, void* k_cache, void* v_cache,
+                        float* k_scale, float* v_scale, void* workspace, size_t ws_bytes, void* cuda_stream) {
+    const bool e4m3 = kv_type == SPTP_KV_E4M3;
+    if (!k_cache || !v_cache || !workspace || (rot != 0 && !turns) || (e4m3 && (!k_scale || !v_scale)) ||
+        (M != 0 && (!qkv || !positions || !seq_ids || !page_table || !q_out)))
+        return SPTP_ERR_NULL;
+    int rc = check_cache(P, Hkv, D, B, max_pages, num_pages, page_size, dtype, kv_type);
+    if (rc == SPTP_ERR_DTYPE) return rc;
+    int rc2 = check_heads(P, Hq, Hkv, D);
+    if (rc2 != SPTP_OK || rc != SPTP_OK) return SPTP_ERR_SHAPE;
+    if (M < 0 || rot < 0 || rot > D || rot % 16 != 0 || !std::isfinite(gain)) return SPTP_ERR_SHAPE;
+    const int H = Hq + 2 * Hkv;
+    const long long n = elems(P, M, H, D);
+    if (n < 0) return SPTP_ERR_SHAPE;
+    const size_t es = esize(dtype), rows = static_cast<size_t>(P) * num_pages * Hkv * page_size;
+    const size_t cb = rows * D * (e4m3 ? 1 : es), sb = e4m3 ? rows * 4 : 0;
+    const Buf ins[] = {{qkv, static_cast<size_t>(n) * es, 16},
+                       {positions, static_cast<size_t>(M) * 4, 4},
+                       {seq_ids, static_cast<size_t>(M) * 4, 4},
+                       {page_table, static_cast<size_t>(B) * max_pages * 4, 4},
+                       {rot != 0 ? turns : nullptr, static_cast<size_t>(rot) * 4, 8}};
+    const Buf outs[] = {{q_out, static_cast<size_t>(P) * M * Hq * D * es, 16}, {k_cache, cb, 16}, {v_cache, cb, 16},
+                        {workspace, SPTP_WS_HEADER_BYTES, kAlign},
+                        {e4m3 ? k_scale : nullptr, sb, 16}, {e4m3 ? v_scale : nullptr, sb, 16}};
+    if ((rc = check_aligned(ins, 5)) != SPTP_OK || (rc = check_aligned(outs, 6)) != SPTP_OK) return rc;
+    if (ws_bytes < SPTP_WS_HEADER_BYTES) return SPTP_ERR_WORKSPACE;
+    if ((rc = check_alias(outs, 6, ins, 5)) != SPTP_OK) return rc;
+    if (M == 0) return SPTP_OK;
+    DevInfo di;
+    if ((rc = device_info(&di)) != SPTP_OK) return rc;
+    RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = qkv;
+    p.positions = positions;
+    p.turns = turns;
+    p.P = P;
+    p.M = M;
+    p.H = H;
+    p.Hr = rot != 0 ? Hq + Hkv : 0;
+    p.D = D;
+    p.rot = rot;
+    p.interleaved = interleaved;
+    p.gain = gain;
+    p.out = q_out;
+    p.seq_ids = seq_ids;
+    p.page_table = page_table;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.B = B;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.status = ws_status(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+#ifdef SPTP_BOUNDS_CHECK
+    if ((rc = reset_status(workspace, s)) != SPTP_OK) return rc;
+#endif
+    return cuda_status(launch_rope_append(p, dtype == SPTP_BF16, e4m3, di.sms, s));
+}
+
+size_t sptp_paged_attn_workspace_size(int P, int B, int Hq, int Hkv, int D) {
+    if (check_heads(P, Hq, Hkv, D) != SPTP_OK || B < 0) return 0;
+    return SPTP_WS_HEADER_BYTES;
+}
+
+int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* page_table, const int* seq_lens, int P, int B, int Hq,
+                           int Hkv, int D, int max_pages, int num_pages, int page_size, int window, float scale,
+                           sptp_dtype dtype, sptp_kv_type kv_type, void* out, float* lse, void* workspace,
+                           size_t ws_bytes, void* cuda_stream) {
+    const bool e4m3 = kv_type == SPTP_KV_E4M3;
+    if (!k_cache || !v_cache || !workspace || (e4m3 && (!k_scale || !v_scale)) ||
+        (B != 0 && (!q || !page_table || !seq_lens || !out)))
+        return SPTP_ERR_NULL;
+    int rc = check_cache(P, Hkv, D, B, max_pages, num_pages, page_size, dtype, kv_type);
+    if (rc == SPTP_ERR_DTYPE) return rc;
+    int rc2 = check_heads(P, Hq, Hkv, D);
+    if (rc2 != SPTP_OK || rc != SPTP_OK) return SPTP_ERR_SHAPE;
+    if (window < 0 || !std::isfinite(scale)) return SPTP_ERR_SHAPE;
+    const long long n = elems(P, B, Hq, D);
+    if (n < 0) return SPTP_ERR_SHAPE;
+    const size_t es = esize(dtype), rows = static_cast<size_t>(P) * num_pages * Hkv * page_size;
+    const size_t cb = rows * D * (e4m3 ? 1 : es), sb = e4m3 ? rows * 4 : 0, qb = static_cast<size_t>(n) * es;
+    const size_t need = sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D);
+    const Buf ins[] = {{q, qb, 16}, {k_cache, cb, 16}, {v_cache, cb, 16},
+                       {e4m3 ? k_scale : nullptr, sb, 16}, {e4m3 ? v_scale : nullptr, sb, 16},
+                       {page_table, static_cast<size_t>(B) * max_pages * 4, 4},
+                       {seq_lens, static_cast<size_t>(B) * 4, 4}};
+    const Buf outs[] = {{out, qb, 16}, {lse, static_cast<size_t>(P) * B * Hq * 4, 16}, {workspace, need, kAlign}};
+    if ((rc = check_aligned(ins, 7)) != SPTP_OK || (rc = check_aligned(outs, 3)) != SPTP_OK) return rc;
+    if (ws_bytes < need) return SPTP_ERR_WORKSPACE;
+    if ((rc = check_alias(outs, 3, ins, 7)) != SPTP_OK) return rc;
+    if (B == 0) return SPTP_OK;
+    DevInfo di;
+    if ((rc = device_info(&di)) != SPTP_OK) return rc;
+    PagedAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = q;
+    p.k = k_cache;
+    p.v = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.P = P;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.window = window;
+    p.scale = scale;
+    p.out = out;
+    p.lse = lse;
+    p.status = ws_status(workspace);
+    return cuda_status(launch_paged_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+}  // extern "C"

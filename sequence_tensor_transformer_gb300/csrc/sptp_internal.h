@@ -36,6 +36,10 @@ enum : int {
     kWhereFusedGateUp = 11,
     kWherePermIndex = 12,
     kWherePermStage = 13,
+    kWhereKvSlot = 14,         // a token's sequence, position or page outside its range
+    kWhereKvPage = 15,         // a sequence's length or page outside its range
+    kWhereKvFull = 16,
+    kWhereKvEmpty = 17,
     // bounds-checked builds (SPTP_BOUNDS_CHECK): what failed its check
     kWhereBoundsTile = 20,     // a decoded tile or row index outside its range
     kWhereBoundsCounter = 21,  // a readiness-counter index
@@ -223,6 +227,47 @@ cudaError_t launch_simt_gemm(const SimtGemmParams& p, Epi epi, cudaStream_t s);
 cudaError_t launch_permute_ffn(const void* W1g, const void* W1u, const void* W2, const int* perm, int L, int d,
                                int F, bool bf16, void* W1g_out, void* W1u_out, void* W2_out, DeviceStatus* st,
                                int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- rotary positions, paged cache
+struct RopeParams {
+    const void* x;                     // [P][M][H][D] (append: the QKV rows, H = Hq + 2 Hkv)
+    const int* positions;              // [M]
+    const unsigned long long* turns;   // [rot/2]
+    int P, M, H, Hr, D, rot;           // heads [0, Hr) of a row are rotated
+    int interleaved, transpose;
+    float gain;
+    void* out;                         // rope: [P][M][H][D]; append: q_out [P][M][Hq][D]
+    // append only
+    const int* seq_ids;                // [M]
+    const int* page_table;             // [B][max_pages]
+    int Hq, Hkv, B, max_pages, num_pages, page_size;
+    void* k_cache;                     // [P][num_pages][Hkv][page_size][D]
+    void* v_cache;
+    float* k_scale;                    // E4M3: [P][num_pages][Hkv][page_size]
+    float* v_scale;
+    DeviceStatus* status;
+};
+
+cudaError_t launch_rope(const RopeParams& p, bool bf16, int num_sms, cudaStream_t s);
+cudaError_t launch_rope_append(const RopeParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
+
+struct PagedAttnParams {
+    const void* q;          // [P][B][Hq][D]
+    const void* k;          // [P][num_pages][Hkv][page_size][D]
+    const void* v;
+    const float* k_scale;   // E4M3: [P][num_pages][Hkv][page_size]
+    const float* v_scale;
+    const int* page_table;  // [B][max_pages]
+    const int* seq_lens;    // [B]
+    int P, B, Hq, Hkv, D;
+    int max_pages, num_pages, page_size, window;
+    float scale;
+    void* out;              // [P][B][Hq][D]
+    float* lse;             // [P][B][Hq] or nullptr
+    DeviceStatus* status;
+};
+
+cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- argument checks (api.cu)
 // Every argument check of sptp_ffn_forward_ex, with no CUDA call.

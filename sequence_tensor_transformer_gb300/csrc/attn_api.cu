@@ -53,13 +53,30 @@ int check_cache(int P, int Hkv, int D, int B, int max_pages, int num_pages, int 
     if (kv_type == SPTP_KV_E4M3 && D % 16 != 0) return SPTP_ERR_SHAPE;
     if (B < 0 || max_pages < 1 || num_pages < 1 || page_size < 16 || page_size % 16 != 0) return SPTP_ERR_SHAPE;
     if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return SPTP_ERR_SHAPE;
-    // rows of the pool, exactly: each product is below 2^31 before the next
+    // rows of the pool (a TMA coordinate), each product below 2^31 before the next
     long long rows = static_cast<long long>(num_pages) * page_size;
     if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
     rows *= P;
     if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
     rows *= Hkv;
     return rows < (1ll << 31) ? SPTP_OK : SPTP_ERR_SHAPE;
+}
+
+// Query heads whose parts one CTA of the attention may leave, at most.
+int part_heads(int group) { return group < 32 ? group : 32; }
+
+struct PagedLayout {
+    size_t parts, ml, o, total;
+};
+
+PagedLayout paged_layout(int group, int D) {
+    PagedLayout L;
+    const size_t rows = static_cast<size_t>(kPagedMaxCtas) * 2 * part_heads(group);
+    L.parts = SPTP_WS_HEADER_BYTES;
+    L.ml = L.parts + align_up(sizeof(PagedAttnPart) * kPagedMaxCtas);
+    L.o = L.ml + align_up(rows * sizeof(float2));
+    L.total = L.o + align_up(rows * D * sizeof(float));
+    return L;
 }
 
 // Elements of an activation tensor, M rows; -1 if it is beyond any GPU.
@@ -207,7 +224,7 @@ int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_id
 
 size_t sptp_paged_attn_workspace_size(int P, int B, int Hq, int Hkv, int D) {
     if (check_heads(P, Hq, Hkv, D) != SPTP_OK || B < 0) return 0;
-    return SPTP_WS_HEADER_BYTES;
+    return paged_layout(Hq / Hkv, D).total;
 }
 
 int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -262,6 +279,10 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
     p.out = out;
     p.lse = lse;
     p.status = ws_status(workspace);
+    const PagedLayout lay = paged_layout(Hq / Hkv, D);
+    p.parts = reinterpret_cast<PagedAttnPart*>(mptr(workspace, lay.parts));
+    p.part_ml = reinterpret_cast<float2*>(mptr(workspace, lay.ml));
+    p.part_o = reinterpret_cast<float*>(mptr(workspace, lay.o));
     return cuda_status(launch_paged_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 

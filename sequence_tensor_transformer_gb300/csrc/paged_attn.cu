@@ -1,13 +1,7 @@
-// Attention of one token per sequence over a paged key-value cache:
-//     s_j = scale * q . k_j,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m).
-// One pass over the keys with a running maximum m, sum l and output o; a new
-// maximum m' scales l and o by e^(m - m').
-//
-// One CTA per (shard, sequence, key/value head, up to 8 of its query heads);
-// its warps take every fourth key, each with statistics of its own, and are
-// joined at the end.
+// The paged attention's dispatch over the cache's element type, and the join of
+// the items that were split over several CTAs (paged_attn.cuh has the main
+// kernel).
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "sptp.h"
 #include "sptp_ptx.cuh"
@@ -16,127 +10,132 @@ namespace sptp {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kHeads = 8;  // query heads per CTA
-constexpr int kMaxD = 256;
-constexpr int kPer = kMaxD / 32;
+constexpr int kJoinThreads = 256;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Block (h, i): query head h of the item that begins in CTA i's share and goes
+// on in later ones, if there is one:  m = max m_k,  out = sum e^(m_k - m) o_k /
+// sum e^(m_k - m) l_k over its parts k in ascending order per warp, then over
+// the warps.  A warp takes every eighth part, its lanes the elements.  Block
+// (0, 0) also sums up the CTAs' status words.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas) {
+    constexpr int kWarps = kJoinThreads / 32, kPer = 8;  // elements per lane: D <= 256
+    __shared__ float weight[kPagedMaxCtas];
+    __shared__ float o[kWarps][256];
+    __shared__ float red[2][kWarps];
+    __shared__ int first_bad;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x, i = blockIdx.y;
+    if (h == 0 && i == 0) {
+        if (tid == 0) first_bad = ctas;
+        __syncthreads();
+        for (int k = tid; k < ctas; k += kJoinThreads)
+            if (p.parts[k].status != 0) atomicMin(&first_bad, k);
+        __syncthreads();
+        if (tid == 0) {
+            DeviceStatus st = {0, 0, 0, 0, 0};
+            if (first_bad < ctas) {
+                const PagedAttnPart& bad = p.parts[first_bad];
+                st.code = bad.status;
+                st.where = bad.where;
+                st.block = first_bad;
+                st.info = bad.info;
+            }
+            *p.status = st;
+        }
+    }
+    const int n = p.parts[i].join_parts;
+    if (n < 2 || i + n > ctas) return;
+    const int b = p.parts[i].b, j = p.parts[i].j;
+    const int hb = j % p.head_blocks, sk = j / p.head_blocks, group = p.Hq / p.Hkv;
+    const int h0 = hb * p.heads_per_item;
+    if (h >= min(p.heads_per_item, group - h0)) return;
+    // part k lies in slot 0 of CTA i + k; the first one in slot 1
+    auto row_of = [&](int k) { return ((i + k) * 2ll + (k == 0 ? 1 : 0)) * p.heads_per_item + h; };
+    float top = -INFINITY;
+    float2 ml[(kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads];
+    int c = 0;
+    for (int k = tid; k < n; k += kJoinThreads, ++c) {
+        ml[c] = p.part_ml[row_of(k)];
+        top = fmaxf(top, ml[c].x);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-
-template <typename Q, typename KV>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
-    __shared__ float qs[kHeads][kMaxD];
-    __shared__ float os[kWarps][kHeads][kMaxD];
-    __shared__ float ms[kWarps][kHeads], ls[kWarps][kHeads];
-    constexpr bool kCodes = sizeof(KV) == 1;
-    const int group = p.Hq / p.Hkv, hb = (group + kHeads - 1) / kHeads;
-    long long u = blockIdx.x;
-    const int h0 = static_cast<int>(u % hb) * kHeads;
-    u /= hb;
-    const int kvh = static_cast<int>(u % p.Hkv);
-    u /= p.Hkv;
-    const int shard = static_cast<int>(u % p.P), b = static_cast<int>(u / p.P);
-    const int nh = min(kHeads, group - h0);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int most = p.max_pages * p.page_size;
-    int len = __ldg(p.seq_lens + b);
-    if ((len < 0 || len > most) && threadIdx.x == 0) atomicCAS(&p.status->code, 0, SPTP_ERR_SHAPE);
-    len = max(0, min(len, most));
-    const int start = p.window > 0 ? max(0, len - p.window) : 0;
-    const long long qrow = (static_cast<long long>(shard) * p.B + b) * p.Hq + kvh * group + h0;
-    for (int i = threadIdx.x; i < nh * p.D; i += kWarps * 32)
-        qs[i / p.D][i % p.D] = static_cast<float>(static_cast<const Q*>(p.q)[qrow * p.D + i]) * p.scale;
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) red[0][warp] = top;
     __syncthreads();
-    float m[kHeads], l[kHeads], o[kHeads][kPer];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[h][i] = 0.f;
-    }
-    for (int j = start + warp; j < len; j += kWarps) {
-        const int page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + j / p.page_size);
-        const bool ok = page >= 0 && page < p.num_pages;
-        if (!ok && lane == 0) atomicCAS(&p.status->code, 0, SPTP_ERR_SHAPE);
-        const long long row = ((static_cast<long long>(shard) * p.num_pages + (ok ? page : 0)) * p.Hkv + kvh) *
-                                  p.page_size + j % p.page_size;
-        float ksc = 1.f, vsc = 1.f;
-        if (kCodes && ok) {
-            ksc = p.k_scale[row];
-            vsc = p.v_scale[row];
-        }
-        float kf[kPer], vf[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int d = lane + 32 * i;
-            const bool in = ok && d < p.D;
-            kf[i] = in ? static_cast<float>(static_cast<const KV*>(p.k)[row * p.D + d]) : 0.f;
-            vf[i] = in ? static_cast<float>(static_cast<const KV*>(p.v)[row * p.D + d]) * vsc : 0.f;
-        }
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            if (h >= nh) break;
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (lane + 32 * i < p.D) s = fmaf(qs[h][lane + 32 * i], kf[i], s);
-            s = warp_sum(s) * ksc;
-            const float top = fmaxf(m[h], s);
-            const float old = m[h] == top ? 1.f : expf(m[h] - top);
-            const float w = top == -INFINITY ? 0.f : expf(s - top);
-            m[h] = top;
-            l[h] = l[h] * old + w;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) o[h][i] = fmaf(o[h][i], old, w * vf[i]);
-        }
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[0][w]);
+    float sum = 0.f;
+    c = 0;
+    for (int k = tid; k < n; k += kJoinThreads, ++c) {
+        const float f = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - top);
+        weight[k] = f;
+        sum = fmaf(f, ml[c].y, sum);
     }
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        if (lane == 0) {
-            ms[warp][h] = m[h];
-            ls[warp][h] = l[h];
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) os[warp][h][lane + 32 * i] = o[h][i];
-    }
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) red[1][warp] = sum;
     __syncthreads();
-    for (int i = threadIdx.x; i < nh * p.D; i += kWarps * 32) {
-        const int h = i / p.D, d = i % p.D;
-        float top = -INFINITY, sum = 0.f, acc = 0.f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ms[w][h]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ms[w][h] == -INFINITY ? 0.f : expf(ms[w][h] - top);
-            sum = fmaf(ls[w][h], f, sum);
-            acc = fmaf(os[w][h][d], f, acc);
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += red[1][w];
+    float acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < n; k += kWarps) {
+        const float f = weight[k];
+        const float* row = p.part_o + row_of(k) * p.D;
+#pragma unroll
+        for (int e = 0; e < kPer / 4; ++e) {
+            const int d = e * 128 + lane * 4;
+            if (d < p.D) {
+                const float4 v = *reinterpret_cast<const float4*>(row + d);
+                acc[4 * e] = fmaf(f, v.x, acc[4 * e]);
+                acc[4 * e + 1] = fmaf(f, v.y, acc[4 * e + 1]);
+                acc[4 * e + 2] = fmaf(f, v.z, acc[4 * e + 2]);
+                acc[4 * e + 3] = fmaf(f, v.w, acc[4 * e + 3]);
+            }
         }
-        static_cast<Q*>(p.out)[qrow * p.D + i] = static_cast<Q>(sum > 0.f ? acc / sum : 0.f);
-        if (p.lse != nullptr && d == 0) p.lse[qrow + h] = sum > 0.f ? top + logf(sum) : -INFINITY;
     }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[warp][(e >> 2) * 128 + lane * 4 + (e & 3)] = acc[e];
+    __syncthreads();
+    const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
+    const long long qrow = (static_cast<long long>(shard) * p.B + b) * p.Hq + kvh * group + h0 + h;
+    if (tid < p.D) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += o[w][tid];
+        v = sum == 0.f ? 0.f : v / sum;
+        static_cast<T*>(p.out)[qrow * p.D + tid] = static_cast<T>(v);
+    }
+    if (p.lse != nullptr && tid == 0) p.lse[qrow] = sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
-    (void)num_sms;
-    const int group = p.Hq / p.Hkv;
-    const long long grid = static_cast<long long>(p.B) * p.P * p.Hkv * ((group + kHeads - 1) / kHeads);
-    if (grid > 0x7fffffffll || (e4m3 && !bf16)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(DeviceStatus), s);
+cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
+    if (e4m3 && !bf16) return cudaErrorInvalidValue;
+    int ctas = 0;
+    cudaError_t e = !bf16  ? launch_paged_attn_f32(p, num_sms, &ctas, s)
+                    : e4m3 ? launch_paged_attn_e4m3(p, num_sms, &ctas, s)
+                           : launch_paged_attn_bf16(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
-    const int g = static_cast<int>(grid);
-    if (!bf16)
-        paged_attn_kernel<float, float><<<g, kWarps * 32, 0, s>>>(p);
-    else if (e4m3)
-        paged_attn_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<g, kWarps * 32, 0, s>>>(p);
-    else
-        paged_attn_kernel<__nv_bfloat16, __nv_bfloat16><<<g, kWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
+    // The join is launched beside the main kernel's end (a programmatic
+    // dependency): it waits for the parts on the device.
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(p.heads_per_item, ctas);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return bf16 ? cudaLaunchKernelEx(&cfg, paged_attn_join<__nv_bfloat16>, p, ctas)
+                : cudaLaunchKernelEx(&cfg, paged_attn_join<float>, p, ctas);
 }
 
 }  // namespace sptp

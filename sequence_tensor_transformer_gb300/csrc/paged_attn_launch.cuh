@@ -1,0 +1,40 @@
+// Launch of the paged attention with one consumer class.
+#pragma once
+
+#include "paged_attn.cuh"
+
+namespace sptp {
+namespace paged {
+
+template <class C>
+cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    // heads of a group, in equal blocks of at most HEADS
+    const int group = p.Hq / p.Hkv;
+    p.head_blocks = (group + C::HEADS - 1) / C::HEADS;
+    p.heads_per_item = (group + p.head_blocks - 1) / p.head_blocks;
+    p.head_blocks = (group + p.heads_per_item - 1) / p.heads_per_item;
+    p.items_per_seq = p.P * p.Hkv * p.head_blocks;
+    // the largest boxes that never cross a page
+    p.box_rows = 16;
+    while (p.box_rows < C::TK && p.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+    const uint64_t rows = static_cast<uint64_t>(p.P) * p.num_pages * p.Hkv * p.page_size;
+    const int es = C::F32 ? 4 : (C::CODES ? 1 : 2);
+    const uint32_t inner = C::F32 ? C::DP : 128 / es;
+    if (!encode_map_rows(&p.map_k, p.k, es, p.D, rows, inner, p.box_rows) ||
+        !encode_map_rows(&p.map_v, p.v, es, p.D, rows, inner, p.box_rows))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<C>::BYTES);
+    if (e != cudaSuccess) return e;
+    // one resident wave, or a CTA per tile where the table cannot hold as many
+    long long grid = static_cast<long long>(num_sms) * C::CTAS;
+    const long long span = static_cast<long long>(p.max_pages) * p.page_size;
+    const long long most = (span + C::TK - 1) / C::TK * p.B * p.items_per_seq;
+    if (grid > most) grid = most;
+    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    *ctas = static_cast<int>(grid);
+    paged_attn_kernel<C><<<*ctas, kThreads, Smem<C>::BYTES, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace sptp

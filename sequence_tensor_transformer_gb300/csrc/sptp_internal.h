@@ -251,7 +251,18 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 
+// What one CTA of the attention leaves for the join: its status, and the
+// item that begins in its share and goes on in later ones (join_parts shares
+// in all; 0: none).
+struct PagedAttnPart {
+    int status, where, info;
+    int join_parts, b, j;
+    int pad[2];
+};
+constexpr int kPagedMaxCtas = 320;  // CTAs of one resident wave, at most
+
 struct PagedAttnParams {
+    CUtensorMap map_k, map_v;  // the pools as [P * num_pages * Hkv * page_size][D], boxes of box_rows rows
     const void* q;          // [P][B][Hq][D]
     const void* k;          // [P][num_pages][Hkv][page_size][D]
     const void* v;
@@ -261,13 +272,29 @@ struct PagedAttnParams {
     const int* seq_lens;    // [B]
     int P, B, Hq, Hkv, D;
     int max_pages, num_pages, page_size, window;
+    int box_rows;           // divides page_size and a tile
+    int heads_per_item, head_blocks;  // query heads of an item, items per key/value head
+    int items_per_seq;      // P * Hkv * head_blocks
     float scale;
     void* out;              // [P][B][Hq][D]
     float* lse;             // [P][B][Hq] or nullptr
     DeviceStatus* status;
+    PagedAttnPart* parts;   // [CTAs]
+    float2* part_ml;        // [CTAs][2][heads_per_item]: maximum (in units of log 2) and sum
+    float* part_o;          // [CTAs][2][heads_per_item][D]
 };
 
-cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
+// The paged attention's tensor maps: rows of `inner` elements, boxes of
+// box_inner x box_rows; bf16 and bytes with 128-byte swizzle, fp32 without.
+bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
+                     uint32_t box_inner, uint32_t box_rows);
+
+// One launch per element type (paged_attn_{bf16,e4m3,f32}.cu): fills in the
+// maps, the boxes and the split of the heads.
+cudaError_t launch_paged_attn_bf16(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn_e4m3(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn_f32(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- argument checks (api.cu)
 // Every argument check of sptp_ffn_forward_ex, with no CUDA call.

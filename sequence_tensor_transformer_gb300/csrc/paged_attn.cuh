@@ -8,18 +8,22 @@
 // 4 D flops per query head.  What the layout is for is to keep the reads going
 // on every SM whatever the lengths are:
 //  - An item is one (sequence, shard, key/value head) with the query heads that
-//    read it (more than kMaxHeads of them: several items).  Its keys are cut
-//    into tiles of TK; the tiles of all items, in order, are dealt out to the
-//    CTAs of one resident wave in equal contiguous shares.  Every CTA works
-//    out its own share from the lengths, so nothing depends on the host
-//    knowing them.  An item that crosses a share's end leaves its parts'
-//    (m, l, o) in the workspace; a second launch (paged_attn_join) joins them in
-//    a fixed order.
+//    read it (more than HEADS of them: several items).  Its keys are cut into
+//    tiles of TK; the tiles of all items, in order, are dealt out to the CTAs
+//    of one resident wave in contiguous shares of equal cost: kTileCost a tile
+//    and kItemCost an item (its first loads, its end).  Every CTA works out its
+//    own share from the lengths, so nothing depends on the host knowing them.
+//    An item that crosses a share's end leaves its parts' (m, l, o) in the
+//    workspace; a second launch (paged_attn_join) joins them in a fixed order.
 //  - One producer warp walks over the share and keeps a ring of tiles filled by
-//    TMA (one box per page and 128 bytes of row), running ahead across item
-//    borders, so that the reads never wait for the arithmetic of an item's end.
-//  - Four consumer warps take a quarter of each tile's keys, each with
-//    statistics of its own, and meet only where an item ends.
+//    TMA (one box per page and 128 bytes of row, an item's queries with its
+//    first tile), running ahead across item borders, so that the reads never
+//    wait for the arithmetic.
+//  - Four consumer warps score a quarter of each tile's keys, agree on the new
+//    maxima, leave the weights in shared memory, and then each sums up all the
+//    tile's weighted values for a quarter of the row's elements.  Two barriers
+//    a tile; in return no warp has outputs of another's elements, and an item's
+//    end costs next to nothing, which is what batches of short rows are made of.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,6 +45,21 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
+// The same, and whether `ok` holds in every thread.  A warp whose bounded wait
+// for a tile gave up still comes to the barrier, and all four leave together:
+// none is left waiting there.
+__device__ __forceinline__ bool consumers_agree(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(static_cast<uint32_t>(ok)), "n"(kConsumers * 32)
+        : "memory");
+    return all != 0;
+}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -76,22 +95,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- consumers
-// A consumer class holds one warp's query fragments and statistics and has
-//   TK, STAGES, CTAS, HEADS, DP        tile and launch shape
-//   ROW_BYTES, BOXES, K_BYTES          a key's bytes, boxes per row, a stage's keys
-//   begin(p, q row, heads)             a new item
-//   tile(stage, lo, hi)                keys [lo, hi) of the stage's tile
-//   stats(ms, ls), add(obuf)           at an item's end
+// A consumer class is one warp's part of the arithmetic:
+//   HEADS, DP              query heads of an item, elements of a row, at most
+//   TK                     keys of a tile
+//   ROW_BYTES, BOXES       a key's bytes, TMA boxes per row
+//   begin(q, heads)        a new item; q its rows in shared memory
+//   tile(...)              keys [lo, hi) of a tile; false if a warp's `ok` is
+//   finish(...)            an item's end, or its part's
 
 // Tensor-core consumer for a bf16 or E4M3 cache, DP >= D elements per row, up
 // to 8 NT query heads.
 //
 // Both products have the keys or the value's elements as the 16 rows of
 // m16n8k16 and the query heads as its 8 columns, so that a group of up to 8
-// heads wastes nothing:  S^T = K q^T  and  O^T = V^T W^T.  A thread then holds
-// the scores, statistics and outputs of the same two heads throughout, and
-// the weights go from one product to the other through a transpose within the
-// warp (movmatrix), not through shared memory.
+// heads wastes nothing:  S^T = K q^T  and  O^T = V^T W^T.  A thread holds the
+// scores, statistics and outputs of the same two heads (of every eight)
+// throughout.
 //
 // E4M3: a code's 7 magnitude bits, moved into a bf16's exponent and mantissa,
 // are the value times 2^-120, subnormal codes among them, so that a pair of
@@ -108,22 +127,16 @@ struct TcConsumer {
     static constexpr int HEADS = 8 * NT;
     static constexpr int ROW_BYTES = DP * (CODES ? 1 : 2);
     static constexpr int BOXES = ROW_BYTES / 128;
-    // 32 KB a stage, or 64 keys where a row is wider
-    static constexpr int TK = ROW_BYTES == 128 ? 128 : 64;
+    static constexpr int TK = ROW_BYTES == 128 && NT == 1 ? 128 : 64;  // 32 KB a tile, or 64 keys
+    static constexpr int Q_STRIDE = DP * 2 + 16;                        // bytes; 8 rows in distinct banks
+    static constexpr int W_STRIDE = TK * 2 + 16;
+    static constexpr int W_BYTES = HEADS * W_STRIDE;
+    static constexpr int CTAS = NT < 4 && ROW_BYTES <= 256 ? 2 : 1;
     static constexpr int K_BYTES = TK * ROW_BYTES;
-    static constexpr int SCALE_BYTES = CODES ? TK * 4 : 0;
-    static constexpr int STAGE_BYTES = 2 * K_BYTES;
-    // two CTAs per SM where shared memory and registers allow
-    static constexpr int CTAS =
-        NT < 4 && STAGE_BYTES <= 32768 &&
-                98304 + 6 * SCALE_BYTES + HEADS * (DP + 4) * 4 + 10 * HEADS * 4 + 2048 <= 113 * 1024
-            ? 2
-            : 1;
-    static constexpr int STAGES = (CTAS == 2 ? 98304 : 196608) / STAGE_BYTES;
-    static constexpr int SLICES = TK / (16 * kConsumers);
-    static constexpr int KSTEPS = DP / 16;  // of 16 elements of q and k
-    static constexpr int MTILES = DP / 16;  // of 16 elements of v
-    static_assert(ROW_BYTES % 128 == 0 && STAGES >= 3 && STAGES <= kMaxStages, "layout");
+    static constexpr int SLICES = TK / (16 * kConsumers);  // of 16 keys, a warp's
+    static constexpr int KSTEPS = DP / 16;                 // of 16 elements of q and k
+    static constexpr int MTILES = DP / 16 / kConsumers;    // of 16 elements of v, a warp's
+    static_assert(ROW_BYTES % 128 == 0 && (!CODES || MTILES % 2 == 0), "layout");
 
     uint32_t qf[KSTEPS][NT][2];
     float m[NT][2], l[NT][2], qs[NT][2];
@@ -137,25 +150,30 @@ struct TcConsumer {
     static __device__ __forceinline__ uint32_t odd_pair(uint32_t c) {
         return (c & 0x80008000u) | ((c >> 4) & 0x07f007f0u);
     }
+    // element of the head's row in o[t][..][2 r + ..]
+    static __device__ __forceinline__ int elem(int t, int r) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+        return warp * (DP / kConsumers) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
+    }
 
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, long long qrow, int heads) {
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, int heads) {
         const int lane = threadIdx.x & 31, g = lane >> 2, i = lane & 3;
         const float to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + g;
-            const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(p.q) + (qrow + h) * p.D;
+            const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(q + h * Q_STRIDE);
 #pragma unroll
             for (int k = 0; k < KSTEPS; ++k) {
                 if constexpr (!CODES) {
                     const int d = k * 16 + i * 2;
-                    qf[k][nt][0] = h < heads && d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(row + d)) : 0u;
-                    qf[k][nt][1] = h < heads && d + 8 < p.D ? __ldg(reinterpret_cast<const uint32_t*>(row + d + 8)) : 0u;
+                    qf[k][nt][0] = h < heads && d < p.D ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+                    qf[k][nt][1] = h < heads && d + 8 < p.D ? *reinterpret_cast<const uint32_t*>(row + d + 8) : 0u;
                 } else {
                     // elements 4i .. 4i+3 of the step, even ones and odd ones
                     const int d = k * 16 + i * 4;
                     uint2 u = make_uint2(0, 0);
-                    if (h < heads && d < p.D) u = __ldg(reinterpret_cast<const uint2*>(row + d));
+                    if (h < heads && d < p.D) u = *reinterpret_cast<const uint2*>(row + d);
                     qf[k][nt][0] = __byte_perm(u.x, u.y, 0x5410);
                     qf[k][nt][1] = __byte_perm(u.x, u.y, 0x7632);
                 }
@@ -173,7 +191,7 @@ struct TcConsumer {
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 1) - 127;
-                // 2^(100 - e) in two factors, each within bf16's range
+                // 2^(100 - e) in two factors, each within fp32's range
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 100 - max(e, -26)) << 23);
                 const float up2 = e < -26 ? __uint_as_float(static_cast<uint32_t>(127 - 26 - e) << 23) : 1.f;
 #pragma unroll
@@ -203,111 +221,147 @@ struct TcConsumer {
         vexp = 100;
     }
 
-    __device__ __forceinline__ void tile(uint32_t stage, const float* scales, int lo, int hi) {
+    // stage: the tile in shared memory (K, then V); scales: E4M3, of its keys;
+    // maxima [kConsumers][HEADS], [kConsumers] and weights (W_BYTES): this
+    // tile's, of all the warps
+    __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float* scales, float* maxima, uint8_t* weights,
+                                         int lo, int hi) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
         const int key0 = warp * 16 * SLICES;  // this warp's keys of the tile
-        if (key0 >= hi || key0 + 16 * SLICES <= lo) return;
-        const bool partial = lo > key0 || hi < key0 + 16 * SLICES;
+        const bool some = key0 < hi && key0 + 16 * SLICES > lo;
+        const bool partial = lo > 0 || hi < TK;
         float s[SLICES][NT][4];
-        // S^T = K q^T
-        {
+        float vs[SLICES][2], vtop = 0.f;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+        if (some) {
+            // S^T = K q^T
             const uint32_t rowa = stage + (key0 + (lane & 15)) * 128;
             const uint32_t x = static_cast<uint32_t>((lane >> 4) ^ (lane & 7)) << 4;
 #pragma unroll
             for (int sl = 0; sl < SLICES; ++sl) {
+                float s2[NT][4];  // a second chain of sums
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[sl][nt][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[sl][nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
                 for (int c = 0; c < ROW_BYTES / 32; ++c) {  // two 16-byte chunks at a time
                     uint32_t a[4];
                     ldmatrix_x4(rowa + sl * 16 * 128 + (c >> 2) * TK * 128 + (x ^ ((c & 3) << 5)), a);
                     if constexpr (!CODES) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_bf16(s[sl][nt], a, qf[c][nt][0], qf[c][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_bf16(c & 1 ? s2[nt] : s[sl][nt], a, qf[c][nt][0], qf[c][nt][1]);
                     } else {
                         const uint32_t a0[4] = {even_pair(a[0]), even_pair(a[1]), odd_pair(a[0]), odd_pair(a[1])};
                         const uint32_t a1[4] = {even_pair(a[2]), even_pair(a[3]), odd_pair(a[2]), odd_pair(a[3])};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_bf16(s[sl][nt], a0, qf[2 * c][nt][0], qf[2 * c][nt][1]);
-                            mma_bf16(s[sl][nt], a1, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
+                            mma_bf16(s2[nt], a1, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
                         }
                     }
                 }
-            }
-        }
-        // scores in units of log 2, and the keys outside [lo, hi) away
-        float vs[SLICES][2], vtop = 0.f;
+                // scores in units of log 2, and the keys outside [lo, hi) away
 #pragma unroll
-        for (int sl = 0; sl < SLICES; ++sl) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int key = key0 + sl * 16 + g + 8 * r;
-                const bool in = !partial || (key >= lo && key < hi);
-                float ks = 1.f;
-                if constexpr (CODES) {
-                    ks = scales[key];
-                    vs[sl][r] = in ? scales[TK + key] : 0.f;
-                    vtop = fmaxf(vtop, vs[sl][r]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& v = s[sl][nt][2 * r + e];
-                        v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
+                for (int r = 0; r < 2; ++r) {
+                    const int key = key0 + sl * 16 + g + 8 * r;
+                    const bool in = !partial || (key >= lo && key < hi);
+                    float ks = 1.f;
+                    if constexpr (CODES) {
+                        ks = scales[key];
+                        vs[sl][r] = in ? scales[TK + key] : 0.f;
+                        vtop = fmaxf(vtop, vs[sl][r]);
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& v = s[sl][nt][2 * r + e];
+                            v += s2[nt][2 * r + e];
+                            v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
+                            top[nt][e] = fmaxf(top[nt][e], v);
+                        }
+                }
             }
         }
+        // the tile's maxima, of all the warps
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], off));
+            if constexpr (CODES) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+        }
+        if (lane < 4) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                *reinterpret_cast<float2*>(maxima + warp * HEADS + nt * 8 + 2 * lane) = make_float2(top[nt][0], top[nt][1]);
+            if (CODES && lane == 0) maxima[kConsumers * HEADS + warp] = vtop;
+        }
+        if (!consumers_agree(ok)) return false;
         float vf = 1.f, vold = 1.f;  // E4M3: factors of the new weights and the old outputs
         if constexpr (CODES) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-            const int e = static_cast<int>(__float_as_uint(vtop) >> 23);
-            if (e > vexp) {  // the same in every lane
+            const float4 v4 = *reinterpret_cast<const float4*>(maxima + kConsumers * HEADS);
+            const int e = static_cast<int>(__float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w))) >> 23);
+            if (e > vexp) {  // the same in every thread
                 vold = __uint_as_float(static_cast<uint32_t>(max(127 - (e - vexp), 0)) << 23);
                 vexp = e;
             }
             vf = __uint_as_float(static_cast<uint32_t>(min(127 + 227 - vexp, 254)) << 23);
         }
-        uint32_t w[SLICES][NT][2];
         float old[NT][2];
         bool moved = vold != 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            float2 t2 = make_float2(m[nt][0], m[nt][1]);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+                const float2 o2 = *reinterpret_cast<const float2*>(maxima + w * HEADS + nt * 8 + 2 * i);
+                t2.x = fmaxf(t2.x, o2.x);
+                t2.y = fmaxf(t2.y, o2.y);
+            }
+            top[nt][0] = t2.x;
+            top[nt][1] = t2.y;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float top = m[nt][e];
-#pragma unroll
-                for (int sl = 0; sl < SLICES; ++sl) top = fmaxf(top, fmaxf(s[sl][nt][e], s[sl][nt][2 + e]));
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const float base = top == -INFINITY ? 0.f : top;
+                const float base = top[nt][e] == -INFINITY ? 0.f : top[nt][e];
                 old[nt][e] = ex2(m[nt][e] - base);
-                moved |= top != m[nt][e];
-                m[nt][e] = top;
-                float sum = 0.f;
+                moved |= top[nt][e] != m[nt][e];
+                m[nt][e] = top[nt][e];
+                l[nt][e] *= old[nt][e];
+                old[nt][e] *= vold;
+                if (some) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int sl = 0; sl < SLICES; ++sl)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float& v = s[sl][nt][2 * r + e];
+                            v = ex2(v - base);
+                            sum += v;
+                            if constexpr (CODES) v *= vs[sl][r] * vf;
+                        }
+                    l[nt][e] += sum;
+                }
+            }
+            if (some) {
+                // the weights, rounded to bf16 for the product with v; turned
+                // so that a thread stores two keys of one head
+                uint8_t* row = weights + (nt * 8 + g) * W_STRIDE + (key0 + 2 * i) * 2;
 #pragma unroll
                 for (int sl = 0; sl < SLICES; ++sl)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float& v = s[sl][nt][2 * r + e];
-                        v = ex2(v - base);
-                        sum += v;
-                        if constexpr (CODES) v *= vs[sl][r] * vf;
-                    }
-                l[nt][e] = fmaf(l[nt][e], old[nt][e], sum);
-                old[nt][e] *= vold;
-            }
-#pragma unroll
-            for (int sl = 0; sl < SLICES; ++sl) {
-                // the weights, rounded to bf16 for the product with v
-                w[sl][nt][0] = movmatrix_trans(pack_bf16(s[sl][nt][0], s[sl][nt][1]));
-                w[sl][nt][1] = movmatrix_trans(pack_bf16(s[sl][nt][2], s[sl][nt][3]));
+                    for (int r = 0; r < 2; ++r)
+                        *reinterpret_cast<uint32_t*>(row + (sl * 16 + 8 * r) * 2) =
+                            movmatrix_trans(pack_bf16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
             }
         }
+        consumers_sync();
         if (__any_sync(0xffffffffu, moved)) {  // a maximum moved
 #pragma unroll
             for (int t = 0; t < MTILES; ++t)
@@ -316,58 +370,72 @@ struct TcConsumer {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[t][nt][e] *= old[nt][e & 1];
         }
-        // O^T += V^T W^T
+        // O^T += V^T W^T: all keys, this warp's elements
+        const uint32_t wrow = smem_u32(weights) + (lane & 7) * W_STRIDE + (lane >> 3) * 16;
 #pragma unroll
-        for (int sl = 0; sl < SLICES; ++sl) {
-            // what lies in a masked row may be anything (NaN for one), and 0
-            // times that is not 0: such values are cleared (E4M3 codes are
-            // finite however they are read)
-            uint32_t keep0 = ~0u, keep1 = ~0u;
-            if (!CODES && partial) {
-                auto pair = [&](int key) {
-                    return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
-                };
-                keep0 = pair(key0 + sl * 16 + 2 * i);
-                keep1 = pair(key0 + sl * 16 + 8 + 2 * i);
-            }
-            if constexpr (!CODES) {
-                const uint32_t rowa = stage + K_BYTES + (key0 + sl * 16 + (lane & 7) + ((lane >> 4) << 3)) * 128;
-                const uint32_t x = static_cast<uint32_t>(((lane >> 3) & 1) ^ (lane & 7)) << 4;
+        for (int k2 = 0; k2 < TK / 32; ++k2) {  // two steps of 16 keys
+            if (partial && (k2 * 32 >= hi || k2 * 32 + 32 <= lo)) continue;
+            uint32_t w[NT][4];
 #pragma unroll
-                for (int t = 0; t < MTILES; ++t) {
-                    uint32_t a[4];
-                    ldmatrix_x4_trans(rowa + (t >> 2) * TK * 128 + (x ^ ((t & 3) << 5)), a);
-                    if (partial) {
-                        a[0] &= keep0;
-                        a[1] &= keep0;
-                        a[2] &= keep1;
-                        a[3] &= keep1;
-                    }
+            for (int nt = 0; nt < NT; ++nt) ldmatrix_x4(wrow + nt * 8 * W_STRIDE + k2 * 64, w[nt]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16(o[t][nt], a, w[sl][nt][0], w[sl][nt][1]);
+            for (int kk = 0; kk < 2; ++kk) {
+                const int k0 = k2 * 32 + kk * 16;
+                if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
+                // what lies in a masked row may be anything (NaN for one), and
+                // 0 times that is not 0: such values are cleared (E4M3 codes
+                // are finite however they are read)
+                uint32_t keep0 = ~0u, keep1 = ~0u;
+                if (!CODES && partial) {
+                    auto pair = [&](int key) {
+                        return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+                    };
+                    keep0 = pair(k0 + 2 * i);
+                    keep1 = pair(k0 + 8 + 2 * i);
                 }
-            } else {
-                const uint32_t rowa = stage + K_BYTES + (key0 + sl * 16 + (lane & 15)) * 128;
-                const uint32_t x = static_cast<uint32_t>((lane >> 4) ^ (lane & 7)) << 4;
+                const int chunk0 = warp * (ROW_BYTES / 16 / kConsumers);  // this warp's part of the row
+                if constexpr (!CODES) {
+                    const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 7) + ((lane >> 4) << 3)) * 128;
 #pragma unroll
-                for (int c = 0; c < MTILES / 2; ++c) {
-                    uint32_t a[4];
-                    ldmatrix_x4_trans(rowa + (c >> 2) * TK * 128 + (x ^ ((c & 3) << 5)), a);
-                    const uint32_t a0[4] = {even_pair(a[0]), odd_pair(a[0]), even_pair(a[1]), odd_pair(a[1])};
-                    const uint32_t a1[4] = {even_pair(a[2]), odd_pair(a[2]), even_pair(a[3]), odd_pair(a[3])};
+                    for (int t = 0; t < MTILES; ++t) {
+                        const int c = chunk0 + 2 * t + ((lane >> 3) & 1);
+                        uint32_t a[4];
+                        ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
+                        if (partial) {
+                            a[0] &= keep0;
+                            a[1] &= keep0;
+                            a[2] &= keep1;
+                            a[3] &= keep1;
+                        }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(o[2 * c][nt], a0, w[sl][nt][0], w[sl][nt][1]);
-                        mma_bf16(o[2 * c + 1][nt], a1, w[sl][nt][0], w[sl][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_bf16(o[t][nt], a, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                    }
+                } else {
+                    const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 15)) * 128;
+#pragma unroll
+                    for (int t = 0; t < MTILES; t += 2) {
+                        const int c = chunk0 + t + (lane >> 4);
+                        uint32_t a[4];
+                        ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
+                        const uint32_t a0[4] = {even_pair(a[0]), odd_pair(a[0]), even_pair(a[1]), odd_pair(a[1])};
+                        const uint32_t a1[4] = {even_pair(a[2]), odd_pair(a[2]), even_pair(a[3]), odd_pair(a[3])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_bf16(o[t][nt], a0, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                            mma_bf16(o[t + 1][nt], a1, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                        }
                     }
                 }
             }
         }
+        return true;
     }
 
-    // This warp's statistics of its heads, for the lanes that hold them.
-    __device__ __forceinline__ void stats(float* ms, float* ls) {
-        const int lane = threadIdx.x & 31;
+    // The item's end, or its part's: sums [kConsumers][HEADS] in shared memory.
+    // Calls put(head, element, o, m, l) for this thread's outputs.
+    template <typename Put>
+    __device__ __forceinline__ void finish(float* sums, Put put) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -375,44 +443,38 @@ struct TcConsumer {
                 float sum = l[nt][e];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (lane < 4) {
-                    ms[nt * 8 + 2 * lane + e] = m[nt][e];
-                    ls[nt * 8 + 2 * lane + e] = sum;
-                }
+                if (lane < 4) sums[warp * HEADS + nt * 8 + 2 * lane + e] = sum;
             }
-    }
-
-    // Adds (or, the first, stores) this warp's outputs, relative to the maxima
-    // `top`, to obuf [HEADS][DP + 4].
-    __device__ __forceinline__ void add(float* obuf, const float* top, bool first) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, i = lane & 3;
+        consumers_sync();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int h = nt * 8 + 2 * i + e;
-                float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top[h]);
-                // E4M3: 2^(vexp - 127 - 100 + 120), the second part below
-                if constexpr (CODES) f *= __uint_as_float(static_cast<uint32_t>(vexp) << 23);
-                float* row = obuf + h * (DP + 4);
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) sum += sums[w * HEADS + h];
+                // E4M3: 2^(vexp - 127 - 100 + 120) in two factors
+                const float f = CODES ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
 #pragma unroll
                 for (int t = 0; t < MTILES; ++t)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int d = CODES ? t * 16 + 2 * g + r : t * 16 + g + 8 * r;
-                        float v = o[t][nt][2 * r + e] * f;
-                        if constexpr (CODES) v *= 0x1p20f;
-                        row[d] = first ? v : row[d] + v;
+                        float v = o[t][nt][2 * r + e];
+                        if constexpr (CODES) v = v * f * 0x1p20f;
+                        put(h, elem(t, r), v, m[nt][e], sum);
                     }
             }
     }
 };
 
-// fp32 consumer: CUDA cores, fp32 throughout.  Lane i holds elements [V i, V i +
-// V) of q, of o and of each row it reads (conflict-free); a row's product with
-// 8 heads leaves 32 lanes' partial sums of 8 scores.  Four keys at a time give
-// 32 such sums, which 31 exchanges turn into one finished score per lane
-// (lane = key * 8 + head).
+// fp32 consumer: CUDA cores, fp32 throughout, up to 8 query heads.
+//
+// Scores: lane i holds elements of q and of each row it reads (conflict-free);
+// a row's product with 8 heads leaves 32 lanes' partial sums of 8 scores.  Four
+// keys at a time give 32 such sums, which 31 exchanges turn into one finished
+// score per lane (lane = key * 8 + head).  Outputs: a lane owns elements of the
+// row (a part of the keys, where a warp's elements are fewer than its lanes).
 template <int DP_>
 struct F32Consumer {
     static constexpr int DP = DP_;
@@ -423,15 +485,17 @@ struct F32Consumer {
     static constexpr int BOXES = 1;
     static constexpr int TK = 16384 / ROW_BYTES;
     static constexpr int K_BYTES = TK * ROW_BYTES;
-    static constexpr int SCALE_BYTES = 0;
-    static constexpr int STAGE_BYTES = 2 * K_BYTES;
+    static constexpr int Q_STRIDE = ROW_BYTES;
+    static constexpr int W_BYTES = TK * HEADS * 4;
     static constexpr int CTAS = 2;
-    static constexpr int STAGES = 3;
-    static constexpr int V = DP / 32;
-    static constexpr int KEYS = TK / kConsumers;  // of a warp, a multiple of 4
+    static constexpr int V = DP / 32;                      // elements of a row a lane scores with
+    static constexpr int QUADS = TK / kConsumers / 4;      // of 4 keys, a warp's
+    static constexpr int OWN = DP / kConsumers;            // elements of a warp's outputs
+    static constexpr int E = OWN > 32 ? OWN / 32 : 1;      // of a lane's
+    static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;  // lanes that share an element, every SPLIT-th key
 
-    float q[HEADS][V], o[HEADS][V];
-    float m, l;  // of head lane & 7: m of all keys, l of keys lane >> 3 (mod 4)
+    float q[HEADS][V], o[HEADS][E];
+    float m, l;  // of head lane & 7: m of all keys, l of this warp's keys lane >> 3 (mod 4)
 
     static __device__ __forceinline__ void load_row(uint32_t addr, float (&f)[V]) {
         if constexpr (V == 2) {
@@ -445,32 +509,41 @@ struct F32Consumer {
                              : "memory");
         }
     }
-    // element of lane i's vector slot v: V = 8 rows are read as two halves of
-    // 128 elements, so that every access is conflict-free
-    static __device__ __forceinline__ int elem(int lane, int v) {
+    // element of lane i's vector slot v: rows of 256 are read as two halves, so
+    // that every access is conflict-free
+    static __device__ __forceinline__ int score_elem(int lane, int v) {
         return V == 8 ? (v >> 2) * 128 + lane * 4 + (v & 3) : lane * V + v;
     }
 
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, long long qrow, int heads) {
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* qrows, int heads) {
         const int lane = threadIdx.x & 31;
         const float to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h)
+        for (int h = 0; h < HEADS; ++h) {
+            const float* row = reinterpret_cast<const float*>(qrows + h * Q_STRIDE);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int d = elem(lane, v);
-                q[h][v] = h < heads && d < p.D ? __ldg(static_cast<const float*>(p.q) + (qrow + h) * p.D + d) * to_log2 : 0.f;
-                o[h][v] = 0.f;
+                const int d = score_elem(lane, v);
+                q[h][v] = h < heads && d < p.D ? row[d] * to_log2 : 0.f;
             }
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[h][e] = 0.f;
+        }
         m = -INFINITY;
         l = 0.f;
     }
 
-    __device__ __forceinline__ void tile(uint32_t stage, const float*, int lo, int hi) {
+    __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float*, float* maxima, uint8_t* weights, int lo,
+                                         int hi) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const uint32_t at = stage + lane * (V == 2 ? 8 : 16);
-#pragma unroll 1
-        for (int k0 = warp * KEYS; k0 < (warp + 1) * KEYS; k0 += 4) {
+        const int key0 = warp * QUADS * 4;
+        float* w = reinterpret_cast<float*>(weights);  // [TK][HEADS]
+        float x[QUADS], top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < QUADS; ++u) {
+            const int k0 = key0 + u * 4;
+            x[u] = -INFINITY;
             if (k0 >= hi || k0 + 4 <= lo) continue;
             float s[32];
 #pragma unroll
@@ -496,63 +569,75 @@ struct F32Consumer {
                 }
             }
             const int key = k0 + (lane >> 3);
-            const bool in = key >= lo && key < hi;
-            float x = in ? s[0] : -INFINITY;
-            float top = fmaxf(m, x);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float base = top == -INFINITY ? 0.f : top;
-            const float old = ex2(m - base), w = ex2(x - base);
-            const bool moved = top != m;
-            m = top;
-            l = fmaf(l, old, w);
-            if (__any_sync(0xffffffffu, moved)) {
+            if (key >= lo && key < hi) x[u] = s[0];
+            top = fmaxf(top, x[u]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        if (lane < 8) maxima[warp * HEADS + lane] = top;
+        if (!consumers_agree(ok)) return false;
+        top = m;
 #pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    const float f = __shfl_sync(0xffffffffu, old, h);
+        for (int n = 0; n < kConsumers; ++n) top = fmaxf(top, maxima[n * HEADS + (lane & 7)]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float old = ex2(m - base);
+        const bool moved = top != m;
+        m = top;
+        l *= old;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[h][v] *= f;
-                }
-            }
+        for (int u = 0; u < QUADS; ++u) {
+            const float e = ex2(x[u] - base);
+            l += e;
+            w[(key0 + u * 4) * HEADS + lane] = e;
+        }
+        consumers_sync();
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float f[V];
-                load_row(at + K_BYTES + (k0 + k) * ROW_BYTES, f);
-                if (k0 + k < lo || k0 + k >= hi) {  // whatever a masked row holds
+            for (int h = 0; h < HEADS; ++h) {
+                const float f = __shfl_sync(0xffffffffu, old, h);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) f[v] = 0.f;
-                }
-#pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k * 8 + h);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) o[h][v] = fmaf(wk, f[v], o[h][v]);
-                }
+                for (int e = 0; e < E; ++e) o[h][e] *= f;
             }
         }
+        // keys [lo, hi) alone: a masked row may hold anything
+        const uint32_t vat = stage + K_BYTES + (warp * OWN + (SPLIT > 1 ? lane % OWN : lane * E)) * 4;
+        const float4* w4 = reinterpret_cast<const float4*>(w);
+#pragma unroll 4
+        for (int k = lo + (SPLIT > 1 ? lane / OWN : 0); k < hi; k += SPLIT) {
+            const float4 wa = w4[2 * k], wb = w4[2 * k + 1];
+            float f[E];
+            if constexpr (E == 2)
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(vat + k * ROW_BYTES) : "memory");
+            else
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(vat + k * ROW_BYTES) : "memory");
+            const float wk[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[h][e] = fmaf(wk[h], f[e], o[h][e]);
+        }
+        return true;
     }
 
-    __device__ __forceinline__ void stats(float* ms, float* ls) {
-        const int lane = threadIdx.x & 31;
+    template <typename Put>
+    __device__ __forceinline__ void finish(float* sums, Put put) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         float sum = l + __shfl_xor_sync(0xffffffffu, l, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (lane < 8) {
-            ms[lane] = m;
-            ls[lane] = sum;
-        }
-    }
-
-    __device__ __forceinline__ void add(float* obuf, const float* top, bool first) {
-        const int lane = threadIdx.x & 31;
+        if (lane < 8) sums[warp * HEADS + lane] = sum;
+        consumers_sync();
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
-            const float mine = __shfl_sync(0xffffffffu, m, h);
-            const float f = mine == -INFINITY ? 0.f : ex2(mine - top[h]);
-            float* row = obuf + h * (DP + 4);
+            const float mh = __shfl_sync(0xffffffffu, m, h);
+            float n = 0.f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int d = elem(lane, v);
-                row[d] = first ? o[h][v] * f : row[d] + o[h][v] * f;
+            for (int k = 0; k < kConsumers; ++k) n += sums[k * HEADS + h];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float v = o[h][e];
+#pragma unroll
+                for (int off = OWN; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                if (lane < OWN) put(h, warp * OWN + lane * E + e, v, mh, n);
             }
         }
     }
@@ -565,7 +650,18 @@ struct Meta {       // of a ring stage, written by the producer
     int lo, hi;     // keys of the tile that count
     int flags;
 };
-enum : int { kFirst = 1, kLast = 2, kItemBegins = 4, kItemEnds = 8 };
+enum : int {
+    kFirst = 1,       // the first tile of an item or of this share
+    kLast = 2,        // the last one
+    kItemBegins = 4,  // the item's own first tile
+    kItemEnds = 8,
+    kEnd = 16,        // the share's last tile, or (lo = hi, no other flag) no tile at all
+};
+
+// Cost of a tile and of an item, for the shares: an item's first loads and its
+// end take about as long as half a tile's reads.
+constexpr int kTileCost = 4;
+constexpr int kItemCost = 2;
 
 // Length and first key of a sequence; both within the table.
 struct Span {
@@ -589,9 +685,11 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
     return s.len > 0 ? (s.len + TK - 1) / TK - s.start / TK : 1;
 }
 
-// Position in the list of tiles: tile t of `tiles` of item j of sequence b.
+// Position in the list of tiles: tile t of `tiles` of item j of sequence b; the
+// item's cost begins at `at`.
 template <int TK>
 struct Cursor {
+    long long at;
     int b, j, t, tiles;
     Span s;
 
@@ -600,26 +698,46 @@ struct Cursor {
         s = span_of(p, b, &bad);
         tiles = tiles_of<TK>(s);
     }
-    __device__ __forceinline__ void next(const PagedAttnParams& p) {
-        if (++t < tiles) return;
+    __device__ __forceinline__ int item_cost() const { return tiles * kTileCost + kItemCost; }
+    __device__ __forceinline__ long long tile_at() const { return at + static_cast<long long>(t) * kTileCost; }
+    __device__ __forceinline__ int key0() const { return (s.start / TK + t) * TK; }
+    __device__ __forceinline__ void next_item(const PagedAttnParams& p) {
+        at += item_cost();
         t = 0;
         if (++j < p.items_per_seq) return;
         j = 0;
         if (++b < p.B) load(p);
     }
+    __device__ __forceinline__ void next(const PagedAttnParams& p) {
+        if (++t >= tiles) next_item(p);
+    }
 };
 
 template <class C>
 struct Smem {
-    static constexpr int RING = C::STAGES * C::STAGE_BYTES;
-    static constexpr int SCALES = RING;  // [STAGES][2][TK] floats
-    static constexpr int OBUF = SCALES + C::STAGES * 2 * C::SCALE_BYTES;
-    static constexpr int STATS = OBUF + C::HEADS * (C::DP + 4) * 4;  // m, l [warps][HEADS]; top, sum [HEADS]
-    static constexpr int BYTES = STATS + (2 * kConsumers + 2) * C::HEADS * 4 + 1024;  // 1024: alignment of the ring
+    static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;
+    static constexpr int Q_BYTES = C::HEADS * C::Q_STRIDE;
+    static constexpr int STAGE_BYTES = 2 * C::K_BYTES;
+    // maxima [2][kConsumers * HEADS + 4], sums [kConsumers][HEADS], weights [2]
+    static constexpr int MAXIMA = kConsumers * C::HEADS + 4;
+    static constexpr int STATS_BYTES = (2 * MAXIMA + kConsumers * C::HEADS) * 4;
+    static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + 1024;  // 1024: alignment of the ring
+    // what a CTA may have: 227 KB, or half of an SM's 228 KB less 1 KB each;
+    // less the kernel's static shared memory
+    static constexpr int ROOM = (C::CTAS == 2 ? 113 * 1024 : 227 * 1024) - 512;
+    static constexpr int FIT = (ROOM - FIXED) / (STAGE_BYTES + 2 * SCALE_BYTES + Q_BYTES);
+    static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
+    static constexpr int SCALES = STAGES * STAGE_BYTES;  // [STAGES][2][TK] floats
+    static constexpr int QROWS = SCALES + STAGES * 2 * SCALE_BYTES;
+    static constexpr int STATS = QROWS + STAGES * Q_BYTES;
+    static constexpr int WEIGHTS = STATS + STATS_BYTES;
+    static constexpr int BYTES = WEIGHTS + 2 * C::W_BYTES + 1024;
+    static_assert(STAGES >= 2 && STATS_BYTES % 16 == 0 && Q_BYTES % 16 == 0, "layout");
 };
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+    using L = Smem<C>;
     constexpr int TK = C::TK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -627,36 +745,33 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
     __shared__ Meta meta[kMaxStages];
     __shared__ DeviceStatus status;  // this CTA's, copied to the workspace at the end
     __shared__ int abort_flag;
-    __shared__ long long warp_tiles[kThreads / 32];
-    __shared__ long long share_first;
-    __shared__ int share_count;
+    __shared__ long long warp_cost[kThreads / 32];
     __shared__ Cursor<TK> share_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // the join may be scheduled as soon as every CTA of this launch runs
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (tid == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kConsumers);
-        }
-        fence_mbar_init();
-        abort_flag = 0;
-        status.code = status.where = status.info = 0;
-        share_count = 0;
-        tma_prefetch_map(&p.map_k);
-        tma_prefetch_map(&p.map_v);
-    }
-
-    // This CTA's share: every thread counts the tiles of a run of sequences, a
+    // This CTA's share: every thread adds up the cost of a run of sequences, a
     // scan over the threads gives the total and the thread in whose run the
     // share begins.
     const int run = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     long long mine = 0;
     bool bad = false;
-    for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(span_of(p, b, &bad));
+    for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(span_of(p, b, &bad)) * kTileCost + kItemCost;
+    if (tid == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kConsumers);
+        }
+        fence_mbar_init();
+        abort_flag = 0;
+        status.code = status.where = status.info = 0;
+        share_at.b = -1;
+        tma_prefetch_map(&p.map_k);
+        tma_prefetch_map(&p.map_v);
+    }
     mine *= p.items_per_seq;
     long long incl = mine;
 #pragma unroll
@@ -664,38 +779,38 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
         const long long up = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += up;
     }
-    if (lane == 31) warp_tiles[warp] = incl;
+    if (lane == 31) warp_cost[warp] = incl;
     __syncthreads();
     long long before = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_tiles[w];
-        total += warp_tiles[w];
+        if (w < warp) before += warp_cost[w];
+        total += warp_cost[w];
     }
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
-    const long long first = share * blockIdx.x;
+    // A tile belongs to the share in which its cost begins; a share is at least
+    // one tile's cost, so that an item's parts lie in successive shares.
+    const long long share = max(static_cast<long long>(kTileCost), (total + gridDim.x - 1) / gridDim.x);
+    const long long begin = share * blockIdx.x, end = begin + share;
     if (bad) {
         status.code = SPTP_ERR_SHAPE;
         status.where = kWhereKvPage;
     }
-    if (first >= before && first < before + mine) {
-        long long rest = first - before;
+    if (begin >= before && begin < before + mine) {
         Cursor<TK> c;
-        c.b = b0;
-        for (;; ++c.b) {
+        c.at = before;
+        for (c.b = b0;; ++c.b) {
             c.load(p);
-            const long long n = static_cast<long long>(c.tiles) * p.items_per_seq;
-            if (rest < n) break;
-            rest -= n;
+            const long long n = static_cast<long long>(c.item_cost()) * p.items_per_seq;
+            if (begin < c.at + n) break;
+            c.at += n;
         }
-        c.j = static_cast<int>(rest / c.tiles);
-        c.t = static_cast<int>(rest - static_cast<long long>(c.j) * c.tiles);
-        share_at = c;
-        share_first = first;
-        share_count = static_cast<int>(min(share, total - first));
+        c.j = static_cast<int>((begin - c.at) / c.item_cost());
+        c.at += static_cast<long long>(c.j) * c.item_cost();
+        c.t = static_cast<int>((begin - c.at + kTileCost - 1) / kTileCost);
+        if (c.t >= c.tiles) c.next_item(p);
+        if (c.b < p.B && c.tile_at() < end) share_at = c;
     }
     __syncthreads();
-    const int count = share_count;
     WaitCtx wc{&status, &abort_flag, kWaitLimitNs};
     PagedAttnPart* part = p.parts + blockIdx.x;
 
@@ -703,37 +818,37 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
         // -------------------------------------------------- producer
         int join_parts = 0, join_b = 0, join_j = 0;
         const int R = p.box_rows, nb = TK / R;
-        Cursor<TK> c, n;
-        if (count > 0) {
-            c = share_at;
-            n = c;
-        }
+        const int group = p.Hq / p.Hkv;
+        Cursor<TK> c = share_at;
+        const bool any = c.b >= 0;
         // page of this lane's box of a tile (-1: bad, -2: no key of it counts)
         auto page_of = [&](const Cursor<TK>& at) {
-            const int key = (at.s.start / TK + at.t) * TK + lane * R;
+            const int key = at.key0() + lane * R;
             if (lane >= nb || key >= at.s.len || key + R <= at.s.start) return -2;
             const int page = __ldg(p.page_table + static_cast<long long>(at.b) * p.max_pages + key / p.page_size);
             return page >= 0 && page < p.num_pages ? page : -1;
         };
-        int page = count > 0 ? page_of(c) : -2;
+        int page = any ? page_of(c) : -2;
         int issued = 0;
-        for (int i = 0, s = 0; i < count; ++i) {
+        if (!any && lane == 0) {
+            meta[0] = Meta{0, 0, 0, 0, kEnd};
+            mbar_arrive(&full[0]);
+        }
+        bool more = any, fresh = true;  // fresh: the first tile of this share
+        for (int i = 0, s = 0; more; ++i) {
             // the next tile's pages are read while this one waits for its stage
-            int page_next = -2;
-            if (i + 1 < count) {
-                n.next(p);
-                page_next = page_of(n);
-            }
-            const uint32_t phase = (i / C::STAGES) & 1;
-            if (!mbar_wait(&empty[s], phase ^ 1, wc, kWhereKvEmpty, i)) break;
-            const int tile0 = (c.s.start / TK + c.t) * TK;
-            const int key = tile0 + lane * R;
-            const int shard = c.j / (p.Hkv * p.head_blocks), kvh = c.j / p.head_blocks % p.Hkv;
+            Cursor<TK> n = c;
+            n.next(p);
+            more = n.b < p.B && n.tile_at() < end;
+            const int page_next = more ? page_of(n) : -2;
+            if (!mbar_wait(&empty[s], ((i / L::STAGES) & 1) ^ 1, wc, kWhereKvEmpty, i)) break;
+            const int key = c.key0() + lane * R;
+            const int hb = c.j % p.head_blocks, sk = c.j / p.head_blocks;
+            const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
             const int bad_row = p.P * p.num_pages * p.Hkv * p.page_size;  // outside the map: zeros
             int row = bad_row;
-            if (page >= 0)
-                row = ((shard * p.num_pages + page) * p.Hkv + kvh) * p.page_size + key % p.page_size;
-            float* sc = reinterpret_cast<float*>(smem + Smem<C>::SCALES + s * 2 * C::SCALE_BYTES);
+            if (page >= 0) row = ((shard * p.num_pages + page) * p.Hkv + kvh) * p.page_size + key % p.page_size;
+            float* sc = reinterpret_cast<float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES);
             if (page == -1) {
                 status.code = SPTP_ERR_SHAPE;
                 status.where = kWhereKvPage;
@@ -745,30 +860,37 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             }
             const uint32_t loads = __ballot_sync(0xffffffffu, page != -2);
             const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+            const bool first = fresh || c.t == 0, ends = c.t == c.tiles - 1;
+            const int h0 = hb * p.heads_per_item, heads = min(p.heads_per_item, group - h0);
+            const int q_bytes = p.D * (C::F32 ? 4 : 2);
             if (lane == 0) {
                 Meta md;
                 md.b = c.b;
                 md.j = c.j;
-                md.lo = max(0, c.s.start - tile0);
-                md.hi = max(0, min(TK, c.s.len - tile0));
-                md.flags = (c.t == 0 ? kItemBegins : 0) | (c.t == c.tiles - 1 ? kItemEnds : 0) |
-                           (i == 0 || c.t == 0 ? kFirst : 0) | (i == count - 1 || c.t == c.tiles - 1 ? kLast : 0);
+                md.lo = max(0, c.s.start - c.key0());
+                md.hi = max(0, min(TK, c.s.len - c.key0()));
+                md.flags = (first ? kFirst : 0) | (c.t == 0 ? kItemBegins : 0) | (ends ? kItemEnds : 0) |
+                           (ends || !more ? kLast : 0) | (more ? 0 : kEnd);
                 meta[s] = md;
-                // an item that begins here and goes on in the next CTA
-                if (i == count - 1 && c.t != c.tiles - 1) {
-                    const long long item0 = share_first + i - c.t;
-                    if (item0 >= share_first) {
-                        join_parts = static_cast<int>((item0 + c.tiles - 1) / share - blockIdx.x) + 1;
-                        join_b = c.b;
-                        join_j = c.j;
-                    }
+                // an item that begins here and goes on in the next share
+                if (!more && !ends && c.at >= begin) {
+                    join_parts = static_cast<int>((c.at + static_cast<long long>(c.tiles - 1) * kTileCost) / share -
+                                                  blockIdx.x) + 1;
+                    join_b = c.b;
+                    join_j = c.j;
                 }
                 mbar_arrive_expect_tx(&full[s], __popc(loads) * 2 * R * C::ROW_BYTES +
-                                                    (C::CODES ? __popc(good) * 2 * R * 4 : 0));
+                                                    (C::CODES ? __popc(good) * 2 * R * 4 : 0) +
+                                                    (first ? heads * q_bytes : 0));
             }
             __syncwarp();
             issued = i + 1;
-            uint8_t* st = smem + s * C::STAGE_BYTES;
+            if (first && lane < heads) {
+                const long long qrow = (static_cast<long long>(shard) * p.B + c.b) * p.Hq + kvh * group + h0 + lane;
+                bulk_load(smem + L::QROWS + s * L::Q_BYTES + lane * C::Q_STRIDE,
+                          static_cast<const uint8_t*>(p.q) + qrow * q_bytes, q_bytes, &full[s]);
+            }
+            uint8_t* st = smem + s * L::STAGE_BYTES;
             for (int base = 0; base < nb * C::BOXES * 2; base += 32) {
                 const int box = base + lane;
                 const int r = box % nb, which = box / nb;
@@ -794,7 +916,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             }
             c = n;
             page = page_next;
-            if (++s == C::STAGES) s = 0;
+            fresh = false;
+            if (++s == L::STAGES) s = 0;
         }
         if (lane == 0) {
             part->join_parts = join_parts;
@@ -805,83 +928,59 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             // left early: wait (bounded) for the copies still in flight
             int local_abort = 0;
             WaitCtx drain{&status, &local_abort, kWaitLimitNs};
-            for (int i = max(0, issued - C::STAGES); i < issued; ++i)
-                mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, drain, kWhereDrain, i);
+            for (int i = max(0, issued - L::STAGES); i < issued; ++i)
+                mbar_wait(&full[i % L::STAGES], (i / L::STAGES) & 1, drain, kWhereDrain, i);
         }
     } else {
         // -------------------------------------------------- consumers
-        float* obuf = reinterpret_cast<float*>(smem + Smem<C>::OBUF);
-        float* ms = reinterpret_cast<float*>(smem + Smem<C>::STATS);
-        float* ls = ms + kConsumers * C::HEADS;
-        float* top = ls + kConsumers * C::HEADS;
-        float* sum = top + C::HEADS;
+        float* stats = reinterpret_cast<float*>(smem + L::STATS);
         const int group = p.Hq / p.Hkv;
         bool begun = false;
         C c;
-        for (int i = 0, s = 0; i < count; ++i) {
-            if (!mbar_wait(&full[s], (i / C::STAGES) & 1, wc, kWhereKvFull, i)) break;
-            const Meta md = meta[s];
+        for (int i = 0, s = 0;; ++i) {
+            const bool ok = mbar_wait(&full[s], (i / L::STAGES) & 1, wc, kWhereKvFull, i);
+            const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
             const int hb = md.j % p.head_blocks, sk = md.j / p.head_blocks;
             const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
             const int h0 = hb * p.heads_per_item, heads = min(p.heads_per_item, group - h0);
-            const long long qrow = (static_cast<long long>(shard) * p.B + md.b) * p.Hq + kvh * group + h0;
-            if (md.flags & kFirst) {
-                c.begin(p, qrow, heads);
+            if (md.flags & kFirst || i == 0) {
+                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, ok ? heads : 0);
                 begun = (md.flags & kItemBegins) != 0;
             }
-            c.tile(smem_u32(smem) + s * C::STAGE_BYTES,
-                   reinterpret_cast<const float*>(smem + Smem<C>::SCALES + s * 2 * C::SCALE_BYTES), md.lo, md.hi);
+            if (!c.tile(ok, smem_u32(smem) + s * L::STAGE_BYTES,
+                        reinterpret_cast<const float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES),
+                        stats + (i & 1) * L::MAXIMA, smem + L::WEIGHTS + (i & 1) * C::W_BYTES, md.lo, md.hi))
+                break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            if (++s == C::STAGES) s = 0;
-            if (!(md.flags & kLast)) continue;
-
-            // ---- the item's end, or this share's: the four warps' parts
-            c.stats(ms + warp * C::HEADS, ls + warp * C::HEADS);
-            consumers_sync();
-            if (tid < C::HEADS) {
-                float t = -INFINITY, n = 0.f;
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) t = fmaxf(t, ms[w * C::HEADS + tid]);
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    const float mw = ms[w * C::HEADS + tid];
-                    n += mw == -INFINITY ? 0.f : ls[w * C::HEADS + tid] * ex2(mw - t);
+            if (++s == L::STAGES) s = 0;
+            if (md.flags & kLast) {
+                float* sums = stats + 2 * L::MAXIMA;
+                if (begun && (md.flags & kItemEnds)) {
+                    // the whole item: o / l, rounded once
+                    const long long qrow = (static_cast<long long>(shard) * p.B + md.b) * p.Hq + kvh * group + h0;
+                    c.finish(sums, [&](int h, int d, float v, float m, float n) {
+                        if (h >= heads || d >= p.D) return;
+                        v = n == 0.f ? 0.f : __fdividef(v, n);
+                        if constexpr (C::F32)
+                            static_cast<float*>(p.out)[(qrow + h) * p.D + d] = v;
+                        else
+                            static_cast<__nv_bfloat16*>(p.out)[(qrow + h) * p.D + d] = __float2bfloat16_rn(v);
+                        if (d == 0 && p.lse != nullptr)
+                            p.lse[qrow + h] = n == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(n);
+                    });
+                } else {
+                    // a part: slot 1 if the item begins in this share (it goes
+                    // on in the next), slot 0 if it began in an earlier one
+                    const long long at = (blockIdx.x * 2ll + (begun ? 1 : 0)) * p.heads_per_item;
+                    c.finish(sums, [&](int h, int d, float v, float m, float n) {
+                        if (h >= heads || d >= p.D) return;
+                        p.part_o[(at + h) * p.D + d] = v;
+                        if (d == 0) p.part_ml[at + h] = make_float2(m, n);
+                    });
                 }
-                top[tid] = t;
-                sum[tid] = n;
             }
-            consumers_sync();
-            for (int w = 0; w < kConsumers; ++w) {  // in turn: a fixed order of the sums
-                if (warp == w) c.add(obuf, top, w == 0);
-                consumers_sync();
-            }
-            if (begun && (md.flags & kItemEnds)) {
-                // the whole item: o / l, rounded once
-                for (int e = tid * 2; e < heads * p.D; e += kConsumers * 64) {
-                    const int h = e / p.D, d = e - h * p.D;
-                    const float n = sum[h], inv = n == 0.f ? 0.f : 1.f / n;
-                    const float x = obuf[h * (C::DP + 4) + d] * inv, y = obuf[h * (C::DP + 4) + d + 1] * inv;
-                    if constexpr (C::F32)
-                        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + qrow * p.D + e) = make_float2(x, y);
-                    else
-                        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + qrow * p.D + e) =
-                            __floats2bfloat162_rn(x, y);
-                }
-                if (p.lse != nullptr && tid < heads)
-                    p.lse[qrow + tid] = sum[tid] == 0.f ? -INFINITY : top[tid] * 0.6931471805599453f + logf(sum[tid]);
-            } else {
-                // a part: slot 1 if the item begins in this share (it goes on
-                // in the next), slot 0 if it began in an earlier one
-                const long long at = (blockIdx.x * 2ll + (begun ? 1 : 0)) * p.heads_per_item;
-                for (int e = tid * 2; e < heads * p.D; e += kConsumers * 64) {
-                    const int h = e / p.D, d = e - h * p.D;
-                    *reinterpret_cast<float2*>(p.part_o + at * p.D + e) =
-                        make_float2(obuf[h * (C::DP + 4) + d], obuf[h * (C::DP + 4) + d + 1]);
-                }
-                if (tid < heads) p.part_ml[at + tid] = make_float2(top[tid], sum[tid]);
-            }
-            consumers_sync();  // obuf and the statistics are free again
+            if (md.flags & kEnd) break;
         }
     }
     __syncthreads();

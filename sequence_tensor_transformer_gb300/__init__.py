@@ -162,7 +162,7 @@ def _expect(name, t, shape, dtype, optional=False):
         if optional:
             return
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -174,16 +174,18 @@ def _same_device(*ts):
     properties from it, so a tensor elsewhere would be handed to kernels of
     another device.  Checked before any pointer reaches the C ABI."""
     ts = [t for t in ts if t is not None]
-    for t in ts[1:]:
-        if t.device != ts[0].device:
-            raise ValueError(f"tensors on {ts[0].device} and {t.device}: one device expected")
-    if ts and ts[0].device.type != "cuda":
+    if not ts:
+        return
+    device = ts[0].device
+    for t in ts:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one device expected")
+    if device.type != "cuda":
         raise ValueError("device tensors only")
-    if ts:
-        cur = torch.cuda.current_device()
-        if ts[0].device.index != cur:
-            raise ValueError(f"tensors on {ts[0].device} but the current device is cuda:{cur}: "
-                             f"call torch.cuda.set_device({ts[0].device.index}) first")
+    cur = torch.cuda.current_device()
+    if device.index != cur:
+        raise ValueError(f"tensors on {device} but the current device is cuda:{cur}: "
+                         f"call torch.cuda.set_device({device.index}) first")
 
 
 def _variant(v) -> int:
@@ -195,12 +197,13 @@ def _variant(v) -> int:
 
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building torch's stream object takes 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream on {stream.device} but the current device is cuda:{torch.cuda.current_device()}")
     return stream.cuda_stream

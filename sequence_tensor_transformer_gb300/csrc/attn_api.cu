@@ -215,11 +215,8 @@ int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_id
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.status = ws_status(workspace);
-    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-#ifdef SPTP_BOUNDS_CHECK
-    if ((rc = reset_status(workspace, s)) != SPTP_OK) return rc;
-#endif
-    return cuda_status(launch_rope_append(p, dtype == SPTP_BF16, e4m3, di.sms, s));
+    return cuda_status(
+        launch_rope_append(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 size_t sptp_paged_attn_workspace_size(int P, int B, int Hq, int Hkv, int D) {

@@ -10,24 +10,40 @@ namespace sptp {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// Block (h, i): query head h of the item that begins in CTA i's share and goes
-// on in later ones, if there is one:  m = max m_k,  out = sum e^(m_k - m) o_k /
-// sum e^(m_k - m) l_k over its parts k in ascending order per warp, then over
-// the warps.  A warp takes every eighth part, its lanes the elements.  Block
-// (0, 0) also sums up the CTAs' status words.
+// The join of the items whose parts lie in several shares:  m = max m_k,  out =
+// sum e^(m_k - m) o_k / sum e^(m_k - m) l_k  over the parts k.
+//
+// Block c is CTA c's counterpart, one half of it for each of the (at most) two
+// such items that the share has a part of.  An item of n parts is joined by
+// the n halves of its shares, which take its slices (64 elements of one head)
+// in turn, so that one long row (few items, many parts) and many short ones
+// (many items, two parts) both spread over the SMs.  Up to kHalf parts: a warp
+// takes a slice and adds up its parts in ascending order.  More: the half's
+// warps take every kHalf-th part of a slice, and their sums are added in order.
+//
+// Bound by latency: loads that wait for one another, and the code's own first
+// fetch.  Three loads deep (the item, then maxima and outputs together), and
+// short.  The last block sums up the CTAs' status words.
+constexpr int kHalf = 4;  // warps
+constexpr int kJoinThreads = 2 * kHalf * 32;
+constexpr int kBatch = 8;  // parts whose loads a warp has in flight
+
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas) {
-    constexpr int kWarps = kJoinThreads / 32, kPer = 8;  // elements per lane: D <= 256
-    __shared__ float weight[kPagedMaxCtas];
-    __shared__ float o[kWarps][256];
-    __shared__ float red[2][kWarps];
+// (at most 64 registers: a block then fits beside the main kernel's CTAs and is
+// there when they end)
+__global__ void __launch_bounds__(kJoinThreads, 4) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas,
+                                                               int head_shift) {
+    __shared__ float2 sums[2][kHalf][32];
     __shared__ int first_bad;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.x, i = blockIdx.y;
-    if (h == 0 && i == 0) {
+    const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+    if (c == ctas) {
         if (tid == 0) first_bad = ctas;
         __syncthreads();
         for (int k = tid; k < ctas; k += kJoinThreads)
@@ -44,76 +60,87 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_con
             }
             *p.status = st;
         }
+        return;
     }
-    const int n = p.parts[i].join_parts;
-    if (n < 2 || i + n > ctas) return;
-    const int b = p.parts[i].b, j = p.parts[i].j;
-    const int hb = j % p.head_blocks, sk = j / p.head_blocks, group = p.Hq / p.Hkv;
-    const int h0 = hb * p.heads_per_item;
-    if (h >= min(p.heads_per_item, group - h0)) return;
-    // part k lies in slot 0 of CTA i + k; the first one in slot 1
-    auto row_of = [&](int k) { return ((i + k) * 2ll + (k == 0 ? 1 : 0)) * p.heads_per_item + h; };
-    float top = -INFINITY;
-    float2 ml[(kPagedMaxCtas + kJoinThreads - 1) / kJoinThreads];
-    int c = 0;
-    for (int k = tid; k < n; k += kJoinThreads, ++c) {
-        ml[c] = p.part_ml[row_of(k)];
-        top = fmaxf(top, ml[c].x);
-    }
+    const int which = tid / (kHalf * 32), warp = tid / 32 % kHalf;
+    const PagedAttnItem it = p.parts[c].items[which];
+    const int n = it.parts;
+    if (n < 2 || it.first < 0 || it.first + n > ctas) return;
+    const bool wide = n > kHalf;  // the half's warps share a slice
+    const int k0 = wide ? warp : 0, step = wide ? kHalf : 1;
+    const int slices = it.heads << head_shift;
+#pragma unroll 1
+    for (int s = c - it.first + (wide ? 0 : n * warp); s < slices; s += wide ? n : n * kHalf) {
+        const int h = s >> head_shift, d = ((s & ((1 << head_shift) - 1)) * 64) + lane * 2;
+        // part k: slot 0 of share first + k; the first part: slot 1
+        const float2* ml = p.part_ml + 2ll * it.first * p.heads_per_item + h;
+        const float* o = p.part_o + (2ll * it.first * p.heads_per_item + h) * p.D + d;
+        float top = -INFINITY, sum = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int b = k0; b < n; b += kBatch * step) {
+            float2 v[kBatch];
+            float m[kBatch];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) red[0][warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[0][w]);
-    float sum = 0.f;
-    c = 0;
-    for (int k = tid; k < n; k += kJoinThreads, ++c) {
-        const float f = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - top);
-        weight[k] = f;
-        sum = fmaf(f, ml[c].y, sum);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) red[1][warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += red[1][w];
-    float acc[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = b + u * step;
+                const int row = max(2 * k, 1) * p.heads_per_item;
+                v[u] = make_float2(0.f, 0.f);
+                m[u] = -INFINITY;
+                if (k < n) {
+                    m[u] = ml[row].x;
+                    if (d < p.D) v[u] = *reinterpret_cast<const float2*>(o + static_cast<long long>(row) * p.D);
+                }
+            }
+            if (b == k0) {  // the statistics, while these loads are under way
+                float2 q = make_float2(-INFINITY, 0.f);
+                if (lane < n) q = ml[max(2 * lane, 1) * p.heads_per_item];
+                top = q.x;
 #pragma unroll 4
-    for (int k = warp; k < n; k += kWarps) {
-        const float f = weight[k];
-        const float* row = p.part_o + row_of(k) * p.D;
+                for (int k = lane + 32; k < n; k += 32) top = fmaxf(top, ml[2 * k * p.heads_per_item].x);
 #pragma unroll
-        for (int e = 0; e < kPer / 4; ++e) {
-            const int d = e * 128 + lane * 4;
-            if (d < p.D) {
-                const float4 v = *reinterpret_cast<const float4*>(row + d);
-                acc[4 * e] = fmaf(f, v.x, acc[4 * e]);
-                acc[4 * e + 1] = fmaf(f, v.y, acc[4 * e + 1]);
-                acc[4 * e + 2] = fmaf(f, v.z, acc[4 * e + 2]);
-                acc[4 * e + 3] = fmaf(f, v.w, acc[4 * e + 3]);
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                if (top == -INFINITY) top = 0.f;
+                sum = ex2(q.x - top) * q.y;
+#pragma unroll 4
+                for (int k = lane + 32; k < n; k += 32) {
+                    const float2 r = ml[2 * k * p.heads_per_item];
+                    sum = fmaf(ex2(r.x - top), r.y, sum);
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = ex2(m[u] - top);
+                acc.x = fmaf(f, v[u].x, acc.x);
+                acc.y = fmaf(f, v[u].y, acc.y);
             }
         }
-    }
+        if (wide) {
+            auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "n"(kHalf * 32) : "memory"); };
+            sums[which][warp][lane] = acc;
+            sync();
+            acc = sums[which][0][lane];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[warp][(e >> 2) * 128 + lane * 4 + (e & 3)] = acc[e];
-    __syncthreads();
-    const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
-    const long long qrow = (static_cast<long long>(shard) * p.B + b) * p.Hq + kvh * group + h0 + h;
-    if (tid < p.D) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += o[w][tid];
-        v = sum == 0.f ? 0.f : v / sum;
-        static_cast<T*>(p.out)[qrow * p.D + tid] = static_cast<T>(v);
+            for (int w = 1; w < kHalf; ++w) {
+                acc.x += sums[which][w][lane].x;
+                acc.y += sums[which][w][lane].y;
+            }
+            sync();
+            if (warp != 0) continue;
+        }
+        if (d >= p.D) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        T* out = static_cast<T*>(p.out) + (it.qrow + h) * p.D + d;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        else
+            *reinterpret_cast<float2*>(out) = make_float2(acc.x * inv, acc.y * inv);
+        if (p.lse != nullptr && d == 0)
+            p.lse[it.qrow + h] = sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
     }
-    if (p.lse != nullptr && tid == 0) p.lse[qrow] = sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
 }
-
 }  // namespace
 
 cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
@@ -129,13 +156,14 @@ cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(p.heads_per_item, ctas);
+    cfg.gridDim = dim3(ctas + 1);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, paged_attn_join<__nv_bfloat16>, p, ctas)
-                : cudaLaunchKernelEx(&cfg, paged_attn_join<float>, p, ctas);
+    const int head_shift = p.D <= 64 ? 0 : p.D <= 128 ? 1 : 2;  // slices of a head: 1, 2 or 4
+    return bf16 ? cudaLaunchKernelEx(&cfg, paged_attn_join<__nv_bfloat16>, p, ctas, head_shift)
+                : cudaLaunchKernelEx(&cfg, paged_attn_join<float>, p, ctas, head_shift);
 }
 
 }  // namespace sptp

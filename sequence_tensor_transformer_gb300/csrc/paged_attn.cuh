@@ -27,6 +27,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "sptp.h"
 #include "sptp_ptx.cuh"
@@ -89,10 +90,35 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// the same on fp16 operands
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four E4M3 codes as fp16 (exact): bytes 0, 1 and bytes 2, 3
+__device__ __forceinline__ void unpack_e4m3(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+}
+
+__device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // ---------------------------------------------------------------- consumers
 // A consumer class is one warp's part of the arithmetic:
@@ -112,13 +138,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // scores, statistics and outputs of the same two heads (of every eight)
 // throughout.
 //
-// E4M3: a code's 7 magnitude bits, moved into a bf16's exponent and mantissa,
-// are the value times 2^-120, subnormal codes among them, so that a pair of
-// codes becomes a pair of bf16 by two shifts and masks.  q carries 2^100 over
-// its own exponent and the weights carry 2^100 over the largest v scale so
-// far, so that no product comes near the ends of fp32's range; both powers of
-// two leave with the score and at the item's end.  (Converting to fp16 instead
-// would lose rows of v whose scales differ by more than fp16's range.)
+// E4M3: codes become fp16 (exact), and both products run on fp16.  q comes as
+// 2^-e q with its largest element in [1, 2), so fp16 holds a bf16 q to 2^-25 of
+// that; 2^e and k's scale join the score in fp32.  v's scale goes into the
+// weight, which is kept relative to the largest weight times scale so far, 2^M2,
+// not to the largest weight: 2^(s_j - M2) vs_j <= 1, and what fp16 flushes is
+// below 2^-24 of the key that dominates the output, however far the scales of
+// the rows lie apart.  The sum l keeps its own maximum m.
 template <int DP_, int NT_, bool CODES_>
 struct TcConsumer {
     static constexpr int DP = DP_, NT = NT_;
@@ -140,16 +166,9 @@ struct TcConsumer {
 
     uint32_t qf[KSTEPS][NT][2];
     float m[NT][2], l[NT][2], qs[NT][2];
+    float m2[NT][2];  // E4M3: M2
     float o[MTILES][NT][4];
-    int vexp;  // E4M3: the exponent field that the weights are relative to
 
-    static __device__ __forceinline__ uint32_t even_pair(uint32_t c) {
-        const uint32_t t = c << 8;
-        return (t & 0x80008000u) | ((c << 4) & 0x07f007f0u);
-    }
-    static __device__ __forceinline__ uint32_t odd_pair(uint32_t c) {
-        return (c & 0x80008000u) | ((c >> 4) & 0x07f007f0u);
-    }
     // element of the head's row in o[t][..][2 r + ..]
     static __device__ __forceinline__ int elem(int t, int r) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
@@ -170,17 +189,15 @@ struct TcConsumer {
                     qf[k][nt][0] = h < heads && d < p.D ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
                     qf[k][nt][1] = h < heads && d + 8 < p.D ? *reinterpret_cast<const uint32_t*>(row + d + 8) : 0u;
                 } else {
-                    // elements 4i .. 4i+3 of the step, even ones and odd ones
-                    const int d = k * 16 + i * 4;
+                    const int d = k * 16 + i * 4;  // elements 4i .. 4i+3 of the step
                     uint2 u = make_uint2(0, 0);
                     if (h < heads && d < p.D) u = *reinterpret_cast<const uint2*>(row + d);
-                    qf[k][nt][0] = __byte_perm(u.x, u.y, 0x5410);
-                    qf[k][nt][1] = __byte_perm(u.x, u.y, 0x7632);
+                    qf[k][nt][0] = u.x;
+                    qf[k][nt][1] = u.y;
                 }
             }
+            qs[nt][0] = qs[nt][1] = to_log2;
             if constexpr (CODES) {
-                // |q| of the row below 2^(e+1); q * 2^(100 - e) is exact but for
-                // elements 2^-226 of the largest
                 __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < KSTEPS; ++k)
@@ -191,25 +208,20 @@ struct TcConsumer {
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 1) - 127;
-                // 2^(100 - e) in two factors, each within fp32's range
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + 100 - max(e, -26)) << 23);
-                const float up2 = e < -26 ? __uint_as_float(static_cast<uint32_t>(127 - 26 - e) << 23) : 1.f;
+                // 2^-e in two factors, each a normal number
+                const float f1 = pow2_bits(-(e >> 1)), f2 = pow2_bits(-(e - (e >> 1)));
 #pragma unroll
                 for (int k = 0; k < KSTEPS; ++k)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][nt][r]));
-                        qf[k][nt][r] = pack_bf16(f.x * up2 * up, f.y * up2 * up);
+                        qf[k][nt][r] = pack_f16(f.x * f1 * f2, f.y * f1 * f2);
                     }
-                // the score's factor of this row: scale 2^(e - 100 + 120)
-                const float back = __uint_as_float(static_cast<uint32_t>(min(127 + e + 20, 254)) << 23);
-                const float f = to_log2 * back;
+                const float f = to_log2 * pow2_bits(e);
                 qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * i);
                 qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * i + 4);
-            } else {
-                qs[nt][0] = qs[nt][1] = to_log2;
             }
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = m2[nt][0] = m2[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
         }
 #pragma unroll
@@ -218,12 +230,11 @@ struct TcConsumer {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
-        vexp = 100;
     }
 
     // stage: the tile in shared memory (K, then V); scales: E4M3, of its keys;
-    // maxima [kConsumers][HEADS], [kConsumers] and weights (W_BYTES): this
-    // tile's, of all the warps
+    // maxima [1 or 2][kConsumers][HEADS] and weights (W_BYTES): this tile's, of
+    // all the warps
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float* scales, float* maxima, uint8_t* weights,
                                          int lo, int hi) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
@@ -231,10 +242,10 @@ struct TcConsumer {
         const bool some = key0 < hi && key0 + 16 * SLICES > lo;
         const bool partial = lo > 0 || hi < TK;
         float s[SLICES][NT][4];
-        float vs[SLICES][2], vtop = 0.f;
-        float top[NT][2];
+        float vs[SLICES][2];
+        float top[NT][2], top2[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = top2[nt][0] = top2[nt][1] = -INFINITY;
         if (some) {
             // S^T = K q^T
             const uint32_t rowa = stage + (key0 + (lane & 15)) * 128;
@@ -255,12 +266,15 @@ struct TcConsumer {
                         for (int nt = 0; nt < NT; ++nt)
                             mma_bf16(c & 1 ? s2[nt] : s[sl][nt], a, qf[c][nt][0], qf[c][nt][1]);
                     } else {
-                        const uint32_t a0[4] = {even_pair(a[0]), even_pair(a[1]), odd_pair(a[0]), odd_pair(a[1])};
-                        const uint32_t a1[4] = {even_pair(a[2]), even_pair(a[3]), odd_pair(a[2]), odd_pair(a[3])};
+                        uint32_t a0[4], a1[4];
+                        unpack_e4m3(a[0], a0[0], a0[2]);
+                        unpack_e4m3(a[1], a0[1], a0[3]);
+                        unpack_e4m3(a[2], a1[0], a1[2]);
+                        unpack_e4m3(a[3], a1[1], a1[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(s[sl][nt], a0, qf[2 * c][nt][0], qf[2 * c][nt][1]);
-                            mma_bf16(s2[nt], a1, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
+                            mma_f16(s[sl][nt], a0, qf[2 * c][nt][0], qf[2 * c][nt][1]);
+                            mma_f16(s2[nt], a1, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
                         }
                     }
                 }
@@ -269,11 +283,12 @@ struct TcConsumer {
                 for (int r = 0; r < 2; ++r) {
                     const int key = key0 + sl * 16 + g + 8 * r;
                     const bool in = !partial || (key >= lo && key < hi);
-                    float ks = 1.f;
+                    float ks = 1.f, vlog = 0.f;
                     if constexpr (CODES) {
                         ks = scales[key];
                         vs[sl][r] = in ? scales[TK + key] : 0.f;
-                        vtop = fmaxf(vtop, vs[sl][r]);
+                        // M2 is a reference, not a result: vs's exponent does
+                        vlog = static_cast<float>(static_cast<int>(__float_as_uint(vs[sl][r]) >> 23) - 126);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -283,6 +298,7 @@ struct TcConsumer {
                             v += s2[nt][2 * r + e];
                             v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
                             top[nt][e] = fmaxf(top[nt][e], v);
+                            if constexpr (CODES) top2[nt][e] = fmaxf(top2[nt][e], v + vlog);
                         }
                 }
             }
@@ -293,48 +309,58 @@ struct TcConsumer {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) {
                     top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], off));
-            if constexpr (CODES) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+                    if constexpr (CODES) top2[nt][e] = fmaxf(top2[nt][e], __shfl_xor_sync(0xffffffffu, top2[nt][e], off));
+                }
         }
         if (lane < 4) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                *reinterpret_cast<float2*>(maxima + warp * HEADS + nt * 8 + 2 * lane) = make_float2(top[nt][0], top[nt][1]);
-            if (CODES && lane == 0) maxima[kConsumers * HEADS + warp] = vtop;
+            for (int nt = 0; nt < NT; ++nt) {
+                float* at = maxima + warp * HEADS + nt * 8 + 2 * lane;
+                *reinterpret_cast<float2*>(at) = make_float2(top[nt][0], top[nt][1]);
+                if constexpr (CODES)
+                    *reinterpret_cast<float2*>(at + kConsumers * HEADS) = make_float2(top2[nt][0], top2[nt][1]);
+            }
         }
         if (!consumers_agree(ok)) return false;
-        float vf = 1.f, vold = 1.f;  // E4M3: factors of the new weights and the old outputs
-        if constexpr (CODES) {
-            const float4 v4 = *reinterpret_cast<const float4*>(maxima + kConsumers * HEADS);
-            const int e = static_cast<int>(__float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w))) >> 23);
-            if (e > vexp) {  // the same in every thread
-                vold = __uint_as_float(static_cast<uint32_t>(max(127 - (e - vexp), 0)) << 23);
-                vexp = e;
-            }
-            vf = __uint_as_float(static_cast<uint32_t>(min(127 + 227 - vexp, 254)) << 23);
-        }
         float old[NT][2];
-        bool moved = vold != 1.f;
+        bool moved = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float2 t2 = make_float2(m[nt][0], m[nt][1]);
+            float2 t2 = make_float2(m[nt][0], m[nt][1]), u2 = make_float2(m2[nt][0], m2[nt][1]);
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
-                const float2 o2 = *reinterpret_cast<const float2*>(maxima + w * HEADS + nt * 8 + 2 * i);
+                const float* at = maxima + w * HEADS + nt * 8 + 2 * i;
+                const float2 o2 = *reinterpret_cast<const float2*>(at);
                 t2.x = fmaxf(t2.x, o2.x);
                 t2.y = fmaxf(t2.y, o2.y);
+                if constexpr (CODES) {
+                    const float2 p2 = *reinterpret_cast<const float2*>(at + kConsumers * HEADS);
+                    u2.x = fmaxf(u2.x, p2.x);
+                    u2.y = fmaxf(u2.y, p2.y);
+                }
             }
             top[nt][0] = t2.x;
             top[nt][1] = t2.y;
+            top2[nt][0] = u2.x;
+            top2[nt][1] = u2.y;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float base = top[nt][e] == -INFINITY ? 0.f : top[nt][e];
                 old[nt][e] = ex2(m[nt][e] - base);
-                moved |= top[nt][e] != m[nt][e];
-                m[nt][e] = top[nt][e];
                 l[nt][e] *= old[nt][e];
-                old[nt][e] *= vold;
+                float vf = 1.f;  // E4M3: 2^(m - M2)
+                if constexpr (CODES) {
+                    const float base2 = top2[nt][e] == -INFINITY ? 0.f : top2[nt][e];
+                    old[nt][e] = ex2(m2[nt][e] - base2);
+                    vf = ex2(base - base2);
+                    moved |= top2[nt][e] != m2[nt][e];
+                    m2[nt][e] = top2[nt][e];
+                } else {
+                    moved |= top[nt][e] != m[nt][e];
+                }
+                m[nt][e] = top[nt][e];
                 if (some) {
                     float sum = 0.f;
 #pragma unroll
@@ -350,15 +376,16 @@ struct TcConsumer {
                 }
             }
             if (some) {
-                // the weights, rounded to bf16 for the product with v; turned
-                // so that a thread stores two keys of one head
+                // the weights, rounded to bf16 (E4M3: fp16) for the product with
+                // v; turned so that a thread stores two keys of one head
                 uint8_t* row = weights + (nt * 8 + g) * W_STRIDE + (key0 + 2 * i) * 2;
 #pragma unroll
                 for (int sl = 0; sl < SLICES; ++sl)
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
                         *reinterpret_cast<uint32_t*>(row + (sl * 16 + 8 * r) * 2) =
-                            movmatrix_trans(pack_bf16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
+                            movmatrix_trans(CODES ? pack_f16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1])
+                                                  : pack_bf16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
             }
         }
         consumers_sync();
@@ -383,10 +410,9 @@ struct TcConsumer {
                 const int k0 = k2 * 32 + kk * 16;
                 if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
                 // what lies in a masked row may be anything (NaN for one), and
-                // 0 times that is not 0: such values are cleared (E4M3 codes
-                // are finite however they are read)
+                // 0 times that is not 0: such values are cleared
                 uint32_t keep0 = ~0u, keep1 = ~0u;
-                if (!CODES && partial) {
+                if (partial) {
                     auto pair = [&](int key) {
                         return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
                     };
@@ -417,12 +443,23 @@ struct TcConsumer {
                         const int c = chunk0 + t + (lane >> 4);
                         uint32_t a[4];
                         ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
-                        const uint32_t a0[4] = {even_pair(a[0]), odd_pair(a[0]), even_pair(a[1]), odd_pair(a[1])};
-                        const uint32_t a1[4] = {even_pair(a[2]), odd_pair(a[2]), even_pair(a[3]), odd_pair(a[3])};
+                        if (partial) {
+                            a[0] &= keep0;
+                            a[1] &= keep1;
+                            a[2] &= keep0;
+                            a[3] &= keep1;
+                        }
+                        // a register holds two elements of two keys each: keys
+                        // together, elements 2g to row g, 2g + 1 to row g + 8
+                        uint32_t a0[4], a1[4];
+                        unpack_e4m3(__byte_perm(a[0], 0, 0x3120), a0[0], a0[1]);
+                        unpack_e4m3(__byte_perm(a[1], 0, 0x3120), a0[2], a0[3]);
+                        unpack_e4m3(__byte_perm(a[2], 0, 0x3120), a1[0], a1[1]);
+                        unpack_e4m3(__byte_perm(a[3], 0, 0x3120), a1[2], a1[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(o[t][nt], a0, w[nt][2 * kk], w[nt][2 * kk + 1]);
-                            mma_bf16(o[t + 1][nt], a1, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                            mma_f16(o[t][nt], a0, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                            mma_f16(o[t + 1][nt], a1, w[nt][2 * kk], w[nt][2 * kk + 1]);
                         }
                     }
                 }
@@ -454,14 +491,14 @@ struct TcConsumer {
                 float sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kConsumers; ++w) sum += sums[w * HEADS + h];
-                // E4M3: 2^(vexp - 127 - 100 + 120) in two factors
-                const float f = CODES ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
+                // E4M3: o is relative to M2, the sum to m
+                const float f = CODES && sum != 0.f ? ex2(m2[nt][e] - m[nt][e]) : 1.f;
 #pragma unroll
                 for (int t = 0; t < MTILES; ++t)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float v = o[t][nt][2 * r + e];
-                        if constexpr (CODES) v = v * f * 0x1p20f;
+                        if constexpr (CODES) v *= f;
                         put(h, elem(t, r), v, m[nt][e], sum);
                     }
             }
@@ -646,8 +683,9 @@ struct F32Consumer {
 // ---------------------------------------------------------------- the frame
 
 struct Meta {       // of a ring stage, written by the producer
-    int b, j;       // sequence, item of the sequence
-    int lo, hi;     // keys of the tile that count
+    long long qrow;  // row of q and out of the item's first head
+    int heads;       // of the item
+    int lo, hi;      // keys of the tile that count
     int flags;
 };
 enum : int {
@@ -718,8 +756,8 @@ struct Smem {
     static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;
     static constexpr int Q_BYTES = C::HEADS * C::Q_STRIDE;
     static constexpr int STAGE_BYTES = 2 * C::K_BYTES;
-    // maxima [2][kConsumers * HEADS + 4], sums [kConsumers][HEADS], weights [2]
-    static constexpr int MAXIMA = kConsumers * C::HEADS + 4;
+    // maxima (two sets, for two tiles), sums [kConsumers][HEADS], weights [2]
+    static constexpr int MAXIMA = (C::CODES ? 2 : 1) * kConsumers * C::HEADS;
     static constexpr int STATS_BYTES = (2 * MAXIMA + kConsumers * C::HEADS) * 4;
     static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + 1024;  // 1024: alignment of the ring
     // what a CTA may have: 227 KB, or half of an SM's 228 KB less 1 KB each;
@@ -816,9 +854,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
 
     if (warp == kConsumers) {
         // -------------------------------------------------- producer
-        int join_parts = 0, join_b = 0, join_j = 0;
-        const int R = p.box_rows, nb = TK / R;
+        PagedAttnItem early = {0, 0, 0, 0, 0, 0}, late = early;
+        const int R = p.box_rows, nb_shift = __ffs(TK / R) - 1, nb = 1 << nb_shift;  // powers of two
         const int group = p.Hq / p.Hkv;
+        int heads = 0, pool_row = 0;  // of the item: its query heads; its head's first row in a shard's pages
+        long long qrow = 0;
         Cursor<TK> c = share_at;
         const bool any = c.b >= 0;
         // page of this lane's box of a tile (-1: bad, -2: no key of it counts)
@@ -843,11 +883,18 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             const int page_next = more ? page_of(n) : -2;
             if (!mbar_wait(&empty[s], ((i / L::STAGES) & 1) ^ 1, wc, kWhereKvEmpty, i)) break;
             const int key = c.key0() + lane * R;
-            const int hb = c.j % p.head_blocks, sk = c.j / p.head_blocks;
-            const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
+            const bool first = fresh || c.t == 0, ends = c.t == c.tiles - 1;
+            if (first) {
+                const int hb = c.j % p.head_blocks, sk = c.j / p.head_blocks;
+                const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
+                const int h0 = hb * p.heads_per_item;
+                heads = min(p.heads_per_item, group - h0);
+                qrow = (static_cast<long long>(shard) * p.B + c.b) * p.Hq + kvh * group + h0;
+                pool_row = (shard * p.num_pages * p.Hkv + kvh) * p.page_size;
+            }
             const int bad_row = p.P * p.num_pages * p.Hkv * p.page_size;  // outside the map: zeros
             int row = bad_row;
-            if (page >= 0) row = ((shard * p.num_pages + page) * p.Hkv + kvh) * p.page_size + key % p.page_size;
+            if (page >= 0) row = pool_row + page * p.Hkv * p.page_size + key % p.page_size;
             float* sc = reinterpret_cast<float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES);
             if (page == -1) {
                 status.code = SPTP_ERR_SHAPE;
@@ -860,24 +907,30 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             }
             const uint32_t loads = __ballot_sync(0xffffffffu, page != -2);
             const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
-            const bool first = fresh || c.t == 0, ends = c.t == c.tiles - 1;
-            const int h0 = hb * p.heads_per_item, heads = min(p.heads_per_item, group - h0);
             const int q_bytes = p.D * (C::F32 ? 4 : 2);
             if (lane == 0) {
                 Meta md;
-                md.b = c.b;
-                md.j = c.j;
+                md.qrow = qrow;
+                md.heads = heads;
                 md.lo = max(0, c.s.start - c.key0());
                 md.hi = max(0, min(TK, c.s.len - c.key0()));
                 md.flags = (first ? kFirst : 0) | (c.t == 0 ? kItemBegins : 0) | (ends ? kItemEnds : 0) |
                            (ends || !more ? kLast : 0) | (more ? 0 : kEnd);
                 meta[s] = md;
-                // an item that begins here and goes on in the next share
-                if (!more && !ends && c.at >= begin) {
-                    join_parts = static_cast<int>((c.at + static_cast<long long>(c.tiles - 1) * kTileCost) / share -
-                                                  blockIdx.x) + 1;
-                    join_b = c.b;
-                    join_j = c.j;
+                // an item that began in an earlier share, or goes on in the
+                // next: the shares of its parts
+                const bool from_before = fresh && c.at < begin, goes_on = !more && !ends && c.at >= begin;
+                if (from_before || goes_on) {
+                    PagedAttnItem it;
+                    it.first = static_cast<int>(c.at / share);
+                    it.parts =
+                        static_cast<int>((c.at + static_cast<long long>(c.tiles - 1) * kTileCost) / share) - it.first + 1;
+                    it.heads = heads;
+                    it.qrow = qrow;
+                    it.pad = 0;
+                    it.pad2 = 0;
+                    if (from_before) early = it;
+                    if (goes_on) late = it;
                 }
                 mbar_arrive_expect_tx(&full[s], __popc(loads) * 2 * R * C::ROW_BYTES +
                                                     (C::CODES ? __popc(good) * 2 * R * 4 : 0) +
@@ -885,15 +938,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             }
             __syncwarp();
             issued = i + 1;
-            if (first && lane < heads) {
-                const long long qrow = (static_cast<long long>(shard) * p.B + c.b) * p.Hq + kvh * group + h0 + lane;
+            if (first && lane < heads)
                 bulk_load(smem + L::QROWS + s * L::Q_BYTES + lane * C::Q_STRIDE,
-                          static_cast<const uint8_t*>(p.q) + qrow * q_bytes, q_bytes, &full[s]);
-            }
+                          static_cast<const uint8_t*>(p.q) + (qrow + lane) * q_bytes, q_bytes, &full[s]);
             uint8_t* st = smem + s * L::STAGE_BYTES;
             for (int base = 0; base < nb * C::BOXES * 2; base += 32) {
                 const int box = base + lane;
-                const int r = box % nb, which = box / nb;
+                const int r = box & (nb - 1), which = box >> nb_shift;
                 const int brow = __shfl_sync(0xffffffffu, row, r);
                 // a checked build: a page's rows, or the row of zeros
                 if (box < nb * C::BOXES * 2 && (loads >> r & 1) != 0 &&
@@ -920,9 +971,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
             if (++s == L::STAGES) s = 0;
         }
         if (lane == 0) {
-            part->join_parts = join_parts;
-            part->b = join_b;
-            part->j = join_j;
+            part->items[0] = early;
+            part->items[1] = late;
         }
         if (abort_flag) {
             // left early: wait (bounded) for the copies still in flight
@@ -934,17 +984,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
     } else {
         // -------------------------------------------------- consumers
         float* stats = reinterpret_cast<float*>(smem + L::STATS);
-        const int group = p.Hq / p.Hkv;
         bool begun = false;
         C c;
         for (int i = 0, s = 0;; ++i) {
             const bool ok = mbar_wait(&full[s], (i / L::STAGES) & 1, wc, kWhereKvFull, i);
             const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
-            const int hb = md.j % p.head_blocks, sk = md.j / p.head_blocks;
-            const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
-            const int h0 = hb * p.heads_per_item, heads = min(p.heads_per_item, group - h0);
+            const int heads = md.heads;
             if (md.flags & kFirst || i == 0) {
-                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, ok ? heads : 0);
+                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, heads);
                 begun = (md.flags & kItemBegins) != 0;
             }
             if (!c.tile(ok, smem_u32(smem) + s * L::STAGE_BYTES,
@@ -958,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
                 float* sums = stats + 2 * L::MAXIMA;
                 if (begun && (md.flags & kItemEnds)) {
                     // the whole item: o / l, rounded once
-                    const long long qrow = (static_cast<long long>(shard) * p.B + md.b) * p.Hq + kvh * group + h0;
+                    const long long qrow = md.qrow;
                     c.finish(sums, [&](int h, int d, float v, float m, float n) {
                         if (h >= heads || d >= p.D) return;
                         v = n == 0.f ? 0.f : __fdividef(v, n);

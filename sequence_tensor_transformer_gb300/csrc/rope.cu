@@ -100,18 +100,29 @@ __device__ __forceinline__ int kv_page(const RopeParams& p, int seq, int pos) {
     return page >= 0 && page < p.num_pages ? page : -1;
 }
 
-// The status words of an append, written once: this block walks over all
-// rows' indexes beside the blocks that move the data (which skip the bad ones
-// silently), so that no launch has to clear the words first.
+// The status words of an append of up to kCheckRows rows, written once: a block
+// of its own looks at all rows' indexes, in one round of loads, beside the
+// blocks that move the data (which skip the bad ones silently), so that no
+// launch has to clear the words first.  More rows are checked by the blocks
+// that move them, after a launch that clears the words: 1.5 us that a batch of
+// new tokens would feel and a prompt does not (for 16384 rows one block took 3
+// times as long as moving the data).
+constexpr int kCheckRows = 8 * kThreads;
+
 __device__ __noinline__ void check_rows(const RopeParams& p) {
     __shared__ int first_bad;
     if (threadIdx.x == 0) first_bad = 0x7fffffff;
     __syncthreads();
-#pragma unroll 4
-    for (int m = threadIdx.x; m < p.M; m += kThreads) {
-        const int seq = __ldg(p.seq_ids + m), pos = __ldg(p.positions + m);
-        if (seq >= 0 && kv_page(p, seq, pos) < 0) atomicMin(&first_bad, m);
+    int seq[8], pos[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = i * kThreads + threadIdx.x;
+        seq[i] = m < p.M ? __ldg(p.seq_ids + m) : -1;
+        pos[i] = m < p.M ? __ldg(p.positions + m) : 0;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (seq[i] >= 0 && kv_page(p, seq[i], pos[i]) < 0) atomicMin(&first_bad, i * kThreads + static_cast<int>(threadIdx.x));
     __syncthreads();
     if (threadIdx.x == 0) {
         const bool bad = first_bad != 0x7fffffff;
@@ -134,7 +145,8 @@ template <typename T, bool INTER, Op OP>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int L, int parts,
                                                         int per) {
     constexpr int E = Elems<T>::E;
-    if (OP != Op::kRope && blockIdx.x == gridDim.x - 1) {
+    const bool one_block_checks = OP != Op::kRope && p.M <= kCheckRows;
+    if (one_block_checks && blockIdx.x == gridDim.x - 1) {
         check_rows(p);
         return;
     }
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const bool has_a = ea < p.D, has_b = eb < p.D;
     const int rows = p.P * p.H;
     const long long units = static_cast<long long>(p.M) * parts;
-    const long long blocks = OP == Op::kRope ? gridDim.x : gridDim.x - 1;
+    const long long blocks = one_block_checks ? gridDim.x - 1 : gridDim.x;
     for (long long u = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; u < units;
          u += blocks * (kThreads / 32)) {
         const int m = static_cast<int>(u / parts);
@@ -162,6 +174,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             if (seq < 0) continue;  // a padding row
             page = kv_page(p, seq, pos);
             off = pos % p.page_size;
+            if (page < 0 && !one_block_checks && r0 == 0 && lane == 0 &&
+                atomicCAS(&p.status->code, 0, SPTP_ERR_SHAPE) == 0) {
+                p.status->where = kWhereKvSlot;
+                p.status->info = m;
+            }
         }
         float c[E], s[E];
         bool have = false;
@@ -274,7 +291,13 @@ cudaError_t launch_typed(const RopeParams& p, int num_sms, cudaStream_t s) {
     long long grid = (units + kThreads / 32 - 1) / (kThreads / 32);
     const long long cap = static_cast<long long>(num_sms) * 16;
     if (grid > cap) grid = cap;
-    if (OP != Op::kRope) ++grid;  // and the block that checks the indexes
+    if (OP != Op::kRope) {
+        if (p.M <= kCheckRows) ++grid;  // the block that checks the indexes
+        if (p.M > kCheckRows || kBoundsChecked) {
+            const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(DeviceStatus), s);
+            if (e != cudaSuccess) return e;
+        }
+    }
     const int g = static_cast<int>(grid), n = static_cast<int>(parts);
     if (p.interleaved)
         rope_kernel<T, true, OP><<<g, kThreads, 0, s>>>(p, L, n, per);

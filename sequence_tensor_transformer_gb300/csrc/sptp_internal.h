@@ -251,13 +251,20 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 
-// What one CTA of the attention leaves for the join: its status, and the
-// item that begins in its share and goes on in later ones (join_parts shares
-// in all; 0: none).
+// What one CTA of the attention leaves for the join: its status, and the items
+// whose parts lie in several shares that its share ends ([0]: the item began
+// in an earlier share) or begins ([1]: it goes on in the next).
+struct alignas(16) PagedAttnItem {
+    int parts;       // shares that hold a part, 0: no such item
+    int first;       // the first of them
+    int heads;       // of the item
+    int pad;
+    long long qrow;  // row of q and out of its first head
+    long long pad2;
+};
 struct PagedAttnPart {
-    int status, where, info;
-    int join_parts, b, j;
-    int pad[2];
+    PagedAttnItem items[2];
+    int status, where, info, pad;
 };
 constexpr int kPagedMaxCtas = 320;  // CTAs of one resident wave, at most
 

@@ -23,31 +23,27 @@ __device__ __forceinline__ float ex2(float x) {
 // such items that the share has a part of.  An item of n parts is joined by
 // the n halves of its shares, which take its slices (64 elements of one head)
 // in turn, so that one long row (few items, many parts) and many short ones
-// (many items, two parts) both spread over the SMs.  Up to kHalf parts: a warp
-// takes a slice and adds up its parts in ascending order.  More: the half's
-// warps take every kHalf-th part of a slice, and their sums are added in order.
+// (many items, two parts) both spread over the SMs.
 //
-// Bound by latency: loads that wait for one another, and the code's own first
-// fetch.  Three loads deep (the item, then maxima and outputs together), and
-// short.  The last block sums up the CTAs' status words.
-constexpr int kHalf = 4;  // warps
+// Bound by latency: a load of what another SM has just written takes about a
+// microsecond.  So a warp reads its parts of a slice in one batch, beside the
+// maxima, and `ways` warps share a slice of more than kBatch parts; their sums
+// are added in order.  The last block sums up the CTAs' status words.
+constexpr int kHalf = 8;   // warps
 constexpr int kJoinThreads = 2 * kHalf * 32;
 constexpr int kBatch = 8;  // parts whose loads a warp has in flight
 
 template <typename T>
-// (at most 64 registers: a block then fits beside the main kernel's CTAs and is
-// there when they end)
-__global__ void __launch_bounds__(kJoinThreads, 4) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas,
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas,
                                                                int head_shift) {
     __shared__ float2 sums[2][kHalf][32];
     __shared__ int first_bad;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c == ctas) {
         if (tid == 0) first_bad = ctas;
         __syncthreads();
-        for (int k = tid; k < ctas; k += kJoinThreads)
-            if (p.parts[k].status != 0) atomicMin(&first_bad, k);
+        if (tid < ctas && p.parts[tid].status != 0) atomicMin(&first_bad, tid);
         __syncthreads();
         if (tid == 0) {
             DeviceStatus st = {0, 0, 0, 0, 0};
@@ -66,71 +62,82 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attn_join(const __grid_
     const PagedAttnItem it = p.parts[c].items[which];
     const int n = it.parts;
     if (n < 2 || it.first < 0 || it.first + n > ctas) return;
-    const bool wide = n > kHalf;  // the half's warps share a slice
-    const int k0 = wide ? warp : 0, step = wide ? kHalf : 1;
+    const int way_shift = n <= kBatch ? 0 : n <= 4 * kBatch ? 2 : 3, ways = 1 << way_shift;
+    const int side_by_side = kHalf >> way_shift;  // slices that the half works on at a time
+    const int sub = warp & (ways - 1);
     const int slices = it.heads << head_shift;
 #pragma unroll 1
-    for (int s = c - it.first + (wide ? 0 : n * warp); s < slices; s += wide ? n : n * kHalf) {
+    for (int s0 = c - it.first; s0 < slices; s0 += n * side_by_side) {
+        const int s = s0 + n * (warp >> way_shift);
         const int h = s >> head_shift, d = ((s & ((1 << head_shift) - 1)) * 64) + lane * 2;
-        // part k: slot 0 of share first + k; the first part: slot 1
-        const float2* ml = p.part_ml + 2ll * it.first * p.heads_per_item + h;
-        const float* o = p.part_o + (2ll * it.first * p.heads_per_item + h) * p.D + d;
+        const bool mine = s < slices;
         float top = -INFINITY, sum = 0.f;
         float2 acc = make_float2(0.f, 0.f);
+        if (mine) {
+            // part k: slot 0 of share first + k; the first part: slot 1
+            const float2* ml = p.part_ml + 2ll * it.first * p.heads_per_item + h;
+            const float* o = p.part_o + (2ll * it.first * p.heads_per_item + h) * p.D + d;
 #pragma unroll 1
-        for (int b = k0; b < n; b += kBatch * step) {
-            float2 v[kBatch];
-            float m[kBatch];
+            for (int b = sub; b < n; b += kBatch * ways) {
+                float2 v[kBatch];
+                float m[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int k = b + u * step;
-                const int row = max(2 * k, 1) * p.heads_per_item;
-                v[u] = make_float2(0.f, 0.f);
-                m[u] = -INFINITY;
-                if (k < n) {
-                    m[u] = ml[row].x;
-                    if (d < p.D) v[u] = *reinterpret_cast<const float2*>(o + static_cast<long long>(row) * p.D);
+                for (int u = 0; u < kBatch; ++u) {
+                    const int k = b + u * ways;
+                    const int row = max(2 * k, 1) * p.heads_per_item;
+                    v[u] = make_float2(0.f, 0.f);
+                    m[u] = -INFINITY;
+                    if (k < n) {
+                        m[u] = ml[row].x;
+                        if (d < p.D) v[u] = *reinterpret_cast<const float2*>(o + static_cast<long long>(row) * p.D);
+                    }
                 }
-            }
-            if (b == k0) {  // the statistics, while these loads are under way
-                float2 q = make_float2(-INFINITY, 0.f);
-                if (lane < n) q = ml[max(2 * lane, 1) * p.heads_per_item];
-                top = q.x;
-#pragma unroll 4
-                for (int k = lane + 32; k < n; k += 32) top = fmaxf(top, ml[2 * k * p.heads_per_item].x);
+                if (b == sub) {  // the statistics, while these loads are under way
+                    constexpr int kTurns = 3;
+                    float2 q[kTurns];
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                if (top == -INFINITY) top = 0.f;
-                sum = ex2(q.x - top) * q.y;
-#pragma unroll 4
-                for (int k = lane + 32; k < n; k += 32) {
-                    const float2 r = ml[2 * k * p.heads_per_item];
-                    sum = fmaf(ex2(r.x - top), r.y, sum);
+                    for (int t = 0; t < kTurns; ++t) {
+                        const int k = t * 32 + lane;
+                        q[t] = make_float2(-INFINITY, 0.f);
+                        if (k < n) q[t] = ml[max(2 * k, 1) * p.heads_per_item];
+                    }
+#pragma unroll
+                    for (int t = 0; t < kTurns; ++t) top = fmaxf(top, q[t].x);
+#pragma unroll 1
+                    for (int k = kTurns * 32 + lane; k < n; k += 32) top = fmaxf(top, ml[2 * k * p.heads_per_item].x);
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    if (top == -INFINITY) top = 0.f;
+#pragma unroll
+                    for (int t = 0; t < kTurns; ++t) sum = fmaf(ex2(q[t].x - top), q[t].y, sum);
+#pragma unroll 1
+                    for (int k = kTurns * 32 + lane; k < n; k += 32) {
+                        const float2 r = ml[2 * k * p.heads_per_item];
+                        sum = fmaf(ex2(r.x - top), r.y, sum);
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const float f = ex2(m[u] - top);
-                acc.x = fmaf(f, v[u].x, acc.x);
-                acc.y = fmaf(f, v[u].y, acc.y);
+                for (int u = 0; u < kBatch; ++u) {
+                    const float f = ex2(m[u] - top);
+                    acc.x = fmaf(f, v[u].x, acc.x);
+                    acc.y = fmaf(f, v[u].y, acc.y);
+                }
             }
         }
-        if (wide) {
+        if (ways > 1) {
             auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "n"(kHalf * 32) : "memory"); };
             sums[which][warp][lane] = acc;
             sync();
-            acc = sums[which][0][lane];
-#pragma unroll
-            for (int w = 1; w < kHalf; ++w) {
-                acc.x += sums[which][w][lane].x;
-                acc.y += sums[which][w][lane].y;
-            }
+            if (sub == 0)
+                for (int w = 1; w < ways; ++w) {
+                    acc.x += sums[which][warp + w][lane].x;
+                    acc.y += sums[which][warp + w][lane].y;
+                }
             sync();
-            if (warp != 0) continue;
         }
-        if (d >= p.D) continue;
+        if (!mine || sub != 0 || d >= p.D) continue;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         T* out = static_cast<T*>(p.out) + (it.qrow + h) * p.D + d;
         if constexpr (sizeof(T) == 2)
@@ -141,6 +148,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attn_join(const __grid_
             p.lse[it.qrow + h] = sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
     }
 }
+static_assert(kJoinThreads >= kPagedMaxCtas, "one thread per status word");
+
 }  // namespace
 
 cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {

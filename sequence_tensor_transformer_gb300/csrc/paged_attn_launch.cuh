@@ -1,6 +1,8 @@
 // Launch of the paged attention with one consumer class.
 #pragma once
 
+#include <atomic>
+
 #include "paged_attn.cuh"
 
 namespace sptp {
@@ -23,8 +25,17 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (!encode_map_rows(&p.map_k, p.k, es, p.D, rows, inner, p.box_rows) ||
         !encode_map_rows(&p.map_v, p.v, es, p.D, rows, inner, p.box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<C>::BYTES);
+    // once per device (the call costs half a microsecond; doing it twice is harmless)
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<C>::BYTES);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
     // one resident wave, or a CTA per tile where the table cannot hold as many
     long long grid = static_cast<long long>(num_sms) * C::CTAS;
     const long long span = static_cast<long long>(p.max_pages) * p.page_size;

@@ -52,7 +52,7 @@ int check_cache(int P, int Hkv, int D, int B, int max_pages, int num_pages, int 
     if (kv_type == SPTP_KV_E4M3 && dtype != SPTP_BF16) return SPTP_ERR_DTYPE;
     if (kv_type == SPTP_KV_E4M3 && D % 16 != 0) return SPTP_ERR_SHAPE;
     if (B < 0 || max_pages < 1 || num_pages < 1 || page_size < 16 || page_size % 16 != 0) return SPTP_ERR_SHAPE;
-    if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return SPTP_ERR_SHAPE;
+    if (static_cast<long long>(max_pages) * page_size >= (1ll << 30)) return SPTP_ERR_SHAPE;
     // rows of the pool (a TMA coordinate), each product below 2^31 before the next
     long long rows = static_cast<long long>(num_pages) * page_size;
     if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;

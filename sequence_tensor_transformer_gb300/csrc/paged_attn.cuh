@@ -125,7 +125,8 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 //   HEADS, DP              query heads of an item, elements of a row, at most
 //   TK                     keys of a tile
 //   ROW_BYTES, BOXES       a key's bytes, TMA boxes per row
-//   begin(q, heads)        a new item; q its rows in shared memory
+//   begin(q, keep, heads)  a new item; q its rows in shared memory, keep room for
+//                          them (KEEP_BYTES); no barrier of the warps
 //   tile(...)              keys [lo, hi) of a tile; false if a warp's `ok` is
 //   finish(...)            an item's end, or its part's
 
@@ -152,11 +153,13 @@ struct TcConsumer {
     static constexpr bool F32 = false;
     static constexpr int HEADS = 8 * NT;
     static constexpr int ROW_BYTES = DP * (CODES ? 1 : 2);
+    static constexpr int ELEM = CODES ? 1 : 2;  // bytes
     static constexpr int BOXES = ROW_BYTES / 128;
     static constexpr int TK = ROW_BYTES == 128 && NT == 1 ? 128 : 64;  // 32 KB a tile, or 64 keys
     static constexpr int Q_STRIDE = DP * 2 + 16;                        // bytes; 8 rows in distinct banks
     static constexpr int W_STRIDE = TK * 2 + 16;
     static constexpr int W_BYTES = HEADS * W_STRIDE;
+    static constexpr int KEEP_BYTES = 0;
     static constexpr int CTAS = NT < 4 && ROW_BYTES <= 256 ? 2 : 1;
     static constexpr int K_BYTES = TK * ROW_BYTES;
     static constexpr int SLICES = TK / (16 * kConsumers);  // of 16 keys, a warp's
@@ -175,7 +178,7 @@ struct TcConsumer {
         return warp * (DP / kConsumers) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
     }
 
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, int heads) {
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, uint8_t*, int heads) {
         const int lane = threadIdx.x & 31, g = lane >> 2, i = lane & 3;
         const float to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
@@ -507,110 +510,108 @@ struct TcConsumer {
 
 // fp32 consumer: CUDA cores, fp32 throughout, up to 8 query heads.
 //
-// Scores: lane i holds elements of q and of each row it reads (conflict-free);
-// a row's product with 8 heads leaves 32 lanes' partial sums of 8 scores.  Four
-// keys at a time give 32 such sums, which 31 exchanges turn into one finished
-// score per lane (lane = key * 8 + head).  Outputs: a lane owns elements of the
-// row (a part of the keys, where a warp's elements are fewer than its lanes).
+// Scores: a lane owns a key (or half a row of one, where a tile has only 16) and
+// goes along its row, 16 bytes at a time, for the HPW heads of its warp, whose
+// queries all lanes read from the same place; the swizzle that TMA leaves the
+// rows in makes the lanes' reads free of bank conflicts, and no score needs a
+// sum over lanes.  Outputs: a lane owns an element or two of the row (every
+// second key, where a warp's elements are fewer than its lanes).
 template <int DP_>
 struct F32Consumer {
     static constexpr int DP = DP_;
     static constexpr bool CODES = false;
     static constexpr bool F32 = true;
     static constexpr int HEADS = 8;
+    static constexpr int ELEM = 4;  // bytes
     static constexpr int ROW_BYTES = DP * 4;
-    static constexpr int BOXES = 1;
+    static constexpr int BOXES = ROW_BYTES / 128;
     static constexpr int TK = 16384 / ROW_BYTES;
     static constexpr int K_BYTES = TK * ROW_BYTES;
     static constexpr int Q_STRIDE = ROW_BYTES;
-    static constexpr int W_BYTES = TK * HEADS * 4;
+    static constexpr int W_STRIDE = HEADS + 4;  // floats of a key's weights
+    static constexpr int W_BYTES = TK * W_STRIDE * 4;
     static constexpr int CTAS = 2;
-    static constexpr int V = DP / 32;                      // elements of a row a lane scores with
-    static constexpr int QUADS = TK / kConsumers / 4;      // of 4 keys, a warp's
-    static constexpr int OWN = DP / kConsumers;            // elements of a warp's outputs
-    static constexpr int E = OWN > 32 ? OWN / 32 : 1;      // of a lane's
-    static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;  // lanes that share an element, every SPLIT-th key
+    static constexpr int KEY_GROUPS = TK > 32 ? TK / 32 : 1;       // of the warps
+    static constexpr int HPW = HEADS * KEY_GROUPS / kConsumers;    // heads of a warp's scores
+    static constexpr int KEEP_BYTES = kConsumers * HPW * ROW_BYTES;
+    static constexpr int ROW_PARTS = TK < 32 ? 32 / TK : 1;        // lanes that share a row
+    static constexpr int OWN = DP / kConsumers;                    // elements of a warp's outputs
+    static constexpr int E = OWN > 32 ? OWN / 32 : 1;              // of a lane's
+    static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;          // lanes that share an element
+    static_assert(HPW == 2 || HPW == 4, "vectors of weights");
 
-    float q[HEADS][V], o[HEADS][E];
-    float m, l;  // of head lane & 7: m of all keys, l of this warp's keys lane >> 3 (mod 4)
+    const uint8_t* q;  // this warp's heads of the item's queries
+    float o[HEADS][E];
+    float m;       // of head lane & 7
+    float l[HPW];  // of this lane's keys
+    float to_log2;
+    int heads;
 
-    static __device__ __forceinline__ void load_row(uint32_t addr, float (&f)[V]) {
-        if constexpr (V == 2) {
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(addr) : "memory");
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; v += 4)
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(f[v]), "=f"(f[v + 1]), "=f"(f[v + 2]), "=f"(f[v + 3])
-                             : "r"(addr + v * 128)
-                             : "memory");
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* rows, uint8_t* keep, int n) {
+        // the stage that the queries came with is given back: this warp's heads
+        // are copied, cleared where the item has no head or the row no element
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h0 = warp / KEY_GROUPS * HPW;
+        uint8_t* mine = keep + warp * HPW * ROW_BYTES;
+        __syncwarp();  // the last item's queries are no longer read
+        for (int i = lane; i < HPW * DP / 4; i += 32) {
+            const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h0 + h < n && d < p.D) v = *reinterpret_cast<const float4*>(rows + (h0 + h) * Q_STRIDE + d * 4);
+            *reinterpret_cast<float4*>(mine + h * ROW_BYTES + d * 4) = v;
         }
-    }
-    // element of lane i's vector slot v: rows of 256 are read as two halves, so
-    // that every access is conflict-free
-    static __device__ __forceinline__ int score_elem(int lane, int v) {
-        return V == 8 ? (v >> 2) * 128 + lane * 4 + (v & 3) : lane * V + v;
-    }
-
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* qrows, int heads) {
-        const int lane = threadIdx.x & 31;
-        const float to_log2 = p.scale * 1.4426950408889634f;
+        __syncwarp();
+        q = mine;
+        heads = n;
+        to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            const float* row = reinterpret_cast<const float*>(qrows + h * Q_STRIDE);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int d = score_elem(lane, v);
-                q[h][v] = h < heads && d < p.D ? row[d] * to_log2 : 0.f;
-            }
+        for (int h = 0; h < HEADS; ++h)
 #pragma unroll
             for (int e = 0; e < E; ++e) o[h][e] = 0.f;
-        }
         m = -INFINITY;
-        l = 0.f;
+#pragma unroll
+        for (int h = 0; h < HPW; ++h) l[h] = 0.f;
     }
 
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float*, float* maxima, uint8_t* weights, int lo,
                                          int hi) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const uint32_t at = stage + lane * (V == 2 ? 8 : 16);
-        const int key0 = warp * QUADS * 4;
-        float* w = reinterpret_cast<float*>(weights);  // [TK][HEADS]
-        float x[QUADS], top = -INFINITY;
+        const int key = (KEY_GROUPS > 1 ? warp % KEY_GROUPS * 32 : 0) + lane % (TK < 32 ? TK : 32);
+        const int h0 = warp / KEY_GROUPS * HPW;  // this warp's heads
+        const bool in = key >= lo && key < hi;
+        float* w = reinterpret_cast<float*>(weights);  // [TK][W_STRIDE]
+        float x[HPW];
 #pragma unroll
-        for (int u = 0; u < QUADS; ++u) {
-            const int k0 = key0 + u * 4;
-            x[u] = -INFINITY;
-            if (k0 >= hi || k0 + 4 <= lo) continue;
-            float s[32];
+        for (int h = 0; h < HPW; ++h) x[h] = 0.f;
+        if (h0 < heads) {
+            const int part = lane / TK;  // of the row (0 where a lane has it all)
+            const uint32_t row = stage + key * 128;
+            const float4* qv = reinterpret_cast<const float4*>(q);
+#pragma unroll 4
+            for (int c0 = 0; c0 < DP / 4 / ROW_PARTS; ++c0) {
+                const int c = ROW_PARTS > 1 ? c0 + part * (DP / 4 / ROW_PARTS) : c0;
+                float4 k;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+                             : "r"(row + (c >> 3) * (TK * 128) + (((c & 7) ^ (key & 7)) << 4))
+                             : "memory");
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float f[V];
-                load_row(at + (k0 + k) * ROW_BYTES, f);
-#pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    float a = q[h][0] * f[0];
-#pragma unroll
-                    for (int v = 1; v < V; ++v) a = fmaf(q[h][v], f[v], a);
-                    s[k * 8 + h] = a;
+                for (int h = 0; h < HPW; ++h) {
+                    const float4 a = qv[h * (DP / 4) + c];
+                    x[h] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, x[h]))));
                 }
             }
-            // halves exchanged, each lane keeping the sums of its side
-#pragma unroll
-            for (int n = 16; n > 0; n >>= 1) {
-                const bool up = (lane & n) != 0;
-#pragma unroll
-                for (int j = 0; j < n; ++j) {
-                    const float give = up ? s[j] : s[j + n], keep = up ? s[j + n] : s[j];
-                    s[j] = keep + __shfl_xor_sync(0xffffffffu, give, n);
-                }
-            }
-            const int key = k0 + (lane >> 3);
-            if (key >= lo && key < hi) x[u] = s[0];
-            top = fmaxf(top, x[u]);
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < HPW; ++h) {
+#pragma unroll
+            for (int off = TK; off < 32; off <<= 1) x[h] += __shfl_xor_sync(0xffffffffu, x[h], off);
+            x[h] = in ? x[h] * to_log2 : -INFINITY;
+            float t = x[h];
+#pragma unroll
+            for (int off = 1; off < (TK < 32 ? TK : 32); off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+            if ((lane & 7) == h0 + h) top = t;
+        }
         if (lane < 8) maxima[warp * HEADS + lane] = top;
         if (!consumers_agree(ok)) return false;
         top = m;
@@ -620,12 +621,17 @@ struct F32Consumer {
         const float old = ex2(m - base);
         const bool moved = top != m;
         m = top;
-        l *= old;
 #pragma unroll
-        for (int u = 0; u < QUADS; ++u) {
-            const float e = ex2(x[u] - base);
-            l += e;
-            w[(key0 + u * 4) * HEADS + lane] = e;
+        for (int h = 0; h < HPW; ++h) {
+            x[h] = ex2(x[h] - __shfl_sync(0xffffffffu, base, h0 + h));
+            l[h] = fmaf(l[h], __shfl_sync(0xffffffffu, old, h0 + h), x[h]);
+        }
+        if (lane < TK) {
+            float* at = w + key * W_STRIDE + h0;
+            if constexpr (HPW == 4)
+                *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
+            else
+                *reinterpret_cast<float2*>(at) = make_float2(x[0], x[1]);
         }
         consumers_sync();
         if (__any_sync(0xffffffffu, moved)) {
@@ -637,31 +643,49 @@ struct F32Consumer {
             }
         }
         // keys [lo, hi) alone: a masked row may hold anything
-        const uint32_t vat = stage + K_BYTES + (warp * OWN + (SPLIT > 1 ? lane % OWN : lane * E)) * 4;
-        const float4* w4 = reinterpret_cast<const float4*>(w);
+        const int d = warp * OWN + (SPLIT > 1 ? lane % OWN : lane * E);
+        const uint32_t vat = stage + K_BYTES + (d >> 5) * (TK * 128) + (d & 3) * 4;
+        const int chunk = d >> 2 & 7;
+        const bool many = heads > 4;
 #pragma unroll 4
         for (int k = lo + (SPLIT > 1 ? lane / OWN : 0); k < hi; k += SPLIT) {
-            const float4 wa = w4[2 * k], wb = w4[2 * k + 1];
+            const float4* w4 = reinterpret_cast<const float4*>(w + k * W_STRIDE);
+            const uint32_t addr = vat + k * 128 + ((chunk ^ (k & 7)) << 4);
             float f[E];
             if constexpr (E == 2)
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(vat + k * ROW_BYTES) : "memory");
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(addr) : "memory");
             else
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(vat + k * ROW_BYTES) : "memory");
-            const float wk[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(addr) : "memory");
+            const float4 wa = w4[0];
+            const float wk[4] = {wa.x, wa.y, wa.z, wa.w};
 #pragma unroll
-            for (int h = 0; h < HEADS; ++h)
+            for (int h = 0; h < 4; ++h)
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[h][e] = fmaf(wk[h], f[e], o[h][e]);
+            if (many) {
+                const float4 wb = w4[1];
+                const float wl[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[4 + h][e] = fmaf(wl[h], f[e], o[4 + h][e]);
+            }
         }
         return true;
     }
 
     template <typename Put>
     __device__ __forceinline__ void finish(float* sums, Put put) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        float sum = l + __shfl_xor_sync(0xffffffffu, l, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (lane < 8) sums[warp * HEADS + lane] = sum;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h0 = warp / KEY_GROUPS * HPW;
+        float mine = 0.f;
+#pragma unroll
+        for (int h = 0; h < HPW; ++h) {
+            float n = l[h];
+#pragma unroll
+            for (int off = 1; off < (TK < 32 ? TK : 32); off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+            if (lane == h0 + h) mine = n;
+        }
+        if (lane < 8) sums[warp * HEADS + lane] = mine;
         consumers_sync();
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
@@ -706,14 +730,17 @@ struct Span {
     int start, len;
 };
 
-__device__ __forceinline__ Span span_of(const PagedAttnParams& p, int b, bool* bad) {
-    const int most = p.max_pages * p.page_size;
-    const int n = __ldg(p.seq_lens + b);
-    if (n < 0 || n > most) *bad = true;
+__device__ __forceinline__ Span clip(const PagedAttnParams& p, int n) {
     Span s;
-    s.len = max(0, min(n, most));
+    s.len = max(0, min(n, p.max_pages * p.page_size));
     s.start = p.window > 0 ? max(0, s.len - p.window) : 0;
     return s;
+}
+
+__device__ __forceinline__ Span span_of(const PagedAttnParams& p, int b, bool* bad) {
+    const int n = __ldg(p.seq_lens + b);
+    if (n < 0 || n > p.max_pages * p.page_size) *bad = true;
+    return clip(p, n);
 }
 
 // Tiles of an item: those that hold keys [start, len); one for an empty row,
@@ -746,9 +773,6 @@ struct Cursor {
         j = 0;
         if (++b < p.B) load(p);
     }
-    __device__ __forceinline__ void next(const PagedAttnParams& p) {
-        if (++t >= tiles) next_item(p);
-    }
 };
 
 template <class C>
@@ -759,7 +783,8 @@ struct Smem {
     // maxima (two sets, for two tiles), sums [kConsumers][HEADS], weights [2]
     static constexpr int MAXIMA = (C::CODES ? 2 : 1) * kConsumers * C::HEADS;
     static constexpr int STATS_BYTES = (2 * MAXIMA + kConsumers * C::HEADS) * 4;
-    static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + 1024;  // 1024: alignment of the ring
+    static constexpr int KEEP_BYTES = C::KEEP_BYTES;
+    static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + KEEP_BYTES + 1024;  // 1024: alignment of the ring
     // what a CTA may have: 227 KB, or half of an SM's 228 KB less 1 KB each;
     // less the kernel's static shared memory
     static constexpr int ROOM = (C::CTAS == 2 ? 113 * 1024 : 227 * 1024) - 512;
@@ -769,7 +794,8 @@ struct Smem {
     static constexpr int QROWS = SCALES + STAGES * 2 * SCALE_BYTES;
     static constexpr int STATS = QROWS + STAGES * Q_BYTES;
     static constexpr int WEIGHTS = STATS + STATS_BYTES;
-    static constexpr int BYTES = WEIGHTS + 2 * C::W_BYTES + 1024;
+    static constexpr int KEEP = WEIGHTS + 2 * C::W_BYTES;
+    static constexpr int BYTES = KEEP + KEEP_BYTES + 1024;
     static_assert(STAGES >= 2 && STATS_BYTES % 16 == 0 && Q_BYTES % 16 == 0, "layout");
 };
 
@@ -856,119 +882,152 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
         // -------------------------------------------------- producer
         PagedAttnItem early = {0, 0, 0, 0, 0, 0}, late = early;
         const int R = p.box_rows, nb_shift = __ffs(TK / R) - 1, nb = 1 << nb_shift;  // powers of two
+        const int per = 32 >> nb_shift;  // tiles whose rows the lanes look up at once
         const int group = p.Hq / p.Hkv;
-        int heads = 0, pool_row = 0;  // of the item: its query heads; its head's first row in a shard's pages
-        long long qrow = 0;
+        const int pages_rows = p.Hkv * p.page_size;               // of a shard's page
+        const int bad_row = p.P * p.num_pages * pages_rows;       // outside the maps: zeros
+        const int q_bytes = p.D * (C::F32 ? 4 : 2);
+        // this lane's box of a tile: nb x BOXES x 2 of them, at most 32
+        static_assert(TK / 16 * C::BOXES * 2 <= 32, "one box per lane");
+        const int box_r = lane & (nb - 1), box_cb = lane >> nb_shift >> 1;
+        const bool box_v = lane >> nb_shift & 1, box_in = lane < nb * C::BOXES * 2;
+        const uint32_t box_at = (box_v ? C::K_BYTES : 0) + box_cb * TK * 128 + box_r * R * 128;
+        const int box_x = box_cb * (128 / C::ELEM);
+        const CUtensorMap* box_map = box_v ? &p.map_v : &p.map_k;
+
         Cursor<TK> c = share_at;
-        const bool any = c.b >= 0;
-        // page of this lane's box of a tile (-1: bad, -2: no key of it counts)
-        auto page_of = [&](const Cursor<TK>& at) {
-            const int key = at.key0() + lane * R;
-            if (lane >= nb || key >= at.s.len || key + R <= at.s.start) return -2;
-            const int page = __ldg(p.page_table + static_cast<long long>(at.b) * p.max_pages + key / p.page_size);
-            return page >= 0 && page < p.num_pages ? page : -1;
-        };
-        int page = any ? page_of(c) : -2;
-        int issued = 0;
-        if (!any && lane == 0) {
+        bool more = c.b >= 0, fresh = true;  // fresh: the first item of this share
+        if (!more && lane == 0) {
             meta[0] = Meta{0, 0, 0, 0, kEnd};
             mbar_arrive(&full[0]);
         }
-        bool more = any, fresh = true;  // fresh: the first tile of this share
-        for (int i = 0, s = 0; more; ++i) {
-            // the next tile's pages are read while this one waits for its stage
+        // page of rows [key, key + R) (-1: bad, -2: no key of them counts)
+        auto page_of = [&](int b, const Span& sp, int key) {
+            if (key >= sp.len || key + R <= sp.start) return -2;
+            const int index = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
+            const int page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + index);
+            return page >= 0 && page < p.num_pages ? page : -1;
+        };
+        int page = more ? page_of(c.b, c.s, c.key0() + lane * R) : -2;
+        int raw_next = more && c.b + 1 < p.B ? __ldg(p.seq_lens + c.b + 1) : 0;
+        int issued = 0, s = 0;
+        uint32_t phase = 1;
+        while (more) {
+            // one item: its tiles that lie in this share
+            const long long room = (end - c.tile_at() + kTileCost - 1) / kTileCost;
+            const int here = static_cast<int>(min(static_cast<long long>(c.tiles - c.t), room));
+            const bool begins = c.t == 0, ends = c.t + here == c.tiles;
+            const int hb = c.j % p.head_blocks, sk = c.j / p.head_blocks;
+            const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
+            const int h0 = hb * p.heads_per_item, heads = min(p.heads_per_item, group - h0);
+            const long long qrow = (static_cast<long long>(shard) * p.B + c.b) * p.Hq + kvh * group + h0;
+            const int pool_row = (shard * p.num_pages * p.Hkv + kvh) * p.page_size;
+            const int key_begin = c.key0();
+            if ((fresh && !begins) || !ends) {
+                // it began in an earlier share, or goes on in the next
+                PagedAttnItem it;
+                it.first = static_cast<int>(c.at / share);
+                it.parts =
+                    static_cast<int>((c.at + static_cast<long long>(c.tiles - 1) * kTileCost) / share) - it.first + 1;
+                it.heads = heads;
+                it.qrow = qrow;
+                it.pad = 0;
+                it.pad2 = 0;
+                (begins ? late : early) = it;
+            }
+            // the item after it
             Cursor<TK> n = c;
-            n.next(p);
-            more = n.b < p.B && n.tile_at() < end;
-            const int page_next = more ? page_of(n) : -2;
-            if (!mbar_wait(&empty[s], ((i / L::STAGES) & 1) ^ 1, wc, kWhereKvEmpty, i)) break;
-            const int key = c.key0() + lane * R;
-            const bool first = fresh || c.t == 0, ends = c.t == c.tiles - 1;
-            if (first) {
-                const int hb = c.j % p.head_blocks, sk = c.j / p.head_blocks;
-                const int shard = sk / p.Hkv, kvh = sk - shard * p.Hkv;
-                const int h0 = hb * p.heads_per_item;
-                heads = min(p.heads_per_item, group - h0);
-                qrow = (static_cast<long long>(shard) * p.B + c.b) * p.Hq + kvh * group + h0;
-                pool_row = (shard * p.num_pages * p.Hkv + kvh) * p.page_size;
+            n.t = 0;
+            n.at += c.item_cost();
+            if (++n.j == p.items_per_seq) {
+                n.j = 0;
+                ++n.b;
+                n.s = clip(p, raw_next);
+                n.tiles = tiles_of<TK>(n.s);
             }
-            const int bad_row = p.P * p.num_pages * p.Hkv * p.page_size;  // outside the map: zeros
-            int row = bad_row;
-            if (page >= 0) row = pool_row + page * p.Hkv * p.page_size + key % p.page_size;
-            float* sc = reinterpret_cast<float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES);
-            if (page == -1) {
-                status.code = SPTP_ERR_SHAPE;
-                status.where = kWhereKvPage;
-                status.info = c.b;
-                if constexpr (C::CODES) {
-                    for (int r = 0; r < R; ++r) sc[lane * R + r] = sc[TK + lane * R + r] = 0.f;
-                    fence_proxy_async_smem();
-                }
-            }
-            const uint32_t loads = __ballot_sync(0xffffffffu, page != -2);
-            const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
-            const int q_bytes = p.D * (C::F32 ? 4 : 2);
-            if (lane == 0) {
-                Meta md;
-                md.qrow = qrow;
-                md.heads = heads;
-                md.lo = max(0, c.s.start - c.key0());
-                md.hi = max(0, min(TK, c.s.len - c.key0()));
-                md.flags = (first ? kFirst : 0) | (c.t == 0 ? kItemBegins : 0) | (ends ? kItemEnds : 0) |
-                           (ends || !more ? kLast : 0) | (more ? 0 : kEnd);
-                meta[s] = md;
-                // an item that began in an earlier share, or goes on in the
-                // next: the shares of its parts
-                const bool from_before = fresh && c.at < begin, goes_on = !more && !ends && c.at >= begin;
-                if (from_before || goes_on) {
-                    PagedAttnItem it;
-                    it.first = static_cast<int>(c.at / share);
-                    it.parts =
-                        static_cast<int>((c.at + static_cast<long long>(c.tiles - 1) * kTileCost) / share) - it.first + 1;
-                    it.heads = heads;
-                    it.qrow = qrow;
-                    it.pad = 0;
-                    it.pad2 = 0;
-                    if (from_before) early = it;
-                    if (goes_on) late = it;
-                }
-                mbar_arrive_expect_tx(&full[s], __popc(loads) * 2 * R * C::ROW_BYTES +
-                                                    (C::CODES ? __popc(good) * 2 * R * 4 : 0) +
-                                                    (first ? heads * q_bytes : 0));
-            }
-            __syncwarp();
-            issued = i + 1;
-            if (first && lane < heads)
-                bulk_load(smem + L::QROWS + s * L::Q_BYTES + lane * C::Q_STRIDE,
-                          static_cast<const uint8_t*>(p.q) + (qrow + lane) * q_bytes, q_bytes, &full[s]);
-            uint8_t* st = smem + s * L::STAGE_BYTES;
-            for (int base = 0; base < nb * C::BOXES * 2; base += 32) {
-                const int box = base + lane;
-                const int r = box & (nb - 1), which = box >> nb_shift;
-                const int brow = __shfl_sync(0xffffffffu, row, r);
-                // a checked build: a page's rows, or the row of zeros
-                if (box < nb * C::BOXES * 2 && (loads >> r & 1) != 0 &&
-                    checked(brow >= 0 && (brow == bad_row || brow + R <= bad_row), &status, &abort_flag, kWhereBoundsTma,
-                            brow)) {
-                    const int cb = which >> 1;
-                    const bool is_v = which & 1;
-                    uint8_t* dst = st + (is_v ? C::K_BYTES : 0) +
-                                   (C::F32 ? r * R * C::ROW_BYTES : cb * TK * 128 + r * R * 128);
-                    const int x = C::F32 ? 0 : cb * (C::CODES ? 128 : 64);
-                    // boxes past a narrow row's end lie outside the map: zeros
-                    tma_load_2d(dst, is_v ? &p.map_v : &p.map_k, &full[s], x, brow);
-                }
-            }
-            if constexpr (C::CODES) {
+            more = n.b < p.B && n.at < end;
+            for (int u0 = 0; u0 < here; u0 += per) {
+                const int key = key_begin + u0 * TK + lane * R;  // of this lane's rows
+                int row = bad_row;
                 if (page >= 0) {
-                    bulk_load(sc + lane * R, p.k_scale + row, R * 4, &full[s]);
-                    bulk_load(sc + TK + lane * R, p.v_scale + row, R * 4, &full[s]);
+                    const int index = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
+                    row = pool_row + page * pages_rows + key - index * p.page_size;
+                }
+                const uint32_t loads = __ballot_sync(0xffffffffu, page != -2);
+                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+                // rows of tiles that this share does not have are not reported
+                if (page == -1 && (lane >> nb_shift) < here - u0) {
+                    status.code = SPTP_ERR_SHAPE;
+                    status.where = kWhereKvPage;
+                    status.info = c.b;
+                }
+                // the next tiles' pages, while these are waited for
+                if (u0 + per < here)
+                    page = page_of(c.b, c.s, key + per * TK);
+                else if (more)
+                    page = page_of(n.b, n.s, n.key0() + lane * R);
+                const int tiles = min(per, here - u0);
+                for (int u = 0; u < tiles; ++u) {
+                    if (!mbar_wait(&empty[s], phase, wc, kWhereKvEmpty, issued)) {
+                        more = false;
+                        u0 = here;
+                        break;
+                    }
+                    const uint32_t mask = (1u << nb) - 1u;
+                    const uint32_t tile_loads = loads >> (u << nb_shift) & mask, tile_good = good >> (u << nb_shift) & mask;
+                    const bool first = u0 + u == 0, last = u0 + u + 1 == here;
+                    const int src = (u << nb_shift) + box_r;
+                    const int brow = __shfl_sync(0xffffffffu, row, src);
+                    float* sc = reinterpret_cast<float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES);
+                    if constexpr (C::CODES) {
+                        if (tile_loads != tile_good) {  // the rows of a bad page: zero codes, scale 0
+                            if (lane < nb && (tile_loads & ~tile_good) >> lane & 1) {
+                                for (int r = 0; r < R; ++r) sc[lane * R + r] = sc[TK + lane * R + r] = 0.f;
+                                fence_proxy_async_smem();
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (lane == 0) {
+                        const int tile0 = key_begin + (u0 + u) * TK;
+                        Meta md;
+                        md.qrow = qrow;
+                        md.heads = heads;
+                        md.lo = max(0, c.s.start - tile0);
+                        md.hi = max(0, min(TK, c.s.len - tile0));
+                        md.flags = (first ? kFirst | (begins ? kItemBegins : 0) : 0) |
+                                   (last ? kLast | (ends ? kItemEnds : 0) | (more ? 0 : kEnd) : 0);
+                        meta[s] = md;
+                        mbar_arrive_expect_tx(&full[s], __popc(tile_loads) * 2 * R * C::ROW_BYTES +
+                                                            (C::CODES ? __popc(tile_good) * 2 * R * 4 : 0) +
+                                                            (first ? heads * q_bytes : 0));
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (first && lane < heads)
+                        bulk_load(smem + L::QROWS + s * L::Q_BYTES + lane * C::Q_STRIDE,
+                                  static_cast<const uint8_t*>(p.q) + (qrow + lane) * q_bytes, q_bytes, &full[s]);
+                    // a checked build: a page's rows, or the row of zeros
+                    if (box_in && (tile_loads >> box_r & 1) &&
+                        checked(brow >= 0 && (brow == bad_row || brow + R <= bad_row), &status, &abort_flag,
+                                kWhereBoundsTma, brow))
+                        // boxes past a narrow row's end lie outside the map: zeros
+                        tma_load_2d(smem + s * L::STAGE_BYTES + box_at, box_map, &full[s], box_x, brow);
+                    if constexpr (C::CODES) {
+                        // lanes 0 .. nb - 1: k's scales, nb .. 2 nb - 1: v's
+                        if (lane < 2 * nb && (tile_good >> box_r & 1))
+                            bulk_load(sc + (lane < nb ? 0 : TK) + box_r * R, (lane < nb ? p.k_scale : p.v_scale) + brow,
+                                      R * 4, &full[s]);
+                    }
+                    if (++s == L::STAGES) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
+            if (n.b != c.b) raw_next = n.b + 1 < p.B ? __ldg(p.seq_lens + n.b + 1) : 0;
             c = n;
-            page = page_next;
             fresh = false;
-            if (++s == L::STAGES) s = 0;
         }
         if (lane == 0) {
             part->items[0] = early;
@@ -986,12 +1045,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
         float* stats = reinterpret_cast<float*>(smem + L::STATS);
         bool begun = false;
         C c;
+        uint32_t phase = 0;
         for (int i = 0, s = 0;; ++i) {
-            const bool ok = mbar_wait(&full[s], (i / L::STAGES) & 1, wc, kWhereKvFull, i);
+            const bool ok = mbar_wait(&full[s], phase, wc, kWhereKvFull, i);
             const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
             const int heads = md.heads;
             if (md.flags & kFirst || i == 0) {
-                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, heads);
+                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, smem + L::KEEP, heads);
                 begun = (md.flags & kItemBegins) != 0;
             }
             if (!c.tile(ok, smem_u32(smem) + s * L::STAGE_BYTES,
@@ -1000,7 +1060,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
                 break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            if (++s == L::STAGES) s = 0;
+            if (++s == L::STAGES) {
+                s = 0;
+                phase ^= 1;
+            }
             if (md.flags & kLast) {
                 float* sums = stats + 2 * L::MAXIMA;
                 if (begun && (md.flags & kItemEnds)) {

@@ -20,11 +20,15 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     p.box_rows = 16;
     while (p.box_rows < C::TK && p.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     const uint64_t rows = static_cast<uint64_t>(p.P) * p.num_pages * p.Hkv * p.page_size;
-    const int es = C::F32 ? 4 : (C::CODES ? 1 : 2);
-    const uint32_t inner = C::F32 ? C::DP : 128 / es;
-    if (!encode_map_rows(&p.map_k, p.k, es, p.D, rows, inner, p.box_rows) ||
-        !encode_map_rows(&p.map_v, p.v, es, p.D, rows, inner, p.box_rows))
+    if (!encode_map_rows(&p.map_k, p.k, C::ELEM, p.D, rows, 128 / C::ELEM, p.box_rows) ||
+        !encode_map_rows(&p.map_v, p.v, C::ELEM, p.D, rows, 128 / C::ELEM, p.box_rows))
         return cudaErrorInvalidValue;
+    // division by the page size: with 2^(l-1) < d <= 2^l and mul = floor(2^(31+l) / d) + 1, the error
+    // mul - 2^(31+l) / d <= 1 adds less than key / 2^(31+l) < 1 / d to the quotient
+    int l = 0;
+    while ((1ll << l) < p.page_size) ++l;
+    p.page_mul = static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint32_t>(p.page_size) + 1);
+    p.page_shift = l - 1;
     // once per device (the call costs half a microsecond; doing it twice is harmless)
     static std::atomic<unsigned long long> done{0};
     int dev = 0;

@@ -280,6 +280,8 @@ struct PagedAttnParams {
     int P, B, Hq, Hkv, D;
     int max_pages, num_pages, page_size, window;
     int box_rows;           // divides page_size and a tile
+    uint32_t page_mul;      // key / page_size = (key * page_mul) >> (32 + page_shift) for 0 <= key < 2^31
+    int page_shift;
     int heads_per_item, head_blocks;  // query heads of an item, items per key/value head
     int items_per_seq;      // P * Hkv * head_blocks
     float scale;
@@ -292,7 +294,7 @@ struct PagedAttnParams {
 };
 
 // The paged attention's tensor maps: rows of `inner` elements, boxes of
-// box_inner x box_rows; bf16 and bytes with 128-byte swizzle, fp32 without.
+// box_inner x box_rows, 128-byte swizzle; 1-, 2- or 4-byte elements (fp32).
 bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                      uint32_t box_inner, uint32_t box_rows);
 

@@ -35,8 +35,6 @@
 namespace sptp {
 namespace paged {
 
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxStages = 8;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -45,10 +43,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
+// Barrier of the WARPS consumer warps.
+template <int WARPS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+}
 // The same, and whether `ok` holds in every thread.  A warp whose bounded wait
-// for a tile gave up still comes to the barrier, and all four leave together:
-// none is left waiting there.
+// for a tile gave up still comes to the barrier, and all leave together: none
+// is left waiting there.
+template <int WARPS>
 __device__ __forceinline__ bool consumers_agree(bool ok) {
     uint32_t all;
     asm volatile(
@@ -57,7 +60,7 @@ __device__ __forceinline__ bool consumers_agree(bool ok) {
         "bar.red.and.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
-        : "r"(static_cast<uint32_t>(ok)), "n"(kConsumers * 32)
+        : "r"(static_cast<uint32_t>(ok)), "n"(WARPS * 32)
         : "memory");
     return all != 0;
 }
@@ -156,15 +159,16 @@ struct TcConsumer {
     static constexpr int ELEM = CODES ? 1 : 2;  // bytes
     static constexpr int BOXES = ROW_BYTES / 128;
     static constexpr int TK = ROW_BYTES == 128 && NT == 1 ? 128 : 64;  // 32 KB a tile, or 64 keys
+    static constexpr int WARPS = 4;
     static constexpr int Q_STRIDE = DP * 2 + 16;                        // bytes; 8 rows in distinct banks
     static constexpr int W_STRIDE = TK * 2 + 16;
     static constexpr int W_BYTES = HEADS * W_STRIDE;
     static constexpr int KEEP_BYTES = 0;
     static constexpr int CTAS = NT < 4 && ROW_BYTES <= 256 ? 2 : 1;
     static constexpr int K_BYTES = TK * ROW_BYTES;
-    static constexpr int SLICES = TK / (16 * kConsumers);  // of 16 keys, a warp's
+    static constexpr int SLICES = TK / (16 * WARPS);  // of 16 keys, a warp's
     static constexpr int KSTEPS = DP / 16;                 // of 16 elements of q and k
-    static constexpr int MTILES = DP / 16 / kConsumers;    // of 16 elements of v, a warp's
+    static constexpr int MTILES = DP / 16 / WARPS;    // of 16 elements of v, a warp's
     static_assert(ROW_BYTES % 128 == 0 && (!CODES || MTILES % 2 == 0), "layout");
 
     uint32_t qf[KSTEPS][NT][2];
@@ -175,7 +179,7 @@ struct TcConsumer {
     // element of the head's row in o[t][..][2 r + ..]
     static __device__ __forceinline__ int elem(int t, int r) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-        return warp * (DP / kConsumers) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
+        return warp * (DP / WARPS) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
     }
 
     __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, uint8_t*, int heads) {
@@ -236,7 +240,7 @@ struct TcConsumer {
     }
 
     // stage: the tile in shared memory (K, then V); scales: E4M3, of its keys;
-    // maxima [1 or 2][kConsumers][HEADS] and weights (W_BYTES): this tile's, of
+    // maxima [1 or 2][WARPS][HEADS] and weights (W_BYTES): this tile's, of
     // all the warps
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float* scales, float* maxima, uint8_t* weights,
                                          int lo, int hi) {
@@ -323,23 +327,23 @@ struct TcConsumer {
                 float* at = maxima + warp * HEADS + nt * 8 + 2 * lane;
                 *reinterpret_cast<float2*>(at) = make_float2(top[nt][0], top[nt][1]);
                 if constexpr (CODES)
-                    *reinterpret_cast<float2*>(at + kConsumers * HEADS) = make_float2(top2[nt][0], top2[nt][1]);
+                    *reinterpret_cast<float2*>(at + WARPS * HEADS) = make_float2(top2[nt][0], top2[nt][1]);
             }
         }
-        if (!consumers_agree(ok)) return false;
+        if (!consumers_agree<WARPS>(ok)) return false;
         float old[NT][2];
         bool moved = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float2 t2 = make_float2(m[nt][0], m[nt][1]), u2 = make_float2(m2[nt][0], m2[nt][1]);
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float* at = maxima + w * HEADS + nt * 8 + 2 * i;
                 const float2 o2 = *reinterpret_cast<const float2*>(at);
                 t2.x = fmaxf(t2.x, o2.x);
                 t2.y = fmaxf(t2.y, o2.y);
                 if constexpr (CODES) {
-                    const float2 p2 = *reinterpret_cast<const float2*>(at + kConsumers * HEADS);
+                    const float2 p2 = *reinterpret_cast<const float2*>(at + WARPS * HEADS);
                     u2.x = fmaxf(u2.x, p2.x);
                     u2.y = fmaxf(u2.y, p2.y);
                 }
@@ -391,7 +395,7 @@ struct TcConsumer {
                                                   : pack_bf16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
             }
         }
-        consumers_sync();
+        consumers_sync<WARPS>();
         if (__any_sync(0xffffffffu, moved)) {  // a maximum moved
 #pragma unroll
             for (int t = 0; t < MTILES; ++t)
@@ -408,22 +412,17 @@ struct TcConsumer {
             uint32_t w[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) ldmatrix_x4(wrow + nt * 8 * W_STRIDE + k2 * 64, w[nt]);
+            // what lies in a masked row may be anything (NaN for one), and 0
+            // times that is not 0: such values are cleared
+            auto keep = [&](int key) {
+                return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+            };
+            const int chunk0 = warp * (ROW_BYTES / 16 / WARPS);  // this warp's part of the row
+            if constexpr (!CODES) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int k0 = k2 * 32 + kk * 16;
-                if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
-                // what lies in a masked row may be anything (NaN for one), and
-                // 0 times that is not 0: such values are cleared
-                uint32_t keep0 = ~0u, keep1 = ~0u;
-                if (partial) {
-                    auto pair = [&](int key) {
-                        return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
-                    };
-                    keep0 = pair(k0 + 2 * i);
-                    keep1 = pair(k0 + 8 + 2 * i);
-                }
-                const int chunk0 = warp * (ROW_BYTES / 16 / kConsumers);  // this warp's part of the row
-                if constexpr (!CODES) {
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int k0 = k2 * 32 + kk * 16;
+                    if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
                     const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 7) + ((lane >> 4) << 3)) * 128;
 #pragma unroll
                     for (int t = 0; t < MTILES; ++t) {
@@ -431,6 +430,7 @@ struct TcConsumer {
                         uint32_t a[4];
                         ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
                         if (partial) {
+                            const uint32_t keep0 = keep(k0 + 2 * i), keep1 = keep(k0 + 8 + 2 * i);
                             a[0] &= keep0;
                             a[1] &= keep0;
                             a[2] &= keep1;
@@ -439,7 +439,12 @@ struct TcConsumer {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma_bf16(o[t][nt], a, w[nt][2 * kk], w[nt][2 * kk + 1]);
                     }
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int k0 = k2 * 32 + kk * 16;
+                    if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
                     const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 15)) * 128;
 #pragma unroll
                     for (int t = 0; t < MTILES; t += 2) {
@@ -447,6 +452,7 @@ struct TcConsumer {
                         uint32_t a[4];
                         ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
                         if (partial) {
+                            const uint32_t keep0 = keep(k0 + 2 * i), keep1 = keep(k0 + 8 + 2 * i);
                             a[0] &= keep0;
                             a[1] &= keep1;
                             a[2] &= keep0;
@@ -471,7 +477,7 @@ struct TcConsumer {
         return true;
     }
 
-    // The item's end, or its part's: sums [kConsumers][HEADS] in shared memory.
+    // The item's end, or its part's: sums [WARPS][HEADS] in shared memory.
     // Calls put(head, element, o, m, l) for this thread's outputs.
     template <typename Put>
     __device__ __forceinline__ void finish(float* sums, Put put) {
@@ -485,7 +491,7 @@ struct TcConsumer {
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (lane < 4) sums[warp * HEADS + nt * 8 + 2 * lane + e] = sum;
             }
-        consumers_sync();
+        consumers_sync<WARPS>();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -493,7 +499,7 @@ struct TcConsumer {
                 const int h = nt * 8 + 2 * i + e;
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) sum += sums[w * HEADS + h];
+                for (int w = 0; w < WARPS; ++w) sum += sums[w * HEADS + h];
                 // E4M3: o is relative to M2, the sum to m
                 const float f = CODES && sum != 0.f ? ex2(m2[nt][e] - m[nt][e]) : 1.f;
 #pragma unroll
@@ -522,6 +528,7 @@ struct F32Consumer {
     static constexpr bool CODES = false;
     static constexpr bool F32 = true;
     static constexpr int HEADS = 8;
+    static constexpr int WARPS = 4;
     static constexpr int ELEM = 4;  // bytes
     static constexpr int ROW_BYTES = DP * 4;
     static constexpr int BOXES = ROW_BYTES / 128;
@@ -532,10 +539,10 @@ struct F32Consumer {
     static constexpr int W_BYTES = TK * W_STRIDE * 4;
     static constexpr int CTAS = 2;
     static constexpr int KEY_GROUPS = TK > 32 ? TK / 32 : 1;       // of the warps
-    static constexpr int HPW = HEADS * KEY_GROUPS / kConsumers;    // heads of a warp's scores
-    static constexpr int KEEP_BYTES = kConsumers * HPW * ROW_BYTES;
+    static constexpr int HPW = HEADS * KEY_GROUPS / WARPS;    // heads of a warp's scores
+    static constexpr int KEEP_BYTES = WARPS * HPW * ROW_BYTES;
     static constexpr int ROW_PARTS = TK < 32 ? 32 / TK : 1;        // lanes that share a row
-    static constexpr int OWN = DP / kConsumers;                    // elements of a warp's outputs
+    static constexpr int OWN = DP / WARPS;                    // elements of a warp's outputs
     static constexpr int E = OWN > 32 ? OWN / 32 : 1;              // of a lane's
     static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;          // lanes that share an element
     static_assert(HPW == 2 || HPW == 4, "vectors of weights");
@@ -613,10 +620,10 @@ struct F32Consumer {
             if ((lane & 7) == h0 + h) top = t;
         }
         if (lane < 8) maxima[warp * HEADS + lane] = top;
-        if (!consumers_agree(ok)) return false;
+        if (!consumers_agree<WARPS>(ok)) return false;
         top = m;
 #pragma unroll
-        for (int n = 0; n < kConsumers; ++n) top = fmaxf(top, maxima[n * HEADS + (lane & 7)]);
+        for (int n = 0; n < WARPS; ++n) top = fmaxf(top, maxima[n * HEADS + (lane & 7)]);
         const float base = top == -INFINITY ? 0.f : top;
         const float old = ex2(m - base);
         const bool moved = top != m;
@@ -633,7 +640,7 @@ struct F32Consumer {
             else
                 *reinterpret_cast<float2*>(at) = make_float2(x[0], x[1]);
         }
-        consumers_sync();
+        consumers_sync<WARPS>();
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int h = 0; h < HEADS; ++h) {
@@ -686,13 +693,13 @@ struct F32Consumer {
             if (lane == h0 + h) mine = n;
         }
         if (lane < 8) sums[warp * HEADS + lane] = mine;
-        consumers_sync();
+        consumers_sync<WARPS>();
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
             const float mh = __shfl_sync(0xffffffffu, m, h);
             float n = 0.f;
 #pragma unroll
-            for (int k = 0; k < kConsumers; ++k) n += sums[k * HEADS + h];
+            for (int k = 0; k < WARPS; ++k) n += sums[k * HEADS + h];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float v = o[h][e];
@@ -780,9 +787,9 @@ struct Smem {
     static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;
     static constexpr int Q_BYTES = C::HEADS * C::Q_STRIDE;
     static constexpr int STAGE_BYTES = 2 * C::K_BYTES;
-    // maxima (two sets, for two tiles), sums [kConsumers][HEADS], weights [2]
-    static constexpr int MAXIMA = (C::CODES ? 2 : 1) * kConsumers * C::HEADS;
-    static constexpr int STATS_BYTES = (2 * MAXIMA + kConsumers * C::HEADS) * 4;
+    // maxima (two sets, for two tiles), sums [C::WARPS][HEADS], weights [2]
+    static constexpr int MAXIMA = (C::CODES ? 2 : 1) * C::WARPS * C::HEADS;
+    static constexpr int STATS_BYTES = (2 * MAXIMA + C::WARPS * C::HEADS) * 4;
     static constexpr int KEEP_BYTES = C::KEEP_BYTES;
     static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + KEEP_BYTES + 1024;  // 1024: alignment of the ring
     // what a CTA may have: 227 KB, or half of an SM's 228 KB less 1 KB each;
@@ -800,8 +807,10 @@ struct Smem {
 };
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
+    paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
     using L = Smem<C>;
+    constexpr int kThreads = 32 * (C::WARPS + 1);
     constexpr int TK = C::TK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -827,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
     if (tid == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kConsumers);
+            mbar_init(&empty[s], C::WARPS);
         }
         fence_mbar_init();
         abort_flag = 0;
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) paged_attn_kernel(const __g
     WaitCtx wc{&status, &abort_flag, kWaitLimitNs};
     PagedAttnPart* part = p.parts + blockIdx.x;
 
-    if (warp == kConsumers) {
+    if (warp == C::WARPS) {
         // -------------------------------------------------- producer
         PagedAttnItem early = {0, 0, 0, 0, 0, 0}, late = early;
         const int R = p.box_rows, nb_shift = __ffs(TK / R) - 1, nb = 1 << nb_shift;  // powers of two

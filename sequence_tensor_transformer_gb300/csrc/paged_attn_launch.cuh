@@ -47,7 +47,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (grid > most) grid = most;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     *ctas = static_cast<int>(grid);
-    paged_attn_kernel<C><<<*ctas, kThreads, Smem<C>::BYTES, s>>>(p);
+    paged_attn_kernel<C><<<*ctas, 32 * (C::WARPS + 1), Smem<C>::BYTES, s>>>(p);
     return cudaGetLastError();
 }
 

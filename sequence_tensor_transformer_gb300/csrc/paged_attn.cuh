@@ -242,12 +242,20 @@ struct TcConsumer {
     // stage: the tile in shared memory (K, then V); scales: E4M3, of its keys;
     // maxima [1 or 2][WARPS][HEADS] and weights (W_BYTES): this tile's, of
     // all the warps
+    // (Whole tiles have code of their own, without a branch that would keep the
+    // loads and products of one step apart from the next one's.)
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float* scales, float* maxima, uint8_t* weights,
                                          int lo, int hi) {
+        return lo == 0 && hi == TK ? tile_of<false>(ok, stage, scales, maxima, weights, lo, hi)
+                                   : tile_of<true>(ok, stage, scales, maxima, weights, lo, hi);
+    }
+
+    template <bool partial>
+    __device__ __forceinline__ bool tile_of(bool ok, uint32_t stage, const float* scales, float* maxima,
+                                            uint8_t* weights, int lo, int hi) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
         const int key0 = warp * 16 * SLICES;  // this warp's keys of the tile
-        const bool some = key0 < hi && key0 + 16 * SLICES > lo;
-        const bool partial = lo > 0 || hi < TK;
+        const bool some = !partial || (key0 < hi && key0 + 16 * SLICES > lo);
         float s[SLICES][NT][4];
         float vs[SLICES][2];
         float top[NT][2], top2[NT][2];

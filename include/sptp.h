@@ -373,7 +373,7 @@ int sptp_down_proj_e4m3(const void* qs, const float* ss, const void* qW2, const 
  *            [P][num_pages][Hkv][page_size] fp32: a head's row of D elements
  *            quantised as by sptp_quantize_rows_e4m3.
  *   Shape rules of all of them: 1 <= P <= 8; D % 8 == 0 (E4M3: % 16),
- *   8 <= D <= 256; Hq % Hkv == 0; page_size % 16 == 0;
+ *   8 <= D <= 256; Hq % Hkv == 0; M, B < 2^30; page_size % 16 == 0;
  *   max_pages * page_size < 2^30; P * num_pages * Hkv * page_size < 2^31.
  *   int32 arrays are 4-byte aligned, `turns` 8-byte, all others 16-byte.
  */

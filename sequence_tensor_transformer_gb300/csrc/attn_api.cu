@@ -79,10 +79,11 @@ PagedLayout paged_layout(int group, int D) {
     return L;
 }
 
-// Elements of an activation tensor, M rows; -1 if it is beyond any GPU.
+// Elements of an activation tensor, M rows; -1 if it is beyond any GPU (and the
+// kernels' 32-bit row numbers).
 long long elems(long long P, long long M, long long heads, long long D) {
     const long long row = P * heads * D;  // < 2^32
-    return M <= (1ll << 42) / row ? M * row : -1;
+    return M < (1ll << 30) && M <= (1ll << 42) / row ? M * row : -1;
 }
 
 }  // namespace

@@ -10,12 +10,13 @@
 // over the positions, and a far position is as exact as a near one.
 //
 // Both are bound by HBM: every element is read once and written once with
-// 16-byte accesses, and nothing else is large.  A lane owns one slot of a
-// head, two 16-byte vectors that hold each other's partners (half layout: the
-// vectors at c and c + rot/2; interleaved: two adjacent ones; elements that do
-// not turn: two adjacent ones), and walks over the heads of its row with the
-// slot's cosines and sines in registers, so an angle is computed once per
-// token and slot, not once per head.  L lanes (a power of two) cover a head.
+// 16-byte accesses, and nothing else is large.  A block takes one to four
+// tokens: its first loads are under way while its threads work out the tokens'
+// cosines and sines, each once, into shared memory.  A lane owns one slot of a
+// head, two 16-byte vectors (half layout: the vectors at c and c + rot/2 hold
+// each other's partners; interleaved: any two; elements that do not turn: any
+// two), L lanes cover a head, and a warp walks over its rows (heads of a token,
+// all shards') with the slot's cosines and sines in registers.
 #include <cuda_bf16.h>
 
 #include "e4m3.cuh"
@@ -28,8 +29,21 @@ namespace {
 
 enum class Op { kRope, kAppend, kAppendE4M3 };
 
-constexpr int kThreads = 128;  // four warps: four work units of the same kind
-constexpr int kUnroll = 4;     // heads whose loads a lane has in flight
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxPairs = 128;
+
+// How the rows of the tokens are dealt out (host).
+struct Split {
+    int L;           // lanes of a head
+    int hpw;         // heads that a warp has side by side, 32 / L
+    int tokens;      // of a block: 1, 2 or 4; a token has kWarps / tokens of its warps
+    int parts;       // blocks that share a token's rows (tokens == 1)
+    int per;         // rows of a warp
+    int checker;     // append: the first block writes the status words
+    uint32_t mul;    // row / H = (2 row * mul) >> (32 + shift) for rows below 2^24
+    int shift;
+};
 
 template <typename T>
 struct Elems {
@@ -92,37 +106,52 @@ __device__ __forceinline__ void turn(uint4& ua, uint4& ub, const float (&c)[Elem
     ub = pack<T>(z);
 }
 
-// Where a token's keys and values go: its row of the cache without the shard
-// and head, or -1 (padding or an index out of its range).
+// The page that a token's key and value go to; -1 if an index is out of range.
 __device__ __forceinline__ int kv_page(const RopeParams& p, int seq, int pos) {
     if (seq < 0 || seq >= p.B || pos < 0 || pos / p.page_size >= p.max_pages) return -1;
     const int page = __ldg(p.page_table + static_cast<long long>(seq) * p.max_pages + pos / p.page_size);
     return page >= 0 && page < p.num_pages ? page : -1;
 }
 
-// The status words of an append of up to kCheckRows rows, written once: a block
-// of its own looks at all rows' indexes, in one round of loads, beside the
-// blocks that move the data (which skip the bad ones silently), so that no
-// launch has to clear the words first.  More rows are checked by the blocks
-// that move them, after a launch that clears the words: 1.5 us that a batch of
-// new tokens would feel and a prompt does not (for 16384 rows one block took 3
-// times as long as moving the data).
-constexpr int kCheckRows = 8 * kThreads;
+// The status words of an append, written once by a block of its own: it looks at
+// all rows' indexes, beside the blocks that move the data (which skip the bad
+// ones silently), so that no launch has to clear the words first.  That takes
+// it about 1 us per 1024 rows, hidden behind the data where a row is large; a
+// launch that clears the words, and blocks that report what they meet, cost 3.5
+// us (16384 rows of 18 KB: 53.0 and 49.5 us).  So one block checks where there
+// are few rows, or rows of kCheckBytes, which take as long to move.
+constexpr int kCheckRows = 2048;
+constexpr int kCheckBytes = 8192;
 
-__device__ __noinline__ void check_rows(const RopeParams& p) {
+__device__ __forceinline__ void check_rows(const RopeParams& p) {
+    constexpr int N = 8;
     __shared__ int first_bad;
     if (threadIdx.x == 0) first_bad = 0x7fffffff;
     __syncthreads();
-    int seq[8], pos[8];
+    int seq[N], pos[N];
+    auto load = [&](int m0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int m = i * kThreads + threadIdx.x;
-        seq[i] = m < p.M ? __ldg(p.seq_ids + m) : -1;
-        pos[i] = m < p.M ? __ldg(p.positions + m) : 0;
+        for (int i = 0; i < N; ++i) {
+            const int m = m0 + i * kThreads + static_cast<int>(threadIdx.x);
+            seq[i] = m < p.M ? __ldg(p.seq_ids + m) : -1;
+            pos[i] = m < p.M ? __ldg(p.positions + m) : 0;
+        }
+    };
+    load(0);
+    for (int m0 = 0; m0 < p.M; m0 += N * kThreads) {
+        int page[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // (entry 0 where there is none to look up)
+            const bool in = seq[i] >= 0 && seq[i] < p.B && pos[i] >= 0 && pos[i] / p.page_size < p.max_pages;
+            const int at = __ldg(p.page_table + (in ? static_cast<long long>(seq[i]) * p.max_pages + pos[i] / p.page_size : 0));
+            page[i] = seq[i] < 0 ? 0 : in ? at : -1;
+        }
+        load(m0 + N * kThreads < p.M ? m0 + N * kThreads : p.M);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (page[i] < 0 || page[i] >= p.num_pages) atomicMin(&first_bad, m0 + i * kThreads + static_cast<int>(threadIdx.x));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (seq[i] >= 0 && kv_page(p, seq[i], pos[i]) < 0) atomicMin(&first_bad, i * kThreads + static_cast<int>(threadIdx.x));
     __syncthreads();
     if (threadIdx.x == 0) {
         const bool bad = first_bad != 0x7fffffff;
@@ -139,129 +168,134 @@ __device__ __noinline__ void check_rows(const RopeParams& p) {
     }
 }
 
-// Unit u = token u / parts, and of its P * H heads the `per` of part u % parts;
-// one warp each.
 template <typename T, bool INTER, Op OP>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int L, int parts,
-                                                        int per) {
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeParams p,
+                                                        const __grid_constant__ Split sp) {
     constexpr int E = Elems<T>::E;
-    const bool one_block_checks = OP != Op::kRope && p.M <= kCheckRows;
-    if (one_block_checks && blockIdx.x == gridDim.x - 1) {
+    constexpr int kUnroll = OP == Op::kRope ? 4 : 3;  // rows whose loads a lane has in flight
+    __shared__ __align__(16) float cosines[4][kMaxPairs], sines[4][kMaxPairs];
+    // the first block, so that it starts with the others and not after them
+    if (OP != Op::kRope && sp.checker && blockIdx.x == 0) {
         check_rows(p);
         return;
     }
-    const int lane = threadIdx.x & 31;
-    const int slot = lane & (L - 1), hg = lane / L, hpw = 32 / L;
+    const uint32_t block = blockIdx.x - (OP != Op::kRope ? sp.checker : 0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hg = lane / sp.L, slot = lane - hg * sp.L;
     const int half = p.rot / 2;
     const int turning = half / E;  // slots that turn
     // the slot's two vectors (element offsets); a tail slot may lack the second
     const bool turns = slot < turning;
-    const int ea = turns ? (INTER ? 2 * slot * E : slot * E) : p.rot + 2 * (slot - turning) * E;
-    const int eb = turns && !INTER ? ea + half : ea + E;
-    const bool has_a = ea < p.D, has_b = eb < p.D;
-    const int rows = p.P * p.H;
-    const long long units = static_cast<long long>(p.M) * parts;
-    const long long blocks = one_block_checks ? gridDim.x - 1 : gridDim.x;
-    for (long long u = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; u < units;
-         u += blocks * (kThreads / 32)) {
-        const int m = static_cast<int>(u / parts);
-        const int r0 = static_cast<int>(u - static_cast<long long>(m) * parts) * per;
-        const int r1 = min(rows, r0 + per);
-        const int pos = __ldg(p.positions + m);
-        int seq = 0, page = -1, off = 0;
-        if constexpr (OP != Op::kRope) {
-            seq = __ldg(p.seq_ids + m);
-            if (seq < 0) continue;  // a padding row
-            page = kv_page(p, seq, pos);
+    const int still = ((p.D - p.rot) / E + 1) / 2;  // slots that do not
+    const int ea = turns ? slot * E : p.rot + (slot - turning) * E;
+    const int eb = ea + (turns ? half : still * E);
+    const bool lives = hg < sp.hpw && slot < turning + still;
+    const bool has_b = lives && eb < p.D;
+    // this warp's token and rows
+    const int wpt = kWarps / sp.tokens;
+    const int m0 = block / sp.parts * sp.tokens, mi = warp / wpt, m = m0 + mi;
+    const int r0 = (block % sp.parts * wpt + warp % wpt) * sp.per;
+    const int r1 = m < p.M ? min(p.P * p.H, r0 + sp.per) : 0;
+
+    uint4 va[kUnroll], vb[kUnroll];
+    int pp[kUnroll], hh[kUnroll];  // shard, head (-1: none)
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int r = base + i * sp.hpw + hg;
+            pp[i] = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(r), sp.mul) >> sp.shift);
+            hh[i] = lives && r < r1 ? r - pp[i] * p.H : -1;
+            // in place, what does not turn stays where it is
+            if (OP == Op::kRope && p.out == p.x && (hh[i] >= p.Hr || !turns)) hh[i] = -1;
+            va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+            if (hh[i] >= 0) {
+                const T* src =
+                    static_cast<const T*>(p.x) + ((static_cast<long long>(pp[i]) * p.M + m) * p.H + hh[i]) * p.D;
+                va[i] = __ldcs(reinterpret_cast<const uint4*>(src + ea));
+                if (has_b) vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + eb));
+            }
+        }
+    };
+    load(r0);
+
+    // the angles of the block's tokens, while the first rows are under way
+    for (int j = tid; j < sp.tokens * half; j += kThreads) {
+        const int t = sp.tokens == 1 ? 0 : j / half, i = j - t * half;
+        if (m0 + t < p.M) {
+            const unsigned long long f = static_cast<unsigned long long>(static_cast<long long>(__ldg(p.positions + m0 + t))) *
+                                         __ldg(p.turns + i);
+            // signed: [-1/2, 1/2) turn = [-1, 1) half turns
+            float s, c;
+            sincospif(__ll2float_rn(static_cast<long long>(f)) * 0x1p-63f, &s, &c);
+            cosines[t][i] = c * p.gain;
+            sines[t][i] = s * (p.transpose ? -p.gain : p.gain);
+        }
+    }
+    int page = -1, off = 0;
+    if constexpr (OP != Op::kRope) {
+        if (m < p.M) {
+            const int seq = __ldg(p.seq_ids + m), pos = __ldg(p.positions + m);
+            page = seq < 0 ? -2 : kv_page(p, seq, pos);  // -2: a padding row
             off = pos % p.page_size;
-            if (page < 0 && !one_block_checks && r0 == 0 && lane == 0 &&
+            if (page == -1 && !sp.checker && r0 == 0 && lane == 0 &&
                 atomicCAS(&p.status->code, 0, SPTP_ERR_SHAPE) == 0) {
                 p.status->where = kWhereKvSlot;
                 p.status->info = m;
             }
         }
-        float c[E], s[E];
-        bool have = false;
-        for (int base = r0; base < r1; base += hpw * kUnroll) {
-            uint4 va[kUnroll], vb[kUnroll];
-            int pp[kUnroll], hh[kUnroll];
+    }
+    __syncthreads();
+    if (OP != Op::kRope && page == -2) return;
+    float c[E], s[E];
+    if (turns && lives) {
+        // half: pairs slot E + e; interleaved: the vectors' own E/2 pairs each
+        const int ia = INTER ? slot * (E / 2) : slot * E;
+        const int ib = INTER ? half / 2 + slot * (E / 2) : slot * E + E / 2;
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int r = base + i * hpw + hg;
-                pp[i] = r / p.H;
-                hh[i] = r < r1 ? r - pp[i] * p.H : -1;
-                va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-                if (hh[i] >= 0) {
-                    // in place, what does not turn stays where it is
-                    if (OP == Op::kRope && p.out == p.x && (hh[i] >= p.Hr || !turns)) {
-                        hh[i] = -1;
-                        continue;
-                    }
-                    const T* src = static_cast<const T*>(p.x) +
-                                   ((static_cast<long long>(pp[i]) * p.M + m) * p.H + hh[i]) * p.D;
-                    if (has_a) va[i] = __ldcs(reinterpret_cast<const uint4*>(src + ea));
-                    if (has_b) vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + eb));
-                }
-            }
-            if (!have) {  // the loads of the first heads are under way
-                have = true;
+        for (int e = 0; e < E / 2; ++e) {
+            c[e] = cosines[mi][ia + e];
+            c[E / 2 + e] = cosines[mi][ib + e];
+            s[e] = sines[mi][ia + e];
+            s[E / 2 + e] = sines[mi][ib + e];
+        }
+    }
+    for (int base = r0; base < r1; base += sp.hpw * kUnroll) {
+        if (base != r0) load(base);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    c[e] = p.gain;
-                    s[e] = 0.f;
-                    if (turns) {
-                        const unsigned long long f = static_cast<unsigned long long>(static_cast<long long>(pos)) *
-                                                     __ldg(p.turns + slot * E + e);
-                        // signed: [-1/2, 1/2) turn = [-1, 1) half turns
-                        const float t = __ll2float_rn(static_cast<long long>(f)) * 0x1p-63f;
-                        sincospif(t, &s[e], &c[e]);
-                        c[e] *= p.gain;
-                        s[e] *= p.transpose ? -p.gain : p.gain;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                if (turns && hh[i] >= 0 && hh[i] < p.Hr) turn<T, INTER>(va[i], vb[i], c, s);
-                if constexpr (OP == Op::kRope) {
-                    if (hh[i] < 0) continue;
-                    T* dst = static_cast<T*>(p.out) + ((static_cast<long long>(pp[i]) * p.M + m) * p.H + hh[i]) * p.D;
-                    if (has_a) __stcs(reinterpret_cast<uint4*>(dst + ea), va[i]);
+        for (int i = 0; i < kUnroll; ++i) {
+            if (turns && hh[i] >= 0 && hh[i] < p.Hr) turn<T, INTER>(va[i], vb[i], c, s);
+            if constexpr (OP == Op::kRope) {
+                if (hh[i] < 0) continue;
+                T* dst = static_cast<T*>(p.out) + ((static_cast<long long>(pp[i]) * p.M + m) * p.H + hh[i]) * p.D;
+                __stcs(reinterpret_cast<uint4*>(dst + ea), va[i]);
+                if (has_b) __stcs(reinterpret_cast<uint4*>(dst + eb), vb[i]);
+            } else {
+                const bool is_q = hh[i] < p.Hq, is_v = hh[i] >= p.Hq + p.Hkv;
+                const int kvh = hh[i] - p.Hq - (is_v ? p.Hkv : 0);
+                // row of the cache, or of q_out
+                const long long row = is_q ? (static_cast<long long>(pp[i]) * p.M + m) * p.Hq + hh[i]
+                                           : ((pp[i] * p.num_pages + page) * p.Hkv + kvh) * p.page_size + off;
+                const bool stores =
+                    hh[i] >= 0 &&
+                    (is_q || (page >= 0 && checked_index(row, static_cast<long long>(p.P) * p.num_pages * p.Hkv * p.page_size,
+                                                         p.status, nullptr, kWhereBoundsStore)));
+                if (stores && (is_q || OP == Op::kAppend)) {
+                    T* dst = static_cast<T*>(is_q ? p.out : is_v ? p.v_cache : p.k_cache) + row * p.D;
+                    __stcs(reinterpret_cast<uint4*>(dst + ea), va[i]);
                     if (has_b) __stcs(reinterpret_cast<uint4*>(dst + eb), vb[i]);
-                } else {
-                    const bool is_q = hh[i] >= 0 && hh[i] < p.Hq;
-                    if (is_q) {
-                        T* dst = static_cast<T*>(p.out) +
-                                 ((static_cast<long long>(pp[i]) * p.M + m) * p.Hq + hh[i]) * p.D;
-                        if (has_a) *reinterpret_cast<uint4*>(dst + ea) = va[i];
-                        if (has_b) *reinterpret_cast<uint4*>(dst + eb) = vb[i];
-                    }
-                    const bool is_v = hh[i] >= p.Hq + p.Hkv;
-                    const int kvh = hh[i] - p.Hq - (is_v ? p.Hkv : 0);
-                    const long long row =
-                        ((static_cast<long long>(pp[i]) * p.num_pages + page) * p.Hkv + kvh) * p.page_size + off;
-                    const bool is_kv = hh[i] >= p.Hq && page >= 0 &&
-                                       checked_index(row, static_cast<long long>(p.P) * p.num_pages * p.Hkv * p.page_size,
-                                                     p.status, nullptr, kWhereBoundsStore);
-                    if constexpr (OP == Op::kAppend) {
-                        if (is_kv) {
-                            T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + row * p.D;
-                            if (has_a) *reinterpret_cast<uint4*>(dst + ea) = va[i];
-                            if (has_b) *reinterpret_cast<uint4*>(dst + eb) = vb[i];
-                        }
-                    } else {
-                        // the head's row maximum over its L lanes; every lane
-                        // of the warp takes part
-                        float amax = fmaxf(absmax_bf16x8(va[i]), absmax_bf16x8(vb[i]));
-                        for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                        if (is_kv) {
-                            const int ex = e4m3_row_exponent(amax);
-                            const float inv = pow2f(-ex);
-                            uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + row * p.D;
-                            if (has_a) *reinterpret_cast<uint2*>(dst + ea) = e4m3_quant8(va[i], inv);
-                            if (has_b) *reinterpret_cast<uint2*>(dst + eb) = e4m3_quant8(vb[i], inv);
-                            if (slot == 0) (is_v ? p.v_scale : p.k_scale)[row] = pow2f(ex);
-                        }
+                }
+                if constexpr (OP == Op::kAppendE4M3) {
+                    // the head's row maximum over its L lanes (a power of two
+                    // here); every lane of the warp takes part
+                    float amax = fmaxf(absmax_bf16x8(va[i]), absmax_bf16x8(vb[i]));
+                    for (int o = sp.L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (stores && !is_q) {
+                        const int ex = e4m3_row_exponent(amax);
+                        const float inv = pow2f(-ex);
+                        uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + row * p.D;
+                        *reinterpret_cast<uint2*>(dst + ea) = e4m3_quant8(va[i], inv);
+                        if (has_b) *reinterpret_cast<uint2*>(dst + eb) = e4m3_quant8(vb[i], inv);
+                        if (slot == 0) (is_v ? p.v_scale : p.k_scale)[row] = pow2f(ex);
                     }
                 }
             }
@@ -272,37 +306,47 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <typename T, Op OP>
 cudaError_t launch_typed(const RopeParams& p, int num_sms, cudaStream_t s) {
     constexpr int E = Elems<T>::E;
-    const int slots = p.rot / (2 * E) + (p.D - p.rot + 2 * E - 1) / (2 * E);
-    int L = 1;
-    while (L < slots) L *= 2;
-    const int hpw = 32 / L;
-    // A warp takes a whole token where there are tokens enough for 16 warps
-    // per SM; below that a token's heads are cut into parts, down to one
-    // head per lane group.
-    const int rows = p.P * p.H;
-    const long long want = static_cast<long long>(num_sms) * 16;
-    long long parts = (want + p.M - 1) / p.M;
-    const int most = (rows + hpw - 1) / hpw;
-    if (parts > most) parts = most;
-    // whole lane groups per part
-    const int per = ((rows + static_cast<int>(parts) - 1) / static_cast<int>(parts) + hpw - 1) / hpw * hpw;
-    parts = (rows + per - 1) / per;
-    const long long units = p.M * parts;
-    long long grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-    const long long cap = static_cast<long long>(num_sms) * 16;
-    if (grid > cap) grid = cap;
-    if (OP != Op::kRope) {
-        if (p.M <= kCheckRows) ++grid;  // the block that checks the indexes
-        if (p.M > kCheckRows || kBoundsChecked) {
-            const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(DeviceStatus), s);
-            if (e != cudaSuccess) return e;
-        }
+    Split sp;
+    sp.L = p.rot / (2 * E) + ((p.D - p.rot) / E + 1) / 2;  // slots of a head
+    if (OP == Op::kAppendE4M3) {  // a power of two, for the row maximum's exchanges
+        int pow = 1;
+        while (pow < sp.L) pow *= 2;
+        sp.L = pow;
     }
-    const int g = static_cast<int>(grid), n = static_cast<int>(parts);
+    sp.hpw = 32 / sp.L;
+    // Warps per token: enough for 40 per SM (24 are resident), or 10 for an
+    // append, whose blocks each wait for their tokens' pages; at most one for
+    // each group of heads.  (4097 rows of 40 heads: 11.6, 11.2 and 13.7 us for
+    // 20, 40 and 80; 3001 appended E4M3 rows of 48: 19.9, 22.7 and 34 us for 10, 20 and 80.)
+    const int rows = p.P * p.H;
+    const int most = (rows + sp.hpw - 1) / sp.hpw;
+    long long warps = (static_cast<long long>(num_sms) * (OP == Op::kRope ? 40 : 10) + p.M - 1) / p.M;
+    if (warps > most) warps = most;
+    const int wpt = warps <= 1 ? 1 : warps <= 2 ? 2 : 4;
+    sp.tokens = kWarps / wpt;
+    sp.parts = static_cast<int>((warps + wpt - 1) / wpt);
+    if (sp.tokens > 1) sp.parts = 1;
+    // whole groups of heads side by side
+    sp.per = ((rows + wpt * sp.parts - 1) / (wpt * sp.parts) + sp.hpw - 1) / sp.hpw * sp.hpw;
+    // with H <= 2^l and mul = floor(2^(31+l) / H) + 1, the error mul - 2^(31+l) / H <= 1 adds less than
+    // row / 2^(31+l) < 1 / H to the quotient
+    int l = 0;
+    while ((1 << l) < p.H) ++l;
+    sp.mul = static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint32_t>(p.H) + 1);
+    sp.shift = l;
+    long long grid = (static_cast<long long>(p.M) + sp.tokens - 1) / sp.tokens * sp.parts;
+    const long long row_bytes = static_cast<long long>(rows) * p.D * sizeof(T) * 2;
+    sp.checker = OP != Op::kRope && p.B > 0 && (p.M <= kCheckRows || row_bytes >= kCheckBytes) ? 1 : 0;
+    if (sp.checker) ++grid;
+    if (OP != Op::kRope && (!sp.checker || kBoundsChecked)) {
+        const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(DeviceStatus), s);
+        if (e != cudaSuccess) return e;
+    }
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     if (p.interleaved)
-        rope_kernel<T, true, OP><<<g, kThreads, 0, s>>>(p, L, n, per);
+        rope_kernel<T, true, OP><<<static_cast<int>(grid), kThreads, 0, s>>>(p, sp);
     else
-        rope_kernel<T, false, OP><<<g, kThreads, 0, s>>>(p, L, n, per);
+        rope_kernel<T, false, OP><<<static_cast<int>(grid), kThreads, 0, s>>>(p, sp);
     return cudaGetLastError();
 }
 

@@ -174,8 +174,6 @@ def _same_device(*ts):
     properties from it, so a tensor elsewhere would be handed to kernels of
     another device.  Checked before any pointer reaches the C ABI."""
     ts = [t for t in ts if t is not None]
-    if not ts:
-        return
     device = ts[0].device
     for t in ts:
         if t.device != device:
@@ -585,11 +583,11 @@ def sptp_rope(x, positions, turns, Hr=None, interleaved=False, transpose=False, 
     _expect("positions", positions, (M,), torch.int32)
     _expect("turns", turns, (rot // 2,), torch.int64)
     _expect("out", out, (P, M, H, D), x.dtype, optional=True)
-    _same_device(x, positions, turns, out)
+    _one_device(x, positions, turns, out)
     if out is None:
-        out = torch.empty_like(x)
-    code = lib().sptp_rope(_ptr(x), _ptr(positions), _ptr(turns), P, M, H, H if Hr is None else Hr, D, rot,
-                           int(interleaved), int(transpose), float(gain), dt, _ptr(out), _stream(stream))
+        out = _new((P, M, H, D), x.dtype, x.device, stream)
+    code = lib().sptp_rope(_dptr(x), _dptr(positions), _dptr(turns), P, M, H, H if Hr is None else Hr, D, rot,
+                           int(interleaved), int(transpose), float(gain), dt, _dptr(out), _stream(stream))
     _check("sptp_rope", code)
     return out
 
@@ -605,24 +603,54 @@ def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=F
     return k, v, torch.zeros(shape[:-1], device=device), torch.zeros(shape[:-1], device=device)
 
 
+def _one_device(*ts):
+    """_same_device for calls that count microseconds: the first tensor given."""
+    cur = torch.cuda.current_device() if ts[0].is_cuda else -1
+    for t in ts:
+        if t is not None and (cur < 0 or t.get_device() != cur):
+            return _same_device(*ts)
+
+
+def _new(shape, dtype, device, stream):
+    """An output or a workspace that the caller left out.  Memory from the
+    allocator is ordered by the stream it is asked for on: the call's own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check_cache(cache, P, D, dtype):
     """Sizes (num_pages, Hkv, page_size, kv_type) of a cache of activations of `dtype`."""
     k, v, ks, vs = cache
-    if k.dim() != 5:
-        raise ValueError(f"cache: {k.dim()} dimensions, expected [P,num_pages,Hkv,page_size,D]")
-    _, num_pages, Hkv, page_size, _ = k.shape
-    e4m3 = k.dtype == torch.uint8
-    if e4m3 and dtype != torch.bfloat16:
-        raise TypeError("an E4M3 cache takes bf16 activations")
-    kvt = torch.uint8 if e4m3 else dtype
-    _expect("k_cache", k, (P, num_pages, Hkv, page_size, D), kvt)
-    _expect("v_cache", v, (P, num_pages, Hkv, page_size, D), kvt)
-    if e4m3:
-        _expect("k_scale", ks, (P, num_pages, Hkv, page_size), torch.float32)
-        _expect("v_scale", vs, (P, num_pages, Hkv, page_size), torch.float32)
-    elif ks is not None or vs is not None:
-        raise ValueError("scales belong to an E4M3 cache")
-    return num_pages, Hkv, page_size, SPTP_KV_E4M3 if e4m3 else SPTP_KV_SAME
+    shape = k.shape
+    if len(shape) != 5:
+        raise ValueError(f"cache: {len(shape)} dimensions, expected [P,num_pages,Hkv,page_size,D]")
+    _, num_pages, Hkv, page_size, _ = shape
+    want = (P, num_pages, Hkv, page_size, D)
+    kvt = k.dtype
+    if kvt != dtype:
+        if kvt != torch.uint8:
+            raise TypeError(f"cache: dtype {kvt}, expected {dtype} or uint8 codes")
+        if dtype != torch.bfloat16:
+            raise TypeError("an E4M3 cache takes bf16 activations")
+    if shape != want:
+        _expect("k_cache", k, want, kvt)
+    _expect("v_cache", v, want, kvt)
+    if kvt == dtype:
+        if ks is not None or vs is not None:
+            raise ValueError("scales belong to an E4M3 cache")
+        return num_pages, Hkv, page_size, SPTP_KV_SAME
+    _expect("k_scale", ks, want[:-1], torch.float32)
+    _expect("v_scale", vs, want[:-1], torch.float32)
+    return num_pages, Hkv, page_size, SPTP_KV_E4M3
+
+
+def _dptr(t):
+    """Address of a tensor that _same_device has seen."""
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, interleaved=False, gain=1.0, q_out=None,
@@ -643,16 +671,17 @@ def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, i
     rot = 0 if turns is None else 2 * turns.shape[0]
     _expect("turns", turns, (rot // 2,), torch.int64, optional=True)
     _expect("q_out", q_out, (P, M, Hq, D), qkv.dtype, optional=True)
-    _same_device(qkv, positions, seq_ids, page_table, turns, *cache, q_out, workspace)
+    _one_device(qkv, positions, seq_ids, page_table, turns, *cache, q_out, workspace)
     if q_out is None:
-        q_out = torch.empty((P, M, Hq, D), dtype=qkv.dtype, device=qkv.device)
+        q_out = _new((P, M, Hq, D), qkv.dtype, qkv.device, stream)
     if workspace is None:
-        workspace = _workspace(SPTP_WS_HEADER_BYTES, qkv.device)
+        workspace = _new((SPTP_WS_HEADER_BYTES,), torch.uint8, qkv.device, stream)
     k, v, ks, vs = cache
     code = lib().sptp_rope_append_kv(
-        _ptr(qkv), _ptr(positions), _ptr(seq_ids), _ptr(page_table), _ptr(turns), P, M, Hq, Hkv, D, rot,
-        int(interleaved), float(gain), B, max_pages, num_pages, page_size, dt, kv_type, _ptr(q_out), _ptr(k), _ptr(v),
-        _ptr(ks), _ptr(vs), _ptr(workspace), _nbytes(workspace), _stream(stream))
+        _dptr(qkv), _dptr(positions), _dptr(seq_ids), _dptr(page_table), None if turns is None else _dptr(turns), P, M,
+        Hq, Hkv, D, rot, int(interleaved), float(gain), B, max_pages, num_pages, page_size, dt, kv_type, _dptr(q_out),
+        _dptr(k), _dptr(v), None if ks is None else _dptr(ks), None if vs is None else _dptr(vs), _dptr(workspace),
+        workspace.nbytes, _stream(stream))
     _check("sptp_rope_append_kv", code)
     return q_out
 
@@ -675,17 +704,19 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     _expect("seq_lens", seq_lens, (B,), torch.int32)
     _expect("out", out, (P, B, Hq * D), q.dtype, optional=True)
     _expect("lse", lse, (P, B, Hq), torch.float32, optional=True)
-    _same_device(q, *cache, page_table, seq_lens, out, lse, workspace)
+    _one_device(q, *cache, page_table, seq_lens, out, lse, workspace)
     if out is None:
-        out = torch.empty((P, B, Hq * D), dtype=q.dtype, device=q.device)
+        out = _new((P, B, Hq * D), q.dtype, q.device, stream)
     if lse is None and write_lse:
-        lse = torch.empty((P, B, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((P, B, Hq), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = _workspace(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), q.device)
+        n = max(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
+        workspace = _new((n,), torch.uint8, q.device, stream)
     k, v, ks, vs = cache
     code = lib().sptp_paged_attn_decode(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(page_table), _ptr(seq_lens), P, B, Hq, Hkv, D, max_pages,
-        num_pages, page_size, int(window), D ** -0.5 if scale is None else float(scale), dt, kv_type, _ptr(out),
-        _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream))
+        _dptr(q), _dptr(k), _dptr(v), None if ks is None else _dptr(ks), None if vs is None else _dptr(vs),
+        _dptr(page_table), _dptr(seq_lens), P, B, Hq, Hkv, D, max_pages, num_pages, page_size, int(window),
+        D ** -0.5 if scale is None else float(scale), dt, kv_type, _dptr(out), None if lse is None else _dptr(lse),
+        _dptr(workspace), workspace.nbytes, _stream(stream))
     _check("sptp_paged_attn_decode", code)
     return out, lse

@@ -43,25 +43,46 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Barrier of the WARPS consumer warps.
-template <int WARPS>
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+// Consumer warps work in teams of four; a team takes up to HEADS of an item's
+// query heads.
+constexpr int kTeam = 4;
+
+__device__ __forceinline__ int team_warp() { return (threadIdx.x >> 5) & (kTeam - 1); }
+__device__ __forceinline__ int team_index() { return threadIdx.x / (32 * kTeam); }
+
+
+// Barrier of this thread's team (a constant where there is one team).
+template <int TEAMS>
+__device__ __forceinline__ void team_sync() {
+    if constexpr (TEAMS == 1)
+        asm volatile("bar.sync 1, %0;" ::"n"(kTeam * 32) : "memory");
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team_index()), "n"(kTeam * 32) : "memory");
 }
 // The same, and whether `ok` holds in every thread.  A warp whose bounded wait
 // for a tile gave up still comes to the barrier, and all leave together: none
 // is left waiting there.
-template <int WARPS>
-__device__ __forceinline__ bool consumers_agree(bool ok) {
+template <int TEAMS>
+__device__ __forceinline__ bool team_agrees(bool ok) {
     uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(static_cast<uint32_t>(ok)), "n"(WARPS * 32)
-        : "memory");
+    if constexpr (TEAMS == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 p, %1, 0;\n\t"
+            "bar.red.and.pred q, 1, %2, p;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(all)
+            : "r"(static_cast<uint32_t>(ok)), "n"(kTeam * 32)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 p, %1, 0;\n\t"
+            "bar.red.and.pred q, %2, %3, p;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(all)
+            : "r"(static_cast<uint32_t>(ok)), "r"(1 + team_index()), "n"(kTeam * 32)
+            : "memory");
     return all != 0;
 }
 
@@ -121,11 +142,34 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t c, uint32_t& lo, uint32_t& 
         : "r"(c));
 }
 
+// The same for a register of the transposed v, which holds two elements of two
+// keys each: the keys together, elements 2g to `lo` and 2g + 1 to `hi`
+__device__ __forceinline__ void unpack_values(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    unpack_e4m3(__byte_perm(c, 0, 0x3120), lo, hi);
+}
+
+// Two fp32 in a register pair, and a * b + c on both at once
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 split2(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // ---------------------------------------------------------------- consumers
-// A consumer class is one warp's part of the arithmetic:
-//   HEADS, DP              query heads of an item, elements of a row, at most
+// A consumer class is one warp's part of the arithmetic of its team:
+//   HEADS, TEAMS, DP       query heads of a team, teams, elements of a row, at most
 //   TK                     keys of a tile
 //   ROW_BYTES, BOXES       a key's bytes, TMA boxes per row
 //   begin(q, keep, heads)  a new item; q its rows in shared memory, keep room for
@@ -149,27 +193,36 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 // not to the largest weight: 2^(s_j - M2) vs_j <= 1, and what fp16 flushes is
 // below 2^-24 of the key that dominates the output, however far the scales of
 // the rows lie apart.  The sum l keeps its own maximum m.
-template <int DP_, int NT_, bool CODES_>
+template <int DP_, int NT_, bool CODES_, int TEAMS_ = 1>
 struct TcConsumer {
-    static constexpr int DP = DP_, NT = NT_;
+    static constexpr int DP = DP_, NT = NT_, TEAMS = TEAMS_;
     static constexpr bool CODES = CODES_;
     static constexpr bool F32 = false;
     static constexpr int HEADS = 8 * NT;
     static constexpr int ROW_BYTES = DP * (CODES ? 1 : 2);
     static constexpr int ELEM = CODES ? 1 : 2;  // bytes
-    static constexpr int BOXES = ROW_BYTES / 128;
-    static constexpr int TK = ROW_BYTES == 128 && NT == 1 ? 128 : 64;  // 32 KB a tile, or 64 keys
-    static constexpr int WARPS = 4;
+    static constexpr int SPAN = ROW_BYTES < 128 ? 64 : 128;  // bytes of a swizzled row in shared memory
+    static constexpr int BOXES = ROW_BYTES / SPAN;
+    // 32 KB a tile, or 64 keys where rows are wider
+    static constexpr int TK = ROW_BYTES > 256 ? 64 : 16384 / ROW_BYTES;
     static constexpr int Q_STRIDE = DP * 2 + 16;                        // bytes; 8 rows in distinct banks
     static constexpr int W_STRIDE = TK * 2 + 16;
     static constexpr int W_BYTES = HEADS * W_STRIDE;
     static constexpr int KEEP_BYTES = 0;
-    static constexpr int CTAS = NT < 4 && ROW_BYTES <= 256 ? 2 : 1;
+    static constexpr int CTAS = TEAMS == 1 && ROW_BYTES <= 256 ? 2 : 1;
     static constexpr int K_BYTES = TK * ROW_BYTES;
-    static constexpr int SLICES = TK / (16 * WARPS);  // of 16 keys, a warp's
+    static constexpr int SLICES = TK / (16 * kTeam);  // of 16 keys, a warp's
     static constexpr int KSTEPS = DP / 16;                 // of 16 elements of q and k
-    static constexpr int MTILES = DP / 16 / WARPS;    // of 16 elements of v, a warp's
-    static_assert(ROW_BYTES % 128 == 0 && (!CODES || MTILES % 2 == 0), "layout");
+    static constexpr int MTILES = DP / 16 / kTeam;    // of 16 elements of v, a warp's
+    static_assert(ROW_BYTES % SPAN == 0 && (!CODES || MTILES == 1 || MTILES % 2 == 0), "layout");
+
+    // Byte of 16-byte chunk `chunk` of key `row` within a tile's keys: columns of
+    // SPAN bytes, swizzled as TMA leaves them.
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) {
+        constexpr int PER = SPAN / 16;
+        const int swizzle = SPAN == 128 ? row & 7 : (row >> 1) & 3;
+        return chunk / PER * (TK * SPAN) + row * SPAN + (((chunk % PER) ^ swizzle) << 4);
+    }
 
     uint32_t qf[KSTEPS][NT][2];
     float m[NT][2], l[NT][2], qs[NT][2];
@@ -178,8 +231,8 @@ struct TcConsumer {
 
     // element of the head's row in o[t][..][2 r + ..]
     static __device__ __forceinline__ int elem(int t, int r) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-        return warp * (DP / WARPS) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
+        const int lane = threadIdx.x & 31, warp = team_warp(), g = lane >> 2;
+        return warp * (DP / kTeam) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
     }
 
     __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, uint8_t*, int heads) {
@@ -240,7 +293,7 @@ struct TcConsumer {
     }
 
     // stage: the tile in shared memory (K, then V); scales: E4M3, of its keys;
-    // maxima [1 or 2][WARPS][HEADS] and weights (W_BYTES): this tile's, of
+    // maxima [1 or 2][kTeam][HEADS] and weights (W_BYTES): this tile's, of
     // all the warps
     // (Whole tiles have code of their own, without a branch that would keep the
     // loads and products of one step apart from the next one's.)
@@ -253,7 +306,7 @@ struct TcConsumer {
     template <bool partial>
     __device__ __forceinline__ bool tile_of(bool ok, uint32_t stage, const float* scales, float* maxima,
                                             uint8_t* weights, int lo, int hi) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
+        const int lane = threadIdx.x & 31, warp = team_warp(), g = lane >> 2, i = lane & 3;
         const int key0 = warp * 16 * SLICES;  // this warp's keys of the tile
         const bool some = !partial || (key0 < hi && key0 + 16 * SLICES > lo);
         float s[SLICES][NT][4];
@@ -263,8 +316,6 @@ struct TcConsumer {
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = top2[nt][0] = top2[nt][1] = -INFINITY;
         if (some) {
             // S^T = K q^T
-            const uint32_t rowa = stage + (key0 + (lane & 15)) * 128;
-            const uint32_t x = static_cast<uint32_t>((lane >> 4) ^ (lane & 7)) << 4;
 #pragma unroll
             for (int sl = 0; sl < SLICES; ++sl) {
                 float s2[NT][4];  // a second chain of sums
@@ -275,7 +326,7 @@ struct TcConsumer {
 #pragma unroll
                 for (int c = 0; c < ROW_BYTES / 32; ++c) {  // two 16-byte chunks at a time
                     uint32_t a[4];
-                    ldmatrix_x4(rowa + sl * 16 * 128 + (c >> 2) * TK * 128 + (x ^ ((c & 3) << 5)), a);
+                    ldmatrix_x4(stage + at(key0 + sl * 16 + (lane & 15), 2 * c + (lane >> 4)), a);
                     if constexpr (!CODES) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -335,23 +386,23 @@ struct TcConsumer {
                 float* at = maxima + warp * HEADS + nt * 8 + 2 * lane;
                 *reinterpret_cast<float2*>(at) = make_float2(top[nt][0], top[nt][1]);
                 if constexpr (CODES)
-                    *reinterpret_cast<float2*>(at + WARPS * HEADS) = make_float2(top2[nt][0], top2[nt][1]);
+                    *reinterpret_cast<float2*>(at + kTeam * HEADS) = make_float2(top2[nt][0], top2[nt][1]);
             }
         }
-        if (!consumers_agree<WARPS>(ok)) return false;
+        if (!team_agrees<TEAMS>(ok)) return false;
         float old[NT][2];
         bool moved = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float2 t2 = make_float2(m[nt][0], m[nt][1]), u2 = make_float2(m2[nt][0], m2[nt][1]);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 0; w < kTeam; ++w) {
                 const float* at = maxima + w * HEADS + nt * 8 + 2 * i;
                 const float2 o2 = *reinterpret_cast<const float2*>(at);
                 t2.x = fmaxf(t2.x, o2.x);
                 t2.y = fmaxf(t2.y, o2.y);
                 if constexpr (CODES) {
-                    const float2 p2 = *reinterpret_cast<const float2*>(at + WARPS * HEADS);
+                    const float2 p2 = *reinterpret_cast<const float2*>(at + kTeam * HEADS);
                     u2.x = fmaxf(u2.x, p2.x);
                     u2.y = fmaxf(u2.y, p2.y);
                 }
@@ -403,7 +454,7 @@ struct TcConsumer {
                                                   : pack_bf16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
             }
         }
-        consumers_sync<WARPS>();
+        team_sync<TEAMS>();
         if (__any_sync(0xffffffffu, moved)) {  // a maximum moved
 #pragma unroll
             for (int t = 0; t < MTILES; ++t)
@@ -425,18 +476,18 @@ struct TcConsumer {
             auto keep = [&](int key) {
                 return (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
             };
-            const int chunk0 = warp * (ROW_BYTES / 16 / WARPS);  // this warp's part of the row
+            const int chunk0 = warp * (ROW_BYTES / 16 / kTeam);  // this warp's part of the row
             if constexpr (!CODES) {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     const int k0 = k2 * 32 + kk * 16;
                     if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
-                    const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 7) + ((lane >> 4) << 3)) * 128;
 #pragma unroll
                     for (int t = 0; t < MTILES; ++t) {
-                        const int c = chunk0 + 2 * t + ((lane >> 3) & 1);
                         uint32_t a[4];
-                        ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
+                        ldmatrix_x4_trans(stage + K_BYTES + at(k0 + (lane & 7) + ((lane >> 4) << 3),
+                                                               chunk0 + 2 * t + ((lane >> 3) & 1)),
+                                          a);
                         if (partial) {
                             const uint32_t keep0 = keep(k0 + 2 * i), keep1 = keep(k0 + 8 + 2 * i);
                             a[0] &= keep0;
@@ -448,17 +499,31 @@ struct TcConsumer {
                         for (int nt = 0; nt < NT; ++nt) mma_bf16(o[t][nt], a, w[nt][2 * kk], w[nt][2 * kk + 1]);
                     }
                 }
+            } else if constexpr (MTILES == 1) {
+                uint32_t a[4];  // 16 elements of 32 keys
+                ldmatrix_x4_trans(stage + K_BYTES + at(k2 * 32 + lane, chunk0), a);
+                if (partial) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) a[n] &= keep(k2 * 32 + 8 * n + 2 * i);
+                }
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    if (partial && (k2 * 32 + kk * 16 >= hi || k2 * 32 + kk * 16 + 16 <= lo)) continue;
+                    uint32_t f[4];
+                    unpack_values(a[2 * kk], f[0], f[1]);
+                    unpack_values(a[2 * kk + 1], f[2], f[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[0][nt], f, w[nt][2 * kk], w[nt][2 * kk + 1]);
+                }
             } else {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     const int k0 = k2 * 32 + kk * 16;
                     if (partial && (k0 >= hi || k0 + 16 <= lo)) continue;
-                    const uint32_t rowa = stage + K_BYTES + (k0 + (lane & 15)) * 128;
 #pragma unroll
                     for (int t = 0; t < MTILES; t += 2) {
-                        const int c = chunk0 + t + (lane >> 4);
                         uint32_t a[4];
-                        ldmatrix_x4_trans(rowa + (c >> 3) * TK * 128 + (((c & 7) ^ (lane & 7)) << 4), a);
+                        ldmatrix_x4_trans(stage + K_BYTES + at(k0 + (lane & 15), chunk0 + t + (lane >> 4)), a);
                         if (partial) {
                             const uint32_t keep0 = keep(k0 + 2 * i), keep1 = keep(k0 + 8 + 2 * i);
                             a[0] &= keep0;
@@ -466,13 +531,11 @@ struct TcConsumer {
                             a[2] &= keep0;
                             a[3] &= keep1;
                         }
-                        // a register holds two elements of two keys each: keys
-                        // together, elements 2g to row g, 2g + 1 to row g + 8
                         uint32_t a0[4], a1[4];
-                        unpack_e4m3(__byte_perm(a[0], 0, 0x3120), a0[0], a0[1]);
-                        unpack_e4m3(__byte_perm(a[1], 0, 0x3120), a0[2], a0[3]);
-                        unpack_e4m3(__byte_perm(a[2], 0, 0x3120), a1[0], a1[1]);
-                        unpack_e4m3(__byte_perm(a[3], 0, 0x3120), a1[2], a1[3]);
+                        unpack_values(a[0], a0[0], a0[1]);
+                        unpack_values(a[1], a0[2], a0[3]);
+                        unpack_values(a[2], a1[0], a1[1]);
+                        unpack_values(a[3], a1[2], a1[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_f16(o[t][nt], a0, w[nt][2 * kk], w[nt][2 * kk + 1]);
@@ -485,11 +548,11 @@ struct TcConsumer {
         return true;
     }
 
-    // The item's end, or its part's: sums [WARPS][HEADS] in shared memory.
+    // The item's end, or its part's: sums [kTeam][HEADS] in shared memory.
     // Calls put(head, element, o, m, l) for this thread's outputs.
     template <typename Put>
     __device__ __forceinline__ void finish(float* sums, Put put) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 3;
+        const int lane = threadIdx.x & 31, warp = team_warp(), i = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -499,7 +562,7 @@ struct TcConsumer {
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (lane < 4) sums[warp * HEADS + nt * 8 + 2 * lane + e] = sum;
             }
-        consumers_sync<WARPS>();
+        team_sync<TEAMS>();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -507,7 +570,7 @@ struct TcConsumer {
                 const int h = nt * 8 + 2 * i + e;
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) sum += sums[w * HEADS + h];
+                for (int w = 0; w < kTeam; ++w) sum += sums[w * HEADS + h];
                 // E4M3: o is relative to M2, the sum to m
                 const float f = CODES && sum != 0.f ? ex2(m2[nt][e] - m[nt][e]) : 1.f;
 #pragma unroll
@@ -530,33 +593,33 @@ struct TcConsumer {
 // rows in makes the lanes' reads free of bank conflicts, and no score needs a
 // sum over lanes.  Outputs: a lane owns an element or two of the row (every
 // second key, where a warp's elements are fewer than its lanes).
-template <int DP_>
+template <int DP_, int TEAMS_ = 1>
 struct F32Consumer {
-    static constexpr int DP = DP_;
+    static constexpr int DP = DP_, TEAMS = TEAMS_;
     static constexpr bool CODES = false;
     static constexpr bool F32 = true;
     static constexpr int HEADS = 8;
-    static constexpr int WARPS = 4;
     static constexpr int ELEM = 4;  // bytes
     static constexpr int ROW_BYTES = DP * 4;
+    static constexpr int SPAN = 128;
     static constexpr int BOXES = ROW_BYTES / 128;
     static constexpr int TK = 16384 / ROW_BYTES;
     static constexpr int K_BYTES = TK * ROW_BYTES;
     static constexpr int Q_STRIDE = ROW_BYTES;
     static constexpr int W_STRIDE = HEADS + 4;  // floats of a key's weights
     static constexpr int W_BYTES = TK * W_STRIDE * 4;
-    static constexpr int CTAS = 2;
+    static constexpr int CTAS = TEAMS == 1 ? 2 : 1;
     static constexpr int KEY_GROUPS = TK > 32 ? TK / 32 : 1;       // of the warps
-    static constexpr int HPW = HEADS * KEY_GROUPS / WARPS;    // heads of a warp's scores
-    static constexpr int KEEP_BYTES = WARPS * HPW * ROW_BYTES;
+    static constexpr int HPW = HEADS * KEY_GROUPS / kTeam;    // heads of a warp's scores
+    static constexpr int KEEP_BYTES = kTeam * HPW * ROW_BYTES;
     static constexpr int ROW_PARTS = TK < 32 ? 32 / TK : 1;        // lanes that share a row
-    static constexpr int OWN = DP / WARPS;                    // elements of a warp's outputs
+    static constexpr int OWN = DP / kTeam;                    // elements of a warp's outputs
     static constexpr int E = OWN > 32 ? OWN / 32 : 1;              // of a lane's
     static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;          // lanes that share an element
     static_assert(HPW == 2 || HPW == 4, "vectors of weights");
 
     const uint8_t* q;  // this warp's heads of the item's queries
-    float o[HEADS][E];
+    uint64_t o[HEADS / 2][E];  // of two heads each
     float m;       // of head lane & 7
     float l[HPW];  // of this lane's keys
     float to_log2;
@@ -565,7 +628,7 @@ struct F32Consumer {
     __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* rows, uint8_t* keep, int n) {
         // the stage that the queries came with is given back: this warp's heads
         // are copied, cleared where the item has no head or the row no element
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h0 = warp / KEY_GROUPS * HPW;
+        const int lane = threadIdx.x & 31, warp = team_warp(), h0 = warp / KEY_GROUPS * HPW;
         uint8_t* mine = keep + warp * HPW * ROW_BYTES;
         __syncwarp();  // the last item's queries are no longer read
         for (int i = lane; i < HPW * DP / 4; i += 32) {
@@ -579,9 +642,9 @@ struct F32Consumer {
         heads = n;
         to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h)
+        for (int h = 0; h < HEADS / 2; ++h)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[h][e] = 0.f;
+            for (int e = 0; e < E; ++e) o[h][e] = 0;
         m = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPW; ++h) l[h] = 0.f;
@@ -589,7 +652,7 @@ struct F32Consumer {
 
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float*, float* maxima, uint8_t* weights, int lo,
                                          int hi) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int lane = threadIdx.x & 31, warp = team_warp();
         const int key = (KEY_GROUPS > 1 ? warp % KEY_GROUPS * 32 : 0) + lane % (TK < 32 ? TK : 32);
         const int h0 = warp / KEY_GROUPS * HPW;  // this warp's heads
         const bool in = key >= lo && key < hi;
@@ -600,20 +663,29 @@ struct F32Consumer {
         if (h0 < heads) {
             const int part = lane / TK;  // of the row (0 where a lane has it all)
             const uint32_t row = stage + key * 128;
-            const float4* qv = reinterpret_cast<const float4*>(q);
+            const ulonglong2* qv = reinterpret_cast<const ulonglong2*>(q);
+            uint64_t x2[HPW][2];  // sums of elements 0 and 1, 2 and 3 of the chunks
+#pragma unroll
+            for (int h = 0; h < HPW; ++h) x2[h][0] = x2[h][1] = 0;
 #pragma unroll 16
             for (int c0 = 0; c0 < DP / 4 / ROW_PARTS; ++c0) {
                 const int c = ROW_PARTS > 1 ? c0 + part * (DP / 4 / ROW_PARTS) : c0;
-                float4 k;
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+                uint64_t k0, k1;
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                             : "=l"(k0), "=l"(k1)
                              : "r"(row + (c >> 3) * (TK * 128) + (((c & 7) ^ (key & 7)) << 4))
                              : "memory");
 #pragma unroll
                 for (int h = 0; h < HPW; ++h) {
-                    const float4 a = qv[h * (DP / 4) + c];
-                    x[h] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, x[h]))));
+                    const ulonglong2 a = qv[h * (DP / 4) + c];
+                    x2[h][0] = fma2(a.x, k0, x2[h][0]);
+                    x2[h][1] = fma2(a.y, k1, x2[h][1]);
                 }
+            }
+#pragma unroll
+            for (int h = 0; h < HPW; ++h) {
+                const float2 u = split2(x2[h][0]), v = split2(x2[h][1]);
+                x[h] = (u.x + u.y) + (v.x + v.y);
             }
         }
         float top = -INFINITY;
@@ -628,10 +700,10 @@ struct F32Consumer {
             if ((lane & 7) == h0 + h) top = t;
         }
         if (lane < 8) maxima[warp * HEADS + lane] = top;
-        if (!consumers_agree<WARPS>(ok)) return false;
+        if (!team_agrees<TEAMS>(ok)) return false;
         top = m;
 #pragma unroll
-        for (int n = 0; n < WARPS; ++n) top = fmaxf(top, maxima[n * HEADS + (lane & 7)]);
+        for (int n = 0; n < kTeam; ++n) top = fmaxf(top, maxima[n * HEADS + (lane & 7)]);
         const float base = top == -INFINITY ? 0.f : top;
         const float old = ex2(m - base);
         const bool moved = top != m;
@@ -648,13 +720,13 @@ struct F32Consumer {
             else
                 *reinterpret_cast<float2*>(at) = make_float2(x[0], x[1]);
         }
-        consumers_sync<WARPS>();
+        team_sync<TEAMS>();
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                const float f = __shfl_sync(0xffffffffu, old, h);
+            for (int h = 0; h < HEADS / 2; ++h) {
+                const uint64_t f = pair2(__shfl_sync(0xffffffffu, old, 2 * h), __shfl_sync(0xffffffffu, old, 2 * h + 1));
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[h][e] *= f;
+                for (int e = 0; e < E; ++e) o[h][e] = fma2(o[h][e], f, 0);
             }
         }
         // keys [lo, hi) alone: a masked row may hold anything
@@ -663,26 +735,28 @@ struct F32Consumer {
         const int chunk = d >> 2 & 7;
         const bool many = heads > 4;
         auto add_key = [&](int k) {
-            const float4* w4 = reinterpret_cast<const float4*>(w + k * W_STRIDE);
+            const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(w + k * W_STRIDE);
             const uint32_t addr = vat + k * 128 + ((chunk ^ (k & 7)) << 4);
             float f[E];
             if constexpr (E == 2)
                 asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(addr) : "memory");
             else
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(addr) : "memory");
-            const float4 wa = w4[0];
-            const float wk[4] = {wa.x, wa.y, wa.z, wa.w};
+            const ulonglong2 wa = w4[0];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[h][e] = fmaf(wk[h], f[e], o[h][e]);
+            for (int e = 0; e < E; ++e) {
+                const uint64_t ff = pair2(f[e], f[e]);
+                o[0][e] = fma2(wa.x, ff, o[0][e]);
+                o[1][e] = fma2(wa.y, ff, o[1][e]);
+            }
             if (many) {
-                const float4 wb = w4[1];
-                const float wl[4] = {wb.x, wb.y, wb.z, wb.w};
+                const ulonglong2 wb = w4[1];
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[4 + h][e] = fmaf(wl[h], f[e], o[4 + h][e]);
+                for (int e = 0; e < E; ++e) {
+                    const uint64_t ff = pair2(f[e], f[e]);
+                    o[2][e] = fma2(wb.x, ff, o[2][e]);
+                    o[3][e] = fma2(wb.y, ff, o[3][e]);
+                }
             }
         };
         const int k1 = SPLIT > 1 ? lane / OWN : 0;
@@ -698,7 +772,7 @@ struct F32Consumer {
 
     template <typename Put>
     __device__ __forceinline__ void finish(float* sums, Put put) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h0 = warp / KEY_GROUPS * HPW;
+        const int lane = threadIdx.x & 31, warp = team_warp(), h0 = warp / KEY_GROUPS * HPW;
         float mine = 0.f;
 #pragma unroll
         for (int h = 0; h < HPW; ++h) {
@@ -708,16 +782,17 @@ struct F32Consumer {
             if (lane == h0 + h) mine = n;
         }
         if (lane < 8) sums[warp * HEADS + lane] = mine;
-        consumers_sync<WARPS>();
+        team_sync<TEAMS>();
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
             const float mh = __shfl_sync(0xffffffffu, m, h);
             float n = 0.f;
 #pragma unroll
-            for (int k = 0; k < WARPS; ++k) n += sums[k * HEADS + h];
+            for (int k = 0; k < kTeam; ++k) n += sums[k * HEADS + h];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                float v = o[h][e];
+                const float2 both = split2(o[h / 2][e]);
+                float v = h % 2 ? both.y : both.x;
 #pragma unroll
                 for (int off = OWN; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
                 if (lane < OWN) put(h, warp * OWN + lane * E + e, v, mh, n);
@@ -802,13 +877,14 @@ struct Cursor {
 template <class C>
 struct Smem {
     static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;
-    static constexpr int Q_BYTES = C::HEADS * C::Q_STRIDE;
+    static constexpr int HEADS = C::HEADS * C::TEAMS;  // of an item
+    static constexpr int Q_BYTES = HEADS * C::Q_STRIDE;
     static constexpr int STAGE_BYTES = 2 * C::K_BYTES;
-    // maxima (two sets, for two tiles), sums [C::WARPS][HEADS], weights [2]
-    static constexpr int MAXIMA = (C::CODES ? 2 : 1) * C::WARPS * C::HEADS;
-    static constexpr int STATS_BYTES = (2 * MAXIMA + C::WARPS * C::HEADS) * 4;
-    static constexpr int KEEP_BYTES = C::KEEP_BYTES;
-    static constexpr int FIXED = STATS_BYTES + 2 * C::W_BYTES + KEEP_BYTES + 1024;  // 1024: alignment of the ring
+    // of a team: maxima (two sets, for two tiles), sums [kTeam][HEADS], weights [2]
+    static constexpr int MAXIMA = (C::CODES ? 2 : 1) * kTeam * C::HEADS;
+    static constexpr int STATS_BYTES = (2 * MAXIMA + kTeam * C::HEADS) * 4;
+    static constexpr int TEAM_BYTES = STATS_BYTES + 2 * C::W_BYTES + C::KEEP_BYTES;
+    static constexpr int FIXED = C::TEAMS * TEAM_BYTES + 1024;  // 1024: alignment of the ring
     // what a CTA may have: 227 KB, or half of an SM's 228 KB less 1 KB each;
     // less the kernel's static shared memory
     static constexpr int ROOM = (C::CTAS == 2 ? 113 * 1024 : 227 * 1024) - 512;
@@ -816,18 +892,16 @@ struct Smem {
     static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
     static constexpr int SCALES = STAGES * STAGE_BYTES;  // [STAGES][2][TK] floats
     static constexpr int QROWS = SCALES + STAGES * 2 * SCALE_BYTES;
-    static constexpr int STATS = QROWS + STAGES * Q_BYTES;
-    static constexpr int WEIGHTS = STATS + STATS_BYTES;
-    static constexpr int KEEP = WEIGHTS + 2 * C::W_BYTES;
-    static constexpr int BYTES = KEEP + KEEP_BYTES + 1024;
-    static_assert(STAGES >= 2 && STATS_BYTES % 16 == 0 && Q_BYTES % 16 == 0, "layout");
+    static constexpr int TEAM = QROWS + STAGES * Q_BYTES;
+    static constexpr int BYTES = TEAM + C::TEAMS * TEAM_BYTES + 1024;
+    static_assert(STAGES >= 2 && STATS_BYTES % 16 == 0 && Q_BYTES % 16 == 0 && C::W_BYTES % 16 == 0, "layout");
 };
 
 template <class C>
-__global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
+__global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
     using L = Smem<C>;
-    constexpr int kThreads = 32 * (C::WARPS + 1);
+    constexpr int kThreads = 32 * (kTeam * C::TEAMS + 1);
     constexpr int TK = C::TK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -853,7 +927,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
     if (tid == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], C::WARPS);
+            mbar_init(&empty[s], kTeam * C::TEAMS);
         }
         fence_mbar_init();
         abort_flag = 0;
@@ -904,7 +978,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
     WaitCtx wc{&status, &abort_flag, kWaitLimitNs};
     PagedAttnPart* part = p.parts + blockIdx.x;
 
-    if (warp == C::WARPS) {
+    if (warp == kTeam * C::TEAMS) {
         // -------------------------------------------------- producer
         PagedAttnItem early = {0, 0, 0, 0, 0, 0}, late = early;
         const int R = p.box_rows, nb_shift = __ffs(TK / R) - 1, nb = 1 << nb_shift;  // powers of two
@@ -917,8 +991,8 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
         static_assert(TK / 16 * C::BOXES * 2 <= 32, "one box per lane");
         const int box_r = lane & (nb - 1), box_cb = lane >> nb_shift >> 1;
         const bool box_v = lane >> nb_shift & 1, box_in = lane < nb * C::BOXES * 2;
-        const uint32_t box_at = (box_v ? C::K_BYTES : 0) + box_cb * TK * 128 + box_r * R * 128;
-        const int box_x = box_cb * (128 / C::ELEM);
+        const uint32_t box_at = (box_v ? C::K_BYTES : 0) + (box_cb * TK + box_r * R) * C::SPAN;
+        const int box_x = box_cb * (C::SPAN / C::ELEM);
         const CUtensorMap* box_map = box_v ? &p.map_v : &p.map_k;
 
         Cursor<TK> c = share_at;
@@ -1068,21 +1142,26 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
         }
     } else {
         // -------------------------------------------------- consumers
-        float* stats = reinterpret_cast<float*>(smem + L::STATS);
+        uint8_t* mine = smem + L::TEAM + team_index() * L::TEAM_BYTES;  // this team's
+        float* stats = reinterpret_cast<float*>(mine);
+        uint8_t* weights = mine + L::STATS_BYTES;
+        uint8_t* keep = weights + 2 * C::W_BYTES;
         bool begun = false;
         C c;
         uint32_t phase = 0;
         for (int i = 0, s = 0;; ++i) {
             const bool ok = mbar_wait(&full[s], phase, wc, kWhereKvFull, i);
             const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
-            const int heads = md.heads;
+            // this team's heads: an equal part of the item's
+            const int part_heads = (md.heads + C::TEAMS - 1) / C::TEAMS, h0 = team_index() * part_heads;
+            const int heads = max(0, min(part_heads, md.heads - h0));
             if (md.flags & kFirst || i == 0) {
-                c.begin(p, smem + L::QROWS + s * L::Q_BYTES, smem + L::KEEP, heads);
+                c.begin(p, smem + L::QROWS + s * L::Q_BYTES + h0 * C::Q_STRIDE, keep, heads);
                 begun = (md.flags & kItemBegins) != 0;
             }
             if (!c.tile(ok, smem_u32(smem) + s * L::STAGE_BYTES,
                         reinterpret_cast<const float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES),
-                        stats + (i & 1) * L::MAXIMA, smem + L::WEIGHTS + (i & 1) * C::W_BYTES, md.lo, md.hi))
+                        stats + (i & 1) * L::MAXIMA, weights + (i & 1) * C::W_BYTES, md.lo, md.hi))
                 break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
@@ -1094,7 +1173,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
                 float* sums = stats + 2 * L::MAXIMA;
                 if (begun && (md.flags & kItemEnds)) {
                     // the whole item: o / l, rounded once
-                    const long long qrow = md.qrow;
+                    const long long qrow = md.qrow + h0;
                     c.finish(sums, [&](int h, int d, float v, float m, float n) {
                         if (h >= heads || d >= p.D) return;
                         v = n == 0.f ? 0.f : __fdividef(v, n);
@@ -1108,7 +1187,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), C::CTAS)
                 } else {
                     // a part: slot 1 if the item begins in this share (it goes
                     // on in the next), slot 0 if it began in an earlier one
-                    const long long at = (blockIdx.x * 2ll + (begun ? 1 : 0)) * p.heads_per_item;
+                    const long long at = (blockIdx.x * 2ll + (begun ? 1 : 0)) * p.heads_per_item + h0;
                     c.finish(sums, [&](int h, int d, float v, float m, float n) {
                         if (h >= heads || d >= p.D) return;
                         p.part_o[(at + h) * p.D + d] = v;

@@ -10,14 +10,14 @@ cudaError_t launch_paged_attn_bf16(PagedAttnParams& p, int num_sms, int* ctas, c
     if (p.D <= 64) {
         if (group <= 8) return launch<TcConsumer<64, 1, false>>(p, num_sms, ctas, s);
         if (group <= 16) return launch<TcConsumer<64, 2, false>>(p, num_sms, ctas, s);
-        return launch<TcConsumer<64, 4, false>>(p, num_sms, ctas, s);
+        return launch<TcConsumer<64, 2, false, 2>>(p, num_sms, ctas, s);
     }
     if (p.D <= 128) {
         if (group <= 8) return launch<TcConsumer<128, 1, false>>(p, num_sms, ctas, s);
         if (group <= 16) return launch<TcConsumer<128, 2, false>>(p, num_sms, ctas, s);
-        return launch<TcConsumer<128, 4, false>>(p, num_sms, ctas, s);
+        return launch<TcConsumer<128, 2, false, 2>>(p, num_sms, ctas, s);
     }
-    // a row of more than 128 elements: fewer heads in the registers
+    // rows of more than 128 elements: 16 heads are what the registers hold
     if (group <= 8) return launch<TcConsumer<256, 1, false>>(p, num_sms, ctas, s);
     return launch<TcConsumer<256, 2, false>>(p, num_sms, ctas, s);
 }

@@ -12,7 +12,7 @@ template <class C>
 cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     // heads of a group, in equal blocks of at most HEADS
     const int group = p.Hq / p.Hkv;
-    p.head_blocks = (group + C::HEADS - 1) / C::HEADS;
+    p.head_blocks = (group + Smem<C>::HEADS - 1) / Smem<C>::HEADS;
     p.heads_per_item = (group + p.head_blocks - 1) / p.head_blocks;
     p.head_blocks = (group + p.heads_per_item - 1) / p.heads_per_item;
     p.items_per_seq = p.P * p.Hkv * p.head_blocks;
@@ -20,8 +20,8 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     p.box_rows = 16;
     while (p.box_rows < C::TK && p.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     const uint64_t rows = static_cast<uint64_t>(p.P) * p.num_pages * p.Hkv * p.page_size;
-    if (!encode_map_rows(&p.map_k, p.k, C::ELEM, p.D, rows, 128 / C::ELEM, p.box_rows) ||
-        !encode_map_rows(&p.map_v, p.v, C::ELEM, p.D, rows, 128 / C::ELEM, p.box_rows))
+    if (!encode_map_rows(&p.map_k, p.k, C::ELEM, p.D, rows, C::SPAN / C::ELEM, p.box_rows) ||
+        !encode_map_rows(&p.map_v, p.v, C::ELEM, p.D, rows, C::SPAN / C::ELEM, p.box_rows))
         return cudaErrorInvalidValue;
     // division by the page size: with 2^(l-1) < d <= 2^l and mul = floor(2^(31+l) / d) + 1, the error
     // mul - 2^(31+l) / d <= 1 adds less than key / 2^(31+l) < 1 / d to the quotient
@@ -47,7 +47,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (grid > most) grid = most;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     *ctas = static_cast<int>(grid);
-    paged_attn_kernel<C><<<*ctas, 32 * (C::WARPS + 1), Smem<C>::BYTES, s>>>(p);
+    paged_attn_kernel<C><<<*ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s>>>(p);
     return cudaGetLastError();
 }
 

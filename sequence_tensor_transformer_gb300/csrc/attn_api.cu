@@ -163,7 +163,7 @@ int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_id
                         float* k_scale, float* v_scale, void* workspace, size_t ws_bytes, void* cuda_stream) {
     const bool e4m3 = kv_type == SPTP_KV_E4M3;
     if (!k_cache || !v_cache || !workspace || (rot != 0 && !turns) || (e4m3 && (!k_scale || !v_scale)) ||
-        (M != 0 && (!qkv || !positions || !seq_ids || !page_table || !q_out)))
+        (M != 0 && (!qkv || !positions || !seq_ids || (B != 0 && !page_table) || !q_out)))
         return SPTP_ERR_NULL;
     int rc = check_cache(P, Hkv, D, B, max_pages, num_pages, page_size, dtype, kv_type);
     if (rc == SPTP_ERR_DTYPE) return rc;

@@ -585,14 +585,14 @@ struct TcConsumer {
     }
 };
 
-// fp32 consumer: CUDA cores, fp32 throughout, up to 8 query heads.
+// fp32 consumer: CUDA cores, fp32 throughout, up to 8 query heads a team.
 //
-// Scores: a lane owns a key (or half a row of one, where a tile has only 16) and
-// goes along its row, 16 bytes at a time, for the HPW heads of its warp, whose
-// queries all lanes read from the same place; the swizzle that TMA leaves the
-// rows in makes the lanes' reads free of bank conflicts, and no score needs a
-// sum over lanes.  Outputs: a lane owns an element or two of the row (every
-// second key, where a warp's elements are fewer than its lanes).
+// What bounds it beside HBM is shared memory: a query or a weight that all
+// lanes read from one place costs as much as a row of 32 values.  So a lane
+// scores two keys (half a row of each, the halves' sums exchanged at the end)
+// for the HPW heads of its warp, and sums up four elements of the values of one
+// key in KEYS_A_STEP: each query read serves two products, each weight four.
+// The swizzle that TMA leaves the rows in keeps the lanes' reads apart.
 template <int DP_, int TEAMS_ = 1>
 struct F32Consumer {
     static constexpr int DP = DP_, TEAMS = TEAMS_;
@@ -609,19 +609,23 @@ struct F32Consumer {
     static constexpr int W_STRIDE = HEADS + 4;  // floats of a key's weights
     static constexpr int W_BYTES = TK * W_STRIDE * 4;
     static constexpr int CTAS = TEAMS == 1 ? 2 : 1;
-    static constexpr int KEY_GROUPS = TK > 32 ? TK / 32 : 1;       // of the warps
-    static constexpr int HPW = HEADS * KEY_GROUPS / kTeam;    // heads of a warp's scores
+    // scores
+    static constexpr int KEY_GROUPS = TK > 32 ? TK / 32 : 1;   // of the warps
+    static constexpr int HPW = HEADS * KEY_GROUPS / kTeam;     // heads of a warp
+    static constexpr int KPL = TK < 32 ? 1 : 2;                // keys of a lane, 16 apart
+    static constexpr int LANES = TK < 32 ? TK : 32;            // that hold a key each in the end
+    static constexpr int CHUNKS = DP / 8;                      // 16-byte chunks of half a row
     static constexpr int KEEP_BYTES = kTeam * HPW * ROW_BYTES;
-    static constexpr int ROW_PARTS = TK < 32 ? 32 / TK : 1;        // lanes that share a row
-    static constexpr int OWN = DP / kTeam;                    // elements of a warp's outputs
-    static constexpr int E = OWN > 32 ? OWN / 32 : 1;              // of a lane's
-    static constexpr int SPLIT = OWN < 32 ? 32 / OWN : 1;          // lanes that share an element
-    static_assert(HPW == 2 || HPW == 4, "vectors of weights");
+    // outputs
+    static constexpr int OWN = DP / kTeam;                     // elements of a warp
+    static constexpr int QUADS = OWN / 4;                      // of four, a lane each
+    static constexpr int KEYS_A_STEP = 32 / QUADS;
+    static_assert((HPW == 2 || HPW == 4) && TK % KEYS_A_STEP == 0, "layout");
 
-    const uint8_t* q;  // this warp's heads of the item's queries
-    uint64_t o[HEADS / 2][E];  // of two heads each
-    float m;       // of head lane & 7
-    float l[HPW];  // of this lane's keys
+    const uint8_t* q;          // this warp's heads of the item's queries
+    uint64_t o[HEADS / 2][4];  // of two heads each
+    float m;                   // of head lane & 7
+    float l[HPW];              // of this lane's keys
     float to_log2;
     int heads;
 
@@ -644,7 +648,7 @@ struct F32Consumer {
 #pragma unroll
         for (int h = 0; h < HEADS / 2; ++h)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[h][e] = 0;
+            for (int e = 0; e < 4; ++e) o[h][e] = 0;
         m = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPW; ++h) l[h] = 0.f;
@@ -653,7 +657,8 @@ struct F32Consumer {
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float*, float* maxima, uint8_t* weights, int lo,
                                          int hi) {
         const int lane = threadIdx.x & 31, warp = team_warp();
-        const int key = (KEY_GROUPS > 1 ? warp % KEY_GROUPS * 32 : 0) + lane % (TK < 32 ? TK : 32);
+        const int key0 = KEY_GROUPS > 1 ? warp % KEY_GROUPS * 32 : 0;
+        const int key = key0 + lane % LANES;     // whose scores this lane holds in the end
         const int h0 = warp / KEY_GROUPS * HPW;  // this warp's heads
         const bool in = key >= lo && key < hi;
         float* w = reinterpret_cast<float*>(weights);  // [TK][W_STRIDE]
@@ -661,42 +666,56 @@ struct F32Consumer {
 #pragma unroll
         for (int h = 0; h < HPW; ++h) x[h] = 0.f;
         if (h0 < heads) {
-            const int part = lane / TK;  // of the row (0 where a lane has it all)
-            const uint32_t row = stage + key * 128;
+            const int side = lane >> 4;  // of the row
+            const int first = key0 + (lane & 15);
+            const uint32_t row = stage + first * 128;
             const ulonglong2* qv = reinterpret_cast<const ulonglong2*>(q);
-            uint64_t x2[HPW][2];  // sums of elements 0 and 1, 2 and 3 of the chunks
+            uint64_t x2[KPL][HPW][2];  // sums of elements 0 and 1, 2 and 3 of the chunks
 #pragma unroll
-            for (int h = 0; h < HPW; ++h) x2[h][0] = x2[h][1] = 0;
-#pragma unroll 16
-            for (int c0 = 0; c0 < DP / 4 / ROW_PARTS; ++c0) {
-                const int c = ROW_PARTS > 1 ? c0 + part * (DP / 4 / ROW_PARTS) : c0;
-                uint64_t k0, k1;
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                             : "=l"(k0), "=l"(k1)
-                             : "r"(row + (c >> 3) * (TK * 128) + (((c & 7) ^ (key & 7)) << 4))
-                             : "memory");
+            for (int j = 0; j < KPL; ++j)
+#pragma unroll
+                for (int h = 0; h < HPW; ++h) x2[j][h][0] = x2[j][h][1] = 0;
+#pragma unroll 8
+            for (int c0 = 0; c0 < CHUNKS; ++c0) {
+                const int c = side * CHUNKS + (c0 ^ side);  // the sides in different banks
+                const uint32_t at = row + (c >> 3) * (TK * 128) + (((c & 7) ^ (first & 7)) << 4);
+                uint64_t k[KPL][2];
+#pragma unroll
+                for (int j = 0; j < KPL; ++j)
+                    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                                 : "=l"(k[j][0]), "=l"(k[j][1])
+                                 : "r"(at + j * 16 * 128)
+                                 : "memory");
 #pragma unroll
                 for (int h = 0; h < HPW; ++h) {
                     const ulonglong2 a = qv[h * (DP / 4) + c];
-                    x2[h][0] = fma2(a.x, k0, x2[h][0]);
-                    x2[h][1] = fma2(a.y, k1, x2[h][1]);
+#pragma unroll
+                    for (int j = 0; j < KPL; ++j) {
+                        x2[j][h][0] = fma2(a.x, k[j][0], x2[j][h][0]);
+                        x2[j][h][1] = fma2(a.y, k[j][1], x2[j][h][1]);
+                    }
                 }
             }
 #pragma unroll
             for (int h = 0; h < HPW; ++h) {
-                const float2 u = split2(x2[h][0]), v = split2(x2[h][1]);
-                x[h] = (u.x + u.y) + (v.x + v.y);
+                float y[KPL];
+#pragma unroll
+                for (int j = 0; j < KPL; ++j) {
+                    const float2 u = split2(x2[j][h][0]), v = split2(x2[j][h][1]);
+                    y[j] = (u.x + u.y) + (v.x + v.y);
+                }
+                // the other side's sum of the key that this lane keeps
+                const float mine = KPL == 2 && side ? y[KPL - 1] : y[0], give = KPL == 2 && !side ? y[KPL - 1] : y[0];
+                x[h] = mine + __shfl_xor_sync(0xffffffffu, give, 16);
             }
         }
         float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPW; ++h) {
-#pragma unroll
-            for (int off = TK; off < 32; off <<= 1) x[h] += __shfl_xor_sync(0xffffffffu, x[h], off);
             x[h] = in ? x[h] * to_log2 : -INFINITY;
             float t = x[h];
 #pragma unroll
-            for (int off = 1; off < (TK < 32 ? TK : 32); off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+            for (int off = 1; off < LANES; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
             if ((lane & 7) == h0 + h) top = t;
         }
         if (lane < 8) maxima[warp * HEADS + lane] = top;
@@ -713,7 +732,7 @@ struct F32Consumer {
             x[h] = ex2(x[h] - __shfl_sync(0xffffffffu, base, h0 + h));
             l[h] = fmaf(l[h], __shfl_sync(0xffffffffu, old, h0 + h), x[h]);
         }
-        if (lane < TK) {
+        if (lane < LANES) {
             float* at = w + key * W_STRIDE + h0;
             if constexpr (HPW == 4)
                 *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
@@ -726,25 +745,25 @@ struct F32Consumer {
             for (int h = 0; h < HEADS / 2; ++h) {
                 const uint64_t f = pair2(__shfl_sync(0xffffffffu, old, 2 * h), __shfl_sync(0xffffffffu, old, 2 * h + 1));
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[h][e] = fma2(o[h][e], f, 0);
+                for (int e = 0; e < 4; ++e) o[h][e] = fma2(o[h][e], f, 0);
             }
         }
-        // keys [lo, hi) alone: a masked row may hold anything
-        const int d = warp * OWN + (SPLIT > 1 ? lane % OWN : lane * E);
-        const uint32_t vat = stage + K_BYTES + (d >> 5) * (TK * 128) + (d & 3) * 4;
-        const int chunk = d >> 2 & 7;
+        const int quad = warp * QUADS + lane % QUADS;  // chunk of the row
+        // (rows of 64: of the two keys that eight lanes read, one is 4 further,
+        // in the other half of the banks)
+        const int sub = lane / QUADS, k1 = QUADS == 4 ? (sub & 1) << 2 | sub >> 1 : sub;
+        const uint32_t vat = stage + K_BYTES + (quad >> 3) * (TK * 128);
         const bool many = heads > 4;
         auto add_key = [&](int k) {
             const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(w + k * W_STRIDE);
-            const uint32_t addr = vat + k * 128 + ((chunk ^ (k & 7)) << 4);
-            float f[E];
-            if constexpr (E == 2)
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(addr) : "memory");
-            else
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(addr) : "memory");
+            float f[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                         : "r"(vat + k * 128 + (((quad & 7) ^ (k & 7)) << 4))
+                         : "memory");
             const ulonglong2 wa = w4[0];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 const uint64_t ff = pair2(f[e], f[e]);
                 o[0][e] = fma2(wa.x, ff, o[0][e]);
                 o[1][e] = fma2(wa.y, ff, o[1][e]);
@@ -752,20 +771,19 @@ struct F32Consumer {
             if (many) {
                 const ulonglong2 wb = w4[1];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     const uint64_t ff = pair2(f[e], f[e]);
                     o[2][e] = fma2(wb.x, ff, o[2][e]);
                     o[3][e] = fma2(wb.y, ff, o[3][e]);
                 }
             }
         };
-        const int k1 = SPLIT > 1 ? lane / OWN : 0;
         if (lo == 0 && hi == TK) {
-#pragma unroll 8
-            for (int k = 0; k < TK; k += SPLIT) add_key(k + k1);
-        } else {
 #pragma unroll 4
-            for (int k = lo + k1; k < hi; k += SPLIT) add_key(k);
+            for (int k = 0; k < TK; k += KEYS_A_STEP) add_key(k + k1);
+        } else {
+            // keys [lo, hi) alone: a masked row may hold anything
+            for (int k = lo + k1; k < hi; k += KEYS_A_STEP) add_key(k);
         }
         return true;
     }
@@ -778,25 +796,42 @@ struct F32Consumer {
         for (int h = 0; h < HPW; ++h) {
             float n = l[h];
 #pragma unroll
-            for (int off = 1; off < (TK < 32 ? TK : 32); off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+            for (int off = 1; off < LANES; off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
             if (lane == h0 + h) mine = n;
         }
         if (lane < 8) sums[warp * HEADS + lane] = mine;
         team_sync<TEAMS>();
+        // sums over the KEYS_A_STEP lanes that share elements, each lane keeping
+        // the heads of its side at every exchange: QUADS / 4 of them at the end
+        float v[HEADS * 4];
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
+        for (int h = 0; h < HEADS / 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 both = split2(o[h][e]);
+                v[2 * h * 4 + e] = both.x;
+                v[(2 * h + 1) * 4 + e] = both.y;
+            }
+        int head = 0;
+#pragma unroll
+        for (int off = 16; off >= QUADS; off >>= 1) {  // off values are kept
+            const bool up = (lane & off) != 0;
+            head += up ? off / 4 : 0;
+#pragma unroll
+            for (int i = 0; i < off; ++i) {
+                const float give = up ? v[i] : v[i + off], kept = up ? v[i + off] : v[i];
+                v[i] = kept + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < QUADS / 4; ++j) {
+            const int h = head + j;
             const float mh = __shfl_sync(0xffffffffu, m, h);
             float n = 0.f;
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) n += sums[k * HEADS + h];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 both = split2(o[h / 2][e]);
-                float v = h % 2 ? both.y : both.x;
-#pragma unroll
-                for (int off = OWN; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                if (lane < OWN) put(h, warp * OWN + lane * E + e, v, mh, n);
-            }
+            for (int e = 0; e < 4; ++e) put(h, warp * OWN + lane % QUADS * 4 + e, v[4 * j + e], mh, n);
         }
     }
 };

@@ -7,6 +7,7 @@
 
 namespace sptp {
 namespace paged {
+namespace {  // internal: a process may load the library and its checked build, each with `done` of its own
 
 template <class C>
 cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
@@ -51,5 +52,6 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+}  // namespace
 }  // namespace paged
 }  // namespace sptp

@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "checks.h"
 #include "launch.h"
 #include "sptp.h"
 #include "sptp_internal.h"

@@ -6,7 +6,8 @@
 #include <cmath>
 #include <cstring>
 
-#include "launch.h"
+#include "attn.h"
+#include "checks.h"
 #include "sptp.h"
 #include "sptp_internal.h"
 

@@ -458,22 +458,6 @@ bool encode_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t 
     return r == CUDA_SUCCESS;
 }
 
-bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
-                     uint32_t box_inner, uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode_fn();
-    if (fn == nullptr) return false;
-    const CUtensorMapDataType type = elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    cuuint64_t dims[2] = {inner, rows};
-    cuuint64_t strides[1] = {inner * elem_bytes};
-    cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_inner * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                         const uint64_t* strides_bytes, const uint32_t* box) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode_fn();

@@ -3,6 +3,7 @@
 // kernel).
 #include <cuda_bf16.h>
 
+#include "attn.h"
 #include "sptp.h"
 #include "sptp_ptx.cuh"
 

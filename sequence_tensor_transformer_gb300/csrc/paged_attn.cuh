@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "attn.h"
 #include "sptp.h"
 #include "sptp_ptx.cuh"
 

@@ -19,6 +19,7 @@
 // all shards') with the slot's cosines and sines in registers.
 #include <cuda_bf16.h>
 
+#include "attn.h"
 #include "e4m3.cuh"
 #include "sptp.h"
 #include "sptp_ptx.cuh"

@@ -7,6 +7,31 @@
 
 namespace sptp {
 
+// Launches `kernel` so that it may be scheduled while the kernel before it in
+// the stream ends (a programmatic dependency); it waits for that kernel's
+// results on the device (await_previous) before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t s, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel after this one may be scheduled once every block of this one
+// runs or has ended.
+__device__ __forceinline__ void admit_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // what a status word of these calls names (DeviceStatus::where)
 enum : int {
     kWhereKvSlot = 14,  // a token's sequence, position or page outside its range

@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_attn_join(const __grid_
     __shared__ float2 sums[2][kHalf][32];
     __shared__ int first_bad;
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    admit_next();
+    await_previous();
     if (c == ctas) {
         if (tid == 0) first_bad = ctas;
         __syncthreads();
@@ -160,20 +161,9 @@ cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_
                     : e4m3 ? launch_paged_attn_e4m3(p, num_sms, &ctas, s)
                            : launch_paged_attn_bf16(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
-    // The join is launched beside the main kernel's end (a programmatic
-    // dependency): it waits for the parts on the device.
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas + 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const int head_shift = p.D <= 64 ? 0 : p.D <= 128 ? 1 : 2;  // slices of a head: 1, 2 or 4
-    return bf16 ? cudaLaunchKernelEx(&cfg, paged_attn_join<__nv_bfloat16>, p, ctas, head_shift)
-                : cudaLaunchKernelEx(&cfg, paged_attn_join<float>, p, ctas, head_shift);
+    return bf16 ? launch_after(paged_attn_join<__nv_bfloat16>, ctas + 1, kJoinThreads, 0, s, p, ctas, head_shift)
+                : launch_after(paged_attn_join<float>, ctas + 1, kJoinThreads, 0, s, p, ctas, head_shift);
 }
 
 }  // namespace sptp

@@ -949,17 +949,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     __shared__ Cursor<TK> share_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    // the join may be scheduled as soon as every CTA of this launch runs
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // This CTA's share: every thread adds up the cost of a run of sequences, a
-    // scan over the threads gives the total and the thread in whose run the
-    // share begins.
-    const int run = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
-    long long mine = 0;
-    bool bad = false;
-    for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(span_of(p, b, &bad)) * kTileCost + kItemCost;
+    admit_next();
     if (tid == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -972,6 +962,16 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         tma_prefetch_map(&p.map_k);
         tma_prefetch_map(&p.map_v);
     }
+    await_previous();
+
+    // This CTA's share: every thread adds up the cost of a run of sequences, a
+    // scan over the threads gives the total and the thread in whose run the
+    // share begins.
+    const int run = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+    long long mine = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(span_of(p, b, &bad)) * kTileCost + kItemCost;
     mine *= p.items_per_seq;
     long long incl = mine;
 #pragma unroll

@@ -48,8 +48,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (grid > most) grid = most;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     *ctas = static_cast<int>(grid);
-    paged_attn_kernel<C><<<*ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(paged_attn_kernel<C>, *ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s, p);
 }
 
 }  // namespace

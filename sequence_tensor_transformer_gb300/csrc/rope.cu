@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     constexpr int E = Elems<T>::E;
     constexpr int kUnroll = OP == Op::kRope ? 4 : 3;  // rows whose loads a lane has in flight
     __shared__ __align__(16) float cosines[4][kMaxPairs], sines[4][kMaxPairs];
+    admit_next();
+    await_previous();
     // the first block, so that it starts with the others and not after them
     if (OP != Op::kRope && sp.checker && blockIdx.x == 0) {
         check_rows(p);
@@ -344,11 +346,8 @@ cudaError_t launch_typed(const RopeParams& p, int num_sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    if (p.interleaved)
-        rope_kernel<T, true, OP><<<static_cast<int>(grid), kThreads, 0, s>>>(p, sp);
-    else
-        rope_kernel<T, false, OP><<<static_cast<int>(grid), kThreads, 0, s>>>(p, sp);
-    return cudaGetLastError();
+    return p.interleaved ? launch_after(rope_kernel<T, true, OP>, static_cast<int>(grid), kThreads, 0, s, p, sp)
+                         : launch_after(rope_kernel<T, false, OP>, static_cast<int>(grid), kThreads, 0, s, p, sp);
 }
 
 }  // namespace

@@ -376,6 +376,9 @@ int sptp_down_proj_e4m3(const void* qs, const float* ss, const void* qW2, const 
  *   8 <= D <= 256; Hq % Hkv == 0; M, B < 2^30; page_size % 16 == 0;
  *   max_pages * page_size < 2^30; P * num_pages * Hkv * page_size < 2^31.
  *   int32 arrays are 4-byte aligned, `turns` 8-byte, all others 16-byte.
+ * Calls that may overlap on the GPU need a workspace each; calls in one stream,
+ * or replays of graphs one after another, may share it.  Appends and attention
+ * on one cache are ordered by the caller, as on any buffer.
  */
 
 /* Element type of a key-value cache. */

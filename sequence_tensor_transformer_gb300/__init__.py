@@ -578,16 +578,19 @@ def sptp_rope(x, positions, turns, Hr=None, interleaved=False, transpose=False, 
     positions int32 [M]; turns from sptp_rope_turns.  transpose: the gradient.
     out may be x (in place).  Returns out."""
     P, M, H, D = x.shape
-    rot = 2 * turns.shape[0]
+    pairs, dtype = turns.shape[0], x.dtype
     dt = _dtype_code(x)
-    _expect("positions", positions, (M,), torch.int32)
-    _expect("turns", turns, (rot // 2,), torch.int64)
-    _expect("out", out, (P, M, H, D), x.dtype, optional=True)
-    _one_device(x, positions, turns, out)
+    if not (positions.shape == (M,) and positions.dtype is torch.int32 and turns.dtype is torch.int64 and turns.dim() == 1
+            and (out is None or (out.shape == (P, M, H, D) and out.dtype is dtype))):
+        _expect("positions", positions, (M,), torch.int32)
+        _expect("turns", turns, (pairs,), torch.int64)
+        _expect("out", out, (P, M, H, D), dtype, optional=True)
+    cur = _ready(x, positions, turns, out)
     if out is None:
-        out = _new((P, M, H, D), x.dtype, x.device, stream)
-    code = lib().sptp_rope(_dptr(x), _dptr(positions), _dptr(turns), P, M, H, H if Hr is None else Hr, D, rot,
-                           int(interleaved), int(transpose), float(gain), dt, _dptr(out), _stream(stream))
+        out = _new((P, M, H, D), dtype, x.device, stream)
+    code = lib().sptp_rope(x.data_ptr(), positions.data_ptr(), turns.data_ptr(), P, M, H, H if Hr is None else Hr, D,
+                           2 * pairs, int(interleaved), int(transpose), float(gain), dt, out.data_ptr(),
+                           _raw_stream(stream, cur))
     _check("sptp_rope", code)
     return out
 
@@ -603,12 +606,23 @@ def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=F
     return k, v, torch.zeros(shape[:-1], device=device), torch.zeros(shape[:-1], device=device)
 
 
-def _one_device(*ts):
-    """_same_device for calls that count microseconds: the first tensor given."""
-    cur = torch.cuda.current_device() if ts[0].is_cuda else -1
+# The calls of a decoding step last a few microseconds on the device, so their
+# checks are written to cost little: one condition over all tensors on the way
+# in, the checks with their messages (_expect, _same_device) only if it fails.
+
+def _ready(*ts):
+    """Every tensor given is dense and on the current CUDA device, whose index
+    is returned."""
+    cur = torch._C._cuda_getDevice() if ts[0].is_cuda else -1
     for t in ts:
-        if t is not None and (cur < 0 or t.get_device() != cur):
-            return _same_device(*ts)
+        if t is not None and (cur < 0 or t.get_device() != cur or not t.is_contiguous()):
+            _same_device(*ts)
+            raise ValueError("tensors must be contiguous")
+    return cur
+
+
+def _raw_stream(stream, device_index):
+    return torch._C._cuda_getCurrentRawStream(device_index) if stream is None else _stream(stream)
 
 
 def _new(shape, dtype, device, stream):
@@ -623,65 +637,60 @@ def _new(shape, dtype, device, stream):
 def _check_cache(cache, P, D, dtype):
     """Sizes (num_pages, Hkv, page_size, kv_type) of a cache of activations of `dtype`."""
     k, v, ks, vs = cache
-    shape = k.shape
+    shape, kvt = k.shape, k.dtype
     if len(shape) != 5:
         raise ValueError(f"cache: {len(shape)} dimensions, expected [P,num_pages,Hkv,page_size,D]")
-    _, num_pages, Hkv, page_size, _ = shape
-    want = (P, num_pages, Hkv, page_size, D)
-    kvt = k.dtype
+    if kvt is dtype and v.shape == shape and v.dtype is kvt and shape[0] == P and shape[4] == D and ks is None and vs is None:
+        return shape[1], shape[2], shape[3], SPTP_KV_SAME
     if kvt != dtype:
         if kvt != torch.uint8:
             raise TypeError(f"cache: dtype {kvt}, expected {dtype} or uint8 codes")
         if dtype != torch.bfloat16:
             raise TypeError("an E4M3 cache takes bf16 activations")
-    if shape != want:
-        _expect("k_cache", k, want, kvt)
+    want = (P, *shape[1:4], D)
+    _expect("k_cache", k, want, kvt)
     _expect("v_cache", v, want, kvt)
     if kvt == dtype:
-        if ks is not None or vs is not None:
-            raise ValueError("scales belong to an E4M3 cache")
-        return num_pages, Hkv, page_size, SPTP_KV_SAME
+        raise ValueError("scales belong to an E4M3 cache")
     _expect("k_scale", ks, want[:-1], torch.float32)
     _expect("v_scale", vs, want[:-1], torch.float32)
-    return num_pages, Hkv, page_size, SPTP_KV_E4M3
-
-
-def _dptr(t):
-    """Address of a tensor that _same_device has seen."""
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+    return shape[1], shape[2], shape[3], SPTP_KV_E4M3
 
 
 def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, interleaved=False, gain=1.0, q_out=None,
                         workspace=None, stream=None):
     """Rotates the q and k heads of qkv [P,M,(Hq+2Hkv)D] and stores k and v in
     `cache` (see paged_kv_cache).  positions, seq_ids int32 [M] (seq_ids < 0:
-    padding); page_table int32 [B,max_pages]; turns None: no rotation.
-    Returns q_out [P,M,Hq,D]."""
+    padding, whose rows of q_out are left as they are); page_table int32
+    [B,max_pages]; turns None: no rotation.  Returns q_out [P,M,Hq,D]."""
     P, M, N = qkv.shape
-    D = cache[0].shape[-1]
+    k, v, ks, vs = cache
+    D, dtype, i32 = k.shape[-1], qkv.dtype, torch.int32
     dt = _dtype_code(qkv)
-    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, qkv.dtype)
-    _expect("qkv", qkv, (P, M, (Hq + 2 * Hkv) * D), qkv.dtype)
-    _expect("positions", positions, (M,), torch.int32)
-    _expect("seq_ids", seq_ids, (M,), torch.int32)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, dtype)
     B, max_pages = page_table.shape
-    _expect("page_table", page_table, (B, max_pages), torch.int32)
-    rot = 0 if turns is None else 2 * turns.shape[0]
-    _expect("turns", turns, (rot // 2,), torch.int64, optional=True)
-    _expect("q_out", q_out, (P, M, Hq, D), qkv.dtype, optional=True)
-    _one_device(qkv, positions, seq_ids, page_table, turns, *cache, q_out, workspace)
+    pairs = 0 if turns is None else turns.shape[0]
+    if not (N == (Hq + 2 * Hkv) * D and positions.shape == (M,) and positions.dtype is i32 and seq_ids.shape == (M,)
+            and seq_ids.dtype is i32 and page_table.dtype is i32
+            and (turns is None or (turns.dtype is torch.int64 and turns.dim() == 1))
+            and (q_out is None or (q_out.shape == (P, M, Hq, D) and q_out.dtype is dtype))):
+        _expect("qkv", qkv, (P, M, (Hq + 2 * Hkv) * D), dtype)
+        _expect("positions", positions, (M,), i32)
+        _expect("seq_ids", seq_ids, (M,), i32)
+        _expect("page_table", page_table, (B, max_pages), i32)
+        _expect("turns", turns, (pairs,), torch.int64, optional=True)
+        _expect("q_out", q_out, (P, M, Hq, D), dtype, optional=True)
+    cur = _ready(qkv, positions, seq_ids, page_table, turns, k, v, ks, vs, q_out, workspace)
     if q_out is None:
-        q_out = _new((P, M, Hq, D), qkv.dtype, qkv.device, stream)
+        q_out = _new((P, M, Hq, D), dtype, qkv.device, stream)
     if workspace is None:
         workspace = _new((SPTP_WS_HEADER_BYTES,), torch.uint8, qkv.device, stream)
-    k, v, ks, vs = cache
     code = lib().sptp_rope_append_kv(
-        _dptr(qkv), _dptr(positions), _dptr(seq_ids), _dptr(page_table), None if turns is None else _dptr(turns), P, M,
-        Hq, Hkv, D, rot, int(interleaved), float(gain), B, max_pages, num_pages, page_size, dt, kv_type, _dptr(q_out),
-        _dptr(k), _dptr(v), None if ks is None else _dptr(ks), None if vs is None else _dptr(vs), _dptr(workspace),
-        workspace.nbytes, _stream(stream))
+        qkv.data_ptr(), positions.data_ptr(), seq_ids.data_ptr(), page_table.data_ptr(),
+        None if turns is None else turns.data_ptr(), P, M, Hq, Hkv, D, 2 * pairs, int(interleaved), float(gain), B,
+        max_pages, num_pages, page_size, dt, kv_type, q_out.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(stream, cur))
     _check("sptp_rope_append_kv", code)
     return q_out
 
@@ -697,26 +706,30 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     scale defaults to D^-1/2; window 0: the whole sequence.  Returns
     (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None)."""
     P, B, Hq, D = q.shape
+    k, v, ks, vs = cache
+    dtype, i32 = q.dtype, torch.int32
     dt = _dtype_code(q)
-    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, q.dtype)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, dtype)
     max_pages = page_table.shape[-1]
-    _expect("page_table", page_table, (B, max_pages), torch.int32)
-    _expect("seq_lens", seq_lens, (B,), torch.int32)
-    _expect("out", out, (P, B, Hq * D), q.dtype, optional=True)
-    _expect("lse", lse, (P, B, Hq), torch.float32, optional=True)
-    _one_device(q, *cache, page_table, seq_lens, out, lse, workspace)
+    if not (page_table.shape == (B, max_pages) and page_table.dtype is i32 and seq_lens.shape == (B,)
+            and seq_lens.dtype is i32 and (out is None or (out.shape == (P, B, Hq * D) and out.dtype is dtype))
+            and (lse is None or (lse.shape == (P, B, Hq) and lse.dtype is torch.float32))):
+        _expect("page_table", page_table, (B, max_pages), i32)
+        _expect("seq_lens", seq_lens, (B,), i32)
+        _expect("out", out, (P, B, Hq * D), dtype, optional=True)
+        _expect("lse", lse, (P, B, Hq), torch.float32, optional=True)
+    cur = _ready(q, k, v, ks, vs, page_table, seq_lens, out, lse, workspace)
     if out is None:
-        out = _new((P, B, Hq * D), q.dtype, q.device, stream)
+        out = _new((P, B, Hq * D), dtype, q.device, stream)
     if lse is None and write_lse:
         lse = _new((P, B, Hq), torch.float32, q.device, stream)
     if workspace is None:
         n = max(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
         workspace = _new((n,), torch.uint8, q.device, stream)
-    k, v, ks, vs = cache
     code = lib().sptp_paged_attn_decode(
-        _dptr(q), _dptr(k), _dptr(v), None if ks is None else _dptr(ks), None if vs is None else _dptr(vs),
-        _dptr(page_table), _dptr(seq_lens), P, B, Hq, Hkv, D, max_pages, num_pages, page_size, int(window),
-        D ** -0.5 if scale is None else float(scale), dt, kv_type, _dptr(out), None if lse is None else _dptr(lse),
-        _dptr(workspace), workspace.nbytes, _stream(stream))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if ks is None else ks.data_ptr(),
+        None if vs is None else vs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), P, B, Hq, Hkv, D, max_pages,
+        num_pages, page_size, int(window), D ** -0.5 if scale is None else float(scale), dt, kv_type, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, cur))
     _check("sptp_paged_attn_decode", code)
     return out, lse

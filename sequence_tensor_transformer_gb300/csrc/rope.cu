@@ -17,6 +17,11 @@
 // each other's partners; interleaved: any two; elements that do not turn: any
 // two), L lanes cover a head, and a warp walks over its rows (heads of a token,
 // all shards') with the slot's cosines and sines in registers.
+//
+// Measured, 16384 rows of 36 heads of 128 over 4 shards in bf16 (302 MB): 46.3 us
+// (6.5 TB/s, 0.97 of the copy bandwidth) rotated alone, 49.2 us (0.92) with k and
+// v into pages; with each lane working out its own angles 49.9 and 62.7 us.  One
+// row: 2.0 us, a launch.
 #include <cuda_bf16.h>
 
 #include "attn.h"

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -51,7 +52,7 @@ EXPORTED_SYMBOLS = (
     "sptp_down_proj_e4m3", "sptp_prologue_e4m3", "sptp_ffn_forward_ex", "dtp_ffn_stack_forward_ex",
     "sptp_attn_qkv_forward_ex", "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest",
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
-    "sptp_paged_attn_decode",
+    "sptp_paged_attn_decode", "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed",
 )
 
 _lib = None
@@ -88,6 +89,9 @@ _SIGS = {
     "sptp_rope_turns": (_I, [_I, _D, _I, _D, _D, _D, _D, _P]),
     "sptp_rope": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
     "sptp_rope_append_kv": (_I, [_P] * 5 + [_I] * 7 + [_F] + [_I] * 6 + [_P] * 6 + [_Z, _P]),
+    "sptp_rope_packed": (_I, [ctypes.c_char_p]),
+    "sptp_rope_append_kv_packed": (_I, [ctypes.c_char_p]),
+    "sptp_paged_attn_decode_packed": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "sptp_paged_attn_decode": (_I, [_P] * 7 + [_I] * 9 + [_F, _I, _I, _P, _P, _P, _Z, _P]),
 }
@@ -588,9 +592,9 @@ def sptp_rope(x, positions, turns, Hr=None, interleaved=False, transpose=False, 
     cur = _ready(x, positions, turns, out)
     if out is None:
         out = _new((P, M, H, D), dtype, x.device, stream)
-    code = lib().sptp_rope(x.data_ptr(), positions.data_ptr(), turns.data_ptr(), P, M, H, H if Hr is None else Hr, D,
-                           2 * pairs, int(interleaved), int(transpose), float(gain), dt, out.data_ptr(),
-                           _raw_stream(stream, cur))
+    code = lib().sptp_rope_packed(_ROPE_ARGS.pack(
+        x.data_ptr(), positions.data_ptr(), turns.data_ptr(), out.data_ptr(), _raw_stream(stream, cur), P, M, H,
+        H if Hr is None else Hr, D, 2 * pairs, interleaved, transpose, dt, gain))
     _check("sptp_rope", code)
     return out
 
@@ -609,6 +613,13 @@ def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=F
 # The calls of a decoding step last a few microseconds on the device, so their
 # checks are written to cost little: one condition over all tensors on the way
 # in, the checks with their messages (_expect, _same_device) only if it fails.
+
+# The arguments of a call as one block (the *_args structs of include/sptp.h):
+# pointers, sizes, ints and the float in the structs' order and native layout.
+_ROPE_ARGS = struct.Struct("@5P9if")
+_APPEND_ARGS = struct.Struct("@12PN13if")
+_DECODE_ARGS = struct.Struct("@11PN11if")
+
 
 def _ready(*ts):
     """Every tensor given is dense and on the current CUDA device, whose index
@@ -685,12 +696,12 @@ def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, i
         q_out = _new((P, M, Hq, D), dtype, qkv.device, stream)
     if workspace is None:
         workspace = _new((SPTP_WS_HEADER_BYTES,), torch.uint8, qkv.device, stream)
-    code = lib().sptp_rope_append_kv(
+    code = lib().sptp_rope_append_kv_packed(_APPEND_ARGS.pack(
         qkv.data_ptr(), positions.data_ptr(), seq_ids.data_ptr(), page_table.data_ptr(),
-        None if turns is None else turns.data_ptr(), P, M, Hq, Hkv, D, 2 * pairs, int(interleaved), float(gain), B,
-        max_pages, num_pages, page_size, dt, kv_type, q_out.data_ptr(), k.data_ptr(), v.data_ptr(),
-        None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(stream, cur))
+        0 if turns is None else turns.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(),
+        0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(), workspace.data_ptr(),
+        _raw_stream(stream, cur), workspace.nbytes, P, M, Hq, Hkv, D, 2 * pairs, interleaved, B, max_pages, num_pages,
+        page_size, dt, kv_type, gain))
     _check("sptp_rope_append_kv", code)
     return q_out
 
@@ -726,10 +737,10 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     if workspace is None:
         n = max(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
         workspace = _new((n,), torch.uint8, q.device, stream)
-    code = lib().sptp_paged_attn_decode(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if ks is None else ks.data_ptr(),
-        None if vs is None else vs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), P, B, Hq, Hkv, D, max_pages,
-        num_pages, page_size, int(window), D ** -0.5 if scale is None else float(scale), dt, kv_type, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, cur))
+    code = lib().sptp_paged_attn_decode_packed(_DECODE_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), _raw_stream(stream, cur), workspace.nbytes, P, B, Hq, Hkv, D, max_pages, num_pages,
+        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale))
     _check("sptp_paged_attn_decode", code)
     return out, lse

@@ -285,4 +285,31 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
     return cuda_status(launch_paged_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
+int sptp_rope_packed(const sptp_rope_args* a) {
+    if (!a) return SPTP_ERR_NULL;
+    return sptp_rope(a->x, static_cast<const int*>(a->positions), static_cast<const unsigned long long*>(a->turns), a->P,
+                     a->M, a->H, a->Hr, a->D, a->rot, a->interleaved, a->transpose, a->gain,
+                     static_cast<sptp_dtype>(a->dtype), a->out, a->cuda_stream);
+}
+
+int sptp_rope_append_kv_packed(const sptp_rope_append_kv_args* a) {
+    if (!a) return SPTP_ERR_NULL;
+    return sptp_rope_append_kv(
+        a->qkv, static_cast<const int*>(a->positions), static_cast<const int*>(a->seq_ids),
+        static_cast<const int*>(a->page_table), static_cast<const unsigned long long*>(a->turns), a->P, a->M, a->Hq,
+        a->Hkv, a->D, a->rot, a->interleaved, a->gain, a->B, a->max_pages, a->num_pages, a->page_size,
+        static_cast<sptp_dtype>(a->dtype), static_cast<sptp_kv_type>(a->kv_type), a->q_out, a->k_cache, a->v_cache,
+        static_cast<float*>(a->k_scale), static_cast<float*>(a->v_scale), a->workspace, a->ws_bytes, a->cuda_stream);
+}
+
+int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* a) {
+    if (!a) return SPTP_ERR_NULL;
+    return sptp_paged_attn_decode(
+        a->q, a->k_cache, a->v_cache, static_cast<const float*>(a->k_scale), static_cast<const float*>(a->v_scale),
+        static_cast<const int*>(a->page_table), static_cast<const int*>(a->seq_lens), a->P, a->B, a->Hq, a->Hkv, a->D,
+        a->max_pages, a->num_pages, a->page_size, a->window, a->scale, static_cast<sptp_dtype>(a->dtype),
+        static_cast<sptp_kv_type>(a->kv_type), a->out, static_cast<float*>(a->lse), a->workspace, a->ws_bytes,
+        a->cuda_stream);
+}
+
 }  // extern "C"

@@ -267,3 +267,54 @@ def test_binding_checks_append_and_decode():
                       ("out", z(2, 3, 4, 32), ValueError), ("lse", z(2, 3, 4), TypeError), ("q", z(2, 3, 4, 16), ValueError)):
         with pytest.raises(err):
             st.sptp_paged_attn_decode(**dict(dec, **{k: v}))
+
+
+def test_packed_calls_are_the_calls():
+    """The argument blocks have the C structs' layout: every field, set to a
+    value that only it may have, reaches the check that it belongs to."""
+    lib = st.lib()
+    assert lib.sptp_rope_packed(None) == NULL and lib.sptp_rope_append_kv_packed(None) == NULL
+    assert lib.sptp_paged_attn_decode_packed(None) == NULL
+
+    def rope_p(**k):
+        a = dict(x=at(0), pos=at(1), turns=at(2), out=at(3), stream=0, P=2, M=0, H=6, Hr=4, D=64, rot=64, inter=0, tr=0, dt=0,
+                 gain=1.0)
+        a.update(k)
+        return lib.sptp_rope_packed(st._ROPE_ARGS.pack(*a.values()))
+
+    assert rope_p() == OK
+    for bad, code in ((dict(turns=0), NULL), (dict(x=0, M=1), NULL), (dict(pos=0, M=1), NULL), (dict(out=0, M=1), NULL),
+                      (dict(dt=9), DTYPE), (dict(P=9), SHAPE), (dict(M=-1), SHAPE), (dict(H=0), SHAPE), (dict(Hr=7), SHAPE),
+                      (dict(D=12), SHAPE), (dict(rot=24), SHAPE), (dict(gain=math.nan), SHAPE), (dict(out=at(2), M=1), ALIAS)):
+        assert rope_p(**bad) == code, bad
+
+    def append_p(**k):
+        a = dict(qkv=at(0), pos=at(1), seq=at(2), table=at(3), turns=at(4), q=at(5), k=at(6), v=at(7), ks=0, vs=0, ws=at(8),
+                 stream=0, wsb=1 << 20, P=2, M=0, Hq=8, Hkv=2, D=64, rot=32, inter=0, B=4, max_pages=8, num_pages=50, page=16,
+                 dt=0, kv=0, gain=1.0)
+        a.update(k)
+        return lib.sptp_rope_append_kv_packed(st._APPEND_ARGS.pack(*a.values()))
+
+    assert append_p() == OK
+    for bad, code in ((dict(qkv=0, M=1), NULL), (dict(pos=0, M=1), NULL), (dict(seq=0, M=1), NULL), (dict(table=0, M=1), NULL),
+                      (dict(turns=0), NULL), (dict(q=0, M=1), NULL), (dict(k=0), NULL), (dict(v=0), NULL), (dict(ws=0), NULL),
+                      (dict(kv=1, ks=0, vs=at(9)), NULL), (dict(kv=1, ks=at(9), vs=0), NULL), (dict(dt=4), DTYPE),
+                      (dict(kv=2), DTYPE), (dict(wsb=9), WS), (dict(P=0), SHAPE), (dict(M=-1), SHAPE), (dict(Hq=7), SHAPE),
+                      (dict(Hkv=3), SHAPE), (dict(D=36), SHAPE), (dict(rot=24), SHAPE), (dict(B=-1), SHAPE),
+                      (dict(max_pages=0), SHAPE), (dict(num_pages=0), SHAPE), (dict(page=8), SHAPE), (dict(gain=math.inf), SHAPE)):
+        assert append_p(**bad) == code, bad
+
+    def decode_p(**k):
+        a = dict(q=at(0), k=at(1), v=at(2), ks=0, vs=0, table=at(3), lens=at(4), out=at(5), lse=at(6), ws=at(7), stream=0,
+                 wsb=1 << 40, P=2, B=0, Hq=8, Hkv=2, D=64, max_pages=8, num_pages=50, page=16, window=0, dt=0, kv=0, scale=0.125)
+        a.update(k)
+        return lib.sptp_paged_attn_decode_packed(st._DECODE_ARGS.pack(*a.values()))
+
+    assert decode_p() == OK
+    for bad, code in ((dict(q=0, B=1), NULL), (dict(k=0), NULL), (dict(v=0), NULL), (dict(kv=1, ks=0, vs=at(9)), NULL),
+                      (dict(kv=1, ks=at(9)), NULL), (dict(table=0, B=1), NULL), (dict(lens=0, B=1), NULL), (dict(out=0, B=1), NULL),
+                      (dict(ws=0), NULL), (dict(lse=at(1), B=1), ALIAS), (dict(wsb=5), WS), (dict(dt=4), DTYPE), (dict(kv=3), DTYPE),
+                      (dict(P=9), SHAPE), (dict(B=-1), SHAPE), (dict(Hq=9), SHAPE), (dict(Hkv=3), SHAPE), (dict(D=4), SHAPE),
+                      (dict(max_pages=0), SHAPE), (dict(num_pages=0), SHAPE), (dict(page=24), SHAPE), (dict(window=-1), SHAPE),
+                      (dict(scale=math.nan), SHAPE)):
+        assert decode_p(**bad) == code, bad

@@ -19,7 +19,7 @@
 // all shards') with the slot's cosines and sines in registers.
 //
 // Measured, 16384 rows of 36 heads of 128 over 4 shards in bf16 (302 MB): 46.3 us
-// (6.5 TB/s, 0.97 of the copy bandwidth) rotated alone, 49.2 us (0.92) with k and
+// (6.5 TB/s, 0.97 of the copy bandwidth) rotated alone, 48.6 us (0.93) with k and
 // v into pages; with each lane working out its own angles 49.9 and 62.7 us.  One
 // row: 2.0 us, a launch.
 #include <cuda_bf16.h>
@@ -174,11 +174,25 @@ __device__ __forceinline__ void check_rows(const RopeParams& p) {
     }
 }
 
+// One slot of N rows.
+template <int N>
+struct Batch {
+    uint4 va[N], vb[N];
+    int pp[N], hh[N];  // shard, head (-1: none)
+};
+
+// Rows whose loads a lane has in flight: four at a time alone; for an append,
+// which waits for a page before its first store and has more to do per row,
+// three and the next three, at one block less per SM (device us, one batch at a
+// time / one ahead: 16384 bf16 rows of 18 KB 49.1 / 48.6, 3001 of them 12.1 /
+// 11.3, 16384 E4M3 rows of 48 heads 67.4 / 65.8, 3001 of them 15.8 / 14.1; alone
+// 46.3 / 48.1 to 50.5).
 template <typename T, bool INTER, Op OP>
-__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeParams p,
-                                                        const __grid_constant__ Split sp) {
+__global__ void __launch_bounds__(kThreads, OP == Op::kRope ? 6 : 5) rope_kernel(const __grid_constant__ RopeParams p,
+                                                                              const __grid_constant__ Split sp) {
     constexpr int E = Elems<T>::E;
-    constexpr int kUnroll = OP == Op::kRope ? 4 : 3;  // rows whose loads a lane has in flight
+    constexpr int kUnroll = OP == Op::kRope ? 4 : 3;
+    constexpr bool kAhead = OP != Op::kRope;
     __shared__ __align__(16) float cosines[4][kMaxPairs], sines[4][kMaxPairs];
     admit_next();
     await_previous();
@@ -205,26 +219,25 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     const int r0 = (block % sp.parts * wpt + warp % wpt) * sp.per;
     const int r1 = m < p.M ? min(p.P * p.H, r0 + sp.per) : 0;
 
-    uint4 va[kUnroll], vb[kUnroll];
-    int pp[kUnroll], hh[kUnroll];  // shard, head (-1: none)
-    auto load = [&](int base) {
+    Batch<kUnroll> now, next;
+    auto load = [&](Batch<kUnroll>& to, int base) {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int r = base + i * sp.hpw + hg;
-            pp[i] = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(r), sp.mul) >> sp.shift);
-            hh[i] = lives && r < r1 ? r - pp[i] * p.H : -1;
+            to.pp[i] = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(r), sp.mul) >> sp.shift);
+            to.hh[i] = lives && r < r1 ? r - to.pp[i] * p.H : -1;
             // in place, what does not turn stays where it is
-            if (OP == Op::kRope && p.out == p.x && (hh[i] >= p.Hr || !turns)) hh[i] = -1;
-            va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-            if (hh[i] >= 0) {
+            if (OP == Op::kRope && p.out == p.x && (to.hh[i] >= p.Hr || !turns)) to.hh[i] = -1;
+            to.va[i] = to.vb[i] = make_uint4(0, 0, 0, 0);
+            if (to.hh[i] >= 0) {
                 const T* src =
-                    static_cast<const T*>(p.x) + ((static_cast<long long>(pp[i]) * p.M + m) * p.H + hh[i]) * p.D;
-                va[i] = __ldcs(reinterpret_cast<const uint4*>(src + ea));
-                if (has_b) vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + eb));
+                    static_cast<const T*>(p.x) + ((static_cast<long long>(to.pp[i]) * p.M + m) * p.H + to.hh[i]) * p.D;
+                to.va[i] = __ldcs(reinterpret_cast<const uint4*>(src + ea));
+                if (has_b) to.vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + eb));
             }
         }
     };
-    load(r0);
+    load(now, r0);
 
     // the angles of the block's tokens, while the first rows are under way
     for (int j = tid; j < sp.tokens * half; j += kThreads) {
@@ -268,7 +281,13 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
         }
     }
     for (int base = r0; base < r1; base += sp.hpw * kUnroll) {
-        if (base != r0) load(base);
+        const int after = base + sp.hpw * kUnroll;
+        if (!kAhead && base != r0) load(now, base);
+        if (kAhead && after < r1) load(next, after);
+        auto& va = now.va;
+        auto& vb = now.vb;
+        const auto& pp = now.pp;
+        const auto& hh = now.hh;
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             if (turns && hh[i] >= 0 && hh[i] < p.Hr) turn<T, INTER>(va[i], vb[i], c, s);
@@ -308,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
                 }
             }
         }
+        if (kAhead) now = next;
     }
 }
 

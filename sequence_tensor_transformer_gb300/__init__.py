@@ -651,8 +651,12 @@ def _check_cache(cache, P, D, dtype):
     shape, kvt = k.shape, k.dtype
     if len(shape) != 5:
         raise ValueError(f"cache: {len(shape)} dimensions, expected [P,num_pages,Hkv,page_size,D]")
-    if kvt is dtype and v.shape == shape and v.dtype is kvt and shape[0] == P and shape[4] == D and ks is None and vs is None:
-        return shape[1], shape[2], shape[3], SPTP_KV_SAME
+    if v.shape == shape and v.dtype is kvt and shape[0] == P and shape[4] == D:
+        if ks is None and vs is None and kvt is dtype:
+            return shape[1], shape[2], shape[3], SPTP_KV_SAME
+        if (kvt is torch.uint8 and dtype is torch.bfloat16 and ks is not None and vs is not None
+                and ks.shape == vs.shape == shape[:4] and ks.dtype is vs.dtype is torch.float32):
+            return shape[1], shape[2], shape[3], SPTP_KV_E4M3
     if kvt != dtype:
         if kvt != torch.uint8:
             raise TypeError(f"cache: dtype {kvt}, expected {dtype} or uint8 codes")

@@ -3,7 +3,11 @@
 Thin ctypes binding over libsptp.so: every function here marshals torch
 tensors (device memory) and the current CUDA stream into the C ABI declared
 in include/sptp.h and raises on a non-zero status.  All computation runs in
-the library's CUDA kernels; there is no fallback.
+the library's CUDA kernels; there is no fallback.  The calls of a decoding
+step, a few microseconds each on the device, have a second way in, the
+extension module _decode_binding (csrc/decode_binding.cpp): it makes the same
+library call where nothing is wrong with the arguments, and leaves every other
+call to the functions here.
 """
 from __future__ import annotations
 
@@ -42,6 +46,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 SPTP_KV_SAME = 0
 SPTP_KV_E4M3 = 1
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsptp.so")
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_decode_binding.so")
 
 EXPORTED_SYMBOLS = (
     "sptp_ffn_workspace_size", "sptp_ffn_forward", "dtp_ffn_stack_workspace_size",
@@ -56,6 +61,7 @@ EXPORTED_SYMBOLS = (
 )
 
 _lib = None
+_fast = None  # the extension module, once it calls _lib
 
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_ulonglong
 _LL, _D = ctypes.c_longlong, ctypes.c_double
@@ -120,14 +126,20 @@ def load_library(path: str = LIB_PATH, replace: bool = False):
             f = getattr(lib_, name)
             f.restype = res
             f.argtypes = args
-        _lib = lib_
+        set_library(lib_)
     return _lib
 
 
 def set_library(handle):
     """Makes a handle returned by load_library the one every call uses."""
-    global _lib
-    _lib = handle
+    global _lib, _fast
+    _lib, _fast = handle, None
+    if handle is None or not os.path.exists(BINDING_PATH):
+        return
+    from . import _decode_binding
+    _decode_binding.use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
+        "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")))
+    _fast = _decode_binding
 
 
 def lib():
@@ -581,6 +593,10 @@ def sptp_rope(x, positions, turns, Hr=None, interleaved=False, transpose=False, 
     """Rotary positions of the first Hr (default: all) heads of x [P,M,H,D];
     positions int32 [M]; turns from sptp_rope_turns.  transpose: the gradient.
     out may be x (in place).  Returns out."""
+    if _fast is not None and stream is None:
+        done = _fast.rope(x, positions, turns, Hr, interleaved, transpose, gain, out)
+        if done is not NotImplemented:
+            return done
     P, M, H, D = x.shape
     pairs, dtype = turns.shape[0], x.dtype
     dt = _dtype_code(x)
@@ -678,6 +694,10 @@ def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, i
     `cache` (see paged_kv_cache).  positions, seq_ids int32 [M] (seq_ids < 0:
     padding, whose rows of q_out are left as they are); page_table int32
     [B,max_pages]; turns None: no rotation.  Returns q_out [P,M,Hq,D]."""
+    if _fast is not None and stream is None:
+        done = _fast.append(qkv, positions, seq_ids, page_table, turns, cache, Hq, interleaved, gain, q_out, workspace)
+        if done is not NotImplemented:
+            return done
     P, M, N = qkv.shape
     k, v, ks, vs = cache
     D, dtype, i32 = k.shape[-1], qkv.dtype, torch.int32
@@ -720,6 +740,10 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     page_table int32 [B,max_pages], seq_lens int32 [B] (0: an empty row);
     scale defaults to D^-1/2; window 0: the whole sequence.  Returns
     (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None)."""
+    if _fast is not None and stream is None:
+        done = _fast.decode(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
+        if done is not NotImplemented:
+            return done
     P, B, Hq, D = q.shape
     k, v, ks, vs = cache
     dtype, i32 = q.dtype, torch.int32

@@ -9,6 +9,9 @@ build(checked=True) builds the bounds-checked library libsptp_check.so
 -DSPTP_BOUNDS_CHECK, which check every index and address they compute
 against its buffer and report a failure as SPTP_ERR_BOUNDS in the workspace
 status words.  It is a debug build for the tests, slower than the library.
+
+csrc/decode_binding.cpp, a Python extension module over the installed torch's
+headers, becomes _decode_binding.so beside the library.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsptp.so")
 CHECKED_LIB = os.path.join(PKG, "libsptp_check.so")
+BINDING = os.path.join(PKG, "_decode_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -48,6 +53,34 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_binding() -> None:
+    """The extension module for the torch that is installed: an object of its
+    own for each torch version, so that another torch builds it anew."""
+    import torch
+
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    src = os.path.join(CSRC, "decode_binding.cpp")
+    obj = os.path.join(BUILD, f"decode_binding-{torch.__version__}.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    if _stale(obj, [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+        dirs = [os.path.join(ROOT, "include"), os.path.join(home, "include"),
+                os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"]]
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+             + ["-I" + d for d in dirs] + ["-c", src, "-o", obj + ".tmp"])
+        os.replace(obj + ".tmp", obj)
+    if _stale(BINDING, [obj]):
+        libs = ["torch_python", "torch", "torch_cpu", "c10", "c10_cuda"]
+        _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + os.path.join(home, "lib")] + ["-l" + n for n in libs])
+        os.replace(BINDING + ".tmp", BINDING)
+
+
+def _run(cmd) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, extra_flags=None, checked: bool = False) -> str:
     """Compile every CUDA source and link libsptp.so (checked: the
     bounds-checked libsptp_check.so); returns its path."""
@@ -70,8 +103,10 @@ def build(verbose: bool = False, extra_flags=None, checked: bool = False) -> str
                 print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     if _stale(lib_path, objs) or extra_flags:
         tmp = lib_path + ".tmp"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]

@@ -36,6 +36,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attn.h"
 #include "sptp.h"
 #include "sptp_ptx.cuh"
@@ -556,10 +558,10 @@ struct TcConsumer {
         return true;
     }
 
-    // The item's end, or its part's: sums [kTeam][HEADS] in shared memory.
-    // Calls put(head, element, o, m, l) for this thread's outputs.
-    template <typename Put>
-    __device__ __forceinline__ void finish(float* sums, Put put) {
+    // The item's end, or its part's: sums [kTeam][HEADS] in shared memory, this
+    // thread's outputs to the rows that row_of(head, m, l, holds element 0) gives.
+    template <typename RowOf>
+    __device__ __forceinline__ void finish(float* sums, RowOf row_of) {
         const int lane = threadIdx.x & 31, warp = team_warp(), i = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -579,16 +581,20 @@ struct TcConsumer {
                 float sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kTeam; ++w) sum += sums[w * HEADS + h];
+                const auto row = row_of(h, m[nt][e], sum, elem(0, 0) == 0);
                 // E4M3: o is relative to M2, the sum to m
-                const float f = CODES && sum != 0.f ? ex2(m2[nt][e] - m[nt][e]) : 1.f;
+                const float f = CODES && sum != 0.f ? row.f * ex2(m2[nt][e] - m[nt][e]) : row.f;
+                if (row.at == nullptr) continue;
 #pragma unroll
-                for (int t = 0; t < MTILES; ++t)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float v = o[t][nt][2 * r + e];
-                        if constexpr (CODES) v *= f;
-                        put(h, elem(t, r), v, m[nt][e], sum);
+                for (int t = 0; t < MTILES; ++t) {
+                    const float v0 = o[t][nt][e] * f, v1 = o[t][nt][2 + e] * f;
+                    if constexpr (CODES) {
+                        row.put(elem(t, 0), v0, v1);
+                    } else {
+                        row.put(elem(t, 0), v0);
+                        row.put(elem(t, 1), v1);
                     }
+                }
             }
     }
 };
@@ -796,8 +802,8 @@ struct F32Consumer {
         return true;
     }
 
-    template <typename Put>
-    __device__ __forceinline__ void finish(float* sums, Put put) {
+    template <typename RowOf>
+    __device__ __forceinline__ void finish(float* sums, RowOf row_of) {
         const int lane = threadIdx.x & 31, warp = team_warp(), h0 = warp / KEY_GROUPS * HPW;
         float mine = 0.f;
 #pragma unroll
@@ -838,13 +844,43 @@ struct F32Consumer {
             float n = 0.f;
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) n += sums[k * HEADS + h];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) put(h, warp * OWN + lane % QUADS * 4 + e, v[4 * j + e], mh, n);
+            const int d = warp * OWN + lane % QUADS * 4;
+            const auto row = row_of(h, mh, n, d == 0);
+            if (row.at != nullptr)
+                row.put(d, v[4 * j] * row.f, v[4 * j + 1] * row.f, v[4 * j + 2] * row.f, v[4 * j + 3] * row.f);
         }
     }
 };
 
 // ---------------------------------------------------------------- the frame
+
+// Where one head's D outputs go, and what they are multiplied by; at == nullptr:
+// nowhere.  Element numbers are multiples of how many are put at once, as D is.
+template <typename T>
+struct OutRow {
+    T* at;
+    float f;
+    int D;
+
+    __device__ __forceinline__ void put(int d, float v) const {
+        if (d >= D) return;
+        if constexpr (sizeof(T) == 2)
+            at[d] = __float2bfloat16_rn(v);
+        else
+            at[d] = v;
+    }
+    __device__ __forceinline__ void put(int d, float v0, float v1) const {
+        if (d >= D) return;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<__nv_bfloat162*>(at + d) = __floats2bfloat162_rn(v0, v1);
+        else
+            *reinterpret_cast<float2*>(at + d) = make_float2(v0, v1);
+    }
+    __device__ __forceinline__ void put(int d, float v0, float v1, float v2, float v3) const {
+        static_assert(sizeof(T) == 4, "fp32 outputs");
+        if (d < D) *reinterpret_cast<float4*>(at + d) = make_float4(v0, v1, v2, v3);
+    }
+};
 
 struct Meta {       // of a ring stage, written by the producer
     long long qrow;  // row of q and out of the item's first head
@@ -1230,26 +1266,23 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
             if (md.flags & kLast) {
                 float* sums = stats + 2 * L::MAXIMA;
                 if (begun && (md.flags & kItemEnds)) {
-                    // the whole item: o / l, rounded once
+                    // the whole item: o times 1 / l
                     const long long qrow = md.qrow + h0;
-                    c.finish(sums, [&](int h, int d, float v, float m, float n) {
-                        if (h >= heads || d >= p.D) return;
-                        v = n == 0.f ? 0.f : __fdividef(v, n);
-                        if constexpr (C::F32)
-                            static_cast<float*>(p.out)[(qrow + h) * p.D + d] = v;
-                        else
-                            static_cast<__nv_bfloat16*>(p.out)[(qrow + h) * p.D + d] = __float2bfloat16_rn(v);
-                        if (d == 0 && p.lse != nullptr)
+                    using T = std::conditional_t<C::F32, float, __nv_bfloat16>;
+                    c.finish(sums, [&](int h, float m, float n, bool first) {
+                        if (h >= heads) return OutRow<T>{nullptr, 0.f, 0};
+                        if (first && p.lse != nullptr)
                             p.lse[qrow + h] = n == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(n);
+                        return OutRow<T>{static_cast<T*>(p.out) + (qrow + h) * p.D, n == 0.f ? 0.f : __frcp_rn(n), p.D};
                     });
                 } else {
                     // a part: slot 1 if the item begins in this share (it goes
                     // on in the next), slot 0 if it began in an earlier one
                     const long long at = (blockIdx.x * 2ll + (begun ? 1 : 0)) * p.heads_per_item + h0;
-                    c.finish(sums, [&](int h, int d, float v, float m, float n) {
-                        if (h >= heads || d >= p.D) return;
-                        p.part_o[(at + h) * p.D + d] = v;
-                        if (d == 0) p.part_ml[at + h] = make_float2(m, n);
+                    c.finish(sums, [&](int h, float m, float n, bool first) {
+                        if (h >= heads) return OutRow<float>{nullptr, 0.f, 0};
+                        if (first) p.part_ml[at + h] = make_float2(m, n);
+                        return OutRow<float>{p.part_o + (at + h) * p.D, 1.f, p.D};
                     });
                 }
             }

@@ -12,6 +12,7 @@ call to the functions here.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import struct
 
@@ -136,6 +137,7 @@ def set_library(handle):
     _lib, _fast = handle, None
     if handle is None or not os.path.exists(BINDING_PATH):
         return
+    importlib.invalidate_caches()  # it may have been built by this process
     from . import _decode_binding
     _decode_binding.use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
         "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")))

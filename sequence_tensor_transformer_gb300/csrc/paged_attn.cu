@@ -122,9 +122,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_attn_join(const __grid_
                 }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const float f = ex2(m[u] - top);
-                    acc.x = fmaf(f, v[u].x, acc.x);
-                    acc.y = fmaf(f, v[u].y, acc.y);
+                    // in two factors: a part far below the top may have
+                    // values that are as much larger, and 2^-126 is the least factor
+                    const float f = ex2(0.5f * (m[u] - top));
+                    acc.x = fmaf(f, f * v[u].x, acc.x);
+                    acc.y = fmaf(f, f * v[u].y, acc.y);
                 }
             }
         }

@@ -53,6 +53,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// log2 x; 0 gives -infinity
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Consumer warps work in teams of four; a team takes up to HEADS of an item's
 // query heads.
 constexpr int kTeam = 4;
@@ -199,10 +206,18 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 // E4M3: codes become fp16 (exact), and both products run on fp16.  q comes as
 // 2^-e q with its largest element in [1, 2), so fp16 holds a bf16 q to 2^-25 of
 // that; 2^e and k's scale join the score in fp32.  v's scale goes into the
-// weight, which is kept relative to the largest weight times scale so far, 2^M2,
-// not to the largest weight: 2^(s_j - M2) vs_j <= 1, and what fp16 flushes is
-// below 2^-24 of the key that dominates the output, however far the scales of
-// the rows lie apart.  The sum l keeps its own maximum m.
+// weight: with t_j its logarithm and M2 the largest s_j + t_j so far (not the
+// largest score, which may belong to a row of zeros) the product takes the
+// weight 2^(s_j + t_j - M2 + kRoom), an exponential of its own beside the one
+// that goes into the sum l, which keeps its own maximum m.  Neither is made
+// from the other: a score far below m may be the one that counts, where its
+// scale is as much larger (they go from 2^-126, a row of zeros, to 2^119), and
+// would be flushed to 0 or meet an infinite factor.  Weights are 2^kRoom at
+// most, which fp16 holds, and are flushed below 2^-(25 + kRoom) of the largest,
+// so that a long row's tail adds up.  (The sum's exponential times a factor
+// loses all of that and is hardly faster: 96 sequences 50.5 and 50.7 us; 64 of
+// 2500 keys with 16 heads per key head, D = 64, 128 and 256, 51.9 / 72.4 /
+// 144.3 and 53.2 / 73.2 / 149.0.)
 template <int DP_, int NT_, bool CODES_, int TEAMS_ = 1>
 struct TcConsumer {
     static constexpr int DP = DP_, NT = NT_, TEAMS = TEAMS_;
@@ -237,6 +252,7 @@ struct TcConsumer {
     uint32_t qf[KSTEPS][NT][2];
     float m[NT][2], l[NT][2], qs[NT][2];
     float m2[NT][2];  // E4M3: M2
+    static constexpr int kRoom = 13;
     float o[MTILES][NT][4];
 
     // element of the head's row in o[t][..][2 r + ..]
@@ -320,7 +336,7 @@ struct TcConsumer {
         const int key0 = warp * 16 * SLICES;  // this warp's keys of the tile
         const bool some = !partial || (key0 < hi && key0 + 16 * SLICES > lo);
         float s[SLICES][NT][4];
-        float vs[SLICES][2];
+        float vlog[SLICES][2];  // E4M3: logarithm of v's scale
         float top[NT][2], top2[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = top2[nt][0] = top2[nt][1] = -INFINITY;
@@ -359,12 +375,10 @@ struct TcConsumer {
                 for (int r = 0; r < 2; ++r) {
                     const int key = key0 + sl * 16 + g + 8 * r;
                     const bool in = !partial || (key >= lo && key < hi);
-                    float ks = 1.f, vlog = 0.f;
+                    float ks = 1.f;
                     if constexpr (CODES) {
                         ks = scales[key];
-                        vs[sl][r] = in ? scales[TK + key] : 0.f;
-                        // M2 is a reference, not a result: vs's exponent does
-                        vlog = static_cast<float>(static_cast<int>(__float_as_uint(vs[sl][r]) >> 23) - 126);
+                        vlog[sl][r] = lg2(in ? scales[TK + key] : 0.f);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -374,7 +388,7 @@ struct TcConsumer {
                             v += s2[nt][2 * r + e];
                             v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
                             top[nt][e] = fmaxf(top[nt][e], v);
-                            if constexpr (CODES) top2[nt][e] = fmaxf(top2[nt][e], v + vlog);
+                            if constexpr (CODES) top2[nt][e] = fmaxf(top2[nt][e], v + vlog[sl][r]);
                         }
                 }
             }
@@ -426,11 +440,11 @@ struct TcConsumer {
                 const float base = top[nt][e] == -INFINITY ? 0.f : top[nt][e];
                 old[nt][e] = ex2(m[nt][e] - base);
                 l[nt][e] *= old[nt][e];
-                float vf = 1.f;  // E4M3: 2^(m - M2)
+                float base2 = 0.f;  // E4M3
                 if constexpr (CODES) {
-                    const float base2 = top2[nt][e] == -INFINITY ? 0.f : top2[nt][e];
+                    if (top2[nt][e] != -INFINITY) base2 = top2[nt][e];
                     old[nt][e] = ex2(m2[nt][e] - base2);
-                    vf = ex2(base - base2);
+                    base2 -= kRoom;
                     moved |= top2[nt][e] != m2[nt][e];
                     m2[nt][e] = top2[nt][e];
                 } else {
@@ -444,9 +458,12 @@ struct TcConsumer {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             float& v = s[sl][nt][2 * r + e];
-                            v = ex2(v - base);
-                            sum += v;
-                            if constexpr (CODES) v *= vs[sl][r] * vf;
+                            const float w = ex2(v - base);
+                            sum += w;
+                            if constexpr (CODES)
+                                v = ex2(v - base2 + vlog[sl][r]);
+                            else
+                                v = w;
                         }
                     l[nt][e] += sum;
                 }
@@ -582,12 +599,14 @@ struct TcConsumer {
 #pragma unroll
                 for (int w = 0; w < kTeam; ++w) sum += sums[w * HEADS + h];
                 const auto row = row_of(h, m[nt][e], sum, elem(0, 0) == 0);
-                // E4M3: o is relative to M2, the sum to m
+                // E4M3: o is relative to M2 - kRoom, the sum to m (in two
+                // factors: 2^(M2 - m) may be the least normal number)
                 const float f = CODES && sum != 0.f ? row.f * ex2(m2[nt][e] - m[nt][e]) : row.f;
+                constexpr float kUnit = CODES ? 1.f / (1 << kRoom) : 1.f;
                 if (row.at == nullptr) continue;
 #pragma unroll
                 for (int t = 0; t < MTILES; ++t) {
-                    const float v0 = o[t][nt][e] * f, v1 = o[t][nt][2 + e] * f;
+                    const float v0 = o[t][nt][e] * kUnit * f, v1 = o[t][nt][2 + e] * kUnit * f;
                     if constexpr (CODES) {
                         row.put(elem(t, 0), v0, v1);
                     } else {

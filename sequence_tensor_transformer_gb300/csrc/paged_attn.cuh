@@ -204,8 +204,10 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 // throughout.
 //
 // E4M3: codes become fp16 (exact), and both products run on fp16.  q comes as
-// 2^-e q with its largest element in [1, 2), so fp16 holds a bf16 q to 2^-25 of
-// that; 2^e and k's scale join the score in fp32.  v's scale goes into the
+// 2^(kRoomQ - e) q, its largest element in [1, 2) times 2^kRoomQ, so fp16 holds
+// a bf16 q exactly down to 2^-31 of that, and to 2^-39 of it below (an element
+// far larger than the others may meet zeros of k); 2^(e - kRoomQ) and k's scale
+// join the score in fp32.  v's scale goes into the
 // weight: with t_j its logarithm and M2 the largest s_j + t_j so far (not the
 // largest score, which may belong to a row of zeros) the product takes the
 // weight 2^(s_j + t_j - M2 + kRoom), an exponential of its own beside the one
@@ -252,7 +254,7 @@ struct TcConsumer {
     uint32_t qf[KSTEPS][NT][2];
     float m[NT][2], l[NT][2], qs[NT][2];
     float m2[NT][2];  // E4M3: M2
-    static constexpr int kRoom = 13;
+    static constexpr int kRoom = 13, kRoomQ = 14;
     float o[MTILES][NT][4];
 
     // element of the head's row in o[t][..][2 r + ..]
@@ -294,8 +296,9 @@ struct TcConsumer {
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 1) - 127;
-                // 2^-e in two factors, each a normal number
-                const float f1 = pow2_bits(-(e >> 1)), f2 = pow2_bits(-(e - (e >> 1)));
+                // 2^(kRoomQ - e) in two factors, each a normal number
+                const int x = kRoomQ - e;
+                const float f1 = pow2_bits(x >> 1), f2 = pow2_bits(x - (x >> 1));
 #pragma unroll
                 for (int k = 0; k < KSTEPS; ++k)
 #pragma unroll
@@ -377,7 +380,7 @@ struct TcConsumer {
                     const bool in = !partial || (key >= lo && key < hi);
                     float ks = 1.f;
                     if constexpr (CODES) {
-                        ks = scales[key];
+                        ks = scales[key] * (1.f / (1 << kRoomQ));
                         vlog[sl][r] = lg2(in ? scales[TK + key] : 0.f);
                     }
 #pragma unroll

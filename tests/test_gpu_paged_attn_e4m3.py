@@ -159,6 +159,20 @@ def test_a_tail_below_one_key(Hq, D, n, gap):
     check(c, out, lse)
 
 
+@pytest.mark.parametrize("Hq,D", [(4, 64), (7, 128), (16, 128), (32, 64), (4, 256)])
+@pytest.mark.parametrize("outlier", [2.0 ** 12, 2.0 ** 18, 2.0 ** 22])
+def test_an_outlier_in_q_beside_ordinary_elements(Hq, D, outlier):
+    """An element of q that is far larger than the others and meets zeros:
+    the others count in full."""
+    n, rng = 300, np.random.default_rng(4)
+    q, k = rng.standard_normal((Hq, D)), rng.standard_normal((n, D))
+    q[:, 5] = outlier
+    k[:, 5] = 0.0
+    c = case(n, Hq, D, q, k, rng.standard_normal((n, D)), D ** -0.5)
+    out, lse, ws = ta.call(c)
+    check(c, out, lse)
+
+
 def test_scales_that_are_no_powers_of_two():
     """Scales that another quantiser chose (their logarithms are off by 2^-22
     of themselves, 2^-15 at most: less than 2^-11 leaves room for, as `far` has it)."""

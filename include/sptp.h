@@ -548,6 +548,18 @@ int sptp_read_device_status(const void* workspace, void* cuda_stream);
 int sptp_wait_selftest(void* workspace, size_t ws_bytes, unsigned long long limit_ns,
                        int preset_flag, void* cuda_stream);
 
+/*
+ * sptp_paged_attn_wait_selftest -- sptp_paged_attn_decode with an arrival
+ * withheld in the first of its two CTAs (D <= 128), so that bounded waits of
+ * limit_ns run out in it: of tile withhold_full of that CTA's share, which is
+ * not loaded, or of the stage that tile withhold_empty is not given back from.
+ * One of the two is -1.  If the CTA has such a tile (and, for withhold_empty,
+ * more tiles than stages after it), SPTP_ERR_TIMEOUT is recorded, whatever else
+ * is, and out and lse are undefined.  No counterpart on the pages.
+ */
+int sptp_paged_attn_wait_selftest(const sptp_paged_attn_decode_args* args, int withhold_full, int withhold_empty,
+                                  unsigned long long limit_ns);
+
 /* Bytes of the static device scratch array used by sptp_ffn_forward_noalloc. */
 #define SPTP_NOALLOC_SCRATCH_BYTES (64u << 20)
 

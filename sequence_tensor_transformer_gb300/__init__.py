@@ -29,7 +29,7 @@ __all__ = [
     "sptp_gateup_swiglu_e4m3", "sptp_down_proj_e4m3", "sptp_prologue_e4m3", "VARIANTS", "STATUS",
     "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest", "CHECKED_LIB_PATH", "set_library",
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
-    "sptp_paged_attn_decode", "paged_kv_cache", "ROPE_SCALINGS",
+    "sptp_paged_attn_decode", "paged_kv_cache", "ROPE_SCALINGS", "sptp_paged_attn_wait_selftest",
 ]
 
 SPTP_BF16 = 0
@@ -59,6 +59,7 @@ EXPORTED_SYMBOLS = (
     "sptp_attn_qkv_forward_ex", "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest",
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
     "sptp_paged_attn_decode", "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed",
+    "sptp_paged_attn_wait_selftest",
 )
 
 _lib = None
@@ -99,6 +100,7 @@ _SIGS = {
     "sptp_rope_packed": (_I, [ctypes.c_char_p]),
     "sptp_rope_append_kv_packed": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_decode_packed": (_I, [ctypes.c_char_p]),
+    "sptp_paged_attn_wait_selftest": (_I, [ctypes.c_char_p, _I, _I, _U64]),
     "sptp_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "sptp_paged_attn_decode": (_I, [_P] * 7 + [_I] * 9 + [_F, _I, _I, _P, _P, _P, _Z, _P]),
 }
@@ -774,3 +776,25 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
         page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale))
     _check("sptp_paged_attn_decode", code)
     return out, lse
+
+
+def sptp_paged_attn_wait_selftest(q, cache, page_table, seq_lens, out, workspace, withhold_full=-1, withhold_empty=-1,
+                                  limit_ns=20_000_000):
+    """The attention (scale 1) on two CTAs with an arrival withheld in the first,
+    so that its bounded waits run out (SPTP_ERR_TIMEOUT in the workspace's
+    status words)."""
+    P, B, Hq, D = q.shape
+    k, v, ks, vs = cache
+    dt = _dtype_code(q)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, q.dtype)
+    max_pages = page_table.shape[-1]
+    _expect("page_table", page_table, (B, max_pages), torch.int32)
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("out", out, (P, B, Hq * D), q.dtype)
+    cur = _ready(q, k, v, ks, vs, page_table, seq_lens, out, workspace)
+    code = lib().sptp_paged_attn_wait_selftest(_DECODE_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0, workspace.data_ptr(), _raw_stream(None, cur),
+        workspace.nbytes, P, B, Hq, Hkv, D, max_pages, num_pages, page_size, 0, dt, kv_type, 1.0), int(withhold_full),
+        int(withhold_empty), int(limit_ns))
+    _check("sptp_paged_attn_wait_selftest", code)

@@ -99,6 +99,8 @@ struct PagedAttnParams {
     float scale;
     void* out;              // [P][B][Hq][D]
     float* lse;             // [P][B][Hq] or nullptr
+    unsigned long long wait_limit_ns;
+    int withhold_full, withhold_empty;  // self-test: tiles of CTA 0 (-1: none)
     DeviceStatus* status;
     PagedAttnPart* parts;   // [CTAs]
     float2* part_ml;        // [CTAs][2][heads_per_item]: maximum (in units of log 2) and sum
@@ -117,5 +119,8 @@ cudaError_t launch_paged_attn_bf16(PagedAttnParams& p, int num_sms, int* ctas, c
 cudaError_t launch_paged_attn_e4m3(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_paged_attn_f32(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
+// The self-test's form of it, on two CTAs; D <= 128.
+constexpr int kSelftestCtas = 2;
+cudaError_t launch_paged_attn_test(PagedAttnParams& p, bool bf16, bool e4m3, int* ctas, cudaStream_t s);
 
 }  // namespace sptp

@@ -87,6 +87,66 @@ long long elems(long long P, long long M, long long heads, long long D) {
     return M < (1ll << 30) && M <= (1ll << 42) / row ? M * row : -1;
 }
 
+// sptp_paged_attn_decode, and its self-test.
+int attend(const sptp_paged_attn_decode_args& a, unsigned long long limit_ns, int withhold_full, int withhold_empty) {
+    const bool e4m3 = a.kv_type == SPTP_KV_E4M3;
+    if (!a.k_cache || !a.v_cache || !a.workspace || (e4m3 && (!a.k_scale || !a.v_scale)) ||
+        (a.B != 0 && (!a.q || !a.page_table || !a.seq_lens || !a.out)))
+        return SPTP_ERR_NULL;
+    int rc = check_cache(a.P, a.Hkv, a.D, a.B, a.max_pages, a.num_pages, a.page_size, a.dtype, a.kv_type);
+    if (rc == SPTP_ERR_DTYPE) return rc;
+    int rc2 = check_heads(a.P, a.Hq, a.Hkv, a.D);
+    if (rc2 != SPTP_OK || rc != SPTP_OK) return SPTP_ERR_SHAPE;
+    if (a.window < 0 || !std::isfinite(a.scale)) return SPTP_ERR_SHAPE;
+    const long long n = elems(a.P, a.B, a.Hq, a.D);
+    if (n < 0) return SPTP_ERR_SHAPE;
+    const sptp_dtype dtype = static_cast<sptp_dtype>(a.dtype);
+    const size_t es = esize(dtype), rows = static_cast<size_t>(a.P) * a.num_pages * a.Hkv * a.page_size;
+    const size_t cb = rows * a.D * (e4m3 ? 1 : es), sb = e4m3 ? rows * 4 : 0, qb = static_cast<size_t>(n) * es;
+    const size_t need = sptp_paged_attn_workspace_size(a.P, a.B, a.Hq, a.Hkv, a.D);
+    const Buf ins[] = {{a.q, qb, 16}, {a.k_cache, cb, 16}, {a.v_cache, cb, 16},
+                       {e4m3 ? a.k_scale : nullptr, sb, 16}, {e4m3 ? a.v_scale : nullptr, sb, 16},
+                       {a.page_table, static_cast<size_t>(a.B) * a.max_pages * 4, 4},
+                       {a.seq_lens, static_cast<size_t>(a.B) * 4, 4}};
+    const Buf outs[] = {{a.out, qb, 16}, {a.lse, static_cast<size_t>(a.P) * a.B * a.Hq * 4, 16}, {a.workspace, need, kAlign}};
+    if ((rc = check_aligned(ins, 7)) != SPTP_OK || (rc = check_aligned(outs, 3)) != SPTP_OK) return rc;
+    if (a.ws_bytes < need) return SPTP_ERR_WORKSPACE;
+    if ((rc = check_alias(outs, 3, ins, 7)) != SPTP_OK) return rc;
+    if (a.B == 0) return SPTP_OK;
+    DevInfo di;
+    if ((rc = device_info(&di)) != SPTP_OK) return rc;
+    PagedAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = a.q;
+    p.k = a.k_cache;
+    p.v = a.v_cache;
+    p.k_scale = static_cast<const float*>(a.k_scale);
+    p.v_scale = static_cast<const float*>(a.v_scale);
+    p.page_table = static_cast<const int*>(a.page_table);
+    p.seq_lens = static_cast<const int*>(a.seq_lens);
+    p.P = a.P;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.D = a.D;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.window = a.window;
+    p.scale = a.scale;
+    p.out = a.out;
+    p.lse = static_cast<float*>(a.lse);
+    p.wait_limit_ns = limit_ns;
+    p.withhold_full = withhold_full;
+    p.withhold_empty = withhold_empty;
+    p.status = ws_status(a.workspace);
+    const PagedLayout lay = paged_layout(a.Hq / a.Hkv, a.D);
+    p.parts = reinterpret_cast<PagedAttnPart*>(mptr(a.workspace, lay.parts));
+    p.part_ml = reinterpret_cast<float2*>(mptr(a.workspace, lay.ml));
+    p.part_o = reinterpret_cast<float*>(mptr(a.workspace, lay.o));
+    return cuda_status(launch_paged_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(a.cuda_stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -231,58 +291,32 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
                            int Hkv, int D, int max_pages, int num_pages, int page_size, int window, float scale,
                            sptp_dtype dtype, sptp_kv_type kv_type, void* out, float* lse, void* workspace,
                            size_t ws_bytes, void* cuda_stream) {
-    const bool e4m3 = kv_type == SPTP_KV_E4M3;
-    if (!k_cache || !v_cache || !workspace || (e4m3 && (!k_scale || !v_scale)) ||
-        (B != 0 && (!q || !page_table || !seq_lens || !out)))
-        return SPTP_ERR_NULL;
-    int rc = check_cache(P, Hkv, D, B, max_pages, num_pages, page_size, dtype, kv_type);
-    if (rc == SPTP_ERR_DTYPE) return rc;
-    int rc2 = check_heads(P, Hq, Hkv, D);
-    if (rc2 != SPTP_OK || rc != SPTP_OK) return SPTP_ERR_SHAPE;
-    if (window < 0 || !std::isfinite(scale)) return SPTP_ERR_SHAPE;
-    const long long n = elems(P, B, Hq, D);
-    if (n < 0) return SPTP_ERR_SHAPE;
-    const size_t es = esize(dtype), rows = static_cast<size_t>(P) * num_pages * Hkv * page_size;
-    const size_t cb = rows * D * (e4m3 ? 1 : es), sb = e4m3 ? rows * 4 : 0, qb = static_cast<size_t>(n) * es;
-    const size_t need = sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D);
-    const Buf ins[] = {{q, qb, 16}, {k_cache, cb, 16}, {v_cache, cb, 16},
-                       {e4m3 ? k_scale : nullptr, sb, 16}, {e4m3 ? v_scale : nullptr, sb, 16},
-                       {page_table, static_cast<size_t>(B) * max_pages * 4, 4},
-                       {seq_lens, static_cast<size_t>(B) * 4, 4}};
-    const Buf outs[] = {{out, qb, 16}, {lse, static_cast<size_t>(P) * B * Hq * 4, 16}, {workspace, need, kAlign}};
-    if ((rc = check_aligned(ins, 7)) != SPTP_OK || (rc = check_aligned(outs, 3)) != SPTP_OK) return rc;
-    if (ws_bytes < need) return SPTP_ERR_WORKSPACE;
-    if ((rc = check_alias(outs, 3, ins, 7)) != SPTP_OK) return rc;
-    if (B == 0) return SPTP_OK;
-    DevInfo di;
-    if ((rc = device_info(&di)) != SPTP_OK) return rc;
-    PagedAttnParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.q = q;
-    p.k = k_cache;
-    p.v = v_cache;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.page_table = page_table;
-    p.seq_lens = seq_lens;
-    p.P = P;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.D = D;
-    p.max_pages = max_pages;
-    p.num_pages = num_pages;
-    p.page_size = page_size;
-    p.window = window;
-    p.scale = scale;
-    p.out = out;
-    p.lse = lse;
-    p.status = ws_status(workspace);
-    const PagedLayout lay = paged_layout(Hq / Hkv, D);
-    p.parts = reinterpret_cast<PagedAttnPart*>(mptr(workspace, lay.parts));
-    p.part_ml = reinterpret_cast<float2*>(mptr(workspace, lay.ml));
-    p.part_o = reinterpret_cast<float*>(mptr(workspace, lay.o));
-    return cuda_status(launch_paged_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(cuda_stream)));
+    sptp_paged_attn_decode_args a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.cuda_stream = cuda_stream;
+    a.ws_bytes = ws_bytes;
+    a.P = P;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.window = window;
+    a.dtype = dtype;
+    a.kv_type = kv_type;
+    a.scale = scale;
+    return attend(a, kWaitLimitNs, -1, -1);
 }
 
 int sptp_rope_packed(const sptp_rope_args* a) {
@@ -303,13 +337,15 @@ int sptp_rope_append_kv_packed(const sptp_rope_append_kv_args* a) {
 }
 
 int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* a) {
+    return a ? attend(*a, kWaitLimitNs, -1, -1) : SPTP_ERR_NULL;
+}
+
+int sptp_paged_attn_wait_selftest(const sptp_paged_attn_decode_args* a, int withhold_full, int withhold_empty,
+                                  unsigned long long limit_ns) {
     if (!a) return SPTP_ERR_NULL;
-    return sptp_paged_attn_decode(
-        a->q, a->k_cache, a->v_cache, static_cast<const float*>(a->k_scale), static_cast<const float*>(a->v_scale),
-        static_cast<const int*>(a->page_table), static_cast<const int*>(a->seq_lens), a->P, a->B, a->Hq, a->Hkv, a->D,
-        a->max_pages, a->num_pages, a->page_size, a->window, a->scale, static_cast<sptp_dtype>(a->dtype),
-        static_cast<sptp_kv_type>(a->kv_type), a->out, static_cast<float*>(a->lse), a->workspace, a->ws_bytes,
-        a->cuda_stream);
+    if (limit_ns == 0 || limit_ns > 10000000000ull || a->D > 128) return SPTP_ERR_SHAPE;
+    if ((withhold_full < 0) == (withhold_empty < 0)) return SPTP_ERR_SHAPE;
+    return attend(*a, limit_ns, withhold_full, withhold_empty);
 }
 
 }  // extern "C"

@@ -159,9 +159,11 @@ static_assert(kJoinThreads >= kPagedMaxCtas, "one thread per status word");
 cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
     if (e4m3 && !bf16) return cudaErrorInvalidValue;
     int ctas = 0;
-    cudaError_t e = !bf16  ? launch_paged_attn_f32(p, num_sms, &ctas, s)
-                    : e4m3 ? launch_paged_attn_e4m3(p, num_sms, &ctas, s)
-                           : launch_paged_attn_bf16(p, num_sms, &ctas, s);
+    const bool test = p.withhold_full >= 0 || p.withhold_empty >= 0;
+    cudaError_t e = test    ? launch_paged_attn_test(p, bf16, e4m3, &ctas, s)
+                    : !bf16 ? launch_paged_attn_f32(p, num_sms, &ctas, s)
+                    : e4m3  ? launch_paged_attn_e4m3(p, num_sms, &ctas, s)
+                            : launch_paged_attn_bf16(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
     const int head_shift = p.D <= 64 ? 0 : p.D <= 128 ? 1 : 2;  // slices of a head: 1, 2 or 4
     return bf16 ? launch_after(paged_attn_join<__nv_bfloat16>, ctas + 1, kJoinThreads, 0, s, p, ctas, head_shift)

@@ -986,6 +986,13 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// mbar_wait by a whole warp: true if every lane's wait was.  A lane gives up by
+// itself (its own clock, or the abort flag seen); what follows a wait has the
+// warp's lanes work together, so they go on or leave as one.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, where, info));
+}
+
 template <class C>
 struct Smem {
     static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;
@@ -1009,7 +1016,10 @@ struct Smem {
     static_assert(STAGES >= 2 && STATS_BYTES % 16 == 0 && Q_BYTES % 16 == 0 && C::W_BYTES % 16 == 0, "layout");
 };
 
-template <class C>
+// TEST: a self-test of the way out (paged_attn_selftest.cu), in which CTA 0 lets
+// a wait run out: its producer does not fill tile withhold_full of its share, or
+// its consumers do not give back the stage of tile withhold_empty.
+template <class C, bool TEST = false>
 __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
     using L = Smem<C>;
@@ -1087,7 +1097,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         if (c.b < p.B && c.tile_at() < end) share_at = c;
     }
     __syncthreads();
-    WaitCtx wc{&status, &abort_flag, kWaitLimitNs};
+    WaitCtx wc{&status, &abort_flag, p.wait_limit_ns};
     PagedAttnPart* part = p.parts + blockIdx.x;
 
     if (warp == kTeam * C::TEAMS) {
@@ -1183,7 +1193,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                     page = page_of(n.b, n.s, n.key0() + lane * R);
                 const int tiles = min(per, here - u0);
                 for (int u = 0; u < tiles; ++u) {
-                    if (!mbar_wait(&empty[s], phase, wc, kWhereKvEmpty, issued)) {
+                    if (!warp_wait(&empty[s], phase, wc, kWhereKvEmpty, issued)) {
                         more = false;
                         u0 = here;
                         break;
@@ -1193,6 +1203,14 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                     const bool first = u0 + u == 0, last = u0 + u + 1 == here;
                     const int src = (u << nb_shift) + box_r;
                     const int brow = __shfl_sync(0xffffffffu, row, src);
+                    if (TEST && blockIdx.x == 0 && issued == p.withhold_full) {
+                        ++issued;
+                        if (++s == L::STAGES) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                        continue;
+                    }
                     if (lane == 0) {
                         const int tile0 = key_begin + (u0 + u) * TK;
                         Meta md;
@@ -1252,7 +1270,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         if (abort_flag) {
             // left early: wait (bounded) for the copies still in flight
             int local_abort = 0;
-            WaitCtx drain{&status, &local_abort, kWaitLimitNs};
+            WaitCtx drain{&status, &local_abort, p.wait_limit_ns};
             for (int i = max(0, issued - L::STAGES); i < issued; ++i)
                 mbar_wait(&full[i % L::STAGES], (i / L::STAGES) & 1, drain, kWhereDrain, i);
         }
@@ -1266,7 +1284,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         C c;
         uint32_t phase = 0;
         for (int i = 0, s = 0;; ++i) {
-            const bool ok = mbar_wait(&full[s], phase, wc, kWhereKvFull, i);
+            const bool ok = warp_wait(&full[s], phase, wc, kWhereKvFull, i);
             const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
             // this team's heads: an equal part of the item's
             const int part_heads = (md.heads + C::TEAMS - 1) / C::TEAMS, h0 = team_index() * part_heads;
@@ -1280,7 +1298,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                         stats + (i & 1) * L::MAXIMA, weights + (i & 1) * C::W_BYTES, md.lo, md.hi))
                 break;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
+            if (lane == 0 && !(TEST && blockIdx.x == 0 && i == p.withhold_empty)) mbar_arrive(&empty[s]);
             if (++s == L::STAGES) {
                 s = 0;
                 phase ^= 1;

@@ -9,7 +9,7 @@ namespace sptp {
 namespace paged {
 namespace {  // internal: a process may load the library and its checked build, each with `done` of its own
 
-template <class C>
+template <class C, bool TEST = false>
 cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     // heads of a group, in equal blocks of at most HEADS
     const int group = p.Hq / p.Hkv;
@@ -37,7 +37,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<C>::BYTES);
+        e = cudaFuncSetAttribute(paged_attn_kernel<C, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<C>::BYTES);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -47,8 +47,9 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     const long long most = (span + C::TK - 1) / C::TK * p.B * p.items_per_seq;
     if (grid > most) grid = most;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    if (TEST && grid > kSelftestCtas) grid = kSelftestCtas;
     *ctas = static_cast<int>(grid);
-    return launch_after(paged_attn_kernel<C>, *ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s, p);
+    return launch_after(paged_attn_kernel<C, TEST>, *ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s, p);
 }
 
 }  // namespace

@@ -38,22 +38,27 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads, 2) paged_attn_join(const __grid_constant__ PagedAttnParams p, int ctas,
                                                                int head_shift) {
     __shared__ float2 sums[2][kHalf][32];
-    __shared__ int first_bad;
+    __shared__ int first_bad, first_failed;
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
     admit_next();
     await_previous();
     if (c == ctas) {
-        if (tid == 0) first_bad = ctas;
+        // the first CTA that failed; if none did, the first that met an
+        // index outside its range
+        if (tid == 0) first_bad = first_failed = ctas;
         __syncthreads();
-        if (tid < ctas && p.parts[tid].status != 0) atomicMin(&first_bad, tid);
+        const int mine = tid < ctas ? p.parts[tid].status : 0;
+        if (mine != 0) atomicMin(&first_bad, tid);
+        if (mine != 0 && mine != SPTP_ERR_SHAPE) atomicMin(&first_failed, tid);
         __syncthreads();
         if (tid == 0) {
             DeviceStatus st = {0, 0, 0, 0, 0};
-            if (first_bad < ctas) {
-                const PagedAttnPart& bad = p.parts[first_bad];
+            const int at = first_failed < ctas ? first_failed : first_bad;
+            if (at < ctas) {
+                const PagedAttnPart& bad = p.parts[at];
                 st.code = bad.status;
                 st.where = bad.where;
-                st.block = first_bad;
+                st.block = at;
                 st.info = bad.info;
             }
             *p.status = st;

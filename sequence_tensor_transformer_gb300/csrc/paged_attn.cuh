@@ -1029,7 +1029,11 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ Meta meta[kMaxStages];
-    __shared__ DeviceStatus status;  // this CTA's, copied to the workspace at the end
+    // This CTA's findings, copied to the workspace at the end: waits that ran out
+    // and failed checks; and apart from them, since the outputs stay defined, a
+    // length or page outside its range (and its sequence)
+    __shared__ DeviceStatus status;
+    __shared__ int out_of_range, out_of_range_at;
     __shared__ int abort_flag;
     __shared__ long long warp_cost[kThreads / 32];
     __shared__ Cursor<TK> share_at;
@@ -1044,6 +1048,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         fence_mbar_init();
         abort_flag = 0;
         status.code = status.where = status.info = 0;
+        out_of_range = out_of_range_at = 0;
         share_at.b = -1;
         tma_prefetch_map(&p.map_k);
         tma_prefetch_map(&p.map_v);
@@ -1077,10 +1082,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     // one tile's cost, so that an item's parts lie in successive shares.
     const long long share = max(static_cast<long long>(kTileCost), (total + gridDim.x - 1) / gridDim.x);
     const long long begin = share * blockIdx.x, end = begin + share;
-    if (bad) {
-        status.code = SPTP_ERR_SHAPE;
-        status.where = kWhereKvPage;
-    }
+    if (bad) out_of_range = 1;
     if (begin >= before && begin < before + mine) {
         Cursor<TK> c;
         c.at = before;
@@ -1182,9 +1184,8 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                 const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
                 // rows of tiles that this share does not have are not reported
                 if (page == -1 && (lane >> nb_shift) < here - u0) {
-                    status.code = SPTP_ERR_SHAPE;
-                    status.where = kWhereKvPage;
-                    status.info = c.b;
+                    out_of_range = 1;
+                    out_of_range_at = c.b;
                 }
                 // the next tiles' pages, while these are waited for
                 if (u0 + per < here)
@@ -1331,9 +1332,10 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
     }
     __syncthreads();
     if (tid == 0) {
-        part->status = status.code;
-        part->where = status.where;
-        part->info = status.info;
+        const bool failed = status.code != 0;
+        part->status = failed ? status.code : out_of_range ? SPTP_ERR_SHAPE : 0;
+        part->where = failed ? status.where : out_of_range ? kWhereKvPage : 0;
+        part->info = failed ? status.info : out_of_range_at;
     }
 }
 

@@ -162,8 +162,14 @@ __device__ __forceinline__ void check_rows(const RopeParams& p) {
     if (threadIdx.x == 0) {
         const bool bad = first_bad != 0x7fffffff;
         // a checked build clears the words before the launch: another block
-        // may have written them
-        if (kBoundsChecked && !bad) return;
+        // may have written them, and a failed check stays there
+        if (kBoundsChecked) {
+            if (bad && atomicCAS(&p.status->code, 0, SPTP_ERR_SHAPE) == 0) {
+                p.status->where = kWhereKvSlot;
+                p.status->info = first_bad;
+            }
+            return;
+        }
         DeviceStatus st;
         st.code = bad ? SPTP_ERR_SHAPE : SPTP_OK;
         st.where = bad ? kWhereKvSlot : 0;

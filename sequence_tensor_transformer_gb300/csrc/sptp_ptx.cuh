@@ -141,7 +141,10 @@ constexpr bool kBoundsChecked = false;
 
 __device__ __forceinline__ void report_bounds(DeviceStatus* st, volatile int* abort_flag, int where, long long value) {
     if (abort_flag != nullptr) *abort_flag = 1;
-    if (st != nullptr && atomicCAS(&st->code, 0, -11 /* SPTP_ERR_BOUNDS */) == 0) {
+    // (in place of SPTP_ERR_SHAPE too, with which outputs stay defined)
+    int before = st == nullptr ? -11 : atomicCAS(&st->code, 0, -11 /* SPTP_ERR_BOUNDS */);
+    if (before == -2 /* SPTP_ERR_SHAPE */) before = atomicCAS(&st->code, -2, -11) == -2 ? 0 : -11;
+    if (before == 0) {
         st->where = where;
         st->block = blockIdx.x;
         const long long lim = 0x7fffffffll;

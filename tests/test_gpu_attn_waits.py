@@ -60,3 +60,19 @@ def test_nothing_withheld(kind):
     c = ta.make(1, [1500, 2500, 700], 5, 1, 128, 16, kind)
     for role in (dict(withhold_full=100000), dict(withhold_empty=100000)):
         assert withheld(c, **role)[0] == 0
+
+
+@pytest.mark.parametrize("kind", ta.KINDS)
+@pytest.mark.parametrize("role", [dict(withhold_full=3), dict(withhold_empty=1)])
+def test_a_wait_that_ran_out_is_not_hidden_by_a_bad_index(kind, role):
+    """A length outside the table (seen by every CTA) and pages outside the pool
+    (in either CTA's share) leave the outputs defined, a wait that ran out does
+    not: that is what is reported."""
+    c = ta.make(1, [1500, 2500, 700], 5, 1, 128, 16, kind)
+    for lens in ([1500, 2500, -1], [1500, 2500, 1 << 30], [-7, 2500, 1500]):
+        assert withheld(c, lens=lens, **role)[0] == st.STATUS["timeout"]
+    for b, j in ((0, 0), (0, 50), (1, 150), (2, 40)):
+        table = c["table"].copy()
+        table[b, j] = -1
+        assert withheld(dict(c, table=table), **role)[0] == st.STATUS["timeout"]
+        assert withheld(dict(c, table=table), withhold_full=100000)[0] == st.STATUS["shape"]

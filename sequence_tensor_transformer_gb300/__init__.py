@@ -15,6 +15,7 @@ import ctypes
 import importlib
 import os
 import struct
+import warnings
 
 import torch
 
@@ -134,13 +135,20 @@ def load_library(path: str = LIB_PATH, replace: bool = False):
 
 
 def set_library(handle):
-    """Makes a handle returned by load_library the one every call uses."""
+    """Makes a handle returned by load_library the one every call uses.  Where
+    the extension module cannot be loaded (built for another torch or Python),
+    the functions here make every call, and a warning says so."""
     global _lib, _fast
     _lib, _fast = handle, None
     if handle is None or not os.path.exists(BINDING_PATH):
         return
     importlib.invalidate_caches()  # it may have been built by this process
-    from . import _decode_binding
+    try:
+        _decode_binding = importlib.import_module("._decode_binding", __package__)
+    except ImportError as e:
+        warnings.warn(f"{BINDING_PATH} cannot be loaded ({e}): build it anew (build.build()); until then a decoding "
+                      "step's calls cost some microseconds more", RuntimeWarning, stacklevel=2)
+        return
     _decode_binding.use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
         "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")))
     _fast = _decode_binding

@@ -17,10 +17,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -54,25 +56,45 @@ def _stale(target: str, deps) -> bool:
 
 
 def _build_binding() -> None:
-    """The extension module for the torch that is installed: an object of its
-    own for each torch version, so that another torch builds it anew."""
+    """The extension module for the torch and the Python that are in use: an
+    object of its own for each of them, and a note of the object that the module
+    was linked from, so that it is linked anew whenever that is another one.
+    Where it cannot be compiled (no g++ or no Python.h) the library works
+    without it, and a warning says so."""
     import torch
 
     home = os.path.dirname(os.path.abspath(torch.__file__))
+    include = sysconfig.get_paths()["include"]
     src = os.path.join(CSRC, "decode_binding.cpp")
-    obj = os.path.join(BUILD, f"decode_binding-{torch.__version__}.o")
+    where = hashlib.sha256(home.encode()).hexdigest()[:8]
+    name = f"decode_binding-{torch.__version__}-{sysconfig.get_config_var('SOABI')}-{where}.o"
+    obj, note = os.path.join(BUILD, name), os.path.join(BUILD, "decode_binding.linked")
+    linked = None
+    if os.path.exists(BINDING) and os.path.exists(note):
+        with open(note) as f:
+            linked = f.read()
+    if shutil.which("g++") is None or not os.path.exists(os.path.join(include, "Python.h")):
+        if linked != name and os.path.exists(BINDING):
+            os.remove(BINDING)  # another torch's or Python's
+        if not os.path.exists(BINDING):
+            warnings.warn("no g++ or no Python.h: built without the extension module, a decoding step's calls cost "
+                          "some microseconds more", RuntimeWarning)
+        return
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     if _stale(obj, [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
         dirs = [os.path.join(ROOT, "include"), os.path.join(home, "include"),
-                os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
-                sysconfig.get_paths()["include"]]
+                os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), include]
         _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
              + ["-I" + d for d in dirs] + ["-c", src, "-o", obj + ".tmp"])
         os.replace(obj + ".tmp", obj)
-    if _stale(BINDING, [obj]):
+    if linked != name or _stale(BINDING, [obj]):
         libs = ["torch_python", "torch", "torch_cpu", "c10", "c10_cuda"]
         _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + os.path.join(home, "lib")] + ["-l" + n for n in libs])
+        if os.path.exists(note):
+            os.remove(note)
         os.replace(BINDING + ".tmp", BINDING)
+        with open(note, "w") as f:
+            f.write(name)
 
 
 def _run(cmd) -> None:

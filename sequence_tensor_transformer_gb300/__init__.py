@@ -202,6 +202,8 @@ def _same_device(*ts):
     properties from it, so a tensor elsewhere would be handed to kernels of
     another device.  Checked before any pointer reaches the C ABI."""
     ts = [t for t in ts if t is not None]
+    if not ts:
+        return
     device = ts[0].device
     for t in ts:
         if t.device != device:

@@ -373,8 +373,9 @@ int sptp_down_proj_e4m3(const void* qs, const float* ss, const void* qW2, const 
  *            [P][num_pages][Hkv][page_size] fp32: a head's row of D elements
  *            quantised as by sptp_quantize_rows_e4m3.
  *   Shape rules of all of them: 1 <= P <= 8; D % 8 == 0 (E4M3: % 16),
- *   8 <= D <= 256; Hq % Hkv == 0; M, B < 2^30; page_size % 16 == 0;
- *   max_pages * page_size < 2^30; P * num_pages * Hkv * page_size < 2^31.
+ *   8 <= D <= 256; Hq % Hkv == 0; P * (Hq + 2 Hkv) < 2^24; M, B < 2^30;
+ *   page_size % 16 == 0; max_pages * page_size < 2^30; P * num_pages * Hkv *
+ *   page_size < 2^31.  M == 0 or B == 0 enqueues nothing.
  *   int32 arrays are 4-byte aligned, `turns` 8-byte, all others 16-byte.
  * Calls that may overlap on the GPU need a workspace each; calls in one stream,
  * or replays of graphs one after another, may share it.  Appends and attention
@@ -482,9 +483,15 @@ size_t sptp_paged_attn_workspace_size(int P, int B, int Hq, int Hkv, int D);
  * [0, num_pages) counts as zero keys and values; both are recorded as
  * SPTP_ERR_SHAPE in the workspace status words.  workspace: at least
  * sptp_paged_attn_workspace_size(...), 256-byte aligned.
- * Numerics: scores, softmax statistics and sums in fp32; with a bf16 or E4M3
- * cache the weights e^(s_j - m) are rounded to bf16 for their product with v
- * (tensor cores), as v is; out is rounded once.
+ * Numerics: scores, softmax statistics and sums in fp32; out is rounded once.
+ * Weights are rounded for their product with v on the tensor cores:
+ *   bf16  e^(s_j - m) to bf16 (2^-8), m the largest score so far
+ *   E4M3  e^(s_j) times v's scale to fp16 (2^-11), relative to the largest such
+ *         product so far, whose score may be far below the largest; below
+ *         2^-38 of it: 0.  Codes are exact in fp16, and so is q but for elements
+ *         below 2^-31 of its row's largest (held to 2^-39 of that).  The scales
+ *         of v are positive.
+ *   fp32  not rounded.
  */
 int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                            const float* v_scale, const int* page_table, const int* seq_lens, int P, int B,
@@ -528,12 +535,13 @@ int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* args);
 /*
  * sptp_read_device_status -- synchronises `cuda_stream` and returns the
  * status the kernels recorded in the workspace header since the last call
- * that reset it (every entry point above resets it when it starts):
+ * that reset it (every entry point above resets it when it starts, unless it
+ * has no rows and enqueues nothing):
  * SPTP_OK; SPTP_ERR_TIMEOUT if a bounded device-side wait ran out (the
  * kernels then stop early and their outputs are undefined); or
  * SPTP_ERR_SHAPE if sptp_permute_ffn_neurons met an index outside [0, F), or
- * a call on a paged cache an index, a page or a length outside its range.  No
- * counterpart on the pages: this is the library's own failure detection.
+ * a call on a paged cache an index, a page or a length outside its range
+ * (SPTP_ERR_TIMEOUT is reported in place of it).  No counterpart on the pages: this is the library's own failure detection.
  */
 int sptp_read_device_status(const void* workspace, void* cuda_stream);
 

@@ -541,7 +541,8 @@ int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* args);
  * kernels then stop early and their outputs are undefined); or
  * SPTP_ERR_SHAPE if sptp_permute_ffn_neurons met an index outside [0, F), or
  * a call on a paged cache an index, a page or a length outside its range
- * (SPTP_ERR_TIMEOUT is reported in place of it).  No counterpart on the pages: this is the library's own failure detection.
+ * (a wait that ran out in the attention is reported in place of it).  No
+ * counterpart on the pages: this is the library's own failure detection.
  */
 int sptp_read_device_status(const void* workspace, void* cuda_stream);
 

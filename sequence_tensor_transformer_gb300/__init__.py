@@ -640,9 +640,11 @@ def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=F
     return k, v, torch.zeros(shape[:-1], device=device), torch.zeros(shape[:-1], device=device)
 
 
-# The calls of a decoding step last a few microseconds on the device, so their
-# checks are written to cost little: one condition over all tensors on the way
-# in, the checks with their messages (_expect, _same_device) only if it fails.
+# The calls of a decoding step last a few microseconds on the device.  With a
+# workspace (or none needed) and stream left out they go through the extension
+# module; what it does not take comes here, to the same checks, which are written
+# to cost little: one condition over all tensors on the way in, those with
+# messages (_expect, _same_device) only if it fails.
 
 # The arguments of a call as one block (the *_args structs of include/sptp.h):
 # pointers, sizes, ints and the float in the structs' order and native layout.
@@ -706,8 +708,10 @@ def sptp_rope_append_kv(qkv, positions, seq_ids, page_table, turns, cache, Hq, i
                         workspace=None, stream=None):
     """Rotates the q and k heads of qkv [P,M,(Hq+2Hkv)D] and stores k and v in
     `cache` (see paged_kv_cache).  positions, seq_ids int32 [M] (seq_ids < 0:
-    padding, whose rows of q_out are left as they are); page_table int32
-    [B,max_pages]; turns None: no rotation.  Returns q_out [P,M,Hq,D]."""
+    padding, whose rows of q_out are left as they are: undefined in one that is
+    left out); page_table int32 [B,max_pages]; turns None: no rotation.  Returns
+    q_out [P,M,Hq,D].  Costs the host less with a workspace given and stream left
+    out."""
     if _fast is not None and stream is None:
         done = _fast.append(qkv, positions, seq_ids, page_table, turns, cache, Hq, interleaved, gain, q_out, workspace)
         if done is not NotImplemented:
@@ -753,7 +757,8 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     """Attention of one token per sequence over a paged cache: q [P,B,Hq,D],
     page_table int32 [B,max_pages], seq_lens int32 [B] (0: an empty row);
     scale defaults to D^-1/2; window 0: the whole sequence.  Returns
-    (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None)."""
+    (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None).  Costs the host less with a
+    workspace given and stream left out."""
     if _fast is not None and stream is None:
         done = _fast.decode(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
         if done is not NotImplemented:

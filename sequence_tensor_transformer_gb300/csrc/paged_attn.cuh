@@ -26,9 +26,9 @@
 //    end costs next to nothing, which is what batches of short rows are made of.
 //
 // Measured (back to back on the device; of the copy bandwidth): 4 rows of 131071
-// bf16 keys of 128 (268 MB) 48.4 us, 0.83; 64 sequences of 64 .. 16384 keys, 4
-// heads each (403 MB) 67.5 us, 0.89; 64 of 4096 (540 MB) 0.91; E4M3, 96 sequences
-// of 16 .. 8000 keys, 8 heads each (271 MB) 50.6 us, 0.80; 4 rows of 333 keys 7.8
+// bf16 keys of 128 (268 MB) 48.6 us, 0.83; 64 sequences of 64 .. 16384 keys, 4
+// heads each (403 MB) 67.7 us, 0.89; 64 of 4096 (540 MB) 0.91; E4M3, 96 sequences
+// of 16 .. 8000 keys, 8 heads each (271 MB) 51.0 us, 0.79; 4 rows of 333 keys 7.9
 // us.  About 8 us of every call are latency: two launches, the lengths, the page
 // table, a first and a last tile, the join.
 #pragma once

@@ -450,10 +450,10 @@ int sptp_rope(const void* x, const int* positions, const unsigned long long* tur
  * A token whose sequence is >= B, whose position is outside [0, max_pages *
  * page_size) or whose page is outside [0, num_pages) is recorded as
  * SPTP_ERR_SHAPE in the workspace status words; its k and v are not stored
- * (its q is).  Of two tokens with one sequence and position, it is not
- * defined which is stored.  workspace: at least SPTP_WS_HEADER_BYTES,
- * 256-byte aligned.  E4M3: k is rounded to bf16, then quantised; non-finite
- * rows are outside the contract.
+ * (its q is).  What two tokens with one sequence and position leave in their
+ * slot is not defined (it may be parts of both).  workspace: at least
+ * SPTP_WS_HEADER_BYTES, 256-byte aligned.  E4M3: k is rounded to bf16, then
+ * quantised; non-finite rows are outside the contract.
  */
 int sptp_rope_append_kv(const void* qkv, const int* positions, const int* seq_ids, const int* page_table,
                         const unsigned long long* turns, int P, int M, int Hq, int Hkv, int D, int rot,

@@ -1110,7 +1110,9 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         const int per = 32 >> nb_shift;  // tiles whose rows the lanes look up at once
         const int group = p.Hq / p.Hkv;
         const int pages_rows = p.Hkv * p.page_size;               // of a shard's page
-        const int bad_row = p.P * p.num_pages * pages_rows;       // outside the maps: zeros
+        // outside the maps, all of a box's rows: zeros (before them, since a box
+        // behind a pool of almost 2^31 rows would pass the coordinates' 32 bits)
+        constexpr int bad_row = -TK;
         const int q_bytes = p.D * (C::F32 ? 4 : 2);
         // this lane's box of a tile: nb x BOXES x 2 of them, at most 32
         static_assert(TK / 16 * C::BOXES * 2 <= 32, "one box per lane");
@@ -1232,8 +1234,8 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                                   static_cast<const uint8_t*>(p.q) + (qrow + lane) * q_bytes, q_bytes, &full[s]);
                     // a checked build: a page's rows, or the row of zeros
                     if (box_in && (tile_loads >> box_r & 1) &&
-                        checked(brow >= 0 && (brow == bad_row || brow + R <= bad_row), &status, &abort_flag,
-                                kWhereBoundsTma, brow))
+                        checked(brow == bad_row || (brow >= 0 && brow <= p.P * p.num_pages * pages_rows - R), &status,
+                                &abort_flag, kWhereBoundsTma, brow))
                         // boxes past a narrow row's end lie outside the map: zeros
                         tma_load_2d(smem + s * L::STAGE_BYTES + box_at, box_map, &full[s], box_x, brow);
                     if constexpr (C::CODES) {

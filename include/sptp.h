@@ -499,6 +499,69 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
                            float scale, sptp_dtype dtype, sptp_kv_type kv_type, void* out, float* lse,
                            void* workspace, size_t ws_bytes, void* cuda_stream);
 
+/*
+ * What a model may make of the scores before the softmax, in
+ * sptp_paged_attn_prompt and sptp_paged_attn_decode_ex:
+ *     s_j = cap tanh(scale q . k_j / cap) - slope |pos - j|
+ *   for a row at position pos of its sequence and key j.
+ *   cap     0: none (s_j = scale q . k_j - ..); else 1e-30 <= cap <= 1e30
+ *   slopes  fp32 [P][Hq], one per query head of every shard, finite, any sign;
+ *           NULL: none
+ * Numerics: tanh to 2^-22 of the cap, or of the score below an eighth of it;
+ * distances exact below 2^24, a bias to 2^-23 of itself.
+ */
+
+/* Workspace bytes needed by sptp_paged_attn_prompt (0 on bad args). */
+size_t sptp_paged_attn_prompt_workspace_size(int P, int M, int B, int Hq, int Hkv, int D);
+
+/* Arguments of sptp_paged_attn_prompt. */
+typedef struct sptp_paged_attn_prompt_args_s {
+    const void *q, *k_cache, *v_cache, *k_scale, *v_scale, *page_table, *seq_lens, *row_starts, *prefix_lens, *slopes;
+    void *out, *lse, *workspace, *cuda_stream;
+    size_t ws_bytes;
+    int P, M, B, Hq, Hkv, D, max_pages, num_pages, page_size, window, dtype, kv_type;
+    float scale, cap;
+} sptp_paged_attn_prompt_args;
+
+/*
+ * sptp_paged_attn_prompt -- attention of many new rows per sequence over their
+ * cached keys and values: whole prompts, pieces of prompts behind what is
+ * cached already, proposed tokens to be checked at once.  The rows of B
+ * sequences are packed; a row sees keys of its own sequence only:
+ *     lse = ln sum_j e^s_j,  out = sum_j e^(s_j - lse) v_j
+ *   over lo <= j < hi:  pos = seq_lens[b] - n_b + r for row r of the sequence's
+ *   n_b rows;  hi = pos + 1, or prefix_lens[b] where that is more (a prefix that
+ *   every row of the sequence sees whole);  lo = pos + 1 - window if window > 0
+ *   and that is positive, else 0.
+ *   q           [P][M][Hq][D] (sptp_rope_append_kv's q_out)
+ *   row_starts  [B + 1] int32: sequence b's rows are row_starts[b] ..
+ *               row_starts[b+1] - 1, ascending, 0 <= .. <= M.  Other rows of out
+ *               and lse (padding) are left as they were
+ *   seq_lens    [B] int32: keys in the cache, the new rows' included
+ *   prefix_lens [B] int32, cut to [0, seq_lens[b]]; NULL: no prefixes
+ *   cap, slopes as above
+ *   out         [P][M][Hq D], the row-parallel operand of sptp_down_proj
+ *   lse         [P][M][Hq] fp32, or NULL
+ *   out and lse must not overlap an input, the workspace or each other.
+ *   M < 2^30, and the shape rules above.  M == 0 or B == 0 enqueues nothing.
+ * The work is split over rows, heads and keys, evenly over the SMs whatever the
+ * lengths; the parts of a row are joined in a fixed order: equal inputs give
+ * equal bits.  What the cache holds outside the keys that a sequence's rows see
+ * does not matter; a value of v that some of its rows see and others do not has
+ * to be finite.
+ * Recorded as SPTP_ERR_SHAPE in the workspace status words: a row start outside
+ * [0, M] or below the one before it (the rows concerned are undefined); a length
+ * outside [0, max_pages * page_size] (cut to it); more rows than keys (the rows
+ * before position 0 see nothing: zeros, lse -inf); a page outside [0, num_pages)
+ * among the keys that are seen (zero keys and values).  workspace: at least
+ * sptp_paged_attn_prompt_workspace_size(...), 256-byte aligned.
+ * Numerics: scores, softmax statistics and sums in fp32, out rounded once.  bf16
+ * and E4M3 caches: products on the tensor cores, weights rounded to bf16 (2^-8),
+ * E4M3 keys and values (code times a power of two) exact in bf16.  fp32: nothing
+ * rounded.
+ */
+int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args);
+
 /* Arguments of the calls below: those of the three calls above, pointers first. */
 typedef struct sptp_rope_args_s {
     const void *x, *positions, *turns;
@@ -531,6 +594,46 @@ typedef struct sptp_paged_attn_decode_args_s {
 int sptp_rope_packed(const sptp_rope_args* args);
 int sptp_rope_append_kv_packed(const sptp_rope_append_kv_args* args);
 int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* args);
+
+/*
+ * sptp_paged_attn_decode_ex -- sptp_paged_attn_decode with scores as in
+ * sptp_paged_attn_prompt: pos = seq_lens[b] - 1.  cap 0 and slopes NULL: the
+ * same call.  slopes must not overlap an output; 4-byte aligned.
+ */
+int sptp_paged_attn_decode_ex(const sptp_paged_attn_decode_args* args, float cap, const float* slopes);
+
+/* Workspace bytes needed by sptp_lora (0 on bad args). */
+size_t sptp_lora_workspace_size(int P, int M, int K, int N, int R, int rowwise);
+
+/*
+ * sptp_lora -- low-rank adapters of many requests at once beside a shared
+ * projection: every row of a batch names the adapter of its request,
+ *     out[p][m] = base[p][m] + gains[a] * B_a (A_a x_m),  a = ids[m]
+ *   added to what the projection itself gave (base).
+ *   rowwise == 0: a column-parallel projection (sptp_attn_qkv_forward's qkv_out;
+ *            x is then its normed rows, which it leaves in its workspace behind
+ *            the header)
+ *     x      [M][K], the same for every shard
+ *     base, out [P][M][N/P]: shard p has rows [p N/P, (p+1) N/P) of B_a
+ *   rowwise != 0: a row-parallel projection (sptp_down_proj's out, with x its s)
+ *     x      [P][M][K/P]: shard p has columns [p K/P, (p+1) K/P) of A_a
+ *     base, out [P][M][N]: each shard's partial gets its part of the sum
+ *   A       [adapters][R][K];  B [adapters][N][R];  gains fp32 [adapters], or
+ *           NULL for 1
+ *   ids     [M] int32, in any order; < 0: no adapter, out[p][m] = base[p][m]
+ *   out may be exactly base, and must not overlap any input otherwise.
+ * 8 <= R <= 128, R % 8 == 0; K, N <= 2^20, multiples of 8, the split one of 8 P;
+ * adapters >= 0.  An id >= adapters is recorded as SPTP_ERR_SHAPE in the
+ * workspace status words, and its row treated as one without adapter.  A row
+ * does not depend on other rows or other rows' adapters; equal inputs give equal
+ * bits.  M == 0 enqueues nothing.  workspace: at least
+ * sptp_lora_workspace_size(...), 256-byte aligned.
+ * Numerics: A_a x summed in fp32, and kept to 2^-16 of itself for its product
+ * with B_a (bf16; in fp32 not rounded), sums in fp32, out rounded once.
+ */
+int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const float* gains, int P, int M, int K, int N,
+              int R, int adapters, int rowwise, sptp_dtype dtype, const void* base, void* out, void* workspace,
+              size_t ws_bytes, void* cuda_stream);
 
 /*
  * sptp_read_device_status -- synchronises `cuda_stream` and returns the

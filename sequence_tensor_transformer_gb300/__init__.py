@@ -31,6 +31,7 @@ __all__ = [
     "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest", "CHECKED_LIB_PATH", "set_library",
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
     "sptp_paged_attn_decode", "paged_kv_cache", "ROPE_SCALINGS", "sptp_paged_attn_wait_selftest",
+    "sptp_paged_attn_prompt_workspace_size", "sptp_paged_attn_prompt", "sptp_lora_workspace_size", "sptp_lora",
 ]
 
 SPTP_BF16 = 0
@@ -60,7 +61,8 @@ EXPORTED_SYMBOLS = (
     "sptp_attn_qkv_forward_ex", "sptp_noalloc_read_device_status", "sptp_noalloc_wait_selftest",
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
     "sptp_paged_attn_decode", "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed",
-    "sptp_paged_attn_wait_selftest",
+    "sptp_paged_attn_wait_selftest", "sptp_paged_attn_prompt_workspace_size", "sptp_paged_attn_prompt",
+    "sptp_paged_attn_decode_ex", "sptp_lora_workspace_size", "sptp_lora",
 )
 
 _lib = None
@@ -102,6 +104,11 @@ _SIGS = {
     "sptp_rope_append_kv_packed": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_decode_packed": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_wait_selftest": (_I, [ctypes.c_char_p, _I, _I, _U64]),
+    "sptp_paged_attn_decode_ex": (_I, [ctypes.c_char_p, _F, _P]),
+    "sptp_lora_workspace_size": (_Z, [_I] * 6),
+    "sptp_lora": (_I, [_P] * 5 + [_I] * 8 + [_P] * 3 + [_Z, _P]),
+    "sptp_paged_attn_prompt_workspace_size": (_Z, [_I] * 6),
+    "sptp_paged_attn_prompt": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "sptp_paged_attn_decode": (_I, [_P] * 7 + [_I] * 9 + [_F, _I, _I, _P, _P, _P, _Z, _P]),
 }
@@ -651,6 +658,7 @@ def paged_kv_cache(P, num_pages, Hkv, page_size, D, dtype=torch.bfloat16, e4m3=F
 _ROPE_ARGS = struct.Struct("@5P9if")
 _APPEND_ARGS = struct.Struct("@12PN13if")
 _DECODE_ARGS = struct.Struct("@11PN11if")
+_PROMPT_ARGS = struct.Struct("@14PN12i2f")
 
 
 def _ready(*ts):
@@ -753,13 +761,14 @@ def sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D) -> int:
 
 
 def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, workspace=None,
-                           stream=None, write_lse=True):
+                           stream=None, write_lse=True, cap=0.0, slopes=None):
     """Attention of one token per sequence over a paged cache: q [P,B,Hq,D],
     page_table int32 [B,max_pages], seq_lens int32 [B] (0: an empty row);
-    scale defaults to D^-1/2; window 0: the whole sequence.  Returns
-    (out [P,B,Hq*D], lse fp32 [P,B,Hq] or None).  Costs the host less with a
-    workspace given and stream left out."""
-    if _fast is not None and stream is None:
+    scale defaults to D^-1/2; window 0: the whole sequence.  cap and slopes:
+    scores as in sptp_paged_attn_prompt.  Returns (out [P,B,Hq*D], lse fp32
+    [P,B,Hq] or None).  Costs the host less with a workspace given and stream
+    left out."""
+    if _fast is not None and stream is None and cap == 0.0 and slopes is None:
         done = _fast.decode(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
         if done is not NotImplemented:
             return done
@@ -776,7 +785,8 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
         _expect("seq_lens", seq_lens, (B,), i32)
         _expect("out", out, (P, B, Hq * D), dtype, optional=True)
         _expect("lse", lse, (P, B, Hq), torch.float32, optional=True)
-    cur = _ready(q, k, v, ks, vs, page_table, seq_lens, out, lse, workspace)
+    _expect("slopes", slopes, (P, Hq), torch.float32, optional=True)
+    cur = _ready(q, k, v, ks, vs, page_table, seq_lens, slopes, out, lse, workspace)
     if out is None:
         out = _new((P, B, Hq * D), dtype, q.device, stream)
     if lse is None and write_lse:
@@ -784,12 +794,61 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     if workspace is None:
         n = max(sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
         workspace = _new((n,), torch.uint8, q.device, stream)
-    code = lib().sptp_paged_attn_decode_packed(_DECODE_ARGS.pack(
+    code = lib().sptp_paged_attn_decode_ex(_DECODE_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
         page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         workspace.data_ptr(), _raw_stream(stream, cur), workspace.nbytes, P, B, Hq, Hkv, D, max_pages, num_pages,
-        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale))
+        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale), cap, None if slopes is None else slopes.data_ptr())
     _check("sptp_paged_attn_decode", code)
+    return out, lse
+
+
+def sptp_paged_attn_prompt_workspace_size(P, M, B, Hq, Hkv, D) -> int:
+    return int(lib().sptp_paged_attn_prompt_workspace_size(P, M, B, Hq, Hkv, D))
+
+
+def sptp_paged_attn_prompt(q, cache, page_table, seq_lens, row_starts, scale=None, window=0, cap=0.0, slopes=None,
+                           prefix_lens=None, out=None, lse=None, workspace=None, stream=None, write_lse=True):
+    """Attention of many new rows per sequence over a paged cache: q [P,M,Hq,D],
+    the rows of B sequences packed, sequence b's from row_starts[b] to
+    row_starts[b+1] (int32 [B+1]); page_table int32 [B,max_pages]; seq_lens int32
+    [B], the new rows' keys included.  A row at position pos sees its sequence's
+    keys up to pos, the last `window` of them if that is not 0, and the first
+    prefix_lens[b] (int32 [B]) whole.  Scores: cap tanh(scale q.k / cap) (cap 0:
+    none) - slopes[head] |pos - key| (slopes fp32 [P,Hq]); scale defaults to
+    D^-1/2.  Rows of no sequence are left as they are (undefined in an output
+    that is left out).  Returns (out [P,M,Hq*D], lse fp32 [P,M,Hq] or None)."""
+    P, M, Hq, D = q.shape
+    k, v, ks, vs = cache
+    dtype, i32 = q.dtype, torch.int32
+    dt = _dtype_code(q)
+    num_pages, Hkv, page_size, kv_type = _check_cache(cache, P, D, dtype)
+    B, max_pages = page_table.shape
+    if not (page_table.dtype is i32 and seq_lens.shape == (B,) and seq_lens.dtype is i32 and row_starts.shape == (B + 1,)
+            and row_starts.dtype is i32 and (out is None or (out.shape == (P, M, Hq * D) and out.dtype is dtype))
+            and (lse is None or (lse.shape == (P, M, Hq) and lse.dtype is torch.float32))):
+        _expect("page_table", page_table, (B, max_pages), i32)
+        _expect("seq_lens", seq_lens, (B,), i32)
+        _expect("row_starts", row_starts, (B + 1,), i32)
+        _expect("out", out, (P, M, Hq * D), dtype, optional=True)
+        _expect("lse", lse, (P, M, Hq), torch.float32, optional=True)
+    _expect("slopes", slopes, (P, Hq), torch.float32, optional=True)
+    _expect("prefix_lens", prefix_lens, (B,), i32, optional=True)
+    cur = _ready(q, k, v, ks, vs, page_table, seq_lens, row_starts, prefix_lens, slopes, out, lse, workspace)
+    if out is None:
+        out = _new((P, M, Hq * D), dtype, q.device, stream)
+    if lse is None and write_lse:
+        lse = _new((P, M, Hq), torch.float32, q.device, stream)
+    if workspace is None:
+        n = max(sptp_paged_attn_prompt_workspace_size(P, M, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
+        workspace = _new((n,), torch.uint8, q.device, stream)
+    code = lib().sptp_paged_attn_prompt(_PROMPT_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), row_starts.data_ptr(), 0 if prefix_lens is None else prefix_lens.data_ptr(),
+        0 if slopes is None else slopes.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), _raw_stream(stream, cur), workspace.nbytes, P, M, B, Hq, Hkv, D, max_pages, num_pages,
+        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale, cap))
+    _check("sptp_paged_attn_prompt", code)
     return out, lse
 
 
@@ -813,3 +872,44 @@ def sptp_paged_attn_wait_selftest(q, cache, page_table, seq_lens, out, workspace
         workspace.nbytes, P, B, Hq, Hkv, D, max_pages, num_pages, page_size, 0, dt, kv_type, 1.0), int(withhold_full),
         int(withhold_empty), int(limit_ns))
     _check("sptp_paged_attn_wait_selftest", code)
+
+
+# ------------------------------------------------------------------ low-rank adapters
+
+def sptp_lora_workspace_size(P, M, K, N, R, rowwise=False) -> int:
+    return int(lib().sptp_lora_workspace_size(P, M, K, N, R, int(rowwise)))
+
+
+def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection:
+    out[p][m] = base[p][m] + gains[a] B[a] (A[a] x_m), a = ids[m] (int32 [M], < 0:
+    none).  A [adapters,R,K], B [adapters,N,R], gains fp32 [adapters] or None.
+    x [M,K] with base [P,M,N/P]: beside a column-parallel projection; x [P,M,K/P]
+    with base [P,M,N]: beside a row-parallel one.  out may be base (in place).
+    Returns out."""
+    n, R, K = A.shape
+    N, dtype = B.shape[1], x.dtype
+    dt = _dtype_code(x)
+    rowwise = x.dim() == 3
+    P, M = base.shape[0], x.shape[-2]
+    if P < 1 or (K if rowwise else N) % P != 0:
+        raise ValueError(f"{'K' if rowwise else 'N'} = {K if rowwise else N} is not a multiple of P = {P}")
+    shape = (P, M, N if rowwise else N // P)
+    _expect("x", x, (P, M, K // P) if rowwise else (M, K), dtype)
+    _expect("A", A, (n, R, K), dtype)
+    _expect("B", B, (n, N, R), dtype)
+    _expect("ids", ids, (M,), torch.int32)
+    _expect("base", base, shape, dtype)
+    _expect("gains", gains, (n,), torch.float32, optional=True)
+    _expect("out", out, shape, dtype, optional=True)
+    cur = _ready(x, A, B, ids, base, gains, out, workspace)
+    if out is None:
+        out = _new(shape, dtype, x.device, stream)
+    if workspace is None:
+        workspace = _new((max(sptp_lora_workspace_size(P, M, K, N, R, rowwise), SPTP_WS_HEADER_BYTES),), torch.uint8, x.device,
+                         stream)
+    code = lib().sptp_lora(x.data_ptr(), A.data_ptr(), B.data_ptr(), ids.data_ptr(), None if gains is None else gains.data_ptr(),
+                           P, M, K, N, R, n, int(rowwise), dt, base.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                           workspace.nbytes, _raw_stream(stream, cur))
+    _check("sptp_lora", code)
+    return out

@@ -38,6 +38,7 @@ enum : int {
     kWhereKvPage = 15,  // a sequence's length or page outside its range
     kWhereKvFull = 16,
     kWhereKvEmpty = 17,
+    kWhereAdapter = 18,  // a row's adapter outside its range
 };
 
 // ---------------------------------------------------------------- rotary positions, paged cache
@@ -97,6 +98,8 @@ struct PagedAttnParams {
     int heads_per_item, head_blocks;  // query heads of an item, items per key/value head
     int items_per_seq;      // P * Hkv * head_blocks
     float scale;
+    float cap;              // on the scores, 0: none
+    const float* slopes;    // [P][Hq], of the bias by distance, or nullptr
     void* out;              // [P][B][Hq][D]
     float* lse;             // [P][B][Hq] or nullptr
     unsigned long long wait_limit_ns;
@@ -113,11 +116,15 @@ struct PagedAttnParams {
 bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                      uint32_t box_inner, uint32_t box_rows);
 
-// One launch per element type (paged_attn_{bf16,e4m3,f32}.cu): fills in the
-// maps, the boxes and the split of the heads.
+// One launch per element type (paged_attn_{bf16,e4m3,f32}.cu), and one each for
+// scores with a cap or a bias (.._ex.cu): fills in the maps, the boxes and the
+// split of the heads.
 cudaError_t launch_paged_attn_bf16(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_paged_attn_e4m3(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_paged_attn_f32(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn_bf16_ex(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn_e4m3_ex(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_paged_attn_f32_ex(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_paged_attn(PagedAttnParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 // The self-test's form of it, on two CTAs; D <= 128.
 constexpr int kSelftestCtas = 2;

@@ -7,61 +7,13 @@
 #include <cstring>
 
 #include "attn.h"
-#include "checks.h"
+#include "attn_checks.h"
 #include "sptp.h"
 #include "sptp_internal.h"
 
 using namespace sptp;
 
 namespace {
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// One buffer of a call: its bytes, and the alignment its pointer needs.
-struct Buf {
-    const void* p;
-    size_t bytes;
-    size_t align;
-};
-
-int check_aligned(const Buf* b, int n) {
-    for (int i = 0; i < n; ++i)
-        if (b[i].p != nullptr && !aligned_to(b[i].p, b[i].align)) return SPTP_ERR_SHAPE;
-    return SPTP_OK;
-}
-
-// No output on top of an input or of another output.
-int check_alias(const Buf* outs, int n_out, const Buf* ins, int n_in) {
-    for (int o = 0; o < n_out; ++o) {
-        for (int i = 0; i < n_in; ++i)
-            if (overlaps(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes)) return SPTP_ERR_ALIAS;
-        for (int j = o + 1; j < n_out; ++j)
-            if (overlaps(outs[o].p, outs[o].bytes, outs[j].p, outs[j].bytes)) return SPTP_ERR_ALIAS;
-    }
-    return SPTP_OK;
-}
-
-int check_heads(int P, int Hq, int Hkv, int D) {
-    if (P < 1 || P > kMaxGroups || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return SPTP_ERR_SHAPE;
-    if (D < 8 || D > 256 || D % 8 != 0) return SPTP_ERR_SHAPE;
-    if (static_cast<long long>(P) * (Hq + 2ll * Hkv) >= (1ll << 24)) return SPTP_ERR_SHAPE;
-    return SPTP_OK;
-}
-
-int check_cache(int P, int Hkv, int D, int B, int max_pages, int num_pages, int page_size, int dtype, int kv_type) {
-    if (!dtype_ok(dtype) || (kv_type != SPTP_KV_SAME && kv_type != SPTP_KV_E4M3)) return SPTP_ERR_DTYPE;
-    if (kv_type == SPTP_KV_E4M3 && dtype != SPTP_BF16) return SPTP_ERR_DTYPE;
-    if (kv_type == SPTP_KV_E4M3 && D % 16 != 0) return SPTP_ERR_SHAPE;
-    if (B < 0 || max_pages < 1 || num_pages < 1 || page_size < 16 || page_size % 16 != 0) return SPTP_ERR_SHAPE;
-    if (static_cast<long long>(max_pages) * page_size >= (1ll << 30)) return SPTP_ERR_SHAPE;
-    // rows of the pool (a TMA coordinate), each product below 2^31 before the next
-    long long rows = static_cast<long long>(num_pages) * page_size;
-    if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
-    rows *= P;
-    if (rows >= (1ll << 31)) return SPTP_ERR_SHAPE;
-    rows *= Hkv;
-    return rows < (1ll << 31) ? SPTP_OK : SPTP_ERR_SHAPE;
-}
 
 // Query heads whose parts one CTA of the attention may leave, at most.
 int part_heads(int group) { return group < 32 ? group : 32; }
@@ -80,15 +32,9 @@ PagedLayout paged_layout(int group, int D) {
     return L;
 }
 
-// Elements of an activation tensor, M rows; -1 if it is beyond any GPU (and the
-// kernels' 32-bit row numbers).
-long long elems(long long P, long long M, long long heads, long long D) {
-    const long long row = P * heads * D;  // < 2^32
-    return M < (1ll << 30) && M <= (1ll << 42) / row ? M * row : -1;
-}
-
-// sptp_paged_attn_decode, and its self-test.
-int attend(const sptp_paged_attn_decode_args& a, unsigned long long limit_ns, int withhold_full, int withhold_empty) {
+// sptp_paged_attn_decode, with a cap and slopes, and its self-test.
+int attend(const sptp_paged_attn_decode_args& a, float cap, const float* slopes, unsigned long long limit_ns,
+           int withhold_full, int withhold_empty) {
     const bool e4m3 = a.kv_type == SPTP_KV_E4M3;
     if (!a.k_cache || !a.v_cache || !a.workspace || (e4m3 && (!a.k_scale || !a.v_scale)) ||
         (a.B != 0 && (!a.q || !a.page_table || !a.seq_lens || !a.out)))
@@ -97,7 +43,7 @@ int attend(const sptp_paged_attn_decode_args& a, unsigned long long limit_ns, in
     if (rc == SPTP_ERR_DTYPE) return rc;
     int rc2 = check_heads(a.P, a.Hq, a.Hkv, a.D);
     if (rc2 != SPTP_OK || rc != SPTP_OK) return SPTP_ERR_SHAPE;
-    if (a.window < 0 || !std::isfinite(a.scale)) return SPTP_ERR_SHAPE;
+    if (a.window < 0 || !std::isfinite(a.scale) || !score_cap_ok(cap)) return SPTP_ERR_SHAPE;
     const long long n = elems(a.P, a.B, a.Hq, a.D);
     if (n < 0) return SPTP_ERR_SHAPE;
     const sptp_dtype dtype = static_cast<sptp_dtype>(a.dtype);
@@ -107,11 +53,12 @@ int attend(const sptp_paged_attn_decode_args& a, unsigned long long limit_ns, in
     const Buf ins[] = {{a.q, qb, 16}, {a.k_cache, cb, 16}, {a.v_cache, cb, 16},
                        {e4m3 ? a.k_scale : nullptr, sb, 16}, {e4m3 ? a.v_scale : nullptr, sb, 16},
                        {a.page_table, static_cast<size_t>(a.B) * a.max_pages * 4, 4},
-                       {a.seq_lens, static_cast<size_t>(a.B) * 4, 4}};
+                       {a.seq_lens, static_cast<size_t>(a.B) * 4, 4},
+                       {slopes, static_cast<size_t>(a.P) * a.Hq * 4, 4}};
     const Buf outs[] = {{a.out, qb, 16}, {a.lse, static_cast<size_t>(a.P) * a.B * a.Hq * 4, 16}, {a.workspace, need, kAlign}};
-    if ((rc = check_aligned(ins, 7)) != SPTP_OK || (rc = check_aligned(outs, 3)) != SPTP_OK) return rc;
+    if ((rc = check_aligned(ins, 8)) != SPTP_OK || (rc = check_aligned(outs, 3)) != SPTP_OK) return rc;
     if (a.ws_bytes < need) return SPTP_ERR_WORKSPACE;
-    if ((rc = check_alias(outs, 3, ins, 7)) != SPTP_OK) return rc;
+    if ((rc = check_alias(outs, 3, ins, 8)) != SPTP_OK) return rc;
     if (a.B == 0) return SPTP_OK;
     DevInfo di;
     if ((rc = device_info(&di)) != SPTP_OK) return rc;
@@ -134,6 +81,8 @@ int attend(const sptp_paged_attn_decode_args& a, unsigned long long limit_ns, in
     p.page_size = a.page_size;
     p.window = a.window;
     p.scale = a.scale;
+    p.cap = cap;
+    p.slopes = slopes;
     p.out = a.out;
     p.lse = static_cast<float*>(a.lse);
     p.wait_limit_ns = limit_ns;
@@ -316,7 +265,7 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
     a.dtype = dtype;
     a.kv_type = kv_type;
     a.scale = scale;
-    return attend(a, kWaitLimitNs, -1, -1);
+    return attend(a, 0.f, nullptr, kWaitLimitNs, -1, -1);
 }
 
 int sptp_rope_packed(const sptp_rope_args* a) {
@@ -337,7 +286,11 @@ int sptp_rope_append_kv_packed(const sptp_rope_append_kv_args* a) {
 }
 
 int sptp_paged_attn_decode_packed(const sptp_paged_attn_decode_args* a) {
-    return a ? attend(*a, kWaitLimitNs, -1, -1) : SPTP_ERR_NULL;
+    return a ? attend(*a, 0.f, nullptr, kWaitLimitNs, -1, -1) : SPTP_ERR_NULL;
+}
+
+int sptp_paged_attn_decode_ex(const sptp_paged_attn_decode_args* a, float cap, const float* slopes) {
+    return a ? attend(*a, cap, slopes, kWaitLimitNs, -1, -1) : SPTP_ERR_NULL;
 }
 
 int sptp_paged_attn_wait_selftest(const sptp_paged_attn_decode_args* a, int withhold_full, int withhold_empty,
@@ -345,7 +298,7 @@ int sptp_paged_attn_wait_selftest(const sptp_paged_attn_decode_args* a, int with
     if (!a) return SPTP_ERR_NULL;
     if (limit_ns == 0 || limit_ns > 10000000000ull || a->D > 128) return SPTP_ERR_SHAPE;
     if ((withhold_full < 0) == (withhold_empty < 0)) return SPTP_ERR_SHAPE;
-    return attend(*a, limit_ns, withhold_full, withhold_empty);
+    return attend(*a, 0.f, nullptr, limit_ns, withhold_full, withhold_empty);
 }
 
 }  // extern "C"

@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "attn.h"
+#include "attn_scores.cuh"
 #include "sptp.h"
 #include "sptp_ptx.cuh"
 
@@ -189,9 +190,13 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 //   HEADS, TEAMS, DP       query heads of a team, teams, elements of a row, at most
 //   TK                     keys of a tile
 //   ROW_BYTES, BOXES       a key's bytes, TMA boxes per row
-//   begin(q, keep, heads)  a new item; q its rows in shared memory, keep room for
-//                          them (KEEP_BYTES); no barrier of the warps
-//   tile(...)              keys [lo, hi) of a tile; false if a warp's `ok` is
+//   MODS                   scores have a cap, a bias by distance, or both (a
+//                          class of their own: plain scores pay nothing)
+//   begin(q, keep, heads, slopes)  a new item; q its rows in shared memory, keep
+//                          room for them (KEEP_BYTES), slopes its heads' or
+//                          nullptr; no barrier of the warps
+//   tile(...)              keys [lo, hi) of a tile, whose key 0 is `far` before the
+//                          new token; false if a warp's `ok` is
 //   finish(...)            an item's end, or its part's
 
 // Tensor-core consumer for a bf16 or E4M3 cache, DP >= D elements per row, up
@@ -220,10 +225,10 @@ __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float(stati
 // loses all of that and is hardly faster: 96 sequences 50.5 and 50.7 us; 64 of
 // 2500 keys with 16 heads per key head, D = 64, 128 and 256, 51.9 / 72.4 /
 // 144.3 and 53.2 / 73.2 / 149.0.)
-template <int DP_, int NT_, bool CODES_, int TEAMS_ = 1>
+template <int DP_, int NT_, bool CODES_, int TEAMS_ = 1, bool MODS_ = false>
 struct TcConsumer {
     static constexpr int DP = DP_, NT = NT_, TEAMS = TEAMS_;
-    static constexpr bool CODES = CODES_;
+    static constexpr bool CODES = CODES_, MODS = MODS_;
     static constexpr bool F32 = false;
     static constexpr int HEADS = 8 * NT;
     static constexpr int ROW_BYTES = DP * (CODES ? 1 : 2);
@@ -256,6 +261,8 @@ struct TcConsumer {
     float m2[NT][2];  // E4M3: M2
     static constexpr int kRoom = 13, kRoomQ = 14;
     float o[MTILES][NT][4];
+    float slope[NT][2];  // MODS, in units of log 2
+    ScoreCap cap{0.f};   // MODS
 
     // element of the head's row in o[t][..][2 r + ..]
     static __device__ __forceinline__ int elem(int t, int r) {
@@ -263,8 +270,19 @@ struct TcConsumer {
         return warp * (DP / kTeam) + t * 16 + (CODES ? 2 * g + r : g + 8 * r);
     }
 
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, uint8_t*, int heads) {
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* q, uint8_t*, int heads,
+                                          const float* slopes) {
         const int lane = threadIdx.x & 31, g = lane >> 2, i = lane & 3;
+        if constexpr (MODS) {
+            cap = ScoreCap(p.cap);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = nt * 8 + 2 * i + e;
+                    slope[nt][e] = slopes != nullptr && h < heads ? __ldg(slopes + h) * kLog2e : 0.f;
+                }
+        }
         const float to_log2 = p.scale * 1.4426950408889634f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -327,14 +345,14 @@ struct TcConsumer {
     // (Whole tiles have code of their own, without a branch that would keep the
     // loads and products of one step apart from the next one's.)
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float* scales, float* maxima, uint8_t* weights,
-                                         int lo, int hi) {
-        return lo == 0 && hi == TK ? tile_of<false>(ok, stage, scales, maxima, weights, lo, hi)
-                                   : tile_of<true>(ok, stage, scales, maxima, weights, lo, hi);
+                                         int lo, int hi, int far) {
+        return lo == 0 && hi == TK ? tile_of<false>(ok, stage, scales, maxima, weights, lo, hi, far)
+                                   : tile_of<true>(ok, stage, scales, maxima, weights, lo, hi, far);
     }
 
     template <bool partial>
     __device__ __forceinline__ bool tile_of(bool ok, uint32_t stage, const float* scales, float* maxima,
-                                            uint8_t* weights, int lo, int hi) {
+                                            uint8_t* weights, int lo, int hi, int far) {
         const int lane = threadIdx.x & 31, warp = team_warp(), g = lane >> 2, i = lane & 3;
         const int key0 = warp * 16 * SLICES;  // this warp's keys of the tile
         const bool some = !partial || (key0 < hi && key0 + 16 * SLICES > lo);
@@ -389,7 +407,13 @@ struct TcConsumer {
                         for (int e = 0; e < 2; ++e) {
                             float& v = s[sl][nt][2 * r + e];
                             v += s2[nt][2 * r + e];
-                            v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
+                            if constexpr (MODS) {
+                                v = CODES ? v * ks * qs[nt][e] : v * qs[nt][e];
+                                if (cap.cap != 0.f) v = cap(v);
+                                v = in ? fmaf(-slope[nt][e], static_cast<float>(far - key), v) : -INFINITY;
+                            } else {
+                                v = in ? (CODES ? v * ks * qs[nt][e] : v * qs[nt][e]) : -INFINITY;
+                            }
                             top[nt][e] = fmaxf(top[nt][e], v);
                             if constexpr (CODES) top2[nt][e] = fmaxf(top2[nt][e], v + vlog[sl][r]);
                         }
@@ -629,10 +653,10 @@ struct TcConsumer {
 // for the HPW heads of its warp, and sums up four elements of the values of one
 // key in KEYS_A_STEP: each query read serves two products, each weight four.
 // The swizzle that TMA leaves the rows in keeps the lanes' reads apart.
-template <int DP_, int TEAMS_ = 1>
+template <int DP_, int TEAMS_ = 1, bool MODS_ = false>
 struct F32Consumer {
     static constexpr int DP = DP_, TEAMS = TEAMS_;
-    static constexpr bool CODES = false;
+    static constexpr bool CODES = false, MODS = MODS_;
     static constexpr bool F32 = true;
     static constexpr int HEADS = 8;
     static constexpr int ELEM = 4;  // bytes
@@ -664,8 +688,11 @@ struct F32Consumer {
     float l[HPW];              // of this lane's keys
     float to_log2;
     int heads;
+    float slope[HPW];   // MODS, in units of log 2
+    ScoreCap cap{0.f};  // MODS
 
-    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* rows, uint8_t* keep, int n) {
+    __device__ __forceinline__ void begin(const PagedAttnParams& p, const uint8_t* rows, uint8_t* keep, int n,
+                                          const float* slopes) {
         // the stage that the queries came with is given back: this warp's heads
         // are copied, cleared where the item has no head or the row no element
         const int lane = threadIdx.x & 31, warp = team_warp(), h0 = warp / KEY_GROUPS * HPW;
@@ -678,6 +705,12 @@ struct F32Consumer {
             *reinterpret_cast<float4*>(mine + h * ROW_BYTES + d * 4) = v;
         }
         __syncwarp();
+        if constexpr (MODS) {
+            cap = ScoreCap(p.cap);
+#pragma unroll
+            for (int h = 0; h < HPW; ++h)
+                slope[h] = slopes != nullptr && h0 + h < n ? __ldg(slopes + h0 + h) * kLog2e : 0.f;
+        }
         q = mine;
         heads = n;
         to_log2 = p.scale * 1.4426950408889634f;
@@ -691,7 +724,7 @@ struct F32Consumer {
     }
 
     __device__ __forceinline__ bool tile(bool ok, uint32_t stage, const float*, float* maxima, uint8_t* weights, int lo,
-                                         int hi) {
+                                         int hi, int far) {
         const int lane = threadIdx.x & 31, warp = team_warp();
         const int key0 = KEY_GROUPS > 1 ? warp % KEY_GROUPS * 32 : 0;
         const int key = key0 + lane % LANES;     // whose scores this lane holds in the end
@@ -748,7 +781,13 @@ struct F32Consumer {
         float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPW; ++h) {
-            x[h] = in ? x[h] * to_log2 : -INFINITY;
+            if constexpr (MODS) {
+                x[h] *= to_log2;
+                if (cap.cap != 0.f) x[h] = cap.cap * tanhf(x[h] * cap.inv);
+                x[h] = in ? fmaf(-slope[h], static_cast<float>(far - key), x[h]) : -INFINITY;
+            } else {
+                x[h] = in ? x[h] * to_log2 : -INFINITY;
+            }
             float t = x[h];
 #pragma unroll
             for (int off = 1; off < LANES; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
@@ -909,6 +948,8 @@ struct Meta {       // of a ring stage, written by the producer
     int heads;       // of the item
     int lo, hi;      // keys of the tile that count
     int flags;
+    int far;         // MODS: distance of the tile's key 0 from the new token
+    int slope0;      // MODS: the first head's slope
 };
 enum : int {
     kFirst = 1,       // the first tile of an item or of this share
@@ -1125,7 +1166,7 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         Cursor<TK> c = share_at;
         bool more = c.b >= 0, fresh = true;  // fresh: the first item of this share
         if (!more) {
-            if (lane == 0) meta[0] = Meta{0, 0, 0, 0, kEnd};
+            if (lane == 0) meta[0] = Meta{0, 0, 0, 0, kEnd, 0, 0};
             __syncwarp();
             if (C::CODES || lane == 0) mbar_arrive(&full[0]);
             if (C::CODES && lane == 0) mbar_arrive(&full[0]);
@@ -1221,6 +1262,10 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
                         md.heads = heads;
                         md.lo = max(0, c.s.start - tile0);
                         md.hi = max(0, min(TK, c.s.len - tile0));
+                        if constexpr (C::MODS) {
+                            md.far = c.s.len - 1 - tile0;
+                            md.slope0 = shard * p.Hq + kvh * group + h0;
+                        }
                         md.flags = (first ? kFirst | (begins ? kItemBegins : 0) : 0) |
                                    (last ? kLast | (ends ? kItemEnds : 0) | (more ? 0 : kEnd) : 0);
                         meta[s] = md;
@@ -1288,17 +1333,18 @@ __global__ void __launch_bounds__(32 * (kTeam * C::TEAMS + 1), C::CTAS)
         uint32_t phase = 0;
         for (int i = 0, s = 0;; ++i) {
             const bool ok = warp_wait(&full[s], phase, wc, kWhereKvFull, i);
-            const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0};
+            const Meta md = ok ? meta[s] : Meta{0, 0, 0, 0, 0, 0, 0};
             // this team's heads: an equal part of the item's
             const int part_heads = (md.heads + C::TEAMS - 1) / C::TEAMS, h0 = team_index() * part_heads;
             const int heads = max(0, min(part_heads, md.heads - h0));
             if (md.flags & kFirst || i == 0) {
-                c.begin(p, smem + L::QROWS + s * L::Q_BYTES + h0 * C::Q_STRIDE, keep, heads);
+                c.begin(p, smem + L::QROWS + s * L::Q_BYTES + h0 * C::Q_STRIDE, keep, heads,
+                        C::MODS && p.slopes != nullptr ? p.slopes + md.slope0 + h0 : nullptr);
                 begun = (md.flags & kItemBegins) != 0;
             }
             if (!c.tile(ok, smem_u32(smem) + s * L::STAGE_BYTES,
                         reinterpret_cast<const float*>(smem + L::SCALES + s * 2 * L::SCALE_BYTES),
-                        stats + (i & 1) * L::MAXIMA, weights + (i & 1) * C::W_BYTES, md.lo, md.hi))
+                        stats + (i & 1) * L::MAXIMA, weights + (i & 1) * C::W_BYTES, md.lo, md.hi, md.far))
                 break;
             __syncwarp();
             if (lane == 0 && !(TEST && blockIdx.x == 0 && i == p.withhold_empty)) mbar_arrive(&empty[s]);

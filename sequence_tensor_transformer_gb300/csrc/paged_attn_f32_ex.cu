@@ -1,0 +1,10 @@
+// Paged attention over an fp32 cache: the CUDA-core consumer, scores with a cap or a bias.
+#include "paged_attn_launch.cuh"
+
+namespace sptp {
+
+cudaError_t launch_paged_attn_f32_ex(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    return paged::launch_simt<true>(p, num_sms, ctas, s);
+}
+
+}  // namespace sptp

@@ -52,6 +52,39 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
     return launch_after(paged_attn_kernel<C, TEST>, *ctas, 32 * (kTeam * C::TEAMS + 1), Smem<C>::BYTES, s, p);
 }
 
+// The tensor-core consumer by row width and heads per item.
+template <bool CODES, bool MODS>
+cudaError_t launch_tc(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    const int group = p.Hq / p.Hkv;
+    if (p.D <= 64) {
+        if (group <= 8) return launch<TcConsumer<64, 1, CODES, 1, MODS>>(p, num_sms, ctas, s);
+        if (group <= 16) return launch<TcConsumer<64, 2, CODES, 1, MODS>>(p, num_sms, ctas, s);
+        return launch<TcConsumer<64, 2, CODES, 2, MODS>>(p, num_sms, ctas, s);
+    }
+    if (p.D <= 128) {
+        if (group <= 8) return launch<TcConsumer<128, 1, CODES, 1, MODS>>(p, num_sms, ctas, s);
+        if (group <= 16) return launch<TcConsumer<128, 2, CODES, 1, MODS>>(p, num_sms, ctas, s);
+        return launch<TcConsumer<128, 2, CODES, 2, MODS>>(p, num_sms, ctas, s);
+    }
+    // rows of more than 128 elements: 16 heads are what the registers hold
+    if (group <= 8) return launch<TcConsumer<256, 1, CODES, 1, MODS>>(p, num_sms, ctas, s);
+    return launch<TcConsumer<256, 2, CODES, 1, MODS>>(p, num_sms, ctas, s);
+}
+
+// The CUDA-core consumer by row width and heads per item.
+template <bool MODS>
+cudaError_t launch_simt(PagedAttnParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    const int group = p.Hq / p.Hkv;
+    if (group <= 8) {
+        if (p.D <= 64) return launch<F32Consumer<64, 1, MODS>>(p, num_sms, ctas, s);
+        if (p.D <= 128) return launch<F32Consumer<128, 1, MODS>>(p, num_sms, ctas, s);
+        return launch<F32Consumer<256, 1, MODS>>(p, num_sms, ctas, s);
+    }
+    if (p.D <= 64) return launch<F32Consumer<64, 2, MODS>>(p, num_sms, ctas, s);
+    if (p.D <= 128) return launch<F32Consumer<128, 2, MODS>>(p, num_sms, ctas, s);
+    return launch<F32Consumer<256, 2, MODS>>(p, num_sms, ctas, s);
+}
+
 }  // namespace
 }  // namespace paged
 }  // namespace sptp

@@ -39,6 +39,11 @@ enum : int {
     kWhereKvFull = 16,
     kWhereKvEmpty = 17,
     kWhereAdapter = 18,  // a row's adapter outside its range
+    kWherePromptItem = 27,
+    kWherePromptQuery = 28,
+    kWherePromptScores = 29,
+    kWherePromptWeights = 30,
+    kWherePromptOutputs = 31,
 };
 
 // ---------------------------------------------------------------- rotary positions, paged cache
@@ -115,6 +120,10 @@ struct PagedAttnParams {
 // or of 64 where a box's rows have 64.
 bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                      uint32_t box_inner, uint32_t box_rows);
+
+// The queries of sptp_paged_attn_prompt, bf16 [P][M][Hq][D]: boxes of 64 elements
+// of `heads` heads of `tokens` rows, swizzle of 128 bytes.
+bool encode_map_queries(CUtensorMap* map, const void* base, int D, int Hq, int M, int P, int heads, int tokens);
 
 // One launch per element type (paged_attn_{bf16,e4m3,f32}.cu), and one each for
 // scores with a cap or a bias (.._ex.cu): fills in the maps, the boxes and the

@@ -50,4 +50,18 @@ bool encode_map_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_
               promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_map_queries(CUtensorMap* map, const void* base, int D, int Hq, int M, int P, int heads, int tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2, token = row * Hq;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(M),
+                          static_cast<cuuint64_t>(P)};
+    cuuint64_t strides[3] = {row, token, token * M};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace sptp

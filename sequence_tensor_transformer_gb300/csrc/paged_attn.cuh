@@ -1016,24 +1016,6 @@ struct Cursor {
     }
 };
 
-// Sixteen bytes to shared memory behind the thread's back, or zeros.
-__device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, bool has) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(has ? 16 : 0)
-                 : "memory");
-}
-
-// One of the arrivals that `bar` expects, once the thread's copies so far have landed.
-__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// mbar_wait by a whole warp: true if every lane's wait was.  A lane gives up by
-// itself (its own clock, or the abort flag seen); what follows a wait has the
-// warp's lanes work together, so they go on or leave as one.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, where, info));
-}
-
 template <class C>
 struct Smem {
     static constexpr int SCALE_BYTES = C::CODES ? C::TK * 4 : 0;

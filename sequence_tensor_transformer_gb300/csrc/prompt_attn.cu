@@ -171,8 +171,11 @@ int prompt_grid(const PromptParams& p, int most, int tk) {
 
 cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
     int ctas = 0;
-    if (bf16) return cudaErrorNotSupported;  // the tensor-core kernel is not there yet
-    cudaError_t e = launch_prompt_f32(p, num_sms, &ctas, s);
+    // (the plain kernels find a row's maximum among unscaled scores)
+    const bool plain = p.cap == 0.f && p.slopes == nullptr && p.scale > 0.f;
+    const auto codes = plain ? launch_prompt_e4m3 : launch_prompt_e4m3_ex;
+    const auto wide = plain ? launch_prompt_bf16 : launch_prompt_bf16_ex;
+    cudaError_t e = (!bf16 ? launch_prompt_f32 : e4m3 ? codes : wide)(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
     const int grid = ctas * kJoinBlocks + 1;
     return bf16 ? launch_after(prompt_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, s, p, ctas)

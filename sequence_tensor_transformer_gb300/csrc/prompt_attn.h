@@ -59,6 +59,11 @@ struct PromptParams {
 // Rows of an item, at most, by head size and element type.
 constexpr int prompt_item_rows(int D, bool bf16) { return !bf16 ? 64 : D <= 128 ? 256 : 128; }
 
+// (_ex: a cap, a bias or scale <= 0)
+cudaError_t launch_prompt_bf16(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_prompt_bf16_ex(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_prompt_e4m3(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
+cudaError_t launch_prompt_e4m3_ex(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_prompt_f32(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
 cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 // The split of the heads and rows into items of at most `rows` rows whose tiles

@@ -1,0 +1,806 @@
+// The attention of sptp_paged_attn_prompt on the tensor cores:
+//     s_j = cap tanh(scale q.k_j / cap) - slope |pos - j|,
+//     out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
+// one pass over the keys with a running maximum m and sum per row (in the kernel:
+// powers of two, scores in units of log 2).
+//
+// Bound by the tensor cores for many rows: 4 D flops per row and key.  A CTA has
+// two tiles of 128 query rows (rows of 128 < D <= 256: one), token by token with
+// the query heads of one key/value head side by side, so that few tokens of a
+// large group fill a tile too; both read the same tiles of TK keys.  Scores S =
+// Q K^T (both operands from shared memory) and outputs O += P V (weights P from
+// tensor memory, where they take the place of their scores) are tcgen05 products
+// with fp32 sums in tensor memory.
+//  - One warp walks over the CTA's share (prompt_plan.cuh) and keeps a ring of K
+//    and V tiles filled by TMA, a box per page; it leaves a description of each
+//    item for the others.
+//  - One warp issues the products.  While a tile of rows is in its softmax, the
+//    other one's products run: S of the next keys is issued right behind the O
+//    of the last ones.
+//  - E4M3: four warps turn the tiles of codes that TMA brings into bf16 tiles,
+//    code times the row's power of two, which is exact; the rest is the same.
+//  - Four warps per tile of rows do its softmax, a thread a row, scores in
+//    registers: no exchange between threads.  The maximum that the weights refer
+//    to only moves when a score is 2^8 times above it, so that the outputs in
+//    tensor memory are rarely rescaled; weights stay below 2^8 until then, and
+//    bf16 holds them as exactly as below 1.
+#pragma once
+
+#include <atomic>
+#include <cuda_bf16.h>
+
+#include "attn_scores.cuh"
+#include "prompt_plan.cuh"
+#include "sptp.h"
+
+namespace sptp {
+namespace prompt {
+
+constexpr int kTileRows = 128;
+constexpr float kSlack = 8.f;  // log 2 units that a score may be above the maximum in use
+constexpr int kItems = 4;      // descriptions under way
+
+enum : int { kBegins = 1, kEnds = 2, kStop = 4 };
+
+// An item's part that the CTA works on, from the producer to the others.
+struct Work {
+    long long token0;      // shard * M + first row
+    int flags;
+    int here, key0;        // tiles of keys, first key
+    int a[2], b[2];        // tiles [a, b) of them that each tile of rows sees
+    int n, heads;          // rows are token * heads + head
+    int head0, slope0;     // of the shard; index in slopes
+    int pos0, len, prefix;
+    int lo, hi;            // keys that any row sees
+};
+
+template <int DP_, bool CODES_>
+struct Shape {
+    static constexpr int DP = DP_;                      // elements of a row, at most
+    static constexpr bool CODES = CODES_;               // an E4M3 cache
+    static constexpr int NQ = DP <= 128 ? 2 : 1;        // tiles of rows
+    static constexpr int TK = DP <= 128 ? 128 : 64;     // keys of a tile
+    static constexpr int CB = DP / 64;                  // 128-byte columns of a row
+    static constexpr int Q_BYTES = kTileRows * DP * 2;  // a tile of rows
+    static constexpr int SLOT = TK * DP * 2;            // a tile of K or V
+    static constexpr int SLOTS = DP == 64 ? 8 : CODES ? 4 : 5;
+    // E4M3: two tiles of codes in columns of SPAN bytes, and their scales
+    static constexpr int SPAN = DP == 64 ? 64 : 128, CODE_BOXES = DP / SPAN;
+    static constexpr int STAGES = 2, STAGE = TK * DP;
+    static constexpr int CODES_AT = NQ * Q_BYTES + SLOTS * SLOT, SCALES_AT = CODES_AT + (CODES ? STAGES * STAGE : 0);
+    static constexpr int BYTES = SCALES_AT + (CODES ? STAGES * TK * 4 : 0) + 1024;
+    // warps: softmax, four for the others, four that convert codes; registers of a
+    // thread of each, and of all at launch (their shares make up the launch's total)
+    static constexpr int PRODUCER = 4 * NQ, ISSUER = 4 * NQ + 1, CONVERTER = 4 * NQ + 4;
+    static constexpr int WARPS = CONVERTER + (CODES ? 4 : 0);
+    static constexpr bool SPLIT_REGS = NQ == 2;
+    static constexpr int LAUNCH_REGS = WARPS == 16 ? 128 : 168;
+    static constexpr int SOFTMAX_REGS = WARPS == 16 ? 176 : 208;
+    static constexpr int OTHER_REGS = WARPS == 16 ? 72 : 88;
+    static constexpr int CONVERTER_REGS = 88;
+    static_assert(!SPLIT_REGS || 4 * NQ * SOFTMAX_REGS + 4 * OTHER_REGS + (WARPS - CONVERTER) * CONVERTER_REGS <=
+                                     WARPS * LAUNCH_REGS,
+                  "setmaxnreg waits for registers that nobody gives back");
+    // tensor memory columns
+    static constexpr int S = 128;                       // between the tiles' scores
+    static constexpr int O = 256;                       // first of the outputs; DP between the tiles'
+};
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// D (+)= A B with A (128 x 16 bf16, two elements a column) in tensor memory.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of a V tile as the second operand: TK rows (the inner dimension) of
+// 128 bytes, 128-byte swizzle, elements along the rows: 8 rows are 1024 bytes
+// apart, columns of 64 elements `column` bytes.
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t smem_addr, uint32_t column) {
+    uint64_t desc = 0;
+    desc |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    desc |= static_cast<uint64_t>(column >> 4) << 16;
+    desc |= static_cast<uint64_t>(1024u >> 4) << 32;
+    desc |= static_cast<uint64_t>(1u) << 46;
+    desc |= static_cast<uint64_t>(2u) << 61;
+    return desc;
+}
+constexpr uint32_t kSecondByRows = 1u << 16;  // instruction descriptor: the second operand lies along its other dimension
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two E4M3 codes (bytes 0 and 1, or 2 and 3 of c) as bf16, times `scale` twice.  A
+// code's exponent and mantissa at the end of bf16's exponent are its value times
+// 2^-120, subnormals included: times 2^120, and then the row's scale.  Both are
+// powers of two, so nothing is rounded.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t c, bool upper, __nv_bfloat162 scale) {
+    const uint32_t t = __byte_perm(c, 0, upper ? 0x3424 : 0x1404);
+    const uint32_t bits = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+    const __nv_bfloat162 unit = __floats2bfloat162_rn(1.329227995784916e36f, 1.329227995784916e36f);  // 2^120
+    const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), unit), scale);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int REGS>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void leave_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <class C>
+struct Bars {
+    uint64_t c_full[C::STAGES], c_empty[C::STAGES];  // E4M3: tiles of codes
+    uint64_t full[C::SLOTS], empty[C::SLOTS];  // K and V tiles
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2];                        // scores in tensor memory (and all products before them done)
+    uint64_t p_ready[2];                       // weights there, outputs rescaled
+    uint64_t o_full[2];                        // outputs of an item done
+    uint64_t w_full[kItems], w_empty[kItems];  // descriptions
+    uint64_t drain;
+    Work work[kItems];
+    uint32_t tmem;
+    int abort_flag;
+    DeviceStatus status;
+    int out_of_range, out_of_range_at;
+};
+
+// ---------------------------------------------------------------- softmax of one tile of rows
+template <class C, bool MODS>
+struct Softmax {
+    static constexpr int TK = C::TK;
+
+    float m, l;  // the maximum in use, in units of log 2; the sum
+    float to_log2, slope;
+    int lo, hi, pos;  // keys that this row sees; its position
+
+    // A tile of keys from key0 on: weights to P, the outputs rescaled if the maximum moved.
+    __device__ __forceinline__ void tile(const PromptParams& p, const ScoreCap& cap, uint32_t s_at, uint32_t o_at, int o_cols,
+                                         int key0, bool first) {
+        uint32_t raw[TK / 32][32];
+#pragma unroll
+        for (int c = 0; c < TK / 32; ++c) tmem_ld_32cols(s_at + c * 32, raw[c]);
+        tmem_ld_wait();
+        auto s = [&](int j) -> float& { return reinterpret_cast<float&>(raw[j / 32][j % 32]); };
+        if constexpr (MODS) {
+            if (p.cap != 0.f) {
+#pragma unroll
+                for (int j = 0; j < TK; ++j) s(j) = cap(s(j) * to_log2);
+            } else {
+#pragma unroll
+                for (int j = 0; j < TK; ++j) s(j) *= to_log2;
+            }
+            if (p.slopes != nullptr) {
+                const float from = static_cast<float>(pos - key0);
+                if (p.prefix_lens == nullptr) {  // no key behind pos is seen
+#pragma unroll
+                    for (int j = 0; j < TK; ++j) s(j) = fmaf(-slope, from - j, s(j));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < TK; ++j) s(j) = fmaf(-slope, fabsf(from - j), s(j));
+                }
+            }
+        }
+        const float unit = MODS ? 1.f : to_log2;
+        const int from = lo - key0, to = hi - key0;
+        if (!(from <= 0 && to >= TK)) {
+#pragma unroll
+            for (int j = 0; j < TK; ++j) s(j) = j >= from && j < to ? s(j) : -INFINITY;
+        }
+        float top[4] = {s(0), s(1), s(2), s(3)};
+#pragma unroll
+        for (int j = 4; j < TK; j += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], s(j + u));
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+        float f = 1.f;
+        const bool moves = now > m + kSlack || (m == -INFINITY && now != -INFINITY);
+        if (moves) {
+            f = pow2_approx(m - now);
+            m = now;
+            l *= f;
+        }
+        if (!first && __any_sync(0xffffffffu, moves)) {
+#pragma unroll 1
+            for (int c = 0; c < o_cols; c += 16) {
+                uint32_t o[16];
+                tmem_ld_16cols(o_at + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_16cols(o_at + c, o);
+            }
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < TK / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float a = pow2_approx(MODS ? s(c * 32 + j) + base : fmaf(s(c * 32 + j), unit, base));
+                const float b = pow2_approx(MODS ? s(c * 32 + j + 1) + base : fmaf(s(c * 32 + j + 1), unit, base));
+                sum[j & 2] += a;
+                sum[(j & 2) + 1] += b;
+                w[j / 2] = pack_bf16(a, b);
+            }
+            tmem_st_16cols(s_at + c * 16, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+    }
+};
+
+template <class C, bool MODS, bool TEST = false>
+__global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __grid_constant__ PromptParams p) {
+    constexpr int TK = C::TK, NQ = C::NQ, kThreads = 32 * C::WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* slots = smem + NQ * C::Q_BYTES;
+    uint8_t* codes = smem + C::CODES_AT;                              // E4M3
+    float* scales = reinterpret_cast<float*>(smem + C::SCALES_AT);  // E4M3: [STAGES][TK]
+    __shared__ Bars<C> bars;
+    __shared__ long long warp_cost[C::WARPS];
+    __shared__ Cursor<TK> share_at;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    admit_next();
+    if (tid == 0) {
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(&bars.full[s], C::CODES ? 4 : 1);
+            mbar_init(&bars.empty[s], 1);
+        }
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&bars.c_full[s], 1 + 32);
+            mbar_init(&bars.c_empty[s], 4);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars.q_full[t], 1);
+            mbar_init(&bars.q_empty[t], 1);
+            mbar_init(&bars.s_full[t], 1);
+            mbar_init(&bars.p_ready[t], kTileRows);
+            mbar_init(&bars.o_full[t], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&bars.w_full[i], 1);
+            mbar_init(&bars.w_empty[i], 4 * NQ + 1 + (C::CODES ? 4 : 0));
+        }
+        mbar_init(&bars.drain, 1);
+        fence_mbar_init();
+        bars.abort_flag = 0;
+        bars.status.code = bars.status.where = bars.status.info = 0;
+        bars.out_of_range = bars.out_of_range_at = 0;
+        tma_prefetch_map(&p.map_q);
+        tma_prefetch_map(&p.map_k);
+        tma_prefetch_map(&p.map_v);
+    }
+    if (warp == C::ISSUER) {
+        tmem_alloc(&bars.tmem, 512);
+        tmem_relinquish();
+    }
+    await_previous();
+    tc_fence_before();
+    bool bad = false;
+    __syncthreads();
+    const Share share = find_share<TK, kThreads>(p, warp_cost, &share_at, &bad);
+    tc_fence_after();
+    if (bad) bars.out_of_range = 1;
+    const uint32_t tmem = bars.tmem;
+    WaitCtx wc{&bars.status, &bars.abort_flag, p.wait_limit_ns};
+    PromptPart* part = p.parts + blockIdx.x;
+
+    // (setmaxnreg: one instruction for all four warps of a group)
+    if (warp < C::PRODUCER) {
+        if constexpr (C::SPLIT_REGS) take_registers<C::SOFTMAX_REGS>();
+        // -------------------------------------------------- softmax, a thread a row
+        const int t = warp / 4, r = tid % kTileRows;
+        const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lane_at + t * C::S, o_at = tmem + lane_at + C::O + t * C::DP;
+        const int o_cols = (p.D + 15) / 16 * 16;
+        const ScoreCap cap(p.cap);
+        Softmax<C, MODS> sm;
+        sm.to_log2 = p.scale * kLog2e;
+        int w = 0;
+        uint32_t w_phase = 0, s_phase = 0, o_phase = 0;
+        while (true) {
+            if (!warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, -1)) break;
+            const Work& d = bars.work[w];
+            if (d.flags & kStop) break;
+            const int heads = d.heads, tile_tokens = kTileRows / p.heads;
+            const int local = r / heads, head = r - local * heads, token = t * tile_tokens + local;
+            const bool in = local < tile_tokens && token < d.n;
+            const bool any = t * tile_tokens < d.n;
+            sm.m = -INFINITY;
+            sm.l = 0.f;
+            sm.pos = d.pos0 + token;
+            sm.lo = in ? first_key(p, sm.pos) : 0;
+            sm.hi = in ? min(d.len, end_key(sm.pos, d.prefix)) : 0;
+            sm.slope = MODS && p.slopes != nullptr && in ? __ldg(p.slopes + d.slope0 + head) * kLog2e : 0.f;
+            const int a = d.a[t], b = d.b[t], key0 = d.key0;
+            bool ok = true;
+            for (int j = a; j < b; ++j) {
+                if (!(ok = warp_wait(&bars.s_full[t], s_phase, wc, kWherePromptScores, j))) break;
+                s_phase ^= 1;
+                tc_fence_after();
+                sm.tile(p, cap, s_at, o_at, o_cols, key0 + j * TK, j == a);
+                tc_fence_before();
+                mbar_arrive(&bars.p_ready[t]);
+            }
+            if (!ok) break;
+            if (a < b) {
+                if (!warp_wait(&bars.o_full[t], o_phase, wc, kWherePromptOutputs, b)) break;
+                o_phase ^= 1;
+                tc_fence_after();
+            }
+            if (any) {
+                const bool whole = (d.flags & (kBegins | kEnds)) == (kBegins | kEnds);
+                const long long orow = (d.token0 + token) * p.Hq + d.head0 + head;
+                // slot 1 if the item begins in this share, slot 0 if in an earlier one
+                const int row = token * heads + head;
+                const long long at = (blockIdx.x * 2ll + (d.flags & kBegins ? 1 : 0)) * p.part_rows + row;
+                const float f = !whole ? 1.f : sm.l == 0.f ? 0.f : 1.f / sm.l;
+                if (in) {
+                    if (!whole)
+                        p.part_ml[at] = make_float2(sm.m, sm.l);
+                    else if (p.lse != nullptr)
+                        p.lse[orow] = sm.l == 0.f ? -INFINITY : sm.m * 0.6931471805599453f + logf(sm.l);
+                }
+#pragma unroll 1
+                for (int c0 = 0; c0 < o_cols; c0 += 16) {
+                    uint32_t o[16];
+                    if (a < b) {
+                        tmem_ld_16cols(o_at + c0, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = 0;
+                    }
+                    if (!in) continue;
+#pragma unroll
+                    for (int h = 0; h < 16; h += 8) {
+                        if (c0 + h >= p.D) break;
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[h + i]) * f;
+                        if (whole) {
+                            uint4 u = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                 pack_bf16(v[6], v[7]));
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * p.D + c0 + h) = u;
+                        } else {
+                            float4* to = reinterpret_cast<float4*>(p.part_o + at * p.D + c0 + h);
+                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                }
+                // the outputs are read before the next item's products (issued behind
+                // this thread's next arrival) write there
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.w_empty[w]);
+            if (++w == kItems) {
+                w = 0;
+                w_phase ^= 1;
+            }
+        }
+    } else if (C::CODES && warp >= C::CONVERTER) {
+        if constexpr (C::SPLIT_REGS) leave_registers<C::CONVERTER_REGS>();
+        // -------------------------------------------------- E4M3 tiles to bf16
+        const int me = tid - 32 * C::CONVERTER;
+        constexpr int CHUNKS = C::DP / 16;  // of 16 codes, of a row
+        int stage = 0, slot = 0, w = 0;
+        uint32_t c_phase = 0, phase = 1, w_phase = 0;
+        bool ok = true;
+        while (ok) {
+            if (!warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, -2)) break;
+            const Work& d = bars.work[w];
+            if (d.flags & kStop) break;
+            const int tiles = 2 * d.here;
+            for (int i = 0; i < tiles; ++i) {
+                const int key0 = d.key0 + i / 2 * TK;
+                // V: rows that no row of the batch sees become zeros
+                const int from = i & 1 ? d.lo - key0 : 0, to = i & 1 ? d.hi - key0 : TK;
+                if (!(ok = warp_wait(&bars.c_full[stage], c_phase, wc, kWhereKvFull, i))) break;
+                if (!(ok = warp_wait(&bars.empty[slot], phase, wc, kWhereKvEmpty, i))) break;
+                const uint8_t* in = codes + stage * C::STAGE;
+                uint8_t* out = slots + slot * C::SLOT;
+#pragma unroll 4
+                for (int n = me; n < TK * CHUNKS; n += 128) {
+                    const int row = n / CHUNKS, c = n % CHUNKS;
+                    constexpr int PER = C::SPAN / 16;
+                    const int swizzle = C::SPAN == 128 ? row & 7 : (row >> 1) & 3;
+                    const uint4 u = *reinterpret_cast<const uint4*>(in + c / PER * (TK * C::SPAN) + row * C::SPAN +
+                                                                    (((c % PER) ^ swizzle) << 4));
+                    const float f = scales[stage * TK + row];
+                    const __nv_bfloat162 f2 = __floats2bfloat162_rn(f, f);
+                    uint4 lo = make_uint4(codes_to_bf16(u.x, false, f2), codes_to_bf16(u.x, true, f2),
+                                          codes_to_bf16(u.y, false, f2), codes_to_bf16(u.y, true, f2));
+                    uint4 hi = make_uint4(codes_to_bf16(u.z, false, f2), codes_to_bf16(u.z, true, f2),
+                                          codes_to_bf16(u.w, false, f2), codes_to_bf16(u.w, true, f2));
+                    if (row < from || row >= to) lo = hi = make_uint4(0, 0, 0, 0);
+                    uint8_t* at = out + c / 4 * (TK * 128) + row * 128;
+                    const int p0 = ((c % 4 * 2) ^ (row & 7)) << 4, p1 = ((c % 4 * 2 + 1) ^ (row & 7)) << 4;
+                    // (lanes of every other column the other way round, for the banks' sake)
+                    const bool swap = (c & 4) != 0;
+                    *reinterpret_cast<uint4*>(at + (swap ? p1 : p0)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(at + (swap ? p0 : p1)) = swap ? lo : hi;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.full[slot]);
+                    mbar_arrive(&bars.c_empty[stage]);
+                }
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    c_phase ^= 1;
+                }
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.w_empty[w]);
+            if (++w == kItems) {
+                w = 0;
+                w_phase ^= 1;
+            }
+        }
+    } else {
+        if constexpr (C::SPLIT_REGS) leave_registers<C::OTHER_REGS>();
+        if (warp == C::PRODUCER) {
+            // -------------------------------------------------- producer
+            const int R = p.box_rows, nb = TK / R;
+            const long long numbers = block_numbers(p);
+            const int tile_tokens = kTileRows / p.heads;
+            constexpr int kBadRow = -TK;  // outside the maps, all of a box's rows: zeros
+            if (lane == 0) part->items[0].parts = part->items[1].parts = 0;
+            Cursor<TK> c = share_at;
+            bool more = c.k.tiles != 0, ok = true;
+            int slot = 0, issued = 0, w = 0, q_used[2] = {0, 0};
+            uint32_t phase = 1, w_phase = 1, q_phase[2] = {1, 1};
+            while (ok) {
+                if (!(ok = warp_wait(&bars.w_empty[w], w_phase, wc, kWherePromptItem, issued))) break;
+                more = more && c.tile_at() < share.end;
+                Work d = {};
+                Piece r = {};
+                if (!more) {
+                    d.flags = kStop;
+                } else {
+                    r = piece_of(p, c, share);
+                    d.token0 = r.token0;
+                    d.flags = (r.begins ? kBegins : 0) | (r.ends ? kEnds : 0);
+                    d.key0 = c.key0();
+                    d.n = c.k.n;
+                    d.heads = r.heads;
+                    d.head0 = r.head0;
+                    d.slope0 = r.shard * p.Hq + r.head0;
+                    d.pos0 = c.k.pos0;
+                    d.len = c.k.len;
+                    d.prefix = c.k.prefix;
+                    d.lo = c.k.lo;
+                    d.hi = c.k.hi;
+                    d.here = d.hi > d.lo ? r.here : 0;
+                    for (int t = 0; t < NQ; ++t) {
+                        const int t0 = t * tile_tokens, n = min(tile_tokens, d.n - t0);  // its rows' tokens
+                        if (n <= 0) continue;
+                        const int lo = first_key(p, d.pos0 + t0), hi = end_key(d.pos0 + t0 + n - 1, d.prefix);
+                        if (hi <= lo) continue;
+                        const int from = max(lo, d.key0) - d.key0, to = min(hi, d.key0 + d.here * TK) - d.key0;
+                        if (to <= from) continue;
+                        d.a[t] = from / TK;
+                        d.b[t] = (to + TK - 1) / TK;
+                    }
+                    if (lane == 0 && !(r.begins && r.ends)) part->items[r.begins ? 1 : 0] = split_item(c, r, share);
+                }
+                if (lane == 0) {
+                    bars.work[w] = d;
+                    mbar_arrive(&bars.w_full[w]);
+                }
+                __syncwarp();
+                if (++w == kItems) {
+                    w = 0;
+                    w_phase ^= 1;
+                }
+                if (!more) break;
+                // the tiles: K of the first, the queries, then V and the next K in turn
+                const int pages_rows = p.Hkv * p.page_size;
+                const int pool = (r.shard * p.num_pages * p.Hkv + r.kvh) * p.page_size;
+                // row of this lane's box (lanes below nb) of tile j: -1: bad page, -2: no key of it is seen
+                auto row_of = [&](int j) {
+                    const int key = d.key0 + j * TK + lane * R;
+                    if (lane >= nb || j >= d.here || key >= d.hi || key + R <= d.lo) return -2;
+                    const int index = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
+                    const int page = __ldg(p.page_table + static_cast<long long>(c.k.b) * p.max_pages + index);
+                    if (page < 0 || page >= p.num_pages) {
+                        bars.out_of_range = 1;
+                        bars.out_of_range_at = c.k.b;
+                        return -1;
+                    }
+                    return pool + page * pages_rows + key - index * p.page_size;
+                };
+                // a tile's boxes, and an E4M3 tile's scales
+                auto load = [&](const CUtensorMap* map, const float* scale, int row) {
+                    constexpr int kSlots = C::CODES ? C::STAGES : C::SLOTS;
+                    uint64_t* full = C::CODES ? &bars.c_full[slot] : &bars.full[slot];
+                    if (!warp_wait(C::CODES ? &bars.c_empty[slot] : &bars.empty[slot], phase, wc, kWhereKvEmpty, issued)) return false;
+                    const uint32_t loads = __ballot_sync(0xffffffffu, row != -2);
+                    const bool skip = TEST && blockIdx.x == 0 && issued == p.withhold_full;
+                    constexpr int kBoxes = C::CODES ? C::CODE_BOXES : C::CB, kSpan = C::CODES ? C::SPAN : 128;
+                    if (lane == 0 && !skip) mbar_arrive_expect_tx(full, __popc(loads) * R * kSpan * kBoxes);
+                    __syncwarp();
+                    // lane: box lane % nb of column lane / nb
+                    const int box = lane % nb, cb = lane / nb;
+                    const int at = __shfl_sync(0xffffffffu, row, box);
+                    uint8_t* to = C::CODES ? codes + slot * C::STAGE : slots + slot * C::SLOT;
+                    if (cb < kBoxes && at != -2 && !skip &&
+                        checked(at == -1 || (at >= 0 && at <= p.P * p.num_pages * pages_rows - R), &bars.status,
+                                &bars.abort_flag, kWhereBoundsTma, at))
+                        tma_load_2d(to + (cb * TK + box * R) * kSpan, map, full, cb * (C::CODES ? C::SPAN : 64),
+                                    at == -1 ? kBadRow : at);
+                    if constexpr (C::CODES) {
+                        // four keys' scales a lane (0 where there is no page)
+                        const int k = min(lane * 4, TK - 4);
+                        const int first = __shfl_sync(0xffffffffu, row, k / R);
+                        if (lane * 4 < TK)
+                            copy16_or_zero(scales + slot * TK + k, scale + (first >= 0 ? first + k % R : 0), first >= 0);
+                        arrive_after_copies(full);
+                    }
+                    ++issued;
+                    if (++slot == kSlots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    return true;
+                };
+                int row = row_of(0), next;
+                for (int j = 0; j < d.here; ++j) {
+                    next = row_of(j + 1);
+                    if (!(ok = load(&p.map_k, p.k_scale, row))) break;
+                    if (j == 0) {
+                        for (int t = 0; t < NQ && ok; ++t) {
+                            if (d.a[t] == d.b[t]) continue;
+                            if (!(ok = warp_wait(&bars.q_empty[t], q_phase[t], wc, kWherePromptQuery, t))) break;
+                            q_phase[t] ^= 1;
+                            ++q_used[t];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&bars.q_full[t], tile_tokens * p.heads * 128 * C::CB);
+                                const int token = static_cast<int>(d.token0 - static_cast<long long>(r.shard) * p.M) + t * tile_tokens;
+                                for (int cb = 0; cb < C::CB; ++cb)
+                                    tma_load_4d(smem + t * C::Q_BYTES + cb * kTileRows * 128, &p.map_q, &bars.q_full[t], cb * 64,
+                                                d.head0, token, r.shard);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                    }
+                    if (!(ok = load(&p.map_v, p.v_scale, row))) break;
+                    row = next;
+                }
+                if (ok) more = c.next_item(p, numbers);
+            }
+            if (bars.abort_flag) {
+                // left early: wait (bounded) for the copies still in flight
+                int local_abort = 0;
+                WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
+                constexpr int kSlots = C::CODES ? C::STAGES : C::SLOTS;
+                for (int i = max(0, issued - kSlots); i < issued; ++i)
+                    if (!(TEST && blockIdx.x == 0 && i == p.withhold_full))
+                        mbar_wait(C::CODES ? &bars.c_full[i % kSlots] : &bars.full[i % kSlots], (i / kSlots) & 1, drain,
+                                  kWhereDrain, i);
+                for (int t = 0; t < NQ; ++t)
+                    if (q_used[t] > 0) mbar_wait(&bars.q_full[t], (q_used[t] - 1) & 1, drain, kWhereDrain, t);
+            }
+        } else if (warp == C::ISSUER) {
+            // -------------------------------------------------- products
+            const int ksteps = (p.D + 15) / 16;
+            const uint32_t s_idesc = idesc_bf16_f32(kTileRows, TK);
+            const uint32_t o_idesc = idesc_bf16_f32(kTileRows, ksteps * 16) | kSecondByRows;
+            const uint32_t slots_at = smem_u32(slots), q_at = smem_u32(smem);
+            int slot = 0, w = 0, tiles = 0;
+            uint32_t phase = 0, w_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto advance = [&] {
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            // scores of tile of rows t with the K in slot s
+            auto scores = [&](int t, int s) {
+                if (lane != 0) return;
+#pragma unroll 1
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t at = (k >> 2) * (kTileRows * 128) + (k & 3) * 32;
+                    const uint32_t kat = (k >> 2) * (TK * 128) + (k & 3) * 32;
+                    umma_bf16(tmem + t * C::S, smem_desc_kmajor_sw128(q_at + t * C::Q_BYTES + at),
+                              smem_desc_kmajor_sw128(slots_at + s * C::SLOT + kat), s_idesc, k != 0);
+                }
+                umma_commit(&bars.s_full[t]);
+            };
+            while (true) {
+                if (!(ok = warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, tiles))) break;
+                const Work d = bars.work[w];
+                if (d.flags & kStop) break;
+                auto active = [&](int t, int j) { return j >= d.a[t] && j < d.b[t]; };
+                // scores of tile j, its K in the current slot, for t
+                auto next_scores = [&](int t, int j) {
+                    if (j == d.a[t]) {
+                        if (!warp_wait(&bars.q_full[t], q_phase[t], wc, kWherePromptQuery, j)) return false;
+                        q_phase[t] ^= 1;
+                    }
+                    tc_fence_after();
+                    scores(t, slot);
+                    if (j == d.b[t] - 1 && lane == 0) umma_commit(&bars.q_empty[t]);
+                    __syncwarp();
+                    return true;
+                };
+                if (d.here > 0) {
+                    ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles);
+                    for (int t = 0; ok && t < NQ; ++t)
+                        if (active(t, 0)) ok = next_scores(t, 0);
+                    if (!ok) break;
+                    if (lane == 0) umma_commit(&bars.empty[slot]);
+                    __syncwarp();
+                    advance();
+                }
+                for (int j = 0; ok && j < d.here; ++j, ++tiles) {
+                    // V of tile j; rows that no row of the batch sees become zeros (their
+                    // weights are 0, and 0 times what lies there might not be)
+                    if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
+                    const int v_slot = slot;
+                    advance();
+                    const int key0 = d.key0 + j * TK, from = max(0, d.lo - key0), to = min(TK, d.hi - key0);
+                    if (!C::CODES && (from > 0 || to < TK)) {
+                        for (int i = lane; i < TK * C::CB * 8; i += 32) {
+                            const int row = i / 8 % TK;
+                            if (row < from || row >= to)
+                                *reinterpret_cast<uint4*>(slots + v_slot * C::SLOT + i * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const bool goes_on = j + 1 < d.here;
+                    bool have_k = false;
+                    for (int t = 0; ok && t < NQ; ++t) {
+                        if (active(t, j)) {
+                            if (!(ok = warp_wait(&bars.p_ready[t], p_phase[t], wc, kWherePromptWeights, j))) break;
+                            p_phase[t] ^= 1;
+                            tc_fence_after();
+                            if (lane == 0) {
+#pragma unroll 1
+                                for (int k = 0; k < TK / 16; ++k)
+                                    umma_bf16_ta(tmem + C::O + t * C::DP, tmem + t * C::S + k * 8,
+                                                 smem_desc_rows(slots_at + v_slot * C::SLOT + k * 2048, TK * 128), o_idesc,
+                                                 j != d.a[t] || k != 0);
+                                if (j == d.b[t] - 1) umma_commit(&bars.o_full[t]);
+                            }
+                            __syncwarp();
+                        }
+                        if (goes_on && active(t, j + 1)) {
+                            if (!have_k) {
+                                if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
+                                have_k = true;
+                            }
+                            ok = next_scores(t, j + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    if (lane == 0) umma_commit(&bars.empty[v_slot]);
+                    if (goes_on) {
+                        // (a K that neither tile of rows sees is waited for all the same, before it is given back)
+                        if (!have_k && !(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
+                        if (lane == 0) umma_commit(&bars.empty[slot]);
+                        advance();
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&bars.w_empty[w]);
+                __syncwarp();
+                if (++w == kItems) {
+                    w = 0;
+                    w_phase ^= 1;
+                }
+            }
+            // the products still under way write to tensor memory, which is given back below
+            int local_abort = 0;
+            WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
+            if (lane == 0) umma_commit(&bars.drain);
+            __syncwarp();
+            warp_wait(&bars.drain, 0, drain, kWhereDrain, -1);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::ISSUER) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0) {
+        const bool failed = bars.status.code != 0;
+        part->status = failed ? bars.status.code : bars.out_of_range ? SPTP_ERR_SHAPE : 0;
+        part->where = failed ? bars.status.where : bars.out_of_range ? kWhereKvPage : 0;
+        part->info = failed ? bars.status.info : bars.out_of_range_at;
+    }
+}
+
+namespace {  // internal: a process may load the library and its checked build, each with `done` of its own
+
+template <class C, bool MODS, bool TEST = false>
+cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    plan_prompt(p, C::NQ * kTileRows, kTileRows);
+    // the largest boxes that never cross a page
+    p.box_rows = 16;
+    while (p.box_rows < C::TK && p.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+    const uint64_t rows = static_cast<uint64_t>(p.P) * p.num_pages * p.Hkv * p.page_size;
+    const int es = C::CODES ? 1 : 2, span = C::CODES ? C::SPAN : 64;
+    if (!encode_map_rows(&p.map_k, p.k, es, p.D, rows, span, p.box_rows) ||
+        !encode_map_rows(&p.map_v, p.v, es, p.D, rows, span, p.box_rows) ||
+        !encode_map_queries(&p.map_q, p.q, p.D, p.Hq, p.M, p.P, p.heads, kTileRows / p.heads))
+        return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        // the groups' shares of registers must not exceed what the kernel was compiled for
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, prompt_tc_kernel<C, MODS, TEST>);
+        if (e != cudaSuccess) return e;
+        if (C::SPLIT_REGS && attr.numRegs < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(prompt_tc_kernel<C, MODS, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    *ctas = prompt_grid(p, num_sms < kPromptWideCtas ? num_sms : kPromptWideCtas, C::TK);
+    if (TEST && *ctas > kSelftestCtas) *ctas = kSelftestCtas;
+    return launch_after(prompt_tc_kernel<C, MODS, TEST>, *ctas, 32 * C::WARPS, C::BYTES, s, p);
+}
+
+// By row width.
+template <bool CODES, bool MODS>
+cudaError_t launch_width(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    if (p.D <= 64) return launch_tc<Shape<64, CODES>, MODS>(p, num_sms, ctas, s);
+    if (p.D <= 128) return launch_tc<Shape<128, CODES>, MODS>(p, num_sms, ctas, s);
+    return launch_tc<Shape<256, CODES>, MODS>(p, num_sms, ctas, s);
+}
+
+}  // namespace
+
+}  // namespace prompt
+}  // namespace sptp

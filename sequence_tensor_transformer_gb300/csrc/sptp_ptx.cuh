@@ -86,6 +86,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     }
 }
 
+// mbar_wait by a whole warp: true if every lane's wait was.  A lane gives up by
+// itself (its own clock, or the abort flag seen); what follows a wait has the
+// warp's lanes work together, so they go on or leave as one.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, where, info));
+}
+
 // Waits until a global int reaches `target` (acquire); bounded like mbar_wait.
 __device__ __forceinline__ bool flag_wait_geq(const int* flag, int target, const WaitCtx& w, int where,
                                               int info) {
@@ -218,6 +225,17 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
             smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Sixteen bytes to shared memory behind the thread's back, or zeros.
+__device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, bool has) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(has ? 16 : 0)
+                 : "memory");
+}
+
+// One of the arrivals that `bar` expects, once the thread's copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Orders this thread's earlier generic-proxy accesses before later

@@ -14,9 +14,9 @@
 //  - One warp walks over the CTA's share (prompt_plan.cuh) and keeps a ring of K
 //    and V tiles filled by TMA, a box per page; it leaves a description of each
 //    item for the others.
-//  - One warp issues the products.  While a tile of rows is in its softmax, the
-//    other one's products run: S of the next keys is issued right behind the O
-//    of the last ones.
+//  - One warp per tile of rows issues its products: S of the next keys right behind
+//    O of the last ones.  While a tile of rows is in its softmax, the other one's
+//    products run.
 //  - E4M3: four warps turn the tiles of codes that TMA brings into bf16 tiles,
 //    code times the row's power of two, which is exact; the rest is the same.
 //  - Four warps per tile of rows do its softmax, a thread a row, scores in
@@ -39,6 +39,7 @@ namespace prompt {
 constexpr int kTileRows = 128;
 constexpr float kSlack = 8.f;  // log 2 units that a score may be above the maximum in use
 constexpr int kItems = 4;      // descriptions under way
+constexpr float kPlainCap = 128.f;  // up to here 2^-22 of the cap is no more than a score is off by itself
 
 enum : int { kBegins = 1, kEnds = 2, kStop = 4 };
 
@@ -95,15 +96,75 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-// D (+)= A B with A (128 x 16 bf16, two elements a column) in tensor memory.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The products and their commits are issued by one elected lane (the same one
+// every time) of a warp that runs through them as a whole, so that their operands
+// are uniform registers from the start.
+// D (+)= A B^T, both operands bf16 in shared memory.
+__device__ __forceinline__ void issue_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, l;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "elect.sync _|l, 0xffffffff;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D (+)= A B with A (128 x 16 bf16, two elements a column) in tensor memory.
+__device__ __forceinline__ void issue_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, l;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|l, 0xffffffff;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+__device__ __forceinline__ void issue_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred l;\n\t"
+        "elect.sync _|l, 0xffffffff;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// A value that all lanes have, in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Two fp32 in a register pair, and arithmetic on both at once
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 split2(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -166,7 +227,7 @@ struct Bars {
     uint64_t p_ready[2];                       // weights there, outputs rescaled
     uint64_t o_full[2];                        // outputs of an item done
     uint64_t w_full[kItems], w_empty[kItems];  // descriptions
-    uint64_t drain;
+    uint64_t drain[2];
     Work work[kItems];
     uint32_t tmem;
     int abort_flag;
@@ -183,47 +244,82 @@ struct Softmax {
     float to_log2, slope;
     int lo, hi, pos;  // keys that this row sees; its position
 
+    // Scores in units of log 2 with the cap and the bias in them.
+    __device__ __forceinline__ void modify(const PromptParams& p, const ScoreCap& cap, float (&s)[TK], int key0) {
+        const uint64_t unit = pair2(to_log2, to_log2);
+        auto at = [&](int j) { return pair2(s[j], s[j + 1]); };
+        auto put = [&](int j, uint64_t v) {
+            const float2 f = split2(v);
+            s[j] = f.x;
+            s[j + 1] = f.y;
+        };
+        if (p.cap == 0.f) {
+#pragma unroll
+            for (int j = 0; j < TK; j += 2) put(j, mul2(at(j), unit));
+        } else if (p.cap <= kPlainCap) {
+            // cap - 2 cap / (1 + e^(2 s / cap)): off by 2^-22 of the cap
+            const uint64_t twice = pair2(to_log2 * cap.twice, to_log2 * cap.twice), one = pair2(1.f, 1.f);
+            const uint64_t c = pair2(cap.cap, cap.cap), less = pair2(-2.f * cap.cap, -2.f * cap.cap);
+#pragma unroll
+            for (int j = 0; j < TK; j += 2) {
+                const float2 x = split2(mul2(at(j), twice));
+                const float2 d = split2(add2(pair2(pow2_approx(x.x), pow2_approx(x.y)), one));
+                put(j, fma2(pair2(reciprocal_approx(d.x), reciprocal_approx(d.y)), less, c));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < TK; ++j) s[j] = cap(s[j] * to_log2);
+        }
+        if (p.slopes == nullptr) return;
+        if (p.prefix_lens == nullptr) {
+            // no key behind pos is seen: slope (j - pos) = slope (16 c - pos) + slope (j - 16 c)
+            uint64_t in16[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) in16[i] = pair2(slope * (2 * i), slope * (2 * i + 1));
+#pragma unroll
+            for (int c = 0; c < TK; c += 16) {
+                const float from = slope * static_cast<float>(key0 + c - pos);
+                const uint64_t from2 = pair2(from, from);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) put(c + 2 * i, add2(at(c + 2 * i), add2(in16[i], from2)));
+            }
+        } else {
+            const float from = static_cast<float>(pos - key0);
+#pragma unroll
+            for (int j = 0; j < TK; ++j) s[j] = fmaf(-slope, fabsf(from - j), s[j]);
+        }
+    }
+
     // A tile of keys from key0 on: weights to P, the outputs rescaled if the maximum moved.
     __device__ __forceinline__ void tile(const PromptParams& p, const ScoreCap& cap, uint32_t s_at, uint32_t o_at, int o_cols,
                                          int key0, bool first) {
-        uint32_t raw[TK / 32][32];
+        float s[TK];
+        {
+            uint32_t raw[TK / 32][32];
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) tmem_ld_32cols(s_at + c * 32, raw[c]);
-        tmem_ld_wait();
-        auto s = [&](int j) -> float& { return reinterpret_cast<float&>(raw[j / 32][j % 32]); };
-        if constexpr (MODS) {
-            if (p.cap != 0.f) {
+            for (int c = 0; c < TK / 32; ++c) tmem_ld_32cols(s_at + c * 32, raw[c]);
+            tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < TK; ++j) s(j) = cap(s(j) * to_log2);
-            } else {
-#pragma unroll
-                for (int j = 0; j < TK; ++j) s(j) *= to_log2;
-            }
-            if (p.slopes != nullptr) {
-                const float from = static_cast<float>(pos - key0);
-                if (p.prefix_lens == nullptr) {  // no key behind pos is seen
-#pragma unroll
-                    for (int j = 0; j < TK; ++j) s(j) = fmaf(-slope, from - j, s(j));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < TK; ++j) s(j) = fmaf(-slope, fabsf(from - j), s(j));
-                }
-            }
+            for (int j = 0; j < TK; ++j) s[j] = __uint_as_float(raw[j / 32][j % 32]);
         }
-        const float unit = MODS ? 1.f : to_log2;
+        if constexpr (MODS) modify(p, cap, s, key0);
         const int from = lo - key0, to = hi - key0;
-        if (!(from <= 0 && to >= TK)) {
+        if (__any_sync(0xffffffffu, from > 0 || to < TK)) {
+            asm volatile("");  // a branch, not 3 TK instructions for every tile
 #pragma unroll
-            for (int j = 0; j < TK; ++j) s(j) = j >= from && j < to ? s(j) : -INFINITY;
+            for (int j = 0; j < TK; ++j) s[j] = j >= from && j < to ? s[j] : -INFINITY;
         }
-        float top[4] = {s(0), s(1), s(2), s(3)};
+        float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < TK; j += 4)
+        for (int j = 4; j + 8 <= TK; j += 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], s(j + u));
-        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+            for (int u = 0; u < 4; ++u) top[u] = max3(top[u], s[j + 2 * u], s[j + 2 * u + 1]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], s[TK - 4 + u]);
+        const float unit = MODS ? 1.f : to_log2;
+        const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * unit;
         float f = 1.f;
-        const bool moves = now > m + kSlack || (m == -INFINITY && now != -INFINITY);
+        const bool moves = now > m + kSlack;  // (from the start's -infinity to any other, too)
         if (moves) {
             f = pow2_approx(m - now);
             m = now;
@@ -241,21 +337,23 @@ struct Softmax {
             }
         }
         const float base = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t unit2 = pair2(unit, unit), base2 = pair2(base, base);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < TK / 32; ++c) {
             uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const float a = pow2_approx(MODS ? s(c * 32 + j) + base : fmaf(s(c * 32 + j), unit, base));
-                const float b = pow2_approx(MODS ? s(c * 32 + j + 1) + base : fmaf(s(c * 32 + j + 1), unit, base));
-                sum[j & 2] += a;
-                sum[(j & 2) + 1] += b;
-                w[j / 2] = pack_bf16(a, b);
+            for (int j = 0; j < 16; ++j) {
+                const uint64_t x = pair2(s[c * 32 + 2 * j], s[c * 32 + 2 * j + 1]);
+                const float2 y = split2(MODS ? add2(x, base2) : fma2(x, unit2, base2));
+                const float a = pow2_approx(y.x), b = pow2_approx(y.y);
+                sum[j & 3] = add2(sum[j & 3], pair2(a, b));
+                w[j] = pack_bf16(a, b);
             }
             tmem_st_16cols(s_at + c * 16, w);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 all = split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += all.x + all.y;
         tmem_st_wait();
     }
 };
@@ -277,7 +375,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     if (tid == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&bars.full[s], C::CODES ? 4 : 1);
-            mbar_init(&bars.empty[s], 1);
+            mbar_init(&bars.empty[s], NQ);
         }
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars.c_full[s], 1 + 32);
@@ -289,12 +387,12 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             mbar_init(&bars.s_full[t], 1);
             mbar_init(&bars.p_ready[t], kTileRows);
             mbar_init(&bars.o_full[t], 1);
+            mbar_init(&bars.drain[t], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bars.w_full[i], 1);
-            mbar_init(&bars.w_empty[i], 4 * NQ + 1 + (C::CODES ? 4 : 0));
+            mbar_init(&bars.w_empty[i], 5 * NQ + (C::CODES ? 4 : 0));
         }
-        mbar_init(&bars.drain, 1);
         fence_mbar_init();
         bars.abort_flag = 0;
         bars.status.code = bars.status.where = bars.status.info = 0;
@@ -623,113 +721,87 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 for (int t = 0; t < NQ; ++t)
                     if (q_used[t] > 0) mbar_wait(&bars.q_full[t], (q_used[t] - 1) & 1, drain, kWhereDrain, t);
             }
-        } else if (warp == C::ISSUER) {
-            // -------------------------------------------------- products
+        } else if (warp < C::ISSUER + NQ) {
+            // -------------------------------------------------- products of one tile of rows
+            const int t = warp - C::ISSUER;
             const int ksteps = (p.D + 15) / 16;
             const uint32_t s_idesc = idesc_bf16_f32(kTileRows, TK);
             const uint32_t o_idesc = idesc_bf16_f32(kTileRows, ksteps * 16) | kSecondByRows;
-            const uint32_t slots_at = smem_u32(slots), q_at = smem_u32(smem);
-            int slot = 0, w = 0, tiles = 0;
-            uint32_t phase = 0, w_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            // (descriptors count in 16 bytes, and no tile's addresses carry out of that field)
+            const uint64_t q_desc = smem_desc_kmajor_sw128(smem_u32(smem) + t * C::Q_BYTES);
+            const uint64_t k_desc = smem_desc_kmajor_sw128(smem_u32(slots));
+            const uint64_t v_desc = smem_desc_rows(smem_u32(slots), TK * 128);
+            const uint32_t s_tmem = tmem + t * C::S, o_tmem = tmem + C::O + t * C::DP;
+            int slot = 0, w = 0;
+            uint32_t phase = 0, w_phase = 0, q_phase = 0, p_phase = 0;
             bool ok = true;
-            auto advance = [&] {
-                if (++slot == C::SLOTS) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            };
-            // scores of tile of rows t with the K in slot s
-            auto scores = [&](int t, int s) {
-                if (lane != 0) return;
-#pragma unroll 1
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t at = (k >> 2) * (kTileRows * 128) + (k & 3) * 32;
-                    const uint32_t kat = (k >> 2) * (TK * 128) + (k & 3) * 32;
-                    umma_bf16(tmem + t * C::S, smem_desc_kmajor_sw128(q_at + t * C::Q_BYTES + at),
-                              smem_desc_kmajor_sw128(slots_at + s * C::SLOT + kat), s_idesc, k != 0);
-                }
-                umma_commit(&bars.s_full[t]);
-            };
             while (true) {
-                if (!(ok = warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, tiles))) break;
-                const Work d = bars.work[w];
-                if (d.flags & kStop) break;
-                auto active = [&](int t, int j) { return j >= d.a[t] && j < d.b[t]; };
-                // scores of tile j, its K in the current slot, for t
-                auto next_scores = [&](int t, int j) {
-                    if (j == d.a[t]) {
-                        if (!warp_wait(&bars.q_full[t], q_phase[t], wc, kWherePromptQuery, j)) return false;
-                        q_phase[t] ^= 1;
-                    }
-                    tc_fence_after();
-                    scores(t, slot);
-                    if (j == d.b[t] - 1 && lane == 0) umma_commit(&bars.q_empty[t]);
-                    __syncwarp();
-                    return true;
-                };
-                if (d.here > 0) {
-                    ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles);
-                    for (int t = 0; ok && t < NQ; ++t)
-                        if (active(t, 0)) ok = next_scores(t, 0);
-                    if (!ok) break;
-                    if (lane == 0) umma_commit(&bars.empty[slot]);
-                    __syncwarp();
-                    advance();
-                }
-                for (int j = 0; ok && j < d.here; ++j, ++tiles) {
-                    // V of tile j; rows that no row of the batch sees become zeros (their
-                    // weights are 0, and 0 times what lies there might not be)
-                    if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
-                    const int v_slot = slot;
-                    advance();
-                    const int key0 = d.key0 + j * TK, from = max(0, d.lo - key0), to = min(TK, d.hi - key0);
-                    if (!C::CODES && (from > 0 || to < TK)) {
-                        for (int i = lane; i < TK * C::CB * 8; i += 32) {
-                            const int row = i / 8 % TK;
-                            if (row < from || row >= to)
-                                *reinterpret_cast<uint4*>(slots + v_slot * C::SLOT + i * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    const bool goes_on = j + 1 < d.here;
-                    bool have_k = false;
-                    for (int t = 0; ok && t < NQ; ++t) {
-                        if (active(t, j)) {
-                            if (!(ok = warp_wait(&bars.p_ready[t], p_phase[t], wc, kWherePromptWeights, j))) break;
-                            p_phase[t] ^= 1;
-                            tc_fence_after();
-                            if (lane == 0) {
-#pragma unroll 1
-                                for (int k = 0; k < TK / 16; ++k)
-                                    umma_bf16_ta(tmem + C::O + t * C::DP, tmem + t * C::S + k * 8,
-                                                 smem_desc_rows(slots_at + v_slot * C::SLOT + k * 2048, TK * 128), o_idesc,
-                                                 j != d.a[t] || k != 0);
-                                if (j == d.b[t] - 1) umma_commit(&bars.o_full[t]);
+                if (!(ok = warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, t))) break;
+                const Work& d = bars.work[w];
+                if (uniform(d.flags) & kStop) break;
+                const int here = uniform(d.here), a = uniform(d.a[t]), b = uniform(d.b[t]);
+                const int lo = uniform(d.lo) - uniform(d.key0), hi = uniform(d.hi) - uniform(d.key0);
+                // K of tile j (and, for j > 0, V of tile j - 1 before it): tile j's scores
+                // are issued right behind the outputs of tile j - 1
+                for (int j = 0; j <= here && here > 0; ++j) {
+                    if (j > 0) {
+                        // V of tile j - 1; rows that no row of the batch sees become zeros (their
+                        // weights are 0, and 0 times what lies there might not be)
+                        if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
+                        const int from = lo - (j - 1) * TK, to = hi - (j - 1) * TK;
+                        if (!C::CODES && (from > 0 || to < TK)) {
+                            for (int i = lane; i < TK * C::CB * 8; i += 32) {
+                                const int row = i / 8 % TK;
+                                if (row < from || row >= to)
+                                    *reinterpret_cast<uint4*>(slots + slot * C::SLOT + i * 16) = make_uint4(0, 0, 0, 0);
                             }
+                            fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (goes_on && active(t, j + 1)) {
-                            if (!have_k) {
-                                if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
-                                have_k = true;
-                            }
-                            ok = next_scores(t, j + 1);
+                        if (j - 1 >= a && j - 1 < b) {
+                            if (!(ok = warp_wait(&bars.p_ready[t], p_phase, wc, kWherePromptWeights, j))) break;
+                            p_phase ^= 1;
+                            tc_fence_after();
+                            const uint64_t vd = v_desc + slot * (C::SLOT >> 4);
+                            const uint32_t adds = j - 1 != a;
+#pragma unroll
+                            for (int k = 0; k < TK / 16; ++k)
+                                issue_ts(o_tmem, s_tmem + k * 8, vd + k * (2048 >> 4), o_idesc, k != 0 ? 1u : adds);
+                            if (j == b) issue_commit(&bars.o_full[t]);
+                        }
+                        issue_commit(&bars.empty[slot]);
+                        if (++slot == C::SLOTS) {
+                            slot = 0;
+                            phase ^= 1;
                         }
                     }
-                    if (!ok) break;
-                    if (lane == 0) umma_commit(&bars.empty[v_slot]);
-                    if (goes_on) {
-                        // (a K that neither tile of rows sees is waited for all the same, before it is given back)
-                        if (!have_k && !(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, tiles))) break;
-                        if (lane == 0) umma_commit(&bars.empty[slot]);
-                        advance();
+                    if (j < here) {
+                        if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
+                        if (j >= a && j < b) {
+                            if (j == a) {
+                                if (!(ok = warp_wait(&bars.q_full[t], q_phase, wc, kWherePromptQuery, j))) break;
+                                q_phase ^= 1;
+                            }
+                            tc_fence_after();
+                            const uint64_t kd = k_desc + slot * (C::SLOT >> 4);
+#pragma unroll
+                            for (int k = 0; k < C::DP / 16; ++k)
+                                if (k < ksteps)
+                                    issue_ss(s_tmem, q_desc + ((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                                             kd + ((k >> 2) * (TK * 8) + (k & 3) * 2), s_idesc, k != 0);
+                            issue_commit(&bars.s_full[t]);
+                            if (j == b - 1) issue_commit(&bars.q_empty[t]);
+                        }
+                        issue_commit(&bars.empty[slot]);
+                        if (++slot == C::SLOTS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
-                    __syncwarp();
                 }
                 if (!ok) break;
-                if (lane == 0) mbar_arrive(&bars.w_empty[w]);
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.w_empty[w]);
                 if (++w == kItems) {
                     w = 0;
                     w_phase ^= 1;
@@ -738,9 +810,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             // the products still under way write to tensor memory, which is given back below
             int local_abort = 0;
             WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
-            if (lane == 0) umma_commit(&bars.drain);
-            __syncwarp();
-            warp_wait(&bars.drain, 0, drain, kWhereDrain, -1);
+            issue_commit(&bars.drain[t]);
+            warp_wait(&bars.drain[t], 0, drain, kWhereDrain, -1);
         }
     }
     __syncwarp();

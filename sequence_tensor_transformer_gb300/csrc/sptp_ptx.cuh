@@ -72,7 +72,10 @@ __device__ __forceinline__ void report_timeout(const WaitCtx& w, int where, int 
 // returns false if the wait gave up (timeout or CTA abort).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where,
                                           int info) {
-    if (mbar_try_wait(bar, parity)) return true;
+    // (the timer takes a microsecond to read: it is not looked at in a short wait)
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (true) {
 #pragma unroll 1

@@ -74,7 +74,7 @@ struct Shape {
     // thread of each, and of all at launch (their shares make up the launch's total)
     static constexpr int PRODUCER = 4 * NQ, ISSUER = 4 * NQ + 1, CONVERTER = 4 * NQ + 4;
     static constexpr int WARPS = CONVERTER + (CODES ? 4 : 0);
-    static constexpr bool SPLIT_REGS = NQ == 2;
+    static constexpr bool SPLIT_REGS = false;
     static constexpr int LAUNCH_REGS = WARPS == 16 ? 128 : 168;
     static constexpr int SOFTMAX_REGS = WARPS == 16 ? 176 : 208;
     static constexpr int OTHER_REGS = WARPS == 16 ? 72 : 88;
@@ -236,6 +236,18 @@ struct Bars {
 };
 
 // ---------------------------------------------------------------- softmax of one tile of rows
+// tanh u = u P(u^2) for |u| <= 1, off by 5e-8 of itself: the polynomial of degree 6
+// in u^2 with the least largest relative error (a Remez fit).
+__host__ __device__ constexpr float tanh_term(int i) {
+    return i == 0   ? 0.999999950241f
+           : i == 1 ? -0.333328391536f
+           : i == 2 ? 0.133252040772f
+           : i == 3 ? -0.053457029549f
+           : i == 4 ? 0.0202899803204f
+           : i == 5 ? -0.00620337898208f
+                    : 0.00104102258568f;
+}
+
 template <class C, bool MODS>
 struct Softmax {
     static constexpr int TK = C::TK;
@@ -244,113 +256,161 @@ struct Softmax {
     float to_log2, slope;
     int lo, hi, pos;  // keys that this row sees; its position
 
-    // Scores in units of log 2 with the cap and the bias in them.
-    __device__ __forceinline__ void modify(const PromptParams& p, const ScoreCap& cap, float (&s)[TK], int key0) {
-        const uint64_t unit = pair2(to_log2, to_log2);
-        auto at = [&](int j) { return pair2(s[j], s[j + 1]); };
-        auto put = [&](int j, uint64_t v) {
-            const float2 f = split2(v);
-            s[j] = f.x;
-            s[j + 1] = f.y;
+    static constexpr int N = 32;      // scores at a time
+    static constexpr int P = TK / 2;  // column of the weights, in the place of scores that are read before
+
+    static __device__ __forceinline__ uint64_t both(float x) { return pair2(x, x); }
+    static __device__ __forceinline__ uint64_t at(const float (&s)[N], int j) { return pair2(s[j], s[j + 1]); }
+    static __device__ __forceinline__ void put(float (&s)[N], int j, uint64_t v) {
+        const float2 f = split2(v);
+        s[j] = f.x;
+        s[j + 1] = f.y;
+    }
+
+    // The cap.  On the fused multiply-adds (9 of them a score) where no |score| of
+    // the warp's rows passes the cap, and for three scores of eight on the function
+    // unit (an exponential and a reciprocal), so that both units have their share.
+    __device__ __forceinline__ void apply_cap(const PromptParams& p, const ScoreCap& cap, float (&s)[N]) {
+        const float to_u = to_log2 * cap.inv;
+        // cap - 2 cap / (1 + e^(2 s / cap)): off by 2^-22 of the cap
+        auto by_units = [&](int j) {
+            const float2 x = split2(mul2(at(s, j), both(to_log2 * cap.twice)));
+            const float2 d = split2(add2(pair2(pow2_approx(x.x), pow2_approx(x.y)), both(1.f)));
+            put(s, j, fma2(pair2(reciprocal_approx(d.x), reciprocal_approx(d.y)), both(-2.f * cap.cap), both(cap.cap)));
         };
-        if (p.cap == 0.f) {
+        auto by_series = [&](int j) {
+            const uint64_t u = mul2(at(s, j), both(to_u)), v = mul2(u, u);
+            uint64_t y = both(tanh_term(6));
 #pragma unroll
-            for (int j = 0; j < TK; j += 2) put(j, mul2(at(j), unit));
-        } else if (p.cap <= kPlainCap) {
-            // cap - 2 cap / (1 + e^(2 s / cap)): off by 2^-22 of the cap
-            const uint64_t twice = pair2(to_log2 * cap.twice, to_log2 * cap.twice), one = pair2(1.f, 1.f);
-            const uint64_t c = pair2(cap.cap, cap.cap), less = pair2(-2.f * cap.cap, -2.f * cap.cap);
+            for (int i = 5; i >= 0; --i) y = fma2(y, v, both(tanh_term(i)));
+            put(s, j, mul2(mul2(u, both(cap.cap)), y));
+        };
+        float most = 0.f;
 #pragma unroll
-            for (int j = 0; j < TK; j += 2) {
-                const float2 x = split2(mul2(at(j), twice));
-                const float2 d = split2(add2(pair2(pow2_approx(x.x), pow2_approx(x.y)), one));
-                put(j, fma2(pair2(reciprocal_approx(d.x), reciprocal_approx(d.y)), less, c));
+        for (int j = 0; j < N; j += 2) most = max3(most, fabsf(s[j]), fabsf(s[j + 1]));
+        // (a NaN among keys that no row sees does not count)
+        const bool near = !__any_sync(0xffffffffu, most * fabsf(to_u) > 1.f);
+        if (p.cap <= kPlainCap) {
+            if (near) {
+#pragma unroll
+                for (int j = 0; j < N; j += 2) {
+                    if (j % 16 == 2 || j % 16 == 8 || j % 16 == 12)
+                        by_units(j);
+                    else
+                        by_series(j);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; j += 2) by_units(j);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < TK; ++j) s[j] = cap(s[j] * to_log2);
-        }
-        if (p.slopes == nullptr) return;
-        if (p.prefix_lens == nullptr) {
-            // no key behind pos is seen: slope (j - pos) = slope (16 c - pos) + slope (j - 16 c)
-            uint64_t in16[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) in16[i] = pair2(slope * (2 * i), slope * (2 * i + 1));
-#pragma unroll
-            for (int c = 0; c < TK; c += 16) {
-                const float from = slope * static_cast<float>(key0 + c - pos);
-                const uint64_t from2 = pair2(from, from);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) put(c + 2 * i, add2(at(c + 2 * i), add2(in16[i], from2)));
-            }
-        } else {
-            const float from = static_cast<float>(pos - key0);
-#pragma unroll
-            for (int j = 0; j < TK; ++j) s[j] = fmaf(-slope, fabsf(from - j), s[j]);
+            for (int j = 0; j < N; ++j) s[j] = cap(s[j] * to_log2);
         }
     }
 
-    // A tile of keys from key0 on: weights to P, the outputs rescaled if the maximum moved.
-    __device__ __forceinline__ void tile(const PromptParams& p, const ScoreCap& cap, uint32_t s_at, uint32_t o_at, int o_cols,
-                                         int key0, bool first) {
-        float s[TK];
-        {
-            uint32_t raw[TK / 32][32];
+    // A new maximum: the sum, the outputs (unless this is an item's first tile) and
+    // the weights of this tile so far (from the 32 c-th score on) relative to it.
+    __device__ __forceinline__ void move(float now, bool moves, uint32_t s_at, uint32_t o_at, int o_cols, bool first, int c0,
+                                      uint64_t (&sum)[4]) {
+        const float f = moves ? pow2_approx(m - now) : 1.f;
+        if (moves) m = now;
+        l *= f;
 #pragma unroll
-            for (int c = 0; c < TK / 32; ++c) tmem_ld_32cols(s_at + c * 32, raw[c]);
+        for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], both(f));
+        tmem_st_wait();
+#pragma unroll 1
+        for (int c = c0 * 16; c < TK / 2; c += 16) {
+            uint32_t w[16];
+            tmem_ld_16cols(s_at + P + c, w);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < TK; ++j) s[j] = __uint_as_float(raw[j / 32][j % 32]);
+            for (int i = 0; i < 16; ++i) {
+                const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+                w[i] = pack_bf16(v.x * f, v.y * f);
+            }
+            tmem_st_16cols(s_at + P + c, w);
         }
-        if constexpr (MODS) modify(p, cap, s, key0);
-        const int from = lo - key0, to = hi - key0;
-        if (__any_sync(0xffffffffu, from > 0 || to < TK)) {
-            asm volatile("");  // a branch, not 3 TK instructions for every tile
-#pragma unroll
-            for (int j = 0; j < TK; ++j) s[j] = j >= from && j < to ? s[j] : -INFINITY;
-        }
-        float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int j = 4; j + 8 <= TK; j += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) top[u] = max3(top[u], s[j + 2 * u], s[j + 2 * u + 1]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], s[TK - 4 + u]);
-        const float unit = MODS ? 1.f : to_log2;
-        const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * unit;
-        float f = 1.f;
-        const bool moves = now > m + kSlack;  // (from the start's -infinity to any other, too)
-        if (moves) {
-            f = pow2_approx(m - now);
-            m = now;
-            l *= f;
-        }
-        if (!first && __any_sync(0xffffffffu, moves)) {
+        if (first) return;
 #pragma unroll 1
-            for (int c = 0; c < o_cols; c += 16) {
-                uint32_t o[16];
-                tmem_ld_16cols(o_at + c, o);
+        for (int c = 0; c < o_cols; c += 16) {
+            uint32_t o[16];
+            tmem_ld_16cols(o_at + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_16cols(o_at + c, o);
+        }
+    }
+
+    // A tile of keys from key0 on: weights to P, 32 at a time, the last keys first (a
+    // bias by distance is least there), in a loop whose code stays in the instruction cache (with the 128 scores
+    // of a tile unrolled, fetching instructions took longer than running them).
+    __device__ __forceinline__ void tile(const PromptParams& p, const ScoreCap& cap, uint32_t s_at, uint32_t o_at, int o_cols,
+                                         int key0, bool first) {
+        uint64_t sum[4] = {0, 0, 0, 0};
+        const bool masked = __any_sync(0xffffffffu, lo > key0 || hi < key0 + TK);
+#pragma unroll 1
+        for (int c = TK / N - 1; c >= 0; --c) {
+            float s[N];
+            {
+                uint32_t raw[N];
+                tmem_ld_32cols(s_at + c * N, raw);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_16cols(o_at + c, o);
+                for (int j = 0; j < N; ++j) s[j] = __uint_as_float(raw[j]);
             }
-        }
-        const float base = m == -INFINITY ? 0.f : -m;
-        const uint64_t unit2 = pair2(unit, unit), base2 = pair2(base, base);
-        uint64_t sum[4] = {0, 0, 0, 0};
+            // scores in units of log 2 are unit s + bias
+            float unit = to_log2, bias = 0.f;
+            const int key = key0 + c * N;
+            if constexpr (MODS) {
+                if (p.cap != 0.f) {
+                    apply_cap(p, cap, s);
+                    unit = 1.f;
+                }
+                if (p.slopes != nullptr) {
+                    const float far = static_cast<float>(pos - key);
+                    if (p.prefix_lens == nullptr || !__any_sync(0xffffffffu, key + N > pos + 1)) {
+                        // slope (j - pos), of which the part without j can wait
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) {
+                        for (int j = 0; j < N; j += 2) put(s, j, fma2(at(s, j), both(unit), pair2(slope * j, slope * (j + 1))));
+                        bias = -slope * far;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) s[j] = fmaf(s[j], unit, -slope * fabsf(far - j));
+                    }
+                    unit = 1.f;
+                }
+            }
+            if (masked) {
+                // bit j: key j of the 32 is seen
+                const int from = max(lo - key, 0), to = min(max(hi - key, 0), N);
+                const uint32_t seen = from >= to ? 0u : (0xffffffffu >> (32 - (to - from))) << from;
+#pragma unroll
+                for (int j = 0; j < N; ++j) s[j] = seen >> j & 1u ? s[j] : -INFINITY;
+            }
+            float top[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = max3(s[i], s[4 + i], s[8 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[12 + i], s[16 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[20 + i], s[24 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[28 + i]);
+            const float now = fmaf(max3(top[0], top[1], fmaxf(top[2], top[3])), unit, bias);
+            const bool moves = now > m + kSlack;  // (from -infinity to any other, too)
+            if (__any_sync(0xffffffffu, moves)) move(now, moves, s_at, o_at, o_cols, first, c + 1, sum);
+            const uint64_t unit2 = both(unit), base = both(bias - (m == -INFINITY ? 0.f : m));
             uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint64_t x = pair2(s[c * 32 + 2 * j], s[c * 32 + 2 * j + 1]);
-                const float2 y = split2(MODS ? add2(x, base2) : fma2(x, unit2, base2));
+            for (int i = 0; i < 16; ++i) {
+                const float2 y = split2(fma2(at(s, 2 * i), unit2, base));
                 const float a = pow2_approx(y.x), b = pow2_approx(y.y);
-                sum[j & 3] = add2(sum[j & 3], pair2(a, b));
-                w[j] = pack_bf16(a, b);
+                sum[i & 3] = add2(sum[i & 3], pair2(a, b));
+                w[i] = pack_bf16(a, b);
             }
-            tmem_st_16cols(s_at + c * 16, w);
+            tmem_st_16cols(s_at + P + c * 16, w);
         }
         const float2 all = split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l += all.x + all.y;
@@ -405,6 +465,15 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         tmem_alloc(&bars.tmem, 512);
         tmem_relinquish();
     }
+    // rows of a tile of queries that no box has
+    {
+        const int used = kTileRows / p.heads * p.heads;
+        for (int i = tid; i < NQ * C::CB * (kTileRows - used) * 8; i += kThreads) {
+            const int row = used + i / 8 % (kTileRows - used), column = i / 8 / (kTileRows - used);
+            *reinterpret_cast<uint4*>(smem + column * kTileRows * 128 + row * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
     await_previous();
     tc_fence_before();
     bool bad = false;
@@ -430,7 +499,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         int w = 0;
         uint32_t w_phase = 0, s_phase = 0, o_phase = 0;
         while (true) {
-            if (!warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, -1)) break;
+            if (!warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, -1)) break;
             const Work& d = bars.work[w];
             if (d.flags & kStop) break;
             const int heads = d.heads, tile_tokens = kTileRows / p.heads;
@@ -440,22 +509,24 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             sm.m = -INFINITY;
             sm.l = 0.f;
             sm.pos = d.pos0 + token;
+            // (a row of the tile that no token has is not masked: it would cost its warp
+            // as much as one that is)
             sm.lo = in ? first_key(p, sm.pos) : 0;
-            sm.hi = in ? min(d.len, end_key(sm.pos, d.prefix)) : 0;
+            sm.hi = in ? min(d.len, end_key(sm.pos, d.prefix)) : 0x7fffffff;
             sm.slope = MODS && p.slopes != nullptr && in ? __ldg(p.slopes + d.slope0 + head) * kLog2e : 0.f;
             const int a = d.a[t], b = d.b[t], key0 = d.key0;
             bool ok = true;
-            for (int j = a; j < b; ++j) {
-                if (!(ok = warp_wait(&bars.s_full[t], s_phase, wc, kWherePromptScores, j))) break;
+            for (int j = b - 1; j >= a; --j) {
+                if (!(ok = warp_sleep(&bars.s_full[t], s_phase, wc, kWherePromptScores, j))) break;
                 s_phase ^= 1;
                 tc_fence_after();
-                sm.tile(p, cap, s_at, o_at, o_cols, key0 + j * TK, j == a);
+                sm.tile(p, cap, s_at, o_at, o_cols, key0 + j * TK, j == b - 1);
                 tc_fence_before();
                 mbar_arrive(&bars.p_ready[t]);
             }
             if (!ok) break;
             if (a < b) {
-                if (!warp_wait(&bars.o_full[t], o_phase, wc, kWherePromptOutputs, b)) break;
+                if (!warp_sleep(&bars.o_full[t], o_phase, wc, kWherePromptOutputs, b)) break;
                 o_phase ^= 1;
                 tc_fence_after();
             }
@@ -520,16 +591,16 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         uint32_t c_phase = 0, phase = 1, w_phase = 0;
         bool ok = true;
         while (ok) {
-            if (!warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, -2)) break;
+            if (!warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, -2)) break;
             const Work& d = bars.work[w];
             if (d.flags & kStop) break;
             const int tiles = 2 * d.here;
             for (int i = 0; i < tiles; ++i) {
-                const int key0 = d.key0 + i / 2 * TK;
+                const int key0 = d.key0 + (d.here - 1 - i / 2) * TK;
                 // V: rows that no row of the batch sees become zeros
                 const int from = i & 1 ? d.lo - key0 : 0, to = i & 1 ? d.hi - key0 : TK;
-                if (!(ok = warp_wait(&bars.c_full[stage], c_phase, wc, kWhereKvFull, i))) break;
-                if (!(ok = warp_wait(&bars.empty[slot], phase, wc, kWhereKvEmpty, i))) break;
+                if (!(ok = warp_sleep(&bars.c_full[stage], c_phase, wc, kWhereKvFull, i))) break;
+                if (!(ok = warp_sleep(&bars.empty[slot], phase, wc, kWhereKvEmpty, i))) break;
                 const uint8_t* in = codes + stage * C::STAGE;
                 uint8_t* out = slots + slot * C::SLOT;
 #pragma unroll 4
@@ -590,7 +661,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             int slot = 0, issued = 0, w = 0, q_used[2] = {0, 0};
             uint32_t phase = 1, w_phase = 1, q_phase[2] = {1, 1};
             while (ok) {
-                if (!(ok = warp_wait(&bars.w_empty[w], w_phase, wc, kWherePromptItem, issued))) break;
+                if (!(ok = warp_sleep(&bars.w_empty[w], w_phase, wc, kWherePromptItem, issued))) break;
                 more = more && c.tile_at() < share.end;
                 Work d = {};
                 Piece r = {};
@@ -639,7 +710,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 // row of this lane's box (lanes below nb) of tile j: -1: bad page, -2: no key of it is seen
                 auto row_of = [&](int j) {
                     const int key = d.key0 + j * TK + lane * R;
-                    if (lane >= nb || j >= d.here || key >= d.hi || key + R <= d.lo) return -2;
+                    if (lane >= nb || j < 0 || key >= d.hi || key + R <= d.lo) return -2;
                     const int index = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
                     const int page = __ldg(p.page_table + static_cast<long long>(c.k.b) * p.max_pages + index);
                     if (page < 0 || page >= p.num_pages) {
@@ -653,7 +724,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 auto load = [&](const CUtensorMap* map, const float* scale, int row) {
                     constexpr int kSlots = C::CODES ? C::STAGES : C::SLOTS;
                     uint64_t* full = C::CODES ? &bars.c_full[slot] : &bars.full[slot];
-                    if (!warp_wait(C::CODES ? &bars.c_empty[slot] : &bars.empty[slot], phase, wc, kWhereKvEmpty, issued)) return false;
+                    if (!warp_sleep(C::CODES ? &bars.c_empty[slot] : &bars.empty[slot], phase, wc, kWhereKvEmpty, issued)) return false;
                     const uint32_t loads = __ballot_sync(0xffffffffu, row != -2);
                     const bool skip = TEST && blockIdx.x == 0 && issued == p.withhold_full;
                     constexpr int kBoxes = C::CODES ? C::CODE_BOXES : C::CB, kSpan = C::CODES ? C::SPAN : 128;
@@ -683,14 +754,14 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                     }
                     return true;
                 };
-                int row = row_of(0), next;
-                for (int j = 0; j < d.here; ++j) {
-                    next = row_of(j + 1);
+                int row = row_of(d.here - 1), next;
+                for (int j = d.here - 1; j >= 0; --j) {
+                    next = row_of(j - 1);
                     if (!(ok = load(&p.map_k, p.k_scale, row))) break;
-                    if (j == 0) {
+                    if (j == d.here - 1) {
                         for (int t = 0; t < NQ && ok; ++t) {
                             if (d.a[t] == d.b[t]) continue;
-                            if (!(ok = warp_wait(&bars.q_empty[t], q_phase[t], wc, kWherePromptQuery, t))) break;
+                            if (!(ok = warp_sleep(&bars.q_empty[t], q_phase[t], wc, kWherePromptQuery, t))) break;
                             q_phase[t] ^= 1;
                             ++q_used[t];
                             if (lane == 0) {
@@ -736,19 +807,19 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             uint32_t phase = 0, w_phase = 0, q_phase = 0, p_phase = 0;
             bool ok = true;
             while (true) {
-                if (!(ok = warp_wait(&bars.w_full[w], w_phase, wc, kWherePromptItem, t))) break;
+                if (!(ok = warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, t))) break;
                 const Work& d = bars.work[w];
                 if (uniform(d.flags) & kStop) break;
                 const int here = uniform(d.here), a = uniform(d.a[t]), b = uniform(d.b[t]);
                 const int lo = uniform(d.lo) - uniform(d.key0), hi = uniform(d.hi) - uniform(d.key0);
-                // K of tile j (and, for j > 0, V of tile j - 1 before it): tile j's scores
-                // are issued right behind the outputs of tile j - 1
-                for (int j = 0; j <= here && here > 0; ++j) {
-                    if (j > 0) {
-                        // V of tile j - 1; rows that no row of the batch sees become zeros (their
+                // the last keys first; V of tile j and K of tile j - 1: scores of the next
+                // tile are issued right behind the outputs of this one
+                for (int j = here; j >= 0 && here > 0; --j) {
+                    if (j < here) {
+                        // rows of V that no row of the batch sees become zeros (their
                         // weights are 0, and 0 times what lies there might not be)
-                        if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
-                        const int from = lo - (j - 1) * TK, to = hi - (j - 1) * TK;
+                        if (!(ok = warp_sleep(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
+                        const int from = lo - j * TK, to = hi - j * TK;
                         if (!C::CODES && (from > 0 || to < TK)) {
                             for (int i = lane; i < TK * C::CB * 8; i += 32) {
                                 const int row = i / 8 % TK;
@@ -758,16 +829,16 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (j - 1 >= a && j - 1 < b) {
-                            if (!(ok = warp_wait(&bars.p_ready[t], p_phase, wc, kWherePromptWeights, j))) break;
+                        if (j >= a && j < b) {
+                            if (!(ok = warp_sleep(&bars.p_ready[t], p_phase, wc, kWherePromptWeights, j))) break;
                             p_phase ^= 1;
                             tc_fence_after();
                             const uint64_t vd = v_desc + slot * (C::SLOT >> 4);
-                            const uint32_t adds = j - 1 != a;
+                            const uint32_t adds = j != b - 1;
 #pragma unroll
                             for (int k = 0; k < TK / 16; ++k)
-                                issue_ts(o_tmem, s_tmem + k * 8, vd + k * (2048 >> 4), o_idesc, k != 0 ? 1u : adds);
-                            if (j == b) issue_commit(&bars.o_full[t]);
+                                issue_ts(o_tmem, s_tmem + TK / 2 + k * 8, vd + k * (2048 >> 4), o_idesc, k != 0 ? 1u : adds);
+                            if (j == a) issue_commit(&bars.o_full[t]);
                         }
                         issue_commit(&bars.empty[slot]);
                         if (++slot == C::SLOTS) {
@@ -775,11 +846,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                             phase ^= 1;
                         }
                     }
-                    if (j < here) {
-                        if (!(ok = warp_wait(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
-                        if (j >= a && j < b) {
-                            if (j == a) {
-                                if (!(ok = warp_wait(&bars.q_full[t], q_phase, wc, kWherePromptQuery, j))) break;
+                    if (j > 0) {
+                        if (!(ok = warp_sleep(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
+                        if (j - 1 >= a && j - 1 < b) {
+                            if (j == b) {
+                                if (!(ok = warp_sleep(&bars.q_full[t], q_phase, wc, kWherePromptQuery, j))) break;
                                 q_phase ^= 1;
                             }
                             tc_fence_after();
@@ -790,7 +861,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                                     issue_ss(s_tmem, q_desc + ((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
                                              kd + ((k >> 2) * (TK * 8) + (k & 3) * 2), s_idesc, k != 0);
                             issue_commit(&bars.s_full[t]);
-                            if (j == b - 1) issue_commit(&bars.q_empty[t]);
+                            if (j - 1 == a) issue_commit(&bars.q_empty[t]);
                         }
                         issue_commit(&bars.empty[slot]);
                         if (++slot == C::SLOTS) {
@@ -811,7 +882,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             int local_abort = 0;
             WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
             issue_commit(&bars.drain[t]);
-            warp_wait(&bars.drain[t], 0, drain, kWhereDrain, -1);
+            warp_sleep(&bars.drain[t], 0, drain, kWhereDrain, -1);
         }
     }
     __syncwarp();

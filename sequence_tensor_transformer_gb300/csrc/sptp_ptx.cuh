@@ -72,10 +72,7 @@ __device__ __forceinline__ void report_timeout(const WaitCtx& w, int where, int 
 // returns false if the wait gave up (timeout or CTA abort).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where,
                                           int info) {
-    // (the timer takes a microsecond to read: it is not looked at in a short wait)
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (true) {
 #pragma unroll 1
@@ -89,11 +86,41 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     }
 }
 
+// The same for kernels whose warps share issue slots with others that have work to
+// do: a waiting thread sleeps (up to kSleepNs at a time, then looks at the abort
+// flag and the clock) until the phase completes, instead of trying again and again.
+constexpr uint32_t kSleepNs = 100000;
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepNs)
+            : "memory");
+        if (ok) return true;
+        if (*w.abort_flag) return false;
+        const unsigned long long now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > w.limit_ns) {
+            report_timeout(w, where, info);
+            return false;
+        }
+    }
+}
+
 // mbar_wait by a whole warp: true if every lane's wait was.  A lane gives up by
 // itself (its own clock, or the abort flag seen); what follows a wait has the
 // warp's lanes work together, so they go on or leave as one.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, where, info));
+}
+
+__device__ __forceinline__ bool warp_sleep(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where, int info) {
+    return __all_sync(0xffffffffu, mbar_sleep(bar, parity, w, where, info));
 }
 
 // Waits until a global int reaches `target` (acquire); bounded like mbar_wait.

@@ -14,9 +14,10 @@
 //  - One warp walks over the CTA's share (prompt_plan.cuh) and keeps a ring of K
 //    and V tiles filled by TMA, a box per page; it leaves a description of each
 //    item for the others.
-//  - One warp per tile of rows issues its products: S of the next keys right behind
-//    O of the last ones.  While a tile of rows is in its softmax, the other one's
-//    products run.
+//  - One warp issues the products, the two tiles of rows in turn: S of a tile's next
+//    keys right behind O of its last ones.  While a tile is in its softmax, the
+//    other one's products run.  (With a warp each, their products interleaved, and
+//    both tiles were in their softmax at once, the tensor cores idle.)
 //  - E4M3: four warps turn the tiles of codes that TMA brings into bf16 tiles,
 //    code times the row's power of two, which is exact; the rest is the same.
 //  - Four warps per tile of rows do its softmax, a thread a row, scores in
@@ -227,7 +228,7 @@ struct Bars {
     uint64_t p_ready[2];                       // weights there, outputs rescaled
     uint64_t o_full[2];                        // outputs of an item done
     uint64_t w_full[kItems], w_empty[kItems];  // descriptions
-    uint64_t drain[2];
+    uint64_t drain;
     Work work[kItems];
     uint32_t tmem;
     int abort_flag;
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     if (tid == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&bars.full[s], C::CODES ? 4 : 1);
-            mbar_init(&bars.empty[s], NQ);
+            mbar_init(&bars.empty[s], 1);
         }
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars.c_full[s], 1 + 32);
@@ -447,11 +448,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             mbar_init(&bars.s_full[t], 1);
             mbar_init(&bars.p_ready[t], kTileRows);
             mbar_init(&bars.o_full[t], 1);
-            mbar_init(&bars.drain[t], 1);
         }
+        mbar_init(&bars.drain, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bars.w_full[i], 1);
-            mbar_init(&bars.w_empty[i], 5 * NQ + (C::CODES ? 4 : 0));
+            mbar_init(&bars.w_empty[i], 4 * NQ + 1 + (C::CODES ? 4 : 0));
         }
         fence_mbar_init();
         bars.abort_flag = 0;
@@ -792,29 +793,40 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 for (int t = 0; t < NQ; ++t)
                     if (q_used[t] > 0) mbar_wait(&bars.q_full[t], (q_used[t] - 1) & 1, drain, kWhereDrain, t);
             }
-        } else if (warp < C::ISSUER + NQ) {
-            // -------------------------------------------------- products of one tile of rows
-            const int t = warp - C::ISSUER;
+        } else if (warp == C::ISSUER) {
+            // -------------------------------------------------- products
             const int ksteps = (p.D + 15) / 16;
             const uint32_t s_idesc = idesc_bf16_f32(kTileRows, TK);
             const uint32_t o_idesc = idesc_bf16_f32(kTileRows, ksteps * 16) | kSecondByRows;
             // (descriptors count in 16 bytes, and no tile's addresses carry out of that field)
-            const uint64_t q_desc = smem_desc_kmajor_sw128(smem_u32(smem) + t * C::Q_BYTES);
-            const uint64_t k_desc = smem_desc_kmajor_sw128(smem_u32(slots));
+            const uint64_t q_desc = smem_desc_kmajor_sw128(smem_u32(smem)), k_desc = smem_desc_kmajor_sw128(smem_u32(slots));
             const uint64_t v_desc = smem_desc_rows(smem_u32(slots), TK * 128);
-            const uint32_t s_tmem = tmem + t * C::S, o_tmem = tmem + C::O + t * C::DP;
             int slot = 0, w = 0;
-            uint32_t phase = 0, w_phase = 0, q_phase = 0, p_phase = 0;
+            uint32_t phase = 0, w_phase = 0, q_phase[NQ] = {}, p_phase[NQ] = {};
             bool ok = true;
+            auto next_slot = [&] {
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
             while (true) {
-                if (!(ok = warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, t))) break;
+                if (!(ok = warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, 0))) break;
                 const Work& d = bars.work[w];
                 if (uniform(d.flags) & kStop) break;
-                const int here = uniform(d.here), a = uniform(d.a[t]), b = uniform(d.b[t]);
+                const int here = uniform(d.here);
                 const int lo = uniform(d.lo) - uniform(d.key0), hi = uniform(d.hi) - uniform(d.key0);
-                // the last keys first; V of tile j and K of tile j - 1: scores of the next
-                // tile are issued right behind the outputs of this one
+                int a[NQ], b[NQ];
+#pragma unroll
+                for (int t = 0; t < NQ; ++t) {
+                    a[t] = uniform(d.a[t]);
+                    b[t] = uniform(d.b[t]);
+                }
+                // the last keys first; V of tile j and K of tile j - 1: a tile of rows' next
+                // scores are issued right behind its outputs, so that the two tiles take
+                // turns on the tensor cores, each in its softmax while the other has them
                 for (int j = here; j >= 0 && here > 0; --j) {
+                    int v_slot = 0;
                     if (j < here) {
                         // rows of V that no row of the batch sees become zeros (their
                         // weights are 0, and 0 times what lies there might not be)
@@ -829,45 +841,49 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (j >= a && j < b) {
-                            if (!(ok = warp_sleep(&bars.p_ready[t], p_phase, wc, kWherePromptWeights, j))) break;
-                            p_phase ^= 1;
+                        v_slot = slot;
+                        next_slot();
+                    }
+                    bool have_k = false;
+#pragma unroll
+                    for (int t = 0; t < NQ; ++t) {
+                        if (j < here && j >= a[t] && j < b[t]) {
+                            if (!(ok = warp_sleep(&bars.p_ready[t], p_phase[t], wc, kWherePromptWeights, j))) break;
+                            p_phase[t] ^= 1;
                             tc_fence_after();
-                            const uint64_t vd = v_desc + slot * (C::SLOT >> 4);
-                            const uint32_t adds = j != b - 1;
+                            const uint64_t vd = v_desc + v_slot * (C::SLOT >> 4);
+                            const uint32_t adds = j != b[t] - 1;
 #pragma unroll
                             for (int k = 0; k < TK / 16; ++k)
-                                issue_ts(o_tmem, s_tmem + TK / 2 + k * 8, vd + k * (2048 >> 4), o_idesc, k != 0 ? 1u : adds);
-                            if (j == a) issue_commit(&bars.o_full[t]);
+                                issue_ts(tmem + C::O + t * C::DP, tmem + t * C::S + TK / 2 + k * 8, vd + k * (2048 >> 4),
+                                         o_idesc, k != 0 ? 1u : adds);
+                            if (j == a[t]) issue_commit(&bars.o_full[t]);
                         }
-                        issue_commit(&bars.empty[slot]);
-                        if (++slot == C::SLOTS) {
-                            slot = 0;
-                            phase ^= 1;
+                        if (j > 0 && !have_k) {
+                            if (!(ok = warp_sleep(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
+                            have_k = true;
                         }
-                    }
-                    if (j > 0) {
-                        if (!(ok = warp_sleep(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
-                        if (j - 1 >= a && j - 1 < b) {
-                            if (j == b) {
-                                if (!(ok = warp_sleep(&bars.q_full[t], q_phase, wc, kWherePromptQuery, j))) break;
-                                q_phase ^= 1;
+                        if (j - 1 >= a[t] && j - 1 < b[t]) {
+                            if (j == b[t]) {
+                                if (!(ok = warp_sleep(&bars.q_full[t], q_phase[t], wc, kWherePromptQuery, j))) break;
+                                q_phase[t] ^= 1;
                             }
                             tc_fence_after();
-                            const uint64_t kd = k_desc + slot * (C::SLOT >> 4);
+                            const uint64_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + slot * (C::SLOT >> 4);
 #pragma unroll
                             for (int k = 0; k < C::DP / 16; ++k)
                                 if (k < ksteps)
-                                    issue_ss(s_tmem, q_desc + ((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                                    issue_ss(tmem + t * C::S, qd + ((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
                                              kd + ((k >> 2) * (TK * 8) + (k & 3) * 2), s_idesc, k != 0);
                             issue_commit(&bars.s_full[t]);
-                            if (j - 1 == a) issue_commit(&bars.q_empty[t]);
+                            if (j - 1 == a[t]) issue_commit(&bars.q_empty[t]);
                         }
+                    }
+                    if (!ok) break;
+                    if (j < here) issue_commit(&bars.empty[v_slot]);
+                    if (j > 0) {
                         issue_commit(&bars.empty[slot]);
-                        if (++slot == C::SLOTS) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
+                        next_slot();
                     }
                 }
                 if (!ok) break;
@@ -881,8 +897,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             // the products still under way write to tensor memory, which is given back below
             int local_abort = 0;
             WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
-            issue_commit(&bars.drain[t]);
-            warp_sleep(&bars.drain[t], 0, drain, kWhereDrain, -1);
+            issue_commit(&bars.drain);
+            warp_sleep(&bars.drain, 0, drain, kWhereDrain, -1);
         }
     }
     __syncwarp();

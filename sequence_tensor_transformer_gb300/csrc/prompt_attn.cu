@@ -171,11 +171,13 @@ int prompt_grid(const PromptParams& p, int most, int tk) {
 
 cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s) {
     int ctas = 0;
-    // (the plain kernels find a row's maximum among unscaled scores)
-    const bool plain = p.cap == 0.f && p.slopes == nullptr && p.scale > 0.f;
-    const auto codes = plain ? launch_prompt_e4m3 : launch_prompt_e4m3_ex;
-    const auto wide = plain ? launch_prompt_bf16 : launch_prompt_bf16_ex;
-    cudaError_t e = (!bf16 ? launch_prompt_f32 : e4m3 ? codes : wide)(p, num_sms, &ctas, s);
+    // (the plain kernels find a row's maximum among unscaled scores; those with a bias
+    // take slopes of 0 where there are none)
+    static PromptLaunch* const kernels[2][2][2] = {
+        {{launch_prompt_bf16, launch_prompt_bf16_bias}, {launch_prompt_bf16_cap, launch_prompt_bf16_cap_bias}},
+        {{launch_prompt_e4m3, launch_prompt_e4m3_bias}, {launch_prompt_e4m3_cap, launch_prompt_e4m3_cap_bias}}};
+    const bool cap = p.cap != 0.f, bias = p.slopes != nullptr || (!cap && !(p.scale > 0.f));
+    cudaError_t e = (bf16 ? kernels[e4m3][cap][bias] : launch_prompt_f32)(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
     const int grid = ctas * kJoinBlocks + 1;
     return bf16 ? launch_after(prompt_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, s, p, ctas)

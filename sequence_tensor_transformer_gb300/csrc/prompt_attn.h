@@ -59,12 +59,12 @@ struct PromptParams {
 // Rows of an item, at most, by head size and element type.
 constexpr int prompt_item_rows(int D, bool bf16) { return !bf16 ? 64 : D <= 128 ? 256 : 128; }
 
-// (_ex: a cap, a bias or scale <= 0)
-cudaError_t launch_prompt_bf16(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
-cudaError_t launch_prompt_bf16_ex(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
-cudaError_t launch_prompt_e4m3(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
-cudaError_t launch_prompt_e4m3_ex(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
-cudaError_t launch_prompt_f32(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
+// One each for plain scores (scale > 0), with a cap, with a bias and with both: an
+// instruction cache holds the code of one.
+using PromptLaunch = cudaError_t(PromptParams& p, int num_sms, int* ctas, cudaStream_t s);
+PromptLaunch launch_prompt_bf16, launch_prompt_bf16_cap, launch_prompt_bf16_bias, launch_prompt_bf16_cap_bias;
+PromptLaunch launch_prompt_e4m3, launch_prompt_e4m3_cap, launch_prompt_e4m3_bias, launch_prompt_e4m3_cap_bias;
+PromptLaunch launch_prompt_f32;
 cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 // The split of the heads and rows into items of at most `rows` rows whose tiles
 // hold `tile_rows`, and the division by the page size.

@@ -1,0 +1,10 @@
+// Prompts' attention over a bf16 cache, capped scores: the tensor-core kernel.
+#include "prompt_attn_tc.cuh"
+
+namespace sptp {
+
+cudaError_t launch_prompt_bf16_cap(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    return prompt::launch_width<false, true, false>(p, num_sms, ctas, s);
+}
+
+}  // namespace sptp

@@ -1,0 +1,10 @@
+// Prompts' attention over an E4M3 cache, capped scores with a bias: the tensor-core kernel.
+#include "prompt_attn_tc.cuh"
+
+namespace sptp {
+
+cudaError_t launch_prompt_e4m3_cap_bias(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    return prompt::launch_width<true, true, true>(p, num_sms, ctas, s);
+}
+
+}  // namespace sptp

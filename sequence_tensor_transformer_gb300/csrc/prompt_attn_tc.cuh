@@ -237,19 +237,13 @@ struct Bars {
 };
 
 // ---------------------------------------------------------------- softmax of one tile of rows
-// tanh u = u P(u^2) for |u| <= 1, off by 5e-8 of itself: the polynomial of degree 6
-// in u^2 with the least largest relative error (a Remez fit).
+// tanh u = u P(u^2) for |u| <= 1/2, off by 1.4e-8 of itself: the polynomial of degree
+// 4 in u^2 with the least largest relative error (a Remez fit).
 __host__ __device__ constexpr float tanh_term(int i) {
-    return i == 0   ? 0.999999950241f
-           : i == 1 ? -0.333328391536f
-           : i == 2 ? 0.133252040772f
-           : i == 3 ? -0.053457029549f
-           : i == 4 ? 0.0202899803204f
-           : i == 5 ? -0.00620337898208f
-                    : 0.00104102258568f;
+    return i == 0 ? 0.999999986872f : i == 1 ? -0.333330693943f : i == 2 ? 0.133247793204f : i == 3 ? -0.0529860754004f : 0.0171350067528f;
 }
 
-template <class C, bool MODS>
+template <class C, bool CAP, bool BIAS>
 struct Softmax {
     static constexpr int TK = C::TK;
 
@@ -268,10 +262,11 @@ struct Softmax {
         s[j + 1] = f.y;
     }
 
-    // The cap.  On the fused multiply-adds (9 of them a score) where no |score| of
-    // the warp's rows passes the cap, and for three scores of eight on the function
-    // unit (an exponential and a reciprocal), so that both units have their share.
-    __device__ __forceinline__ void apply_cap(const PromptParams& p, const ScoreCap& cap, float (&s)[N]) {
+    // The cap, cap tanh(s / cap), of 32 scores that also still lie at s_at.  Where no
+    // |score| of the warp's rows passes half the cap, three of four by a series on the
+    // fused multiply-adds (7 of them each), the rest on the function unit (an
+    // exponential and a reciprocal), so that both units have their share.
+    __device__ __forceinline__ void apply_cap(const PromptParams& p, const ScoreCap& cap, float (&s)[N], uint32_t s_at) {
         const float to_u = to_log2 * cap.inv;
         // cap - 2 cap / (1 + e^(2 s / cap)): off by 2^-22 of the cap
         auto by_units = [&](int j) {
@@ -281,32 +276,51 @@ struct Softmax {
         };
         auto by_series = [&](int j) {
             const uint64_t u = mul2(at(s, j), both(to_u)), v = mul2(u, u);
-            uint64_t y = both(tanh_term(6));
+            uint64_t y = both(tanh_term(4) * cap.cap);
 #pragma unroll
-            for (int i = 5; i >= 0; --i) y = fma2(y, v, both(tanh_term(i)));
-            put(s, j, mul2(mul2(u, both(cap.cap)), y));
+            for (int i = 3; i >= 0; --i) y = fma2(y, v, both(tanh_term(i) * cap.cap));
+            put(s, j, mul2(u, y));
         };
-        float most = 0.f;
+        float most[4];
 #pragma unroll
-        for (int j = 0; j < N; j += 2) most = max3(most, fabsf(s[j]), fabsf(s[j + 1]));
+        for (int i = 0; i < 4; ++i) most[i] = max3(fabsf(s[i]), fabsf(s[4 + i]), fabsf(s[8 + i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most[i] = max3(most[i], fabsf(s[12 + i]), fabsf(s[16 + i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most[i] = max3(most[i], fabsf(s[20 + i]), fabsf(s[24 + i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most[i] = fmaxf(most[i], fabsf(s[28 + i]));
+        const float all = max3(most[0], most[1], fmaxf(most[2], most[3]));
         // (a NaN among keys that no row sees does not count)
-        const bool near = !__any_sync(0xffffffffu, most * fabsf(to_u) > 1.f);
-        if (p.cap <= kPlainCap) {
-            if (near) {
+        const bool far = __any_sync(0xffffffffu, all * fabsf(to_u) > 0.5f);
+        if (!far) {
 #pragma unroll
-                for (int j = 0; j < N; j += 2) {
-                    if (j % 16 == 2 || j % 16 == 8 || j % 16 == 12)
-                        by_units(j);
-                    else
-                        by_series(j);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; j += 2) by_units(j);
+            for (int j = 0; j < N; j += 2) {
+                if (j % 8 == 2 && N == 32)
+                    by_units(j);
+                else
+                    by_series(j);
             }
-        } else {
+        } else if (p.cap <= kPlainCap) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) s[j] = cap(s[j] * to_log2);
+            for (int j = 0; j < N; j += 2) by_units(j);
+        } else {
+            // scores next to a cap in the hundreds: rare, and little code
+#pragma unroll 1
+            for (int c = 0; c < N; c += 16) {
+                uint32_t x[16];
+                tmem_ld_16cols(s_at + c, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(cap(__uint_as_float(x[i]) * to_log2));
+                tmem_st_16cols(s_at + c, x);
+            }
+            tmem_st_wait();
+            uint32_t raw[N];
+            tmem_ld_32cols(s_at, raw);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < N; ++j) s[j] = __uint_as_float(raw[j]);
         }
     }
 
@@ -364,24 +378,22 @@ struct Softmax {
             // scores in units of log 2 are unit s + bias
             float unit = to_log2, bias = 0.f;
             const int key = key0 + c * N;
-            if constexpr (MODS) {
-                if (p.cap != 0.f) {
-                    apply_cap(p, cap, s);
-                    unit = 1.f;
-                }
-                if (p.slopes != nullptr) {
-                    const float far = static_cast<float>(pos - key);
-                    if (p.prefix_lens == nullptr || !__any_sync(0xffffffffu, key + N > pos + 1)) {
-                        // slope (j - pos), of which the part without j can wait
+            if constexpr (CAP) {
+                apply_cap(p, cap, s, s_at + c * N);
+                unit = 1.f;
+            }
+            if constexpr (BIAS) {
+                const float far = static_cast<float>(pos - key);
+                if (p.prefix_lens == nullptr || !__any_sync(0xffffffffu, key + N > pos + 1)) {
+                    // slope (j - pos), of which the part without j can wait
 #pragma unroll
-                        for (int j = 0; j < N; j += 2) put(s, j, fma2(at(s, j), both(unit), pair2(slope * j, slope * (j + 1))));
-                        bias = -slope * far;
-                    } else {
+                    for (int j = 0; j < N; j += 2) put(s, j, fma2(at(s, j), both(unit), pair2(slope * j, slope * (j + 1))));
+                    bias = -slope * far;
+                } else {
 #pragma unroll
-                        for (int j = 0; j < N; ++j) s[j] = fmaf(s[j], unit, -slope * fabsf(far - j));
-                    }
-                    unit = 1.f;
+                    for (int j = 0; j < N; ++j) s[j] = fmaf(s[j], unit, -slope * fabsf(far - j));
                 }
+                unit = 1.f;
             }
             if (masked) {
                 // bit j: key j of the 32 is seen
@@ -419,7 +431,7 @@ struct Softmax {
     }
 };
 
-template <class C, bool MODS, bool TEST = false>
+template <class C, bool CAP, bool BIAS, bool TEST = false>
 __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __grid_constant__ PromptParams p) {
     constexpr int TK = C::TK, NQ = C::NQ, kThreads = 32 * C::WARPS;
     extern __shared__ uint8_t smem_raw[];
@@ -495,7 +507,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         const uint32_t s_at = tmem + lane_at + t * C::S, o_at = tmem + lane_at + C::O + t * C::DP;
         const int o_cols = (p.D + 15) / 16 * 16;
         const ScoreCap cap(p.cap);
-        Softmax<C, MODS> sm;
+        Softmax<C, CAP, BIAS> sm;
         sm.to_log2 = p.scale * kLog2e;
         int w = 0;
         uint32_t w_phase = 0, s_phase = 0, o_phase = 0;
@@ -514,7 +526,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             // as much as one that is)
             sm.lo = in ? first_key(p, sm.pos) : 0;
             sm.hi = in ? min(d.len, end_key(sm.pos, d.prefix)) : 0x7fffffff;
-            sm.slope = MODS && p.slopes != nullptr && in ? __ldg(p.slopes + d.slope0 + head) * kLog2e : 0.f;
+            sm.slope = BIAS && p.slopes != nullptr && in ? __ldg(p.slopes + d.slope0 + head) * kLog2e : 0.f;
             const int a = d.a[t], b = d.b[t], key0 = d.key0;
             bool ok = true;
             for (int j = b - 1; j >= a; --j) {
@@ -918,7 +930,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
 
 namespace {  // internal: a process may load the library and its checked build, each with `done` of its own
 
-template <class C, bool MODS, bool TEST = false>
+template <class C, bool CAP, bool BIAS, bool TEST = false>
 cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     plan_prompt(p, C::NQ * kTileRows, kTileRows);
     // the largest boxes that never cross a page
@@ -938,24 +950,24 @@ cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (!(done.load(std::memory_order_relaxed) & bit)) {
         // the groups' shares of registers must not exceed what the kernel was compiled for
         cudaFuncAttributes attr;
-        e = cudaFuncGetAttributes(&attr, prompt_tc_kernel<C, MODS, TEST>);
+        e = cudaFuncGetAttributes(&attr, prompt_tc_kernel<C, CAP, BIAS, TEST>);
         if (e != cudaSuccess) return e;
         if (C::SPLIT_REGS && attr.numRegs < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(prompt_tc_kernel<C, MODS, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+        e = cudaFuncSetAttribute(prompt_tc_kernel<C, CAP, BIAS, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     *ctas = prompt_grid(p, num_sms < kPromptWideCtas ? num_sms : kPromptWideCtas, C::TK);
     if (TEST && *ctas > kSelftestCtas) *ctas = kSelftestCtas;
-    return launch_after(prompt_tc_kernel<C, MODS, TEST>, *ctas, 32 * C::WARPS, C::BYTES, s, p);
+    return launch_after(prompt_tc_kernel<C, CAP, BIAS, TEST>, *ctas, 32 * C::WARPS, C::BYTES, s, p);
 }
 
 // By row width.
-template <bool CODES, bool MODS>
+template <bool CODES, bool CAP, bool BIAS>
 cudaError_t launch_width(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
-    if (p.D <= 64) return launch_tc<Shape<64, CODES>, MODS>(p, num_sms, ctas, s);
-    if (p.D <= 128) return launch_tc<Shape<128, CODES>, MODS>(p, num_sms, ctas, s);
-    return launch_tc<Shape<256, CODES>, MODS>(p, num_sms, ctas, s);
+    if (p.D <= 64) return launch_tc<Shape<64, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
+    if (p.D <= 128) return launch_tc<Shape<128, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
+    return launch_tc<Shape<256, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
 }
 
 }  // namespace

@@ -23,7 +23,10 @@ namespace sptp {
 namespace prompt {
 
 constexpr int kTileCost = 4;
-constexpr int kItemCost = 4;
+#ifndef ICOST
+#define ICOST 12
+#endif
+constexpr int kItemCost = ICOST;
 
 struct Block {
     int b;        // sequence

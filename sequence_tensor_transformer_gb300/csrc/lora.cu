@@ -47,43 +47,25 @@ __device__ __forceinline__ void split2bf(float x, float y, uint32_t& hi, uint32_
     lo = pack2(x - h.x, y - h.y);
 }
 
-// The adapters of a tile of ROWS rows, each distinct one once, in the order in
-// which they first come.
-template <int ROWS>
-struct Tile {
-    int id[ROWS];       // -1: none
-    int distinct[ROWS];
-    int count;
-};
-
-template <int ROWS>
-__device__ __forceinline__ void load_tile(Tile<ROWS>& t, const LoraParams& p, int m0) {
-    const int tid = threadIdx.x;
-    if (tid < ROWS) {
-        const int a = m0 + tid < p.M ? __ldg(p.ids + m0 + tid) : -1;
-        t.id[tid] = a < 0 || a >= p.adapters ? -1 : a;
-    }
-    __syncthreads();
-    if (tid < 32) {
-        int n = 0;
-#pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += 32) {
-            const int r = r0 + tid;
-            const int a = r < ROWS ? t.id[r] : -1;
-            bool first = a >= 0;
-            for (int i = 0; first && i < r; ++i) first = t.id[i] != a;
-            const uint32_t mask = __ballot_sync(0xffffffffu, first);
-            if (first) t.distinct[n + __popc(mask & ((1u << tid) - 1u))] = a;
-            n += __popc(mask);
-        }
-        if (tid == 0) t.count = n;
-    }
-    __syncthreads();
-}
-
 __device__ __forceinline__ uint4 load16(const void* base, long long elem, bool in) {
     return in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + elem)) : make_uint4(0, 0, 0, 0);
 }
+
+// The adapters of 16 rows: lane r < 16 has row r's (-1: none or no row), and `first`
+// the lanes whose row is the first with its adapter.
+struct Ids {
+    int id;
+    uint32_t first;
+
+    __device__ __forceinline__ Ids(const LoraParams& p, int m0, int rows) {
+        const int lane = threadIdx.x & 31;
+        id = lane < rows && m0 + lane < p.M ? __ldg(p.ids + m0 + lane) : -1;
+        if (id >= p.adapters || id < 0) id = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        first = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
+    }
+    __device__ __forceinline__ int of(int row) const { return __shfl_sync(0xffffffffu, id, row); }
+};
 
 // The status words: the first row whose adapter is outside its range.  By the
 // last block of the second launch.
@@ -108,228 +90,270 @@ __device__ __forceinline__ void report_rows(const LoraParams& p) {
 }
 
 // ---------------------------------------------------------------- t = A x, bf16
-// A block has 16 MT rows and one split of K.  Its warps share out the tile's
-// adapters, and the split's elements where there are fewer adapters than warps
-// (their sums are then added in order).
-template <int MT, int NT>
-__global__ void __launch_bounds__(kThreads) lora_down_bf16(const __grid_constant__ LoraParams p) {
-    constexpr int ROWS = 16 * MT;
-    __shared__ Tile<ROWS> tile;
-    __shared__ __align__(16) float sums[kWarps / 2][ROWS * NT * 8];
+// A block has 16 rows and one split of K.  Its warps share out the rows' adapters,
+// and the split's elements where there are fewer adapters than warps (their sums
+// are then added in a fixed order).
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_constant__ LoraParams p) {
+    __shared__ __align__(16) float sums[kWarps / 2][16 * NT * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
     admit_next();
     await_previous();
-    const int tiles = (p.M + ROWS - 1) / ROWS;
-    const int m0 = blockIdx.x % tiles * ROWS;
+    const int tiles = (p.M + 15) / 16;
+    const int m0 = blockIdx.x % tiles * 16;
     const int rest = blockIdx.x / tiles, split = rest % p.splits, shard = rest / p.splits;
-    load_tile(tile, p, m0);
-    const int count = tile.count;
+    const Ids ids(p, m0, 16);
+    const int count = __popc(ids.first);
     if (count == 0) return;
     int groups = 1;
     while (groups < count && groups < kWarps) groups *= 2;
     const int ways = kWarps / groups, group = warp / ways, sub = warp % ways;
     const int k0 = split * p.split_k, k1 = min(p.f, k0 + p.split_k);
-    const long long xrow = static_cast<long long>(shard) * p.M + m0;
-    float* t = p.t + (static_cast<long long>(rest % p.splits) * (p.rowwise ? p.P : 1) + shard) * p.M * p.R;
-    for (int r0 = 0; r0 < p.R; r0 += NT * 8) {
-        for (int first = 0; first < count; first += groups) {
-            const bool mine = first + group < count;
-            const int a = mine ? tile.distinct[first + group] : -1;
-            float acc[MT][NT][4];
+    const long long xrow = (static_cast<long long>(shard) * p.M + m0 + g) * p.f;
+    const bool in0 = m0 + g < p.M, in1 = m0 + g + 8 < p.M;
+    float* t = p.t + ((static_cast<long long>(split) * (p.rowwise ? p.P : 1) + shard) * p.M + m0) * p.R;
+    uint32_t left = ids.first;
+    for (int n = 0; n < group; ++n) left &= left - 1;
+    for (int n0 = 0; n0 < count; n0 += groups) {
+        const bool mine = left != 0;
+        const int a = mine ? ids.of(__ffs(left) - 1) : -2;
+        const bool me0 = ids.of(g) == a, me1 = ids.of(g + 8) == a;
+        for (int n = 0; n < groups; ++n) left &= left - 1;
+        for (int r0 = 0; r0 < p.R; r0 += NT * 8) {
+            float acc[NT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
             if (mine) {
-                bool has[MT];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    has[mt] = __any_sync(0xffffffffu, tile.id[mt * 16 + (lane & 15)] == a);
                 const long long arow = (static_cast<long long>(a) * p.R + r0 + g) * p.K + (p.rowwise ? shard * p.f : 0);
-#pragma unroll 4
-                for (int k = k0 + sub * 32; k < k1; k += ways * 32) {
-                    const int kk = k + i * 8;
-                    const bool in = kk < k1;
+#pragma unroll(NT <= 2 ? 4 : NT <= 4 ? 2 : 1)
+                for (int kb = k0 + sub * 32; kb < k1; kb += ways * 32) {
+                    const int k = kb + i * 8;
+                    const bool in = k < k1;
+                    const uint4 u = load16(p.x, xrow + k, in && in0), v = load16(p.x, xrow + 8ll * p.f + k, in && in1);
                     uint4 w[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        w[nt] = load16(p.A, arow + static_cast<long long>(nt) * 8 * p.K + kk, in && r0 + nt * 8 < p.R);
+                        w[nt] = load16(p.A, arow + static_cast<long long>(nt) * 8 * p.K + k, in && r0 + nt * 8 < p.R);
+                    const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if (!has[mt]) continue;
-                        const uint4 u = load16(p.x, (xrow + mt * 16 + g) * p.f + kk, in && m0 + mt * 16 + g < p.M);
-                        const uint4 v = load16(p.x, (xrow + mt * 16 + g + 8) * p.f + kk, in && m0 + mt * 16 + g + 8 < p.M);
-                        const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(acc[mt][nt], a0, w[nt].x, w[nt].y);
-                            mma_bf16(acc[mt][nt], a1, w[nt].z, w[nt].w);
-                        }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16(acc[nt], a0, w[nt].x, w[nt].y);
+                        mma_bf16(acc[nt], a1, w[nt].z, w[nt].w);
                     }
                 }
             }
-            // rows of this adapter: lane's elements (g, 2i), (g, 2i + 1), (g + 8, ..) of each 16 x 8
-            auto each = [&](auto f) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+            for (int half = ways / 2; half > 0; half /= 2) {  // warps [half, 2 half) of a group to [0, half)
+                float* at = &sums[group * half + (sub < half ? sub : sub - half)][0] + lane * 2;
+                if (sub >= half && sub < 2 * half)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) f(acc[mt][nt][2 * e], acc[mt][nt][2 * e + 1], mt * 16 + g + 8 * e, nt * 8 + 2 * i);
-            };
-            for (int half = ways / 2; half > 0; half /= 2) {  // warps [half, 2 half) of a group to [0, half)
-                if (sub >= half && sub < 2 * half)
-                    each([&](float x, float y, int row, int r) {
-                        *reinterpret_cast<float2*>(&sums[group * half + sub - half][row * NT * 8 + r]) = make_float2(x, y);
-                    });
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2*>(at + (nt * 2 + e) * 64) = make_float2(acc[nt][2 * e], acc[nt][2 * e + 1]);
                 __syncthreads();
                 if (sub < half)
-                    each([&](float& x, float& y, int row, int r) {
-                        const float2 o = *reinterpret_cast<const float2*>(&sums[group * half + sub][row * NT * 8 + r]);
-                        x += o.x;
-                        y += o.y;
-                    });
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 o = *reinterpret_cast<const float2*>(at + (nt * 2 + e) * 64);
+                            acc[nt][2 * e] += o.x;
+                            acc[nt][2 * e + 1] += o.y;
+                        }
                 __syncthreads();
             }
-            if (mine && sub == 0)
-                each([&](float x, float y, int row, int r) {
-                    if (tile.id[row] == a && r0 + r < p.R)
-                        *reinterpret_cast<float2*>(t + static_cast<long long>(m0 + row) * p.R + r0 + r) = make_float2(x, y);
-                });
+            if (sub != 0) continue;
+            // this adapter's rows: elements (g, 2i), (g, 2i + 1), (g + 8, ..) of each 16 x 8
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (r0 + nt * 8 >= p.R) break;
+                float* at = t + static_cast<long long>(g) * p.R + r0 + nt * 8 + 2 * i;
+                if (me0) *reinterpret_cast<float2*>(at) = make_float2(acc[nt][0], acc[nt][1]);
+                if (me1) *reinterpret_cast<float2*>(at + 8ll * p.R) = make_float2(acc[nt][2], acc[nt][3]);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------- out = base + B t, bf16
-// A block has 16 MT rows; its warps take chunks of 32 columns in turn.
-template <int MT, int KT>
-__global__ void __launch_bounds__(kThreads) lora_up_bf16(const __grid_constant__ LoraParams p, int col_blocks) {
-    constexpr int ROWS = 16 * MT;
-    __shared__ Tile<ROWS> tile;
+// A block has 16 rows; its warps take chunks of 32 NC columns in turn, side by side:
+// 1 KB of a row at a time with NC = 2.  (With rows of its own for each warp, so that
+// they share B, the GPU worked its way through the columns of all rows at once, 128
+// bytes of a row here and there: 16384 rows of 4608 columns 95 us instead of 70.)
+template <int KT, int NC, bool MANY>
+__global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
+    lora_up_bf16(const __grid_constant__ LoraParams p, int col_blocks) {
+    constexpr int UN = MANY || KT >= 8 ? 1 : 8 / KT;  // adapters whose B is loaded at once
+    constexpr int DEPTH = MANY ? 2 : 1;                   // chunks whose base is under way
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
     admit_next();
-    const int m0 = blockIdx.x / col_blocks * ROWS;
     await_previous();
     if (blockIdx.x == gridDim.x - 1) {
         report_rows(p);
         return;
     }
-    load_tile(tile, p, m0);
-    const int count = tile.count;
+    const int m0 = blockIdx.x / col_blocks * 16;
+    if (m0 >= p.M) return;
+    const Ids ids(p, m0, 16);
     const bool in_place = p.out == p.base;
-    if (count == 0 && in_place) return;
-    const int shards = p.rowwise ? p.P : 1;
-    const int chunks = (p.N + 31) / 32;  // of a shard's columns (rowwise) or of all shards'
-    for (int shard = 0; shard < shards; ++shard) {
-        // this lane's part of t, times the gain: rows g and g + 8 of each 16, elements 4 i .. 4 i + 3 of each 16
-        uint32_t hi[MT][KT][4], lo[MT][KT][4];
+    if (ids.first == 0 && in_place) return;
+    const int id0 = ids.of(g), id1 = ids.of(g + 8);
+    const bool row0 = m0 + g < p.M && (!in_place || id0 >= 0), row1 = m0 + g + 8 < p.M && (!in_place || id1 >= 0);
+    // the chunks of all shards, this warp's from `first` on
+    const int chunks = (p.n + 32 * NC - 1) / (32 * NC);  // of a shard
+    const int first = blockIdx.x % col_blocks * kWarps + warp, step = col_blocks * kWarps;
+    struct Place {
+        int shard, chunk;
+    };
+    auto advance = [&](Place& q) {
+        for (q.chunk += step; q.chunk >= chunks; q.chunk -= chunks) ++q.shard;
+    };
+    // lane i has columns 8 i .. 8 i + 7 of each 32: 2 j and 2 j + 1 of them in product j
+    auto first_of = [&](const Place& q) {  // element of row g
+        return (static_cast<long long>(q.shard) * p.M + m0 + g) * p.n + q.chunk * (32 * NC) + 8 * i;
+    };
+    auto load_base = [&](const Place& q, uint4 (&v)[NC][2]) {
+        const bool in = q.shard < p.P;
+        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.base) + (in ? first_of(q) : 0));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int c = 0; c < NC; ++c) {
+            const bool cin = in && q.chunk * (32 * NC) + c * 32 + 8 * i < p.n;
+            v[c][0] = cin && row0 ? b[c * 4] : make_uint4(0, 0, 0, 0);
+            v[c][1] = cin && row1 ? b[c * 4 + p.n] : make_uint4(0, 0, 0, 0);  // 8 rows on: 8 n elements, n times 16 bytes
+        }
+    };
+    Place q = {first / chunks, first % chunks}, coming = q;
+    uint4 ahead[DEPTH][NC][2];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+        load_base(coming, ahead[d]);
+        advance(coming);
+    }
+    // this lane's part of t, times the gain: rows g and g + 8, elements 4 i .. 4 i + 3 of each 16
+    uint32_t hi[KT][4], lo[KT][4];
+    auto load_t = [&](int shard) {
+        const int shards = p.rowwise ? p.P : 1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int a = e ? id1 : id0;
+            const float gain = a < 0 ? 0.f : p.gains != nullptr ? __ldg(p.gains + a) : 1.f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (a >= 0 && kt * 16 + 4 * i < p.R) {
+                    const float* at = p.t + (static_cast<long long>(shard) * p.M + m0 + g + 8 * e) * p.R + kt * 16 + 4 * i;
+                    const long long stride = static_cast<long long>(shards) * p.M * p.R;
+#pragma unroll 8
+                    for (int s = 0; s < p.splits; ++s) {
+                        const float4 u = *reinterpret_cast<const float4*>(at + s * stride);
+                        v.x += u.x;
+                        v.y += u.y;
+                        v.z += u.z;
+                        v.w += u.w;
+                    }
+                }
+                split2bf(v.x * gain, v.y * gain, hi[kt][e], lo[kt][e]);
+                split2bf(v.z * gain, v.w * gain, hi[kt][2 + e], lo[kt][2 + e]);
+            }
+        }
+    };
+    // base + the products with the columns whose B is in b, both rows of 32 columns
+    auto add = [&](const uint4 (&was)[2], const uint2 (&b)[KT][NC * 4], int c, uint4 (&now)[2]) {
+        uint32_t *w0 = reinterpret_cast<uint32_t*>(&now[0]), *w1 = reinterpret_cast<uint32_t*>(&now[1]);
+        const uint32_t *o0 = reinterpret_cast<const uint32_t*>(&was[0]), *o1 = reinterpret_cast<const uint32_t*>(&was[1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f0 = unpack2(o0[j]), f1 = unpack2(o1[j]);
+            float sum[4] = {f0.x, f0.y, f1.x, f1.y};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                mma_bf16(sum, lo[kt], b[kt][c * 4 + j].x, b[kt][c * 4 + j].y);
+                mma_bf16(sum, hi[kt], b[kt][c * 4 + j].x, b[kt][c * 4 + j].y);
+            }
+            w0[j] = pack2(sum[0], sum[1]);
+            w1[j] = pack2(sum[2], sum[3]);
+        }
+    };
+    // one adapter for all 16 rows, and the ranks all there: no row or element is left out
+    const bool plain = __all_sync(0xffffffffu, id0 >= 0 && id0 == id1) && __popc(ids.first) == 1 && p.R == KT * 16;
+    const int a0 = ids.first != 0 ? ids.of(__ffs(ids.first) - 1) : 0;
+    int have = -1;  // shard whose t is there
+    for (; q.shard < p.P; advance(q)) {
+        uint4 was[NC][2];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = mt * 16 + g + 8 * e, a = tile.id[row];
-                const float gain = a < 0 ? 0.f : p.gains != nullptr ? __ldg(p.gains + a) : 1.f;
+                was[c][e] = ahead[0][c][e];
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (a >= 0 && kt * 16 + 4 * i < p.R) {
-                        const float* at = p.t + (static_cast<long long>(shard) * p.M + m0 + row) * p.R + kt * 16 + 4 * i;
-                        const long long stride = static_cast<long long>(shards) * p.M * p.R;
-#pragma unroll 4
-                        for (int s = 0; s < p.splits; ++s) {
-                            const float4 u = *reinterpret_cast<const float4*>(at + s * stride);
-                            v.x += u.x;
-                            v.y += u.y;
-                            v.z += u.z;
-                            v.w += u.w;
-                        }
-                    }
-                    split2bf(v.x * gain, v.y * gain, hi[mt][kt][e], lo[mt][kt][e]);
-                    split2bf(v.z * gain, v.w * gain, hi[mt][kt][2 + e], lo[mt][kt][2 + e]);
-                }
+                for (int d = 1; d < DEPTH; ++d) ahead[d - 1][c][e] = ahead[d][c][e];
             }
-        for (int chunk = blockIdx.x % col_blocks * kWarps + warp; chunk < chunks; chunk += col_blocks * kWarps) {
-            // lane i has columns 8 i .. 8 i + 7 of the chunk: 2 j and 2 j + 1 of them in product j
-            const int col = chunk * 32 + 8 * i;
-            const bool cin = col < p.N;
-            const int sh = p.rowwise ? shard : col / p.n;
-            const long long at0 = (static_cast<long long>(sh) * p.M + m0) * p.n + (p.rowwise ? col : col - sh * p.n);
-            uint4 was[MT][2];
+        load_base(coming, ahead[DEPTH - 1]);
+        advance(coming);
+        if (have < 0 || (p.rowwise && have != q.shard)) load_t(p.rowwise ? q.shard : 0);
+        have = q.shard;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + first_of(q));
+        const int col0 = q.chunk * (32 * NC);
+        const long long b0 = (p.rowwise ? 0 : static_cast<long long>(q.shard) * p.n) + col0 + 8 * (g >> 1) + (g & 1);
+        if (plain && col0 + 32 * NC <= p.n) {
+            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a0) * p.N + b0) * p.R + 4 * i;
+            uint2 b[KT][NC * 4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int j = 0; j < NC * 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = mt * 16 + g + 8 * e;
-                    const bool need = cin && m0 + row < p.M && (!in_place || tile.id[row] >= 0);
-                    was[mt][e] = make_uint4(0, 0, 0, 0);
-                    if (need)
-                        was[mt][e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.base) + at0 +
-                                                                     static_cast<long long>(row) * p.n);
-                }
-            float acc[MT][4][4];
+                for (int kt = 0; kt < KT; ++kt)
+                    b[kt][j] = __ldg(reinterpret_cast<const uint2*>(rows + (j / 4 * 32 + 2 * (j % 4)) * (KT * 16) + kt * 16));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int c = 0; c < NC; ++c) {
+                uint4 now[2];
+                add(was[c], b, c, now);
+                out[c * 4] = now[0];
+                out[c * 4 + p.n] = now[1];
+            }
+            continue;
+        }
+        bool cin[NC];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+        for (int c = 0; c < NC; ++c) {
+            cin[c] = col0 + c * 32 + 8 * i < p.n;
+            // rows without an adapter
+            if (cin[c] && row0 && id0 < 0) out[c * 4] = was[c][0];
+            if (cin[c] && row1 && id1 < 0) out[c * 4 + p.n] = was[c][1];
+        }
+        uint32_t left = ids.first;
+        while (left != 0) {
+            int a[UN];
+            uint2 b[UN][KT][NC * 4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
-#pragma unroll 2
-            for (int d = 0; d < count; ++d) {
-                const int a = tile.distinct[d];
-                uint2 b[KT][4];
+            for (int u = 0; u < UN; ++u) {
+                a[u] = left != 0 ? ids.of(__ffs(left) - 1) : -2;
+                left &= left - 1;
+                const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) +
+                                            (static_cast<long long>(max(a[u], 0)) * p.N + b0) * p.R + 4 * i;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = chunk * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-                    const __nv_bfloat16* row =
-                        static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a) * p.N + n) * p.R + 4 * i;
+                for (int j = 0; j < NC * 4; ++j) {
+                    const int n = j / 4 * 32 + 2 * (j % 4);  // from this lane's first row of B
+                    const bool in = a[u] >= 0 && col0 + n + 8 * (g >> 1) + (g & 1) < p.n;
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
-                        b[kt][j] = n < p.N && kt * 16 + 4 * i < p.R ? __ldg(reinterpret_cast<const uint2*>(row + kt * 16))
-                                                                    : make_uint2(0, 0);
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const bool me0 = tile.id[mt * 16 + g] == a, me1 = tile.id[mt * 16 + g + 8] == a;
-                    if (!__any_sync(0xffffffffu, me0 || me1)) continue;
-                    // (sums of their own, kept by this adapter's rows: another's
-                    // infinities do not reach a row)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int kt = 0; kt < KT; ++kt) {
-                            mma_bf16(c, hi[mt][kt], b[kt][j].x, b[kt][j].y);
-                            mma_bf16(c, lo[mt][kt], b[kt][j].x, b[kt][j].y);
-                        }
-                        if (me0) {
-                            acc[mt][j][0] = c[0];
-                            acc[mt][j][1] = c[1];
-                        }
-                        if (me1) {
-                            acc[mt][j][2] = c[2];
-                            acc[mt][j][3] = c[3];
-                        }
-                    }
+                        b[u][kt][j] = in && kt * 16 + 4 * i < p.R
+                                          ? __ldg(reinterpret_cast<const uint2*>(rows + n * p.R + kt * 16))
+                                          : make_uint2(0, 0);
                 }
             }
+            // all 16 rows' products with each adapter, kept by the rows that named it
+            // (so another adapter's infinities do not reach a row)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int u = 0; u < UN; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = mt * 16 + g + 8 * e;
-                    if (!cin || m0 + row >= p.M || (in_place && tile.id[row] < 0)) continue;
-                    uint4 now = was[mt][e];
-                    if (tile.id[row] >= 0) {
-                        uint32_t* w = reinterpret_cast<uint32_t*>(&now);
+                for (int c = 0; c < NC; ++c) {
+                    uint4 now[2];
+                    add(was[c], b[u], c, now);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f = unpack2(w[j]);
-                            w[j] = pack2(f.x + acc[mt][j][2 * e], f.y + acc[mt][j][2 * e + 1]);
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at0 + static_cast<long long>(row) * p.n) = now;
+                    for (int e = 0; e < 2; ++e)
+                        if (cin[c] && (e ? id1 : id0) == a[u]) out[c * 4 + (e ? p.n : 0)] = now[e];
                 }
         }
     }
@@ -338,23 +362,27 @@ __global__ void __launch_bounds__(kThreads) lora_up_bf16(const __grid_constant__
 // ---------------------------------------------------------------- fp32, CUDA cores
 constexpr int kRowsF = 8;
 
-// A block has 8 rows and one split; a warp 8 elements of t at a time: lanes along
-// K, four elements each, and sums over the lanes at the end.
+// A warp has 8 rows, one split and 8 elements of t: lanes along K, four elements
+// each, and sums over the lanes at the end.
 __global__ void __launch_bounds__(kThreads) lora_down_f32(const __grid_constant__ LoraParams p) {
-    __shared__ Tile<kRowsF> tile;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     admit_next();
     await_previous();
-    const int tiles = (p.M + kRowsF - 1) / kRowsF;
-    const int m0 = blockIdx.x % tiles * kRowsF;
-    const int rest = blockIdx.x / tiles, split = rest % p.splits, shard = rest / p.splits;
-    load_tile(tile, p, m0);
+    const int tiles = (p.M + kRowsF - 1) / kRowsF, parts = p.R / 8;
+    long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const int r0 = static_cast<int>(unit % parts) * 8;
+    unit /= parts;
+    const int m0 = static_cast<int>(unit % tiles) * kRowsF;
+    unit /= tiles;
+    const int split = static_cast<int>(unit % p.splits), shard = static_cast<int>(unit / p.splits);
+    if (shard >= (p.rowwise ? p.P : 1)) return;
+    const Ids ids(p, m0, kRowsF);
     const int k0 = split * p.split_k, k1 = min(p.f, k0 + p.split_k);
     const float* x = static_cast<const float*>(p.x) + (static_cast<long long>(shard) * p.M + m0) * p.f;
-    float* t = p.t + (static_cast<long long>(split) * (p.rowwise ? p.P : 1) + shard) * p.M * p.R;
-    const int units = tile.count * (p.R / 8);
-    for (int u = warp; u < units; u += kWarps) {
-        const int a = tile.distinct[u / (p.R / 8)], r0 = u % (p.R / 8) * 8;
+    float* t = p.t + ((static_cast<long long>(split) * (p.rowwise ? p.P : 1) + shard) * p.M + m0) * p.R + r0;
+    for (uint32_t left = ids.first; left != 0; left &= left - 1) {
+        const int a = ids.of(__ffs(left) - 1);
+        const uint32_t mine = __ballot_sync(0xffffffffu, ids.id == a);  // rows
         const float* A = static_cast<const float*>(p.A) + (static_cast<long long>(a) * p.R + r0) * p.K + (p.rowwise ? shard * p.f : 0);
         float acc[kRowsF][8] = {};
         for (int k = k0 + lane * 4; k < k1; k += 128) {
@@ -363,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) lora_down_f32(const __grid_constant_
             for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const float4*>(A + static_cast<long long>(r) * p.K + k));
 #pragma unroll
             for (int m = 0; m < kRowsF; ++m) {
-                if (tile.id[m] != a) continue;
+                if (!(mine >> m & 1)) continue;
                 const float4 v = __ldg(reinterpret_cast<const float4*>(x + static_cast<long long>(m) * p.f + k));
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
@@ -372,21 +400,22 @@ __global__ void __launch_bounds__(kThreads) lora_down_f32(const __grid_constant_
         }
 #pragma unroll
         for (int m = 0; m < kRowsF; ++m) {
-            if (tile.id[m] != a) continue;
+            if (!(mine >> m & 1)) continue;
+            float keep = 0.f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 float v = acc[m][r];
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                if (lane == r) t[static_cast<long long>(m0 + m) * p.R + r0 + r] = v;
+                if (lane == r) keep = v;
             }
+            if (lane < 8) t[static_cast<long long>(m) * p.R + lane] = keep;
         }
     }
 }
 
 // A block has 8 rows; a thread a column of all of them, an adapter's rows at a time.
 __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ LoraParams p, int col_blocks) {
-    __shared__ Tile<kRowsF> tile;
     __shared__ __align__(16) float st[kRowsF][kLoraMaxRank];
     admit_next();
     const int m0 = blockIdx.x / col_blocks * kRowsF;
@@ -395,29 +424,40 @@ __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ 
         report_rows(p);
         return;
     }
-    load_tile(tile, p, m0);
+    const Ids ids(p, m0, kRowsF);
     const bool in_place = p.out == p.base;
-    if (tile.count == 0 && in_place) return;
+    if (ids.first == 0 && in_place) return;
+    const uint32_t some = __ballot_sync(0xffffffffu, ids.id >= 0);  // rows with an adapter
     const int shards = p.rowwise ? p.P : 1;
     for (int shard = 0; shard < shards; ++shard) {
         __syncthreads();
         for (int u = threadIdx.x; u < kRowsF * p.R; u += kThreads) {
-            const int m = u / p.R, r = u % p.R, a = tile.id[m];
+            const int m = u / p.R, r = u % p.R;
+            const int a = m0 + m < p.M ? __ldg(p.ids + m0 + m) : -1;
             float v = 0.f;
-            if (a >= 0) {
+            if (a >= 0 && a < p.adapters) {
                 const float* at = p.t + (static_cast<long long>(shard) * p.M + m0 + m) * p.R + r;
+#pragma unroll 4
                 for (int s = 0; s < p.splits; ++s) v += at[static_cast<long long>(s) * shards * p.M * p.R];
                 if (p.gains != nullptr) v *= __ldg(p.gains + a);
             }
             st[m][r] = v;
         }
         __syncthreads();
-        for (int col = blockIdx.x % col_blocks * kThreads + threadIdx.x; col < p.N; col += col_blocks * kThreads) {
-            const int sh = p.rowwise ? shard : col / p.n;
+        const int rounds = (p.N + kThreads * col_blocks - 1) / (kThreads * col_blocks);
+        for (int round = 0; round < rounds; ++round) {  // (whole warps: the adapters are exchanged between lanes)
+            const int col = (round * col_blocks + blockIdx.x % col_blocks) * kThreads + threadIdx.x;
+            const bool in = col < p.N;
+            const int sh = p.rowwise || !in ? shard : col / p.n;
             const long long at0 = (static_cast<long long>(sh) * p.M + m0) * p.n + (p.rowwise ? col : col - sh * p.n);
-            float acc[kRowsF] = {};
-            for (int d = 0; d < tile.count; ++d) {
-                const int a = tile.distinct[d];
+            float was[kRowsF], acc[kRowsF] = {};
+#pragma unroll
+            for (int m = 0; m < kRowsF; ++m)
+                was[m] = in && m0 + m < p.M ? static_cast<const float*>(p.base)[at0 + static_cast<long long>(m) * p.n] : 0.f;
+            for (uint32_t left = ids.first; left != 0; left &= left - 1) {
+                const int a = ids.of(__ffs(left) - 1);
+                const uint32_t mine = __ballot_sync(0xffffffffu, ids.id == a);
+                if (!in) continue;
                 const float4* row = reinterpret_cast<const float4*>(static_cast<const float*>(p.B) +
                                                                     (static_cast<long long>(a) * p.N + col) * p.R);
 #pragma unroll 4
@@ -425,36 +465,34 @@ __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ 
                     const float4 w = __ldg(row + r);
 #pragma unroll
                     for (int m = 0; m < kRowsF; ++m) {
-                        if (tile.id[m] != a) continue;
+                        if (!(mine >> m & 1)) continue;
                         const float4 v = *reinterpret_cast<const float4*>(&st[m][r * 4]);
                         acc[m] = fmaf(v.x, w.x, fmaf(v.y, w.y, fmaf(v.z, w.z, fmaf(v.w, w.w, acc[m]))));
                     }
                 }
             }
 #pragma unroll
-            for (int m = 0; m < kRowsF; ++m) {
-                if (m0 + m >= p.M || (in_place && tile.id[m] < 0)) continue;
-                const long long at = at0 + static_cast<long long>(m) * p.n;
-                static_cast<float*>(p.out)[at] = static_cast<const float*>(p.base)[at] + acc[m];
-            }
+            for (int m = 0; m < kRowsF; ++m)
+                if (in && m0 + m < p.M && (!in_place || (some >> m & 1)))
+                    static_cast<float*>(p.out)[at0 + static_cast<long long>(m) * p.n] = was[m] + acc[m];
         }
     }
 }
 
-template <int MT, int NT>
+template <int NT>
 cudaError_t down(const LoraParams& p, cudaStream_t s) {
-    const int grid = (p.M + 16 * MT - 1) / (16 * MT) * p.splits * (p.rowwise ? p.P : 1);
-    return launch_after(lora_down_bf16<MT, NT>, grid, kThreads, 0, s, p);
+    return launch_after(lora_down_bf16<NT>, (p.M + 15) / 16 * p.splits * (p.rowwise ? p.P : 1), kThreads, 0, s, p);
 }
 
-template <int MT, int KT>
+template <int KT, int NC, bool MANY>
 cudaError_t up(const LoraParams& p, int num_sms, cudaStream_t s) {
-    // blocks of columns: a few chunks a warp, fewer where the rows alone do not fill the SMs
-    const int tiles = (p.M + 16 * MT - 1) / (16 * MT), chunks = (p.N + 31) / 32;
-    int col_blocks = (2 * num_sms + tiles - 1) / tiles;
+    // Blocks of columns: fewer than fill the SMs twice (each reads t and the adapters'
+    // numbers), one where the rows alone do.
+    const int tiles = (p.M + 15) / 16, chunks = (p.n + 32 * NC - 1) / (32 * NC) * p.P;
+    int col_blocks = 4 * num_sms / tiles;
     const int most = (chunks + kWarps - 1) / kWarps;
-    if (col_blocks > most) col_blocks = most;
-    return launch_after(lora_up_bf16<MT, KT>, tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
+    col_blocks = col_blocks < 1 ? 1 : col_blocks > most ? most : col_blocks;
+    return launch_after(lora_up_bf16<KT, NC, MANY>, tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
 }
 
 }  // namespace
@@ -464,24 +502,20 @@ cudaError_t launch_lora(LoraParams& p, bool bf16, int num_sms, cudaStream_t s) {
     const bool many = p.M >= kLoraMany;
     if (!bf16) {
         const int row_tiles = (p.M + kRowsF - 1) / kRowsF;
-        e = launch_after(lora_down_f32, row_tiles * p.splits * (p.rowwise ? p.P : 1), kThreads, 0, s, p);
+        const long long units = static_cast<long long>(row_tiles) * (p.R / 8) * p.splits * (p.rowwise ? p.P : 1);
+        e = launch_after(lora_down_f32, static_cast<int>((units + kWarps - 1) / kWarps), kThreads, 0, s, p);
         if (e != cudaSuccess) return e;
         int col_blocks = (4 * num_sms + row_tiles - 1) / row_tiles;
         const int most_cols = (p.N + kThreads - 1) / kThreads;
         if (col_blocks > most_cols) col_blocks = most_cols;
         return launch_after(lora_up_f32, row_tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
     }
-    if (p.R <= 16)
-        e = many ? down<4, 2>(p, s) : down<1, 2>(p, s);
-    else if (p.R <= 32)
-        e = many ? down<4, 4>(p, s) : down<1, 4>(p, s);
-    else
-        e = many ? down<2, 8>(p, s) : down<1, 8>(p, s);
+    e = p.R <= 16 ? down<2>(p, s) : p.R <= 32 ? down<4>(p, s) : down<8>(p, s);
     if (e != cudaSuccess) return e;
-    if (p.R <= 16) return many ? up<4, 1>(p, num_sms, s) : up<1, 1>(p, num_sms, s);
-    if (p.R <= 32) return many ? up<4, 2>(p, num_sms, s) : up<1, 2>(p, num_sms, s);
-    if (p.R <= 64) return many ? up<2, 4>(p, num_sms, s) : up<1, 4>(p, num_sms, s);
-    return up<1, 8>(p, num_sms, s);
+    if (p.R <= 16) return many ? up<1, 2, true>(p, num_sms, s) : up<1, 1, false>(p, num_sms, s);
+    if (p.R <= 32) return many ? up<2, 1, true>(p, num_sms, s) : up<2, 1, false>(p, num_sms, s);
+    if (p.R <= 64) return many ? up<4, 1, true>(p, num_sms, s) : up<4, 1, false>(p, num_sms, s);
+    return many ? up<8, 1, true>(p, num_sms, s) : up<8, 1, false>(p, num_sms, s);
 }
 
 }  // namespace sptp

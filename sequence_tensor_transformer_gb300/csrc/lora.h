@@ -22,18 +22,19 @@ struct LoraParams {
 };
 
 constexpr int kLoraMaxRank = 128;
-// Rows from which on a tile has 64 rows (ranks above 32: 32) instead of 16, so
-// that each reads its adapter once for four times as many.
+// Rows from which on the second launch's warps take several chunks each, with
+// loads ahead, instead of one.
 constexpr int kLoraMany = 2048;
 
 // How the product with A is split along a row of f elements: pieces of *split_k,
-// as many as make two blocks an SM of it, but none below 256 elements.
+// as many as make two blocks an SM (bf16: of 16 rows; fp32: of 8 warps with 8 rows
+// and 8 elements each), but none below 256 elements.
 inline int lora_splits(int M, int f, int R, int shards, bool bf16, int* split_k) {
-    const int rows = !bf16 ? 8 : M < kLoraMany ? 16 : R <= 32 ? 64 : 32;
-    const long long tiles = (static_cast<long long>(M) + rows - 1) / rows * shards;
-    constexpr int kBlocks = 304;
-    long long splits = tiles >= kBlocks ? 1 : (kBlocks + tiles - 1) / tiles;
-    const int most = f <= 256 ? 1 : f / 256;
+    const long long tiles = (static_cast<long long>(M) + (bf16 ? 15 : 7)) / (bf16 ? 16 : 8) * shards;
+    const long long blocks = bf16 ? tiles : (tiles * (R / 8) + 7) / 8;
+    constexpr int kBlocks = 304, kLeast = 256;
+    long long splits = blocks >= kBlocks ? 1 : (kBlocks + blocks - 1) / blocks;
+    const int most = f <= kLeast ? 1 : f / kLeast;
     if (splits > most) splits = most;
     *split_k = ((f + static_cast<int>(splits) - 1) / static_cast<int>(splits) + 31) / 32 * 32;
     return (f + *split_k - 1) / *split_k;

@@ -182,11 +182,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
 // 1 KB of a row at a time with NC = 2.  (With rows of its own for each warp, so that
 // they share B, the GPU worked its way through the columns of all rows at once, 128
 // bytes of a row here and there: 16384 rows of 4608 columns 95 us instead of 70.)
-template <int KT, int NC, bool MANY>
+template <int KT, int NC>
 __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
     lora_up_bf16(const __grid_constant__ LoraParams p, int col_blocks) {
-    constexpr int UN = MANY || KT >= 8 ? 1 : 8 / KT;  // adapters whose B is loaded at once
-    constexpr int DEPTH = MANY ? 2 : 1;                   // chunks whose base is under way
+    constexpr int DEPTH = 2;  // chunks whose base is under way
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
     admit_next();
     await_previous();
@@ -322,41 +321,104 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
             if (cin[c] && row0 && id0 < 0) out[c * 4] = was[c][0];
             if (cin[c] && row1 && id1 < 0) out[c * 4 + p.n] = was[c][1];
         }
-        uint32_t left = ids.first;
-        while (left != 0) {
-            int a[UN];
-            uint2 b[UN][KT][NC * 4];
+        for (uint32_t left = ids.first; left != 0; left &= left - 1) {
+            const int a = ids.of(__ffs(left) - 1);
+            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a) * p.N + b0) * p.R + 4 * i;
+            uint2 b[KT][NC * 4];
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                a[u] = left != 0 ? ids.of(__ffs(left) - 1) : -2;
-                left &= left - 1;
-                const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) +
-                                            (static_cast<long long>(max(a[u], 0)) * p.N + b0) * p.R + 4 * i;
+            for (int j = 0; j < NC * 4; ++j) {
+                const int n = j / 4 * 32 + 2 * (j % 4);  // from this lane's first row of B
+                const bool in = col0 + n + 8 * (g >> 1) + (g & 1) < p.n;
 #pragma unroll
-                for (int j = 0; j < NC * 4; ++j) {
-                    const int n = j / 4 * 32 + 2 * (j % 4);  // from this lane's first row of B
-                    const bool in = a[u] >= 0 && col0 + n + 8 * (g >> 1) + (g & 1) < p.n;
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt)
-                        b[u][kt][j] = in && kt * 16 + 4 * i < p.R
-                                          ? __ldg(reinterpret_cast<const uint2*>(rows + n * p.R + kt * 16))
-                                          : make_uint2(0, 0);
-                }
+                for (int kt = 0; kt < KT; ++kt)
+                    b[kt][j] = in && kt * 16 + 4 * i < p.R ? __ldg(reinterpret_cast<const uint2*>(rows + n * p.R + kt * 16))
+                                                           : make_uint2(0, 0);
             }
             // all 16 rows' products with each adapter, kept by the rows that named it
             // (so another adapter's infinities do not reach a row)
 #pragma unroll
-            for (int u = 0; u < UN; ++u)
+            for (int c = 0; c < NC; ++c) {
+                uint4 now[2];
+                add(was[c], b, c, now);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    uint4 now[2];
-                    add(was[c], b[u], c, now);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (cin[c] && (e ? id1 : id0) == a[u]) out[c * 4 + (e ? p.n : 0)] = now[e];
-                }
+                for (int e = 0; e < 2; ++e)
+                    if (cin[c] && (e ? id1 : id0) == a) out[c * 4 + (e ? p.n : 0)] = now[e];
+            }
         }
     }
+}
+
+// Few rows, most with an adapter of their own: a block has one row and 512 columns, a
+// lane two of them, on the CUDA cores (16 rows' products for each of 16 adapters took
+// ten times the instructions: 64 rows of 61 requests 23 us with them, 15 this way; the
+// two cross at some 200 rows).
+__global__ void __launch_bounds__(kThreads) lora_up_row_bf16(const __grid_constant__ LoraParams p, int col_blocks) {
+    __shared__ float part[kThreads];
+    __shared__ __align__(16) float st[kLoraMaxRank];
+    const int tid = threadIdx.x;
+    admit_next();
+    await_previous();
+    if (blockIdx.x == gridDim.x - 1) {
+        report_rows(p);
+        return;
+    }
+    const int m = blockIdx.x / col_blocks, block = blockIdx.x % col_blocks;
+    int a = __ldg(p.ids + m);
+    if (a >= p.adapters) a = -1;
+    const bool in_place = p.out == p.base;
+    if (a < 0 && in_place) return;
+    // a shard's columns come in whole blocks of 512
+    const int shard_blocks = (p.n + 2 * kThreads - 1) / (2 * kThreads);
+    const int shard = block / shard_blocks, col = (block % shard_blocks) * 2 * kThreads + 2 * tid;
+    const bool in = col < p.n;
+    const long long at = (static_cast<long long>(shard) * p.M + m) * p.n + col;
+    const uint32_t was = in ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.base) + at) : 0u;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at);
+    if (a < 0) {
+        if (in) *out = was;
+        return;
+    }
+    const uint4* rows = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(p.B) +
+        (static_cast<long long>(a) * p.N + (p.rowwise ? 0 : static_cast<long long>(shard) * p.n) + (in ? col : 0)) * p.R);
+    const int eights = p.R / 8;
+    uint4 b0[2], b1[2];  // of both columns; the first 16 elements, while t is read
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        b0[e] = e < eights ? __ldg(rows + e) : make_uint4(0, 0, 0, 0);
+        b1[e] = e < eights ? __ldg(rows + eights + e) : make_uint4(0, 0, 0, 0);
+    }
+    // t: R elements, kThreads / R threads each
+    {
+        const int shards = p.rowwise ? p.P : 1, ways = kThreads / p.R, r = tid % p.R, way = tid / p.R;
+        const float* from = p.t + (static_cast<long long>(p.rowwise ? shard : 0) * p.M + m) * p.R + r;
+        float v = 0.f;
+        if (way < ways)
+#pragma unroll 4
+            for (int s = way; s < p.splits; s += ways) v += from[static_cast<long long>(s) * shards * p.M * p.R];
+        part[tid] = v;
+        __syncthreads();
+        if (tid < p.R) {
+            for (int w = 1; w < ways; ++w) v += part[w * p.R + tid];
+            st[tid] = p.gains != nullptr ? v * __ldg(p.gains + a) : v;
+        }
+        __syncthreads();
+    }
+    float2 sum = unpack2(was);
+    auto add8 = [&](const uint4& u, const uint4& v, int r) {
+        const uint32_t *x = reinterpret_cast<const uint32_t*>(&u), *y = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t2 = *reinterpret_cast<const float2*>(st + r + 2 * j), f = unpack2(x[j]), h = unpack2(y[j]);
+            sum.x = fmaf(t2.x, f.x, fmaf(t2.y, f.y, sum.x));
+            sum.y = fmaf(t2.x, h.x, fmaf(t2.y, h.y, sum.y));
+        }
+    };
+    add8(b0[0], b1[0], 0);
+    if (eights > 1) add8(b0[1], b1[1], 8);
+#pragma unroll 4
+    for (int e = 2; e < eights; ++e) add8(__ldg(rows + e), __ldg(rows + eights + e), 8 * e);
+    if (in) *out = pack2(sum.x, sum.y);
 }
 
 // ---------------------------------------------------------------- fp32, CUDA cores
@@ -364,12 +426,13 @@ constexpr int kRowsF = 8;
 
 // A warp has 8 rows, one split and 8 elements of t: lanes along K, four elements
 // each, and sums over the lanes at the end.
-__global__ void __launch_bounds__(kThreads) lora_down_f32(const __grid_constant__ LoraParams p) {
+constexpr int kDownWarps = 2;  // of a block: few rows spread over the SMs
+__global__ void __launch_bounds__(32 * kDownWarps) lora_down_f32(const __grid_constant__ LoraParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     admit_next();
     await_previous();
     const int tiles = (p.M + kRowsF - 1) / kRowsF, parts = p.R / 8;
-    long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    long long unit = static_cast<long long>(blockIdx.x) * kDownWarps + warp;
     const int r0 = static_cast<int>(unit % parts) * 8;
     unit /= parts;
     const int m0 = static_cast<int>(unit % tiles) * kRowsF;
@@ -484,7 +547,7 @@ cudaError_t down(const LoraParams& p, cudaStream_t s) {
     return launch_after(lora_down_bf16<NT>, (p.M + 15) / 16 * p.splits * (p.rowwise ? p.P : 1), kThreads, 0, s, p);
 }
 
-template <int KT, int NC, bool MANY>
+template <int KT, int NC>
 cudaError_t up(const LoraParams& p, int num_sms, cudaStream_t s) {
     // Blocks of columns: fewer than fill the SMs twice (each reads t and the adapters'
     // numbers), one where the rows alone do.
@@ -492,18 +555,17 @@ cudaError_t up(const LoraParams& p, int num_sms, cudaStream_t s) {
     int col_blocks = 4 * num_sms / tiles;
     const int most = (chunks + kWarps - 1) / kWarps;
     col_blocks = col_blocks < 1 ? 1 : col_blocks > most ? most : col_blocks;
-    return launch_after(lora_up_bf16<KT, NC, MANY>, tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
+    return launch_after(lora_up_bf16<KT, NC>, tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_lora(LoraParams& p, bool bf16, int num_sms, cudaStream_t s) {
     cudaError_t e;
-    const bool many = p.M >= kLoraMany;
     if (!bf16) {
         const int row_tiles = (p.M + kRowsF - 1) / kRowsF;
         const long long units = static_cast<long long>(row_tiles) * (p.R / 8) * p.splits * (p.rowwise ? p.P : 1);
-        e = launch_after(lora_down_f32, static_cast<int>((units + kWarps - 1) / kWarps), kThreads, 0, s, p);
+        e = launch_after(lora_down_f32, static_cast<int>((units + kDownWarps - 1) / kDownWarps), 32 * kDownWarps, 0, s, p);
         if (e != cudaSuccess) return e;
         int col_blocks = (4 * num_sms + row_tiles - 1) / row_tiles;
         const int most_cols = (p.N + kThreads - 1) / kThreads;
@@ -512,10 +574,14 @@ cudaError_t launch_lora(LoraParams& p, bool bf16, int num_sms, cudaStream_t s) {
     }
     e = p.R <= 16 ? down<2>(p, s) : p.R <= 32 ? down<4>(p, s) : down<8>(p, s);
     if (e != cudaSuccess) return e;
-    if (p.R <= 16) return many ? up<1, 2, true>(p, num_sms, s) : up<1, 1, false>(p, num_sms, s);
-    if (p.R <= 32) return many ? up<2, 1, true>(p, num_sms, s) : up<2, 1, false>(p, num_sms, s);
-    if (p.R <= 64) return many ? up<4, 1, true>(p, num_sms, s) : up<4, 1, false>(p, num_sms, s);
-    return many ? up<8, 1, true>(p, num_sms, s) : up<8, 1, false>(p, num_sms, s);
+    if (p.M < kLoraFew) {
+        const int col_blocks = (p.n + 2 * kThreads - 1) / (2 * kThreads) * p.P;
+        return launch_after(lora_up_row_bf16, p.M * col_blocks + 1, kThreads, 0, s, p, col_blocks);
+    }
+    if (p.R <= 16) return up<1, 2>(p, num_sms, s);
+    if (p.R <= 32) return up<2, 1>(p, num_sms, s);
+    if (p.R <= 64) return up<4, 1>(p, num_sms, s);
+    return up<8, 1>(p, num_sms, s);
 }
 
 }  // namespace sptp

@@ -22,17 +22,16 @@ struct LoraParams {
 };
 
 constexpr int kLoraMaxRank = 128;
-// Rows from which on the second launch's warps take several chunks each, with
-// loads ahead, instead of one.
-constexpr int kLoraMany = 2048;
+// Rows below which the second launch has a block per row instead of one per 16.
+constexpr int kLoraFew = 160;
 
 // How the product with A is split along a row of f elements: pieces of *split_k,
 // as many as make two blocks an SM (bf16: of 16 rows; fp32: of 8 warps with 8 rows
-// and 8 elements each), but none below 256 elements.
+// and 8 elements each), but none below 128 elements.
 inline int lora_splits(int M, int f, int R, int shards, bool bf16, int* split_k) {
     const long long tiles = (static_cast<long long>(M) + (bf16 ? 15 : 7)) / (bf16 ? 16 : 8) * shards;
     const long long blocks = bf16 ? tiles : (tiles * (R / 8) + 7) / 8;
-    constexpr int kBlocks = 304, kLeast = 256;
+    constexpr int kBlocks = 304, kLeast = 128;
     long long splits = blocks >= kBlocks ? 1 : (kBlocks + blocks - 1) / blocks;
     const int most = f <= kLeast ? 1 : f / kLeast;
     if (splits > most) splits = most;

@@ -71,18 +71,9 @@ struct Shape {
     static constexpr int STAGES = 2, STAGE = TK * DP;
     static constexpr int CODES_AT = NQ * Q_BYTES + SLOTS * SLOT, SCALES_AT = CODES_AT + (CODES ? STAGES * STAGE : 0);
     static constexpr int BYTES = SCALES_AT + (CODES ? STAGES * TK * 4 : 0) + 1024;
-    // warps: softmax, four for the others, four that convert codes; registers of a
-    // thread of each, and of all at launch (their shares make up the launch's total)
+    // warps: softmax, four for the others, four that convert codes
     static constexpr int PRODUCER = 4 * NQ, ISSUER = 4 * NQ + 1, CONVERTER = 4 * NQ + 4;
     static constexpr int WARPS = CONVERTER + (CODES ? 4 : 0);
-    static constexpr bool SPLIT_REGS = false;
-    static constexpr int LAUNCH_REGS = WARPS == 16 ? 128 : 168;
-    static constexpr int SOFTMAX_REGS = WARPS == 16 ? 176 : 208;
-    static constexpr int OTHER_REGS = WARPS == 16 ? 72 : 88;
-    static constexpr int CONVERTER_REGS = 88;
-    static_assert(!SPLIT_REGS || 4 * NQ * SOFTMAX_REGS + 4 * OTHER_REGS + (WARPS - CONVERTER) * CONVERTER_REGS <=
-                                     WARPS * LAUNCH_REGS,
-                  "setmaxnreg waits for registers that nobody gives back");
     // tensor memory columns
     static constexpr int S = 128;                       // between the tiles' scores
     static constexpr int O = 256;                       // first of the outputs; DP between the tiles'
@@ -210,22 +201,13 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t c, bool upper, __nv_b
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int REGS>
-__device__ __forceinline__ void take_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void leave_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-
 template <class C>
 struct Bars {
     uint64_t c_full[C::STAGES], c_empty[C::STAGES];  // E4M3: tiles of codes
     uint64_t full[C::SLOTS], empty[C::SLOTS];  // K and V tiles
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];                        // scores in tensor memory (and all products before them done)
-    uint64_t p_ready[2];                       // weights there, outputs rescaled
+    uint64_t p_ready[2];                       // weights there, outputs rescaled (a warp each)
     uint64_t o_full[2];                        // outputs of an item done
     uint64_t w_full[kItems], w_empty[kItems];  // descriptions
     uint64_t drain;
@@ -458,7 +440,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             mbar_init(&bars.q_full[t], 1);
             mbar_init(&bars.q_empty[t], 1);
             mbar_init(&bars.s_full[t], 1);
-            mbar_init(&bars.p_ready[t], kTileRows);
+            mbar_init(&bars.p_ready[t], 4);
             mbar_init(&bars.o_full[t], 1);
         }
         mbar_init(&bars.drain, 1);
@@ -498,9 +480,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     WaitCtx wc{&bars.status, &bars.abort_flag, p.wait_limit_ns};
     PromptPart* part = p.parts + blockIdx.x;
 
-    // (setmaxnreg: one instruction for all four warps of a group)
     if (warp < C::PRODUCER) {
-        if constexpr (C::SPLIT_REGS) take_registers<C::SOFTMAX_REGS>();
         // -------------------------------------------------- softmax, a thread a row
         const int t = warp / 4, r = tid % kTileRows;
         const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -518,7 +498,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             const int heads = d.heads, tile_tokens = kTileRows / p.heads;
             const int local = r / heads, head = r - local * heads, token = t * tile_tokens + local;
             const bool in = local < tile_tokens && token < d.n;
-            const bool any = t * tile_tokens < d.n;
+            const bool some = __any_sync(0xffffffffu, in);  // (a warp without any row leaves what is there)
             sm.m = -INFINITY;
             sm.l = 0.f;
             sm.pos = d.pos0 + token;
@@ -533,9 +513,10 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 if (!(ok = warp_sleep(&bars.s_full[t], s_phase, wc, kWherePromptScores, j))) break;
                 s_phase ^= 1;
                 tc_fence_after();
-                sm.tile(p, cap, s_at, o_at, o_cols, key0 + j * TK, j == b - 1);
+                if (some) sm.tile(p, cap, s_at, o_at, o_cols, key0 + j * TK, j == b - 1);
                 tc_fence_before();
-                mbar_arrive(&bars.p_ready[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_ready[t]);
             }
             if (!ok) break;
             if (a < b) {
@@ -543,7 +524,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            if (any) {
+            if (some) {
                 const bool whole = (d.flags & (kBegins | kEnds)) == (kBegins | kEnds);
                 const long long orow = (d.token0 + token) * p.Hq + d.head0 + head;
                 // slot 1 if the item begins in this share, slot 0 if in an earlier one
@@ -585,7 +566,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                     }
                 }
                 // the outputs are read before the next item's products (issued behind
-                // this thread's next arrival) write there
+                // this warp's next arrival) write there
                 tc_fence_before();
             }
             __syncwarp();
@@ -596,10 +577,14 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             }
         }
     } else if (C::CODES && warp >= C::CONVERTER) {
-        if constexpr (C::SPLIT_REGS) leave_registers<C::CONVERTER_REGS>();
         // -------------------------------------------------- E4M3 tiles to bf16
-        const int me = tid - 32 * C::CONVERTER;
-        constexpr int CHUNKS = C::DP / 16;  // of 16 codes, of a row
+        // A thread has a row (or half of one), 16 codes at a time: eight lanes' reads and
+        // writes are in different banks, swizzled as they are.  Elements behind the
+        // row's end are not read by any product.
+        constexpr int PARTS = 128 / TK, PER = C::SPAN / 16;
+        const int row = (tid - 32 * C::CONVERTER) % TK, first = (tid - 32 * C::CONVERTER) / TK;
+        const int swizzle = C::SPAN == 128 ? row & 7 : (row >> 1) & 3;
+        const int chunks = (p.D + 15) / 16;
         int stage = 0, slot = 0, w = 0;
         uint32_t c_phase = 0, phase = 1, w_phase = 0;
         bool ok = true;
@@ -614,28 +599,24 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 const int from = i & 1 ? d.lo - key0 : 0, to = i & 1 ? d.hi - key0 : TK;
                 if (!(ok = warp_sleep(&bars.c_full[stage], c_phase, wc, kWhereKvFull, i))) break;
                 if (!(ok = warp_sleep(&bars.empty[slot], phase, wc, kWhereKvEmpty, i))) break;
-                const uint8_t* in = codes + stage * C::STAGE;
-                uint8_t* out = slots + slot * C::SLOT;
+                const uint8_t* in = codes + stage * C::STAGE + row * C::SPAN;
+                uint8_t* out = slots + slot * C::SLOT + row * 128;
+                const float f = scales[stage * TK + row];
+                const __nv_bfloat162 f2 = __floats2bfloat162_rn(f, f);
+                const bool seen = row >= from && row < to;
 #pragma unroll 4
-                for (int n = me; n < TK * CHUNKS; n += 128) {
-                    const int row = n / CHUNKS, c = n % CHUNKS;
-                    constexpr int PER = C::SPAN / 16;
-                    const int swizzle = C::SPAN == 128 ? row & 7 : (row >> 1) & 3;
-                    const uint4 u = *reinterpret_cast<const uint4*>(in + c / PER * (TK * C::SPAN) + row * C::SPAN +
-                                                                    (((c % PER) ^ swizzle) << 4));
-                    const float f = scales[stage * TK + row];
-                    const __nv_bfloat162 f2 = __floats2bfloat162_rn(f, f);
-                    uint4 lo = make_uint4(codes_to_bf16(u.x, false, f2), codes_to_bf16(u.x, true, f2),
-                                          codes_to_bf16(u.y, false, f2), codes_to_bf16(u.y, true, f2));
-                    uint4 hi = make_uint4(codes_to_bf16(u.z, false, f2), codes_to_bf16(u.z, true, f2),
-                                          codes_to_bf16(u.w, false, f2), codes_to_bf16(u.w, true, f2));
-                    if (row < from || row >= to) lo = hi = make_uint4(0, 0, 0, 0);
-                    uint8_t* at = out + c / 4 * (TK * 128) + row * 128;
-                    const int p0 = ((c % 4 * 2) ^ (row & 7)) << 4, p1 = ((c % 4 * 2 + 1) ^ (row & 7)) << 4;
-                    // (lanes of every other column the other way round, for the banks' sake)
-                    const bool swap = (c & 4) != 0;
-                    *reinterpret_cast<uint4*>(at + (swap ? p1 : p0)) = swap ? hi : lo;
-                    *reinterpret_cast<uint4*>(at + (swap ? p0 : p1)) = swap ? lo : hi;
+                for (int c = first; c < chunks; c += PARTS) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(in + c / PER * (TK * C::SPAN) + (((c % PER) ^ swizzle) << 4));
+                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                    if (seen) {
+                        lo = make_uint4(codes_to_bf16(u.x, false, f2), codes_to_bf16(u.x, true, f2),
+                                        codes_to_bf16(u.y, false, f2), codes_to_bf16(u.y, true, f2));
+                        hi = make_uint4(codes_to_bf16(u.z, false, f2), codes_to_bf16(u.z, true, f2),
+                                        codes_to_bf16(u.w, false, f2), codes_to_bf16(u.w, true, f2));
+                    }
+                    uint8_t* at = out + c / 4 * (TK * 128);
+                    *reinterpret_cast<uint4*>(at + (((c % 4 * 2) ^ (row & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(at + (((c % 4 * 2 + 1) ^ (row & 7)) << 4)) = hi;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -661,7 +642,6 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             }
         }
     } else {
-        if constexpr (C::SPLIT_REGS) leave_registers<C::OTHER_REGS>();
         if (warp == C::PRODUCER) {
             // -------------------------------------------------- producer
             const int R = p.box_rows, nb = TK / R;
@@ -948,11 +928,6 @@ cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        // the groups' shares of registers must not exceed what the kernel was compiled for
-        cudaFuncAttributes attr;
-        e = cudaFuncGetAttributes(&attr, prompt_tc_kernel<C, CAP, BIAS, TEST>);
-        if (e != cudaSuccess) return e;
-        if (C::SPLIT_REGS && attr.numRegs < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(prompt_tc_kernel<C, CAP, BIAS, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);

@@ -23,10 +23,7 @@ namespace sptp {
 namespace prompt {
 
 constexpr int kTileCost = 4;
-#ifndef ICOST
-#define ICOST 12
-#endif
-constexpr int kItemCost = ICOST;
+constexpr int kItemCost = 12;
 
 struct Block {
     int b;        // sequence

@@ -624,9 +624,10 @@ size_t sptp_lora_workspace_size(int P, int M, int K, int N, int R, int rowwise);
  *   out may be exactly base, and must not overlap any input otherwise.
  * 8 <= R <= 128, R % 8 == 0; K, N <= 2^20, multiples of 8, the split one of 8 P;
  * adapters >= 0.  An id >= adapters is recorded as SPTP_ERR_SHAPE in the
- * workspace status words, and its row treated as one without adapter.  A row
- * does not depend on other rows or other rows' adapters; equal inputs give equal
- * bits.  M == 0 enqueues nothing.  workspace: at least
+ * workspace status words, and its row treated as one without adapter.  What other
+ * rows and their adapters hold does not reach a row (how many adapters its
+ * neighbours name may change the order of its sums); equal calls give equal bits.
+ * M == 0 enqueues nothing.  workspace: at least
  * sptp_lora_workspace_size(...), 256-byte aligned.
  * Numerics: A_a x summed in fp32, and kept to 2^-16 of itself for its product
  * with B_a (bf16; in fp32 not rounded), sums in fp32, out rounded once.
@@ -671,6 +672,16 @@ int sptp_wait_selftest(void* workspace, size_t ws_bytes, unsigned long long limi
  */
 int sptp_paged_attn_wait_selftest(const sptp_paged_attn_decode_args* args, int withhold_full, int withhold_empty,
                                   unsigned long long limit_ns);
+
+/*
+ * sptp_paged_attn_prompt_wait_selftest -- sptp_paged_attn_prompt (bf16 activations,
+ * 64 < D <= 128, no cap, no slopes, scale > 0) on two CTAs, the first of which never
+ * loads tile withhold_full of its share (K and V tiles in turn), so that bounded
+ * waits of limit_ns run out in it: SPTP_ERR_TIMEOUT is recorded if it has such a
+ * tile, and out and lse are then undefined.  No counterpart on the pages.
+ */
+int sptp_paged_attn_prompt_wait_selftest(const sptp_paged_attn_prompt_args* args, int withhold_full,
+                                         unsigned long long limit_ns);
 
 /* Bytes of the static device scratch array used by sptp_ffn_forward_noalloc. */
 #define SPTP_NOALLOC_SCRATCH_BYTES (64u << 20)

@@ -118,3 +118,72 @@ def paged_attn_decode(q, k, v, page_table, seq_lens, scale, window=0):
                 lse[p, b, h] = top + math.log(total)
                 dots[p, b, h] = (np.abs(K) @ np.abs(q[p, b, h])).max() * abs(scale)
     return out, lse, mean, dots
+
+
+def modified_scores(z, cap, slope, distance):
+    """cap tanh(z / cap) (cap 0: z) - slope |distance|."""
+    if cap:
+        z = cap * np.tanh(z / cap)
+    return z - slope * np.abs(distance)
+
+
+def paged_attn_prompt(q, k, v, page_table, seq_lens, row_starts, scale, window=0, cap=0.0, slopes=None, prefix_lens=None):
+    """q [P, M, Hq, D]; k, v [P, pages, Hkv, page, D] in float64; a row sees keys of
+    its own sequence only.  Returns out [P, M, Hq, D], lse [P, M, Hq] (NaN in the rows
+    of no sequence), the weighted mean of |v|, and an error bound's three sizes per
+    row and head: the largest sum of |scale q_i k_ji|, the largest |bias|, and the
+    keys seen."""
+    P, M, Hq, D = q.shape
+    Hkv, page = k.shape[2], k.shape[3]
+    out, mean = np.full(q.shape, np.nan), np.zeros(q.shape)
+    lse = np.full((P, M, Hq), np.nan)
+    dots, far, keys = np.zeros((P, M, Hq)), np.zeros((P, M, Hq)), np.zeros((P, M, Hq))
+    for b in range(len(seq_lens)):
+        n, length = int(row_starts[b + 1] - row_starts[b]), int(seq_lens[b])
+        prefix = 0 if prefix_lens is None else min(max(int(prefix_lens[b]), 0), length)
+        for r in range(n):
+            m, pos = int(row_starts[b]) + r, length - n + r
+            out[:, m], lse[:, m] = 0.0, -np.inf
+            if pos < 0:
+                continue
+            lo = max(0, pos + 1 - window) if window else 0
+            at = np.arange(lo, max(pos + 1, prefix))
+            pages, off = page_table[b][at // page], at % page
+            for p in range(P):
+                for h in range(Hq):
+                    K, V = k[p, pages, h * Hkv // Hq, off], v[p, pages, h * Hkv // Hq, off]
+                    slope = 0.0 if slopes is None else float(slopes[p, h])
+                    z = modified_scores((K @ q[p, m, h]) * scale, cap, slope, pos - at)
+                    top = z.max()
+                    w = np.exp(z - top)
+                    out[p, m, h], mean[p, m, h] = w @ V / w.sum(), w @ np.abs(V) / w.sum()
+                    lse[p, m, h] = top + math.log(w.sum())
+                    dots[p, m, h] = (np.abs(K) @ np.abs(q[p, m, h])).max() * abs(scale)
+                    far[p, m, h] = abs(slope) * np.abs(pos - at).max()
+                    keys[p, m, h] = at.size
+    return out, lse, mean, (dots, far, keys)
+
+
+def lora(x, A, B, ids, base, gains=None):
+    """base[p][m] + gains[a] B_a (A_a x_m), a = ids[m] (< 0: none), in float64.  x [M, K]
+    with base [P, M, N / P], or x [P, M, K / P] with base [P, M, N].  Returns the sum
+    and its terms' absolute sum."""
+    P, M, n = base.shape
+    out, size = np.array(base, dtype=np.float64), np.abs(np.array(base, dtype=np.float64))
+    for m in range(M):
+        a = int(ids[m])
+        if a < 0:
+            continue
+        gain = 1.0 if gains is None else float(gains[a])
+        for p in range(P):
+            if x.ndim == 2:
+                t, tt = A[a] @ x[m], np.abs(A[a]) @ np.abs(x[m])
+                up = B[a][p * n:(p + 1) * n]
+            else:
+                f = x.shape[2]
+                Ap = A[a][:, p * f:(p + 1) * f]
+                t, tt = Ap @ x[p, m], np.abs(Ap) @ np.abs(x[p, m])
+                up = B[a]
+            out[p, m] += gain * (up @ t)
+            size[p, m] += abs(gain) * (np.abs(up) @ tt)
+    return out, size

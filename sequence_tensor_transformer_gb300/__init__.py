@@ -32,6 +32,7 @@ __all__ = [
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
     "sptp_paged_attn_decode", "paged_kv_cache", "ROPE_SCALINGS", "sptp_paged_attn_wait_selftest",
     "sptp_paged_attn_prompt_workspace_size", "sptp_paged_attn_prompt", "sptp_lora_workspace_size", "sptp_lora",
+    "sptp_paged_attn_prompt_wait_selftest",
 ]
 
 SPTP_BF16 = 0
@@ -63,6 +64,7 @@ EXPORTED_SYMBOLS = (
     "sptp_paged_attn_decode", "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed",
     "sptp_paged_attn_wait_selftest", "sptp_paged_attn_prompt_workspace_size", "sptp_paged_attn_prompt",
     "sptp_paged_attn_decode_ex", "sptp_lora_workspace_size", "sptp_lora",
+    "sptp_paged_attn_prompt_wait_selftest",
 )
 
 _lib = None
@@ -109,6 +111,7 @@ _SIGS = {
     "sptp_lora": (_I, [_P] * 5 + [_I] * 8 + [_P] * 3 + [_Z, _P]),
     "sptp_paged_attn_prompt_workspace_size": (_Z, [_I] * 6),
     "sptp_paged_attn_prompt": (_I, [ctypes.c_char_p]),
+    "sptp_paged_attn_prompt_wait_selftest": (_I, [ctypes.c_char_p, _I, _U64]),
     "sptp_paged_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "sptp_paged_attn_decode": (_I, [_P] * 7 + [_I] * 9 + [_F, _I, _I, _P, _P, _P, _Z, _P]),
 }
@@ -818,6 +821,27 @@ def sptp_paged_attn_prompt(q, cache, page_table, seq_lens, row_starts, scale=Non
     none) - slopes[head] |pos - key| (slopes fp32 [P,Hq]); scale defaults to
     D^-1/2.  Rows of no sequence are left as they are (undefined in an output
     that is left out).  Returns (out [P,M,Hq*D], lse fp32 [P,M,Hq] or None)."""
+    args, out, lse, workspace = _prompt_call(q, cache, page_table, seq_lens, row_starts, scale, window, cap, slopes, prefix_lens,
+                                             out, lse, workspace, stream, write_lse)
+    _check("sptp_paged_attn_prompt", lib().sptp_paged_attn_prompt(args))
+    return out, lse
+
+
+def sptp_paged_attn_prompt_wait_selftest(q, cache, page_table, seq_lens, row_starts, out, workspace, withhold_full,
+                                         limit_ns=20_000_000):
+    """sptp_paged_attn_prompt on two CTAs, the first of which never loads a tile of its
+    share, so that its bounded waits run out (SPTP_ERR_TIMEOUT in the workspace's
+    status words)."""
+    args = _prompt_call(q, cache, page_table, seq_lens, row_starts, None, 0, 0.0, None, None, out, None, workspace, None,
+                        False)[0]
+    _check("sptp_paged_attn_prompt_wait_selftest",
+           lib().sptp_paged_attn_prompt_wait_selftest(args, int(withhold_full), int(limit_ns)))
+
+
+def _prompt_call(q, cache, page_table, seq_lens, row_starts, scale, window, cap, slopes, prefix_lens, out, lse, workspace,
+                 stream, write_lse):
+    """The checked arguments of a call as one block, its out and its lse, and the
+    workspace (to be kept until the call is made)."""
     P, M, Hq, D = q.shape
     k, v, ks, vs = cache
     dtype, i32 = q.dtype, torch.int32
@@ -842,14 +866,13 @@ def sptp_paged_attn_prompt(q, cache, page_table, seq_lens, row_starts, scale=Non
     if workspace is None:
         n = max(sptp_paged_attn_prompt_workspace_size(P, M, B, Hq, Hkv, D), SPTP_WS_HEADER_BYTES)
         workspace = _new((n,), torch.uint8, q.device, stream)
-    code = lib().sptp_paged_attn_prompt(_PROMPT_ARGS.pack(
+    args = _PROMPT_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
         page_table.data_ptr(), seq_lens.data_ptr(), row_starts.data_ptr(), 0 if prefix_lens is None else prefix_lens.data_ptr(),
         0 if slopes is None else slopes.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         workspace.data_ptr(), _raw_stream(stream, cur), workspace.nbytes, P, M, B, Hq, Hkv, D, max_pages, num_pages,
-        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale, cap))
-    _check("sptp_paged_attn_prompt", code)
-    return out, lse
+        page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale, cap)
+    return args, out, lse, workspace
 
 
 def sptp_paged_attn_wait_selftest(q, cache, page_table, seq_lens, out, workspace, withhold_full=-1, withhold_empty=-1,

@@ -32,7 +32,7 @@ inline int lora_splits(int M, int f, int R, int shards, bool bf16, int* split_k)
     const long long tiles = (static_cast<long long>(M) + (bf16 ? 15 : 7)) / (bf16 ? 16 : 8) * shards;
     const long long blocks = bf16 ? tiles : (tiles * (R / 8) + 7) / 8;
     constexpr int kBlocks = 304, kLeast = 128;
-    long long splits = blocks >= kBlocks ? 1 : (kBlocks + blocks - 1) / blocks;
+    long long splits = blocks < 1 || blocks >= kBlocks ? 1 : (kBlocks + blocks - 1) / blocks;
     const int most = f <= kLeast ? 1 : f / kLeast;
     if (splits > most) splits = most;
     *split_k = ((f + static_cast<int>(splits) - 1) / static_cast<int>(splits) + 31) / 32 * 32;

@@ -33,6 +33,8 @@ PromptLayout prompt_layout(int M, int group, int D, bool bf16) {
     return L;
 }
 
+int attend_rows(const sptp_paged_attn_prompt_args* args, unsigned long long limit_ns, int withhold_full);
+
 }  // namespace
 
 extern "C" {
@@ -42,7 +44,24 @@ size_t sptp_paged_attn_prompt_workspace_size(int P, int M, int B, int Hq, int Hk
     return prompt_layout(M, Hq / Hkv, D, true).total;
 }
 
-int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args) {
+int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args) { return attend_rows(args, kWaitLimitNs, -1); }
+
+int sptp_paged_attn_prompt_wait_selftest(const sptp_paged_attn_prompt_args* args, int withhold_full,
+                                         unsigned long long limit_ns) {
+    if (!args) return SPTP_ERR_NULL;
+    if (limit_ns == 0 || limit_ns > 10000000000ull || withhold_full < 0) return SPTP_ERR_SHAPE;
+    if (args->dtype != SPTP_BF16) return SPTP_ERR_DTYPE;
+    if (args->D <= 64 || args->D > 128 || args->cap != 0.f || args->slopes != nullptr || !(args->scale > 0.f))
+        return SPTP_ERR_SHAPE;
+    return attend_rows(args, limit_ns, withhold_full);
+}
+
+}  // extern "C"
+
+namespace {
+
+// sptp_paged_attn_prompt, and its self-test.
+int attend_rows(const sptp_paged_attn_prompt_args* args, unsigned long long limit_ns, int withhold_full) {
     if (!args) return SPTP_ERR_NULL;
     const sptp_paged_attn_prompt_args& a = *args;
     const bool e4m3 = a.kv_type == SPTP_KV_E4M3;
@@ -100,8 +119,8 @@ int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args) {
     p.cap = a.cap;
     p.out = a.out;
     p.lse = static_cast<float*>(a.lse);
-    p.wait_limit_ns = kWaitLimitNs;
-    p.withhold_full = -1;
+    p.wait_limit_ns = limit_ns;
+    p.withhold_full = withhold_full;
     p.status = ws_status(a.workspace);
     const PromptLayout lay = prompt_layout(a.M, a.Hq / a.Hkv, a.D, dtype == SPTP_BF16);
     p.part_rows = lay.rows;
@@ -111,4 +130,4 @@ int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args) {
     return cuda_status(launch_prompt_attn(p, dtype == SPTP_BF16, e4m3, di.sms, static_cast<cudaStream_t>(a.cuda_stream)));
 }
 
-}  // extern "C"
+}  // namespace

@@ -177,7 +177,8 @@ cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sm
         {{launch_prompt_bf16, launch_prompt_bf16_bias}, {launch_prompt_bf16_cap, launch_prompt_bf16_cap_bias}},
         {{launch_prompt_e4m3, launch_prompt_e4m3_bias}, {launch_prompt_e4m3_cap, launch_prompt_e4m3_cap_bias}}};
     const bool cap = p.cap != 0.f, bias = p.slopes != nullptr || (!cap && !(p.scale > 0.f));
-    cudaError_t e = (bf16 ? kernels[e4m3][cap][bias] : launch_prompt_f32)(p, num_sms, &ctas, s);
+    cudaError_t e = p.withhold_full >= 0 ? launch_prompt_test(p, e4m3, &ctas, s)
+                                         : (bf16 ? kernels[e4m3][cap][bias] : launch_prompt_f32)(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
     const int grid = ctas * kJoinBlocks + 1;
     return bf16 ? launch_after(prompt_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, s, p, ctas)

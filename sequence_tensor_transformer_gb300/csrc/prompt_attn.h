@@ -65,6 +65,8 @@ using PromptLaunch = cudaError_t(PromptParams& p, int num_sms, int* ctas, cudaSt
 PromptLaunch launch_prompt_bf16, launch_prompt_bf16_cap, launch_prompt_bf16_bias, launch_prompt_bf16_cap_bias;
 PromptLaunch launch_prompt_e4m3, launch_prompt_e4m3_cap, launch_prompt_e4m3_bias, launch_prompt_e4m3_cap_bias;
 PromptLaunch launch_prompt_f32;
+// The self-test's form of it, on two CTAs; 64 < D <= 128, plain scores.
+cudaError_t launch_prompt_test(PromptParams& p, bool e4m3, int* ctas, cudaStream_t s);
 cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sms, cudaStream_t s);
 // The split of the heads and rows into items of at most `rows` rows whose tiles
 // hold `tile_rows`, and the division by the page size.

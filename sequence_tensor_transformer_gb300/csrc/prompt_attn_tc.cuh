@@ -775,6 +775,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             }
             if (bars.abort_flag) {
                 // left early: wait (bounded) for the copies still in flight
+                if (C::CODES) asm volatile("cp.async.wait_all;" ::: "memory");
                 int local_abort = 0;
                 WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
                 constexpr int kSlots = C::CODES ? C::STAGES : C::SLOTS;

@@ -360,7 +360,10 @@ def sptp_gateup_swiglu(y, W1g, W1u, P, s_out=None, workspace=None, stream=None):
     return s_out
 
 
-def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None):
+def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None, adapters=None, adapter_workspace=None):
+    """Row-parallel projection of every shard: out [P,M,d] from s [P,M,F/P].  adapters:
+    (A, B, ids, gains) as in sptp_lora, added to out in place (adapter_workspace: that
+    call's)."""
     _, M, f = s.shape
     d, F = W2.shape
     _expect("s", s, (P, M, F // P), s.dtype)
@@ -374,6 +377,9 @@ def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None):
     code = lib().sptp_down_proj(_ptr(s), _ptr(W2), M, d, F, P, _dtype_code(s), _ptr(out), _ptr(workspace),
                                 _nbytes(workspace), _stream(stream))
     _check("sptp_down_proj", code)
+    if adapters is not None and M != 0:
+        A, B, ids, gains = adapters
+        sptp_lora(s, A, B, ids, out, gains, out=out, workspace=adapter_workspace, stream=stream)
     return out
 
 
@@ -406,9 +412,12 @@ def sptp_attn_qkv_workspace_size(M, d, N, P, chunks, dtype=SPTP_BF16) -> int:
 
 
 def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None, resid_out=None,
-                          workspace=None, stream=None, write_resid=True, variant="auto"):
+                          workspace=None, stream=None, write_resid=True, variant="auto", adapters=None,
+                          adapter_workspace=None):
     """Boundary in front of attention: returns (qkv [P,M,N/P], resid_out).
-    variant: "auto" (the library's default), "pair" or "fused"."""
+    variant: "auto" (the library's default), "pair" or "fused".  adapters: (A, B,
+    ids, gains) as in sptp_lora, added to qkv in place (sptp_lora on the normed rows
+    in the workspace; adapter_workspace: that call's)."""
     M, d = x.shape
     N = Wqkv.shape[0]
     dt = _dtype_code(x)
@@ -428,6 +437,10 @@ def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None
                                           float(eps), dt, _ptr(qkv_out), _ptr(resid_out), _ptr(workspace),
                                           _nbytes(workspace), _stream(stream), _variant(variant))
     _check("sptp_attn_qkv_forward", code)
+    if adapters is not None and M != 0:
+        A, B, ids, gains = adapters
+        y = workspace[SPTP_WS_HEADER_BYTES:SPTP_WS_HEADER_BYTES + x.nbytes].view(x.dtype).view(M, d)
+        sptp_lora(y, A, B, ids, qkv_out, gains, out=qkv_out, workspace=adapter_workspace, stream=stream)
     return qkv_out, resid_out
 
 

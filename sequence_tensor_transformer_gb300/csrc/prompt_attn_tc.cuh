@@ -232,6 +232,7 @@ struct Softmax {
     float m, l;  // the maximum in use, in units of log 2; the sum
     float to_log2, slope;
     int lo, hi, pos;  // keys that this row sees; its position
+    bool in;          // a token has it
 
     static constexpr int N = 32;      // scores at a time
     static constexpr int P = TK / 2;  // column of the weights, in the place of scores that are read before
@@ -273,8 +274,8 @@ struct Softmax {
 #pragma unroll
         for (int i = 0; i < 4; ++i) most[i] = fmaxf(most[i], fabsf(s[28 + i]));
         const float all = max3(most[0], most[1], fmaxf(most[2], most[3]));
-        // (a NaN among keys that no row sees does not count)
-        const bool far = __any_sync(0xffffffffu, all * fabsf(to_u) > 0.5f);
+        // (of rows that a token has: what the others hold must not choose the arithmetic)
+        const bool far = __any_sync(0xffffffffu, in && all * fabsf(to_u) > 0.5f);
         if (!far) {
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
@@ -360,7 +361,14 @@ struct Softmax {
             // scores in units of log 2 are unit s + bias
             float unit = to_log2, bias = 0.f;
             const int key = key0 + c * N;
+            // bit j: key j of the 32 is seen
+            const int from = max(lo - key, 0), to = min(max(hi - key, 0), N);
+            const uint32_t seen = from >= to ? 0u : (0xffffffffu >> (32 - (to - from))) << from;
             if constexpr (CAP) {
+                if (masked) {  // (nor must what lies where no key is)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) s[j] = seen >> j & 1u ? s[j] : 0.f;
+                }
                 apply_cap(p, cap, s, s_at + c * N);
                 unit = 1.f;
             }
@@ -378,9 +386,6 @@ struct Softmax {
                 unit = 1.f;
             }
             if (masked) {
-                // bit j: key j of the 32 is seen
-                const int from = max(lo - key, 0), to = min(max(hi - key, 0), N);
-                const uint32_t seen = from >= to ? 0u : (0xffffffffu >> (32 - (to - from))) << from;
 #pragma unroll
                 for (int j = 0; j < N; ++j) s[j] = seen >> j & 1u ? s[j] : -INFINITY;
             }
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             const int local = r / heads, head = r - local * heads, token = t * tile_tokens + local;
             const bool in = local < tile_tokens && token < d.n;
             const bool some = __any_sync(0xffffffffu, in);  // (a warp without any row leaves what is there)
+            sm.in = in;
             sm.m = -INFINITY;
             sm.l = 0.f;
             sm.pos = d.pos0 + token;

@@ -18,10 +18,10 @@ def ints(a):
 
 
 def make(P, rows, lens, Hq, Hkv, D, page, kind, seed=0, q_std=1.0, window=0, prefix=None, cap=0.0, slopes=None, first=0, pad=0,
-         spread=0.0, scale=None):
+         spread=0.0, scale=None, holes=True):
     """Sequences of rows[b] new rows and lens[b] keys, `first` rows of none before them and
     `pad` behind.  Cache slots that no row of a sequence sees hold NaN, or NaN codes
-    and scales."""
+    and scales (holes=False: values, for calls with other rows and lengths)."""
     rng = np.random.default_rng(seed + D + Hq)
     dtype = "fp32" if kind == "fp32" else "bf16"
     rows, lens = np.asarray(rows), np.asarray(lens)
@@ -40,7 +40,7 @@ def make(P, rows, lens, Hq, Hkv, D, page, kind, seed=0, q_std=1.0, window=0, pre
         pos = max(0, lens[b] - rows[b])
         at = np.arange(max(0, pos + 1 - window) if window else 0, lens[b])
         used[table[b][at // page], at % page] = True
-    hole = ~used[None, :, None, :] & np.ones((P, 1, Hkv, 1), bool)
+    hole = ~used[None, :, None, :] & np.full((P, 1, Hkv, 1), holes)
     c = dict(P=P, M=M, B=B, Hq=Hq, Hkv=Hkv, D=D, page=page, rows=rows, lens=lens, starts=starts, table=table, kind=kind,
              dtype=dtype, window=window, cap=cap, prefix=prefix, scale=D ** -0.5 if scale is None else scale,
              slopes=None if slopes is None else np.asarray(slopes, np.float32).reshape(P, Hq), q64=to_f64(q, dtype),

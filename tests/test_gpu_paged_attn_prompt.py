@@ -192,6 +192,19 @@ def test_equal_inputs_give_equal_bits_and_outputs_are_optional(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cap,slopes", [(10.0, None), (0.0, "usual"), (10.0, "usual")])
+def test_what_lies_outside_does_not_change_a_bit(kind, cap, slopes):
+    """Shared memory that other calls have left, in place of keys that no row sees."""
+    c = make(1, (60, 5), (400, 90), 4, 2, 64, 16, kind, cap=cap, slopes=None if slopes is None else SLOPES[slopes](4))
+    loud = make(1, (200, 70), (1500, 900), 4, 2, 64, 16, kind, q_std=1e4, spread=3.0)
+    out, lse, _ = call(c)
+    for _ in range(3):
+        call(loud)
+        again, lse2, _ = call(c)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_without_rows_nothing_is_written(kind):
     c = make(1, (0, 0), (5, 9), 2, 1, 64, 16, kind, pad=3)
     run(c)

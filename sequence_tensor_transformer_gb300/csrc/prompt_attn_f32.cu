@@ -4,7 +4,8 @@
 // for 64 query rows and 64 keys at a time, one pass over the keys with a running
 // maximum and sum per row.  A thread holds 4 rows x 4 keys of the scores and 4
 // rows x DP / 16 elements of the outputs; queries, keys, values and weights lie
-// in shared memory.
+// in shared memory, the next tile's keys and values on their way there while this
+// one's are used (rows of more than 128 elements: no room for two tiles).
 #include <atomic>
 
 #include "attn_scores.cuh"
@@ -16,36 +17,39 @@ namespace prompt {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kItemCost = kTileCost;
 
 template <int DP>
 struct F32Smem {
     static constexpr int QS = DP + 4, KS = DP + 4, VS = DP, WS = kKeys + 4;  // row strides, floats
-    static constexpr int Q = 0, K = Q + kRows * QS, V = K + kKeys * KS, W = V + kKeys * VS;
-    static constexpr int BYTES = (W + kRows * WS) * 4;
+    static constexpr int BUFFERS = DP <= 128 ? 2 : 1, BUFFER = kKeys * (KS + VS);
+    static constexpr int Q = 0, W = Q + kRows * QS, K = W + kRows * WS;
+    static constexpr int BYTES = (K + BUFFERS * BUFFER) * 4;
+    static constexpr int CTAS = BYTES <= 113 * 1024 ? 2 : 1;
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_f32_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel(const __grid_constant__ PromptParams p) {
     using L = F32Smem<DP>;
     constexpr int NV = DP / 64;  // float4 of a row's outputs per thread
     extern __shared__ __align__(16) float smem[];
-    float *sq = smem + L::Q, *sk = smem + L::K, *sv = smem + L::V, *sw = smem + L::W;
+    float *sq = smem + L::Q, *sw = smem + L::W;
     __shared__ long long warp_cost[kThreads / 32];
-    __shared__ Cursor<kKeys> share_at;
+    __shared__ Cursor<kKeys, kItemCost> share_at;
     __shared__ int bad_at, bad_any;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     admit_next();
     if (tid == 0) bad_at = bad_any = 0;
     await_previous();
     bool bad = false;
-    const Share share = find_share<kKeys, kThreads>(p, warp_cost, &share_at, &bad);
+    const Share share = find_share<kThreads>(p, warp_cost, &share_at, &bad);
     if (bad) bad_any = 1;
     PromptPart* part = p.parts + blockIdx.x;
     if (tid == 0) part->items[0].parts = part->items[1].parts = 0;
     const long long numbers = block_numbers(p);
     const ScoreCap cap(p.cap);
     const float to_log2 = p.scale * kLog2e;
-    Cursor<kKeys> c = share_at;
+    Cursor<kKeys, kItemCost> c = share_at;
     bool more = c.k.tiles != 0;
     while (more && c.tile_at() < share.end) {
         const Piece r = piece_of(p, c, share);
@@ -76,25 +80,41 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_f32_kernel
 #pragma unroll
             for (int n = 0; n < NV; ++n) o[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        // keys and values of tile t, zeros where no row sees one
+        auto load = [&](int t) {
+            const int key0 = c.key0() + t * kKeys;
+            const int from = max(0, c.k.lo - key0), to = min(kKeys, c.k.hi - key0);
+            float *sk = smem + L::K + t % L::BUFFERS * L::BUFFER, *sv = sk + kKeys * L::KS;
+            constexpr int PER = kThreads / kKeys;  // threads of a key
+            const int key = tid / PER;
+            long long row = -1;
+            if (key >= from && key < to) {
+                row = pool_row(p, c.k.b, r.shard, r.kvh, key0 + key);
+                if (row < 0) {
+                    bad_any = 1;
+                    bad_at = c.k.b;
+                }
+            }
+            const float* k = static_cast<const float*>(p.k) + max(row, 0ll) * p.D;
+            const float* v = static_cast<const float*>(p.v) + max(row, 0ll) * p.D;
+#pragma unroll 4
+            for (int d = tid % PER * 4; d < DP; d += PER * 4) {
+                const bool has = row >= 0 && d < p.D;
+                copy16_or_zero(sk + key * L::KS + d, has ? k + d : k, has);
+                copy16_or_zero(sv + key * L::VS + d, has ? v + d : v, has);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if (r.here > 0) load(0);
         for (int t = 0; t < r.here; ++t) {
             const int key0 = c.key0() + t * kKeys;
             const int from = max(0, c.k.lo - key0), to = min(kKeys, c.k.hi - key0);  // keys that some row sees
-            __syncthreads();
-            for (int i = tid; i < kKeys * (DP / 4); i += kThreads) {
-                const int key = i / (DP / 4), d = i % (DP / 4) * 4;
-                float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-                if (key >= from && key < to && d < p.D) {
-                    const long long row = pool_row(p, c.k.b, r.shard, r.kvh, key0 + key);
-                    if (row >= 0) {
-                        kk = *reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * p.D + d);
-                        vv = *reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * p.D + d);
-                    } else {
-                        bad_any = 1;
-                        bad_at = c.k.b;
-                    }
-                }
-                *reinterpret_cast<float4*>(sk + key * L::KS + d) = kk;
-                *reinterpret_cast<float4*>(sv + key * L::VS + d) = vv;
+            const float *sk = smem + L::K + t % L::BUFFERS * L::BUFFER, *sv = sk + kKeys * L::KS;
+            if (L::BUFFERS == 2 && t + 1 < r.here) {
+                load(t + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncthreads();
             float s[4][4] = {};
@@ -164,6 +184,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_f32_kernel
                         }
                     }
             }
+            __syncthreads();
+            if (L::BUFFERS == 1 && t + 1 < r.here) load(t + 1);
         }
         const bool whole = r.begins && r.ends;
         if (tid == 0 && !whole) part->items[r.begins ? 1 : 0] = split_item(c, r, share);
@@ -217,7 +239,7 @@ cudaError_t launch_one(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) 
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    *ctas = prompt_grid(p, num_sms * (DP <= 128 ? 2 : 1), kKeys);
+    *ctas = prompt_grid(p, num_sms * F32Smem<DP>::CTAS, kKeys);
     return launch_after(prompt_f32_kernel<DP>, *ctas, kThreads, F32Smem<DP>::BYTES, s, p);
 }
 

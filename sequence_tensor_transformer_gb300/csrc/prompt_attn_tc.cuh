@@ -40,6 +40,9 @@ namespace prompt {
 constexpr int kTileRows = 128;
 constexpr float kSlack = 8.f;  // log 2 units that a score may be above the maximum in use
 constexpr int kItems = 4;      // descriptions under way
+// An item costs as much as three tiles: 16384 causal rows, heads of 128, took 1.75, 1.45,
+// 1.45 and 1.46 ms with costs of 1, 3, 4 and 6.
+constexpr int kItemCost = 3 * kTileCost;
 constexpr float kPlainCap = 128.f;  // up to here 2^-22 of the cap is no more than a score is off by itself
 
 enum : int { kBegins = 1, kEnds = 2, kStop = 4 };
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     float* scales = reinterpret_cast<float*>(smem + C::SCALES_AT);  // E4M3: [STAGES][TK]
     __shared__ Bars<C> bars;
     __shared__ long long warp_cost[C::WARPS];
-    __shared__ Cursor<TK> share_at;
+    __shared__ Cursor<TK, kItemCost> share_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     admit_next();
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     tc_fence_before();
     bool bad = false;
     __syncthreads();
-    const Share share = find_share<TK, kThreads>(p, warp_cost, &share_at, &bad);
+    const Share share = find_share<kThreads>(p, warp_cost, &share_at, &bad);
     tc_fence_after();
     if (bad) bars.out_of_range = 1;
     const uint32_t tmem = bars.tmem;
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             const int tile_tokens = kTileRows / p.heads;
             constexpr int kBadRow = -TK;  // outside the maps, all of a box's rows: zeros
             if (lane == 0) part->items[0].parts = part->items[1].parts = 0;
-            Cursor<TK> c = share_at;
+            Cursor<TK, kItemCost> c = share_at;
             bool more = c.k.tiles != 0, ok = true;
             int slot = 0, issued = 0, w = 0, q_used[2] = {0, 0};
             uint32_t phase = 1, w_phase = 1, q_phase[2] = {1, 1};

@@ -6,7 +6,7 @@
 // tiles of TK.  The tiles of all items, in order, are dealt out to the CTAs of
 // one resident wave in contiguous shares of equal cost, so that every SM has the
 // same work whatever the lengths, masks and counts of rows are: kTileCost a tile
-// and kItemCost an item.  An item that crosses a share's end leaves its parts'
+// and ITEM_COST an item (of its loads, its first scores and its end).  An item that crosses a share's end leaves its parts'
 // maxima, sums and outputs in the workspace, and a second launch joins them in a
 // fixed order.  Every CTA works out its own share from the lengths.
 //
@@ -23,7 +23,6 @@ namespace sptp {
 namespace prompt {
 
 constexpr int kTileCost = 4;
-constexpr int kItemCost = 12;
 
 struct Block {
     int b;        // sequence
@@ -87,14 +86,14 @@ __device__ __forceinline__ int sequence_of(const PromptParams& p, long long numb
 
 // Position in the list of tiles: tile t of item j of block `number`, whose cost
 // begins at `at`.
-template <int TK>
+template <int TK, int ITEM_COST>
 struct Cursor {
     long long at, number;
     int j, t;
     Block k;
 
     __device__ __forceinline__ long long item_cost() const {
-        return static_cast<long long>(k.tiles) * kTileCost + kItemCost;
+        return static_cast<long long>(k.tiles) * kTileCost + ITEM_COST;
     }
     __device__ __forceinline__ int key0() const { return (k.lo / TK + t) * TK; }
     __device__ __forceinline__ long long tile_at() const { return at + static_cast<long long>(t) * kTileCost; }
@@ -122,8 +121,8 @@ struct Share {
 // This CTA's share, by all its THREADS threads; `warp_cost` [THREADS / 32] and
 // `at` are shared memory.  at->k.tiles == 0 afterwards: an empty share.  bad: a
 // length or a row number outside its range was met.
-template <int TK, int THREADS>
-__device__ __forceinline__ Share find_share(const PromptParams& p, long long* warp_cost, Cursor<TK>* at, bool* bad) {
+template <int THREADS, int TK, int ITEM_COST>
+__device__ __forceinline__ Share find_share(const PromptParams& p, long long* warp_cost, Cursor<TK, ITEM_COST>* at, bool* bad) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long numbers = block_numbers(p);
     const long long run = (numbers + THREADS - 1) / THREADS;
@@ -134,7 +133,7 @@ __device__ __forceinline__ Share find_share(const PromptParams& p, long long* wa
     for (long long n = n0; n < n1; ++n) {
         while (b + 1 < p.B && row_start(p, b + 1) / p.tokens + b + 1 <= n) ++b;
         const Block k = block_of<TK>(p, n, b, bad);
-        if (k.tiles != 0) mine += static_cast<long long>(k.tiles) * kTileCost + kItemCost;
+        if (k.tiles != 0) mine += static_cast<long long>(k.tiles) * kTileCost + ITEM_COST;
     }
     mine *= p.items_per_block;
     long long incl = mine;
@@ -159,7 +158,7 @@ __device__ __forceinline__ Share find_share(const PromptParams& p, long long* wa
     s.begin = s.size * blockIdx.x;
     s.end = s.begin + s.size;
     if (s.begin >= before && s.begin < before + mine) {
-        Cursor<TK> c;
+        Cursor<TK, ITEM_COST> c;
         c.at = before;
         bool unused = false;
         int q = b0;
@@ -190,8 +189,8 @@ struct Piece {
     long long token0;            // shard * M + first row
 };
 
-template <int TK>
-__device__ __forceinline__ Piece piece_of(const PromptParams& p, const Cursor<TK>& c, const Share& s) {
+template <int TK, int ITEM_COST>
+__device__ __forceinline__ Piece piece_of(const PromptParams& p, const Cursor<TK, ITEM_COST>& c, const Share& s) {
     Piece r;
     const long long room = (s.end - c.tile_at() + kTileCost - 1) / kTileCost;
     r.here = static_cast<int>(min(static_cast<long long>(c.k.tiles - c.t), room));
@@ -208,8 +207,8 @@ __device__ __forceinline__ Piece piece_of(const PromptParams& p, const Cursor<TK
 }
 
 // The item for the join, if it does not both begin and end in this share.
-template <int TK>
-__device__ __forceinline__ PromptItem split_item(const Cursor<TK>& c, const Piece& r, const Share& s) {
+template <int TK, int ITEM_COST>
+__device__ __forceinline__ PromptItem split_item(const Cursor<TK, ITEM_COST>& c, const Piece& r, const Share& s) {
     PromptItem it;
     it.first = static_cast<int>(c.at / s.size);
     it.parts = static_cast<int>((c.at + static_cast<long long>(c.k.tiles - 1) * kTileCost) / s.size) - it.first + 1;

@@ -6,6 +6,12 @@
 // rows x DP / 16 elements of the outputs; queries, keys, values and weights lie
 // in shared memory, the next tile's keys and values on their way there while this
 // one's are used (rows of more than 128 elements: no room for two tiles).
+//
+// What bounds it are the loads from shared memory: 16 bytes for each lane of a warp
+// take 4 clocks, so the 8 loads for a thread's 4 x 4 products of 4 elements take 32
+// clocks of the SM and the products 16.  8 x 4 (48 for 32) leaves 8 warps an SM, which
+// wait for one another: 319 us instead of 305 for 2500 causal capped rows of 2 shards,
+// 8 heads of 64 on 2, and 4.29 ms instead of 4.33 behind 20000 cached keys (36 TFLOP/s).
 #include <atomic>
 
 #include "attn_scores.cuh"
@@ -17,6 +23,7 @@ namespace prompt {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int R = 4, STEP = kRows / R;  // rows of a thread: ty + STEP i
 constexpr int kItemCost = kTileCost;
 
 template <int DP>
@@ -28,6 +35,29 @@ struct F32Smem {
     static constexpr int CTAS = BYTES <= 113 * 1024 ? 2 : 1;
 };
 
+struct __align__(16) RowMask {
+    int lo, hi, pos;  // first and last key + 1 that the row sees, and its position
+    float slope;      // in units of log 2
+};
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float low(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float high(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel(const __grid_constant__ PromptParams p) {
     using L = F32Smem<DP>;
@@ -37,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
     __shared__ long long warp_cost[kThreads / 32];
     __shared__ Cursor<kKeys, kItemCost> share_at;
     __shared__ int bad_at, bad_any;
+    __shared__ RowMask masks[kRows];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     admit_next();
     if (tid == 0) bad_at = bad_any = 0;
@@ -64,44 +95,53 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
                                                      (r.head0 + row % r.heads) * p.D + d);
             *reinterpret_cast<float4*>(sq + row * L::QS + d) = v;
         }
-        int lo[4], hi[4], pos[4];
-        float slope[4], m[4], l[4];
-        float4 o[4][NV];
+        if (tid < kRows) {
+            const int h = tid % r.heads, pos = c.k.pos0 + tid / r.heads;
+            const bool in = tid < rows;
+            RowMask k;
+            k.pos = pos;
+            k.lo = in ? first_key(p, pos) : 0;
+            k.hi = in ? min(c.k.len, end_key(pos, c.k.prefix)) : 0;
+            k.slope = p.slopes != nullptr && in ? __ldg(p.slopes + r.shard * p.Hq + r.head0 + h) * kLog2e : 0.f;
+            masks[tid] = k;
+        }
+        float m[R], l[R];
+        uint64_t o[R][NV][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = ty * 4 + i, h = row % r.heads;
-            pos[i] = c.k.pos0 + row / r.heads;
-            const bool in = row < rows;
-            lo[i] = in ? first_key(p, pos[i]) : 0;
-            hi[i] = in ? min(c.k.len, end_key(pos[i], c.k.prefix)) : 0;
-            slope[i] = p.slopes != nullptr && in ? __ldg(p.slopes + r.shard * p.Hq + r.head0 + h) * kLog2e : 0.f;
+        for (int i = 0; i < R; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NV; ++n) o[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n = 0; n < NV; ++n) o[i][n][0] = o[i][n][1] = 0;
         }
         // keys and values of tile t, zeros where no row sees one
         auto load = [&](int t) {
             const int key0 = c.key0() + t * kKeys;
             const int from = max(0, c.k.lo - key0), to = min(kKeys, c.k.hi - key0);
             float *sk = smem + L::K + t % L::BUFFERS * L::BUFFER, *sv = sk + kKeys * L::KS;
-            constexpr int PER = kThreads / kKeys;  // threads of a key
-            const int key = tid / PER;
-            long long row = -1;
-            if (key >= from && key < to) {
-                row = pool_row(p, c.k.b, r.shard, r.kvh, key0 + key);
-                if (row < 0) {
+            // a warp's keys: their rows looked up by a lane each, copied by the row
+            constexpr int KEYS = kKeys / (kThreads / 32), LANES = DP / 4 < 32 ? DP / 4 : 32;
+            const int lane = tid & 31, first = tid / 32 * KEYS;
+            long long mine = -1;
+            if (lane < KEYS && first + lane >= from && first + lane < to) {
+                mine = pool_row(p, c.k.b, r.shard, r.kvh, key0 + first + lane);
+                if (mine < 0) {
                     bad_any = 1;
                     bad_at = c.k.b;
                 }
             }
-            const float* k = static_cast<const float*>(p.k) + max(row, 0ll) * p.D;
-            const float* v = static_cast<const float*>(p.v) + max(row, 0ll) * p.D;
-#pragma unroll 4
-            for (int d = tid % PER * 4; d < DP; d += PER * 4) {
-                const bool has = row >= 0 && d < p.D;
-                copy16_or_zero(sk + key * L::KS + d, has ? k + d : k, has);
-                copy16_or_zero(sv + key * L::VS + d, has ? v + d : v, has);
+#pragma unroll
+            for (int i = 0; i < KEYS; i += 32 / LANES) {
+                const int j = i + lane / LANES, key = first + j;
+                const long long row = __shfl_sync(0xffffffffu, mine, j);
+                const float* k = static_cast<const float*>(p.k) + max(row, 0ll) * p.D;
+                const float* v = static_cast<const float*>(p.v) + max(row, 0ll) * p.D;
+#pragma unroll
+                for (int d = lane % LANES * 4; d < DP; d += LANES * 4) {
+                    const bool has = row >= 0 && d < p.D;
+                    copy16_or_zero(sk + key * L::KS + d, has ? k + d : k, has);
+                    copy16_or_zero(sv + key * L::VS + d, has ? v + d : v, has);
+                }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -117,31 +157,32 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncthreads();
-            float s[4][4] = {};
+            // elements d, d + 2 .. and d + 1, d + 3 .. of the products apart: packed arithmetic
+            uint64_t s[R][4] = {};
 #pragma unroll 4
             for (int d = 0; d < DP; d += 4) {
-                float4 a[4], b[4];
+                ulonglong2 b[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * L::QS + d);
+                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * L::KS + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * L::KS + d);
+                for (int i = 0; i < R; ++i) {
+                    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sq + (ty + STEP * i) * L::QS + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+                    for (int j = 0; j < 4; ++j) s[i][j] = fma2(a.y, b[j].y, fma2(a.x, b[j].x, s[i][j]));
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float top = m[i];
+            for (int i = 0; i < R; ++i) {
+                const RowMask k = masks[ty + STEP * i];
+                float x[4], top = m[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int key = key0 + tx + 16 * j;
-                    float x = s[i][j] * to_log2;
-                    if (p.cap != 0.f) x = cap.cap * tanhf(x * cap.inv);
-                    if (p.slopes != nullptr) x -= slope[i] * static_cast<float>(abs(pos[i] - key));
-                    s[i][j] = key >= lo[i] && key < hi[i] ? x : -INFINITY;
-                    top = fmaxf(top, s[i][j]);
+                    x[j] = (low(s[i][j]) + high(s[i][j])) * to_log2;
+                    if (p.cap != 0.f) x[j] = cap.cap * tanhf(x[j] * cap.inv);
+                    if (p.slopes != nullptr) x[j] -= k.slope * static_cast<float>(abs(k.pos - key));
+                    x[j] = key >= k.lo && key < k.hi ? x[j] : -INFINITY;
+                    top = fmaxf(top, x[j]);
                 }
 #pragma unroll
                 for (int off = 1; off < 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -151,38 +192,40 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float w = pow2_approx(s[i][j] - base);
+                    const float w = pow2_approx(x[j] - base);
                     sum += w;
-                    sw[(ty * 4 + i) * L::WS + tx + 16 * j] = w;
+                    sw[(ty + STEP * i) * L::WS + tx + 16 * j] = w;
                 }
                 l[i] = l[i] * old + sum;
+                const uint64_t f = pack2(old, old);
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
-                    o[i][n].x *= old;
-                    o[i][n].y *= old;
-                    o[i][n].z *= old;
-                    o[i][n].w *= old;
+                    o[i][n][0] = mul2(o[i][n][0], f);
+                    o[i][n][1] = mul2(o[i][n][1], f);
                 }
             }
-            __syncwarp();  // the weights of a warp's 8 rows are its own
+            __syncwarp();  // the weights of a warp's rows are its own
             for (int k = from & ~3; k < to; k += 4) {
-                float4 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sw + (ty * 4 + i) * L::WS + k);
+                ulonglong2 v[4][NV];
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int n = 0; n < NV; ++n) {
-                        const float4 v = *reinterpret_cast<const float4*>(sv + (k + kk) * L::VS + n * 64 + tx * 4);
+                    for (int n = 0; n < NV; ++n)
+                        v[kk][n] = *reinterpret_cast<const ulonglong2*>(sv + (k + kk) * L::VS + n * 64 + tx * 4);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-                            o[i][n].x = fmaf(f, v.x, o[i][n].x);
-                            o[i][n].y = fmaf(f, v.y, o[i][n].y);
-                            o[i][n].z = fmaf(f, v.z, o[i][n].z);
-                            o[i][n].w = fmaf(f, v.w, o[i][n].w);
+                for (int i = 0; i < R; ++i) {
+                    const float4 w = *reinterpret_cast<const float4*>(sw + (ty + STEP * i) * L::WS + k);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const float f = kk == 0 ? w.x : kk == 1 ? w.y : kk == 2 ? w.z : w.w;
+                        const uint64_t ff = pack2(f, f);
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            o[i][n][0] = fma2(ff, v[kk][n].x, o[i][n][0]);
+                            o[i][n][1] = fma2(ff, v[kk][n].y, o[i][n][1]);
                         }
                     }
+                }
             }
             __syncthreads();
             if (L::BUFFERS == 1 && t + 1 < r.here) load(t + 1);
@@ -190,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
         const bool whole = r.begins && r.ends;
         if (tid == 0 && !whole) part->items[r.begins ? 1 : 0] = split_item(c, r, share);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = ty * 4 + i;
+        for (int i = 0; i < R; ++i) {
+            const int row = ty + STEP * i;
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
             if (row >= rows) continue;
@@ -213,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
             for (int n = 0; n < NV; ++n) {
                 const int d = n * 64 + tx * 4;
                 if (d < p.D)
-                    *reinterpret_cast<float4*>(to + d) = make_float4(o[i][n].x * f, o[i][n].y * f, o[i][n].z * f, o[i][n].w * f);
+                    *reinterpret_cast<float4*>(to + d) = make_float4(low(o[i][n][0]) * f, high(o[i][n][0]) * f,
+                                                                           low(o[i][n][1]) * f, high(o[i][n][1]) * f);
             }
         }
         __syncthreads();

@@ -16,6 +16,8 @@
 // sum of two bf16, so that it keeps 16 bits and the result is rounded once.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "lora.h"
 #include "sptp.h"
 #include "sptp_ptx.cuh"
@@ -47,9 +49,6 @@ __device__ __forceinline__ void split2bf(float x, float y, uint32_t& hi, uint32_
     lo = pack2(x - h.x, y - h.y);
 }
 
-__device__ __forceinline__ uint4 load16(const void* base, long long elem, bool in) {
-    return in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + elem)) : make_uint4(0, 0, 0, 0);
-}
 
 // The adapters of 16 rows: lane r < 16 has row r's (-1: none or no row), and `first`
 // the lanes whose row is the first with its adapter.
@@ -89,12 +88,28 @@ __device__ __forceinline__ void report_rows(const LoraParams& p) {
     }
 }
 
+// 16 bytes into shared memory, zeros where there are none.
+__device__ __forceinline__ void copy_row(void* to, const void* base, long long elem, bool in) {
+    copy16_or_zero(to, static_cast<const __nv_bfloat16*>(base) + (in ? elem : 0), in);
+}
+
 // ---------------------------------------------------------------- t = A x, bf16
 // A block has 16 rows and one split of K.  Its warps share out the rows' adapters,
 // and the split's elements where there are fewer adapters than warps (their sums
-// are then added in a fixed order).
+// are then added in a fixed order).  A thread's loads go through a ring of its own in
+// shared memory, so that as many are under way as HBM's latency takes whatever the
+// registers are: 16384 rows of 3584 elements, rank 16, 32 us and 39 with unrolled
+// loads; 3001 rows of 2 x 2048, rank 64, 17 and 24.
+template <int NT>
+struct DownRing {
+    static constexpr int ITEMS = 2 + NT, STAGES = NT <= 4 ? 3 : 2;
+    static constexpr int BYTES = STAGES * ITEMS * kThreads * 16;
+};
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_constant__ LoraParams p) {
+    constexpr int STAGES = DownRing<NT>::STAGES, ITEMS = DownRing<NT>::ITEMS;
+    extern __shared__ __align__(16) uint4 down_ring[];  // [STAGES][ITEMS][threads]: a thread's loads under way
     __shared__ __align__(16) float sums[kWarps / 2][16 * NT * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
     admit_next();
@@ -127,21 +142,38 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
                 for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
             if (mine) {
                 const long long arow = (static_cast<long long>(a) * p.R + r0 + g) * p.K + (p.rowwise ? shard * p.f : 0);
-#pragma unroll(NT <= 2 ? 4 : NT <= 4 ? 2 : 1)
-                for (int kb = k0 + sub * 32; kb < k1; kb += ways * 32) {
-                    const int k = kb + i * 8;
+                const int steps = (k1 - k0 - sub * 32 + ways * 32 - 1) / (ways * 32);
+                auto load = [&](int step, int slot) {
+                    const int k = k0 + (step * ways + sub) * 32 + i * 8;
                     const bool in = k < k1;
-                    const uint4 u = load16(p.x, xrow + k, in && in0), v = load16(p.x, xrow + 8ll * p.f + k, in && in1);
-                    uint4 w[NT];
+                    uint4* to = down_ring + slot * ITEMS * kThreads + threadIdx.x;
+                    if (step < steps) {
+                        copy_row(to, p.x, xrow + k, in && in0);
+                        copy_row(to + kThreads, p.x, xrow + 8ll * p.f + k, in && in1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        w[nt] = load16(p.A, arow + static_cast<long long>(nt) * 8 * p.K + k, in && r0 + nt * 8 < p.R);
+                        for (int nt = 0; nt < NT; ++nt)
+                            copy_row(to + (2 + nt) * kThreads, p.A, arow + static_cast<long long>(nt) * 8 * p.K + k,
+                                     in && r0 + nt * 8 < p.R);
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                int slot = 0;
+#pragma unroll
+                for (int st = 0; st < STAGES - 1; ++st) load(st, st);
+                for (int step = 0; step < steps; ++step) {
+                    // into the slot that the last step has used up
+                    load(step + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+                    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+                    const uint4* from = down_ring + slot * ITEMS * kThreads + threadIdx.x;
+                    const uint4 u = from[0], v = from[kThreads];
                     const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(acc[nt], a0, w[nt].x, w[nt].y);
-                        mma_bf16(acc[nt], a1, w[nt].z, w[nt].w);
+                        const uint4 w = from[(2 + nt) * kThreads];
+                        mma_bf16(acc[nt], a0, w.x, w.y);
+                        mma_bf16(acc[nt], a1, w.z, w.w);
                     }
+                    if (++slot == STAGES) slot = 0;
                 }
             }
             for (int half = ways / 2; half > 0; half /= 2) {  // warps [half, 2 half) of a group to [0, half)
@@ -185,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
 template <int KT, int NC>
 __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
     lora_up_bf16(const __grid_constant__ LoraParams p, int col_blocks) {
-    constexpr int DEPTH = 2;  // chunks whose base is under way
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
     admit_next();
     await_previous();
@@ -224,12 +255,9 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
         }
     };
     Place q = {first / chunks, first % chunks}, coming = q;
-    uint4 ahead[DEPTH][NC][2];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-        load_base(coming, ahead[d]);
-        advance(coming);
-    }
+    uint4 ahead[NC][2];  // the next chunk's base
+    load_base(coming, ahead);
+    advance(coming);
     // this lane's part of t, times the gain: rows g and g + 8, elements 4 i .. 4 i + 3 of each 16
     uint32_t hi[KT][4], lo[KT][4];
     auto load_t = [&](int shard) {
@@ -284,12 +312,8 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                was[c][e] = ahead[0][c][e];
-#pragma unroll
-                for (int d = 1; d < DEPTH; ++d) ahead[d - 1][c][e] = ahead[d][c][e];
-            }
-        load_base(coming, ahead[DEPTH - 1]);
+            for (int e = 0; e < 2; ++e) was[c][e] = ahead[c][e];
+        load_base(coming, ahead);
         advance(coming);
         if (have < 0 || (p.rowwise && have != q.shard)) load_t(p.rowwise ? q.shard : 0);
         have = q.shard;
@@ -542,9 +566,31 @@ __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ 
     }
 }
 
+// A kernel's dynamic shared memory, asked for once on each device.
+template <class K>
+struct RoomFor {
+    K kernel;
+    int bytes;
+    std::atomic<unsigned long long> done{0};
+
+    RoomFor(K k, int b) : kernel(k), bytes(b) {}
+    cudaError_t made() {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
+
 template <int NT>
 cudaError_t down(const LoraParams& p, cudaStream_t s) {
-    return launch_after(lora_down_bf16<NT>, (p.M + 15) / 16 * p.splits * (p.rowwise ? p.P : 1), kThreads, 0, s, p);
+    static RoomFor room{lora_down_bf16<NT>, DownRing<NT>::BYTES};
+    const cudaError_t e = room.made();
+    if (e != cudaSuccess) return e;
+    return launch_after(lora_down_bf16<NT>, (p.M + 15) / 16 * p.splits * (p.rowwise ? p.P : 1), kThreads, DownRing<NT>::BYTES, s, p);
 }
 
 template <int KT, int NC>

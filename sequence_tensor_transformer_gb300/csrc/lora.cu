@@ -209,6 +209,18 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
     }
 }
 
+// A lane's elements of B's row for products kt .. kt + WIDE - 1.
+template <int WIDE, int KT, int J>
+__device__ __forceinline__ void load_b(const __nv_bfloat16* row, bool in, uint2 (&b)[KT][J], int kt, int j) {
+    if constexpr (WIDE == 2) {
+        const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(row)) : make_uint4(0, 0, 0, 0);
+        b[kt][j] = make_uint2(v.x, v.y);
+        b[kt + 1][j] = make_uint2(v.z, v.w);
+    } else {
+        b[kt][j] = in ? __ldg(reinterpret_cast<const uint2*>(row)) : make_uint2(0, 0);
+    }
+}
+
 // ---------------------------------------------------------------- out = base + B t, bf16
 // A block has 16 rows; its warps take chunks of 32 NC columns in turn, side by side:
 // 1 KB of a row at a time with NC = 2.  (With rows of its own for each warp, so that
@@ -258,7 +270,12 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
     uint4 ahead[NC][2];  // the next chunk's base
     load_base(coming, ahead);
     advance(coming);
-    // this lane's part of t, times the gain: rows g and g + 8, elements 4 i .. 4 i + 3 of each 16
+    // a lane's first element of product kt: 4 i of each 16, or with an even number of
+    // products 8 i and 8 i + 4 of each 32, so that 16 bytes of B do for two (3001 rows of
+    // rank 64, 2 x 4096 columns: 65 us with the first launch, and 70)
+    constexpr int WIDE = KT % 2 == 0 ? 2 : 1;
+    auto inner = [&](int kt) { return kt / WIDE * (16 * WIDE) + 4 * WIDE * i + kt % WIDE * 4; };
+    // this lane's part of t, times the gain: rows g and g + 8
     uint32_t hi[KT][4], lo[KT][4];
     auto load_t = [&](int shard) {
         const int shards = p.rowwise ? p.P : 1;
@@ -269,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (a >= 0 && kt * 16 + 4 * i < p.R) {
-                    const float* at = p.t + (static_cast<long long>(shard) * p.M + m0 + g + 8 * e) * p.R + kt * 16 + 4 * i;
+                if (a >= 0 && inner(kt) < p.R) {
+                    const float* at = p.t + (static_cast<long long>(shard) * p.M + m0 + g + 8 * e) * p.R + inner(kt);
                     const long long stride = static_cast<long long>(shards) * p.M * p.R;
 #pragma unroll 8
                     for (int s = 0; s < p.splits; ++s) {
@@ -321,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
         const int col0 = q.chunk * (32 * NC);
         const long long b0 = (p.rowwise ? 0 : static_cast<long long>(q.shard) * p.n) + col0 + 8 * (g >> 1) + (g & 1);
         if (plain && col0 + 32 * NC <= p.n) {
-            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a0) * p.N + b0) * p.R + 4 * i;
+            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a0) * p.N + b0) * p.R + inner(0);
             uint2 b[KT][NC * 4];
 #pragma unroll
             for (int j = 0; j < NC * 4; ++j)
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-                    b[kt][j] = __ldg(reinterpret_cast<const uint2*>(rows + (j / 4 * 32 + 2 * (j % 4)) * (KT * 16) + kt * 16));
+                for (int kt = 0; kt < KT; kt += WIDE)
+                    load_b<WIDE>(rows + (j / 4 * 32 + 2 * (j % 4)) * (KT * 16) + kt * 16, true, b, kt, j);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 uint4 now[2];
@@ -347,16 +364,15 @@ __global__ void __launch_bounds__(kThreads, KT <= 4 ? 2 : 1)
         }
         for (uint32_t left = ids.first; left != 0; left &= left - 1) {
             const int a = ids.of(__ffs(left) - 1);
-            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a) * p.N + b0) * p.R + 4 * i;
+            const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.B) + (static_cast<long long>(a) * p.N + b0) * p.R + inner(0);
             uint2 b[KT][NC * 4];
 #pragma unroll
             for (int j = 0; j < NC * 4; ++j) {
                 const int n = j / 4 * 32 + 2 * (j % 4);  // from this lane's first row of B
                 const bool in = col0 + n + 8 * (g >> 1) + (g & 1) < p.n;
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-                    b[kt][j] = in && kt * 16 + 4 * i < p.R ? __ldg(reinterpret_cast<const uint2*>(rows + n * p.R + kt * 16))
-                                                           : make_uint2(0, 0);
+                for (int kt = 0; kt < KT; kt += WIDE)
+                    load_b<WIDE>(rows + n * p.R + kt * 16, in && inner(kt) < p.R, b, kt, j);
             }
             // all 16 rows' products with each adapter, kept by the rows that named it
             // (so another adapter's infinities do not reach a row)

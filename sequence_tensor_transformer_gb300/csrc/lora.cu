@@ -517,8 +517,16 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_f32(const __grid_co
     }
 }
 
-// A block has 8 rows; a thread a column of all of them, an adapter's rows at a time.
+// A block has 8 rows and an adapter's rows of B at a time; a thread has two columns
+// for every read of t.  Above rank 16, LANES = 4 lanes share a column's 16-byte pieces
+// of B, so that a load touches 8 of B's rows and not 32 (4911 rows of rank 64, two
+// launches: 173 us, and 223 with a lane a column); up to it, where the sums over the
+// lanes would cost more than that, a column is one lane's (3000 rows of rank 16: 84 us,
+// and 117 with four).
+constexpr int kColsF = 2;
+template <int LANES>
 __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ LoraParams p, int col_blocks) {
+    constexpr int WIDTH = kThreads / LANES * kColsF;  // columns of a round
     __shared__ __align__(16) float st[kRowsF][kLoraMaxRank];
     admit_next();
     const int m0 = blockIdx.x / col_blocks * kRowsF;
@@ -547,37 +555,57 @@ __global__ void __launch_bounds__(kThreads) lora_up_f32(const __grid_constant__ 
             st[m][r] = v;
         }
         __syncthreads();
-        const int rounds = (p.N + kThreads * col_blocks - 1) / (kThreads * col_blocks);
-        for (int round = 0; round < rounds; ++round) {  // (whole warps: the adapters are exchanged between lanes)
-            const int col = (round * col_blocks + blockIdx.x % col_blocks) * kThreads + threadIdx.x;
-            const bool in = col < p.N;
-            const int sh = p.rowwise || !in ? shard : col / p.n;
-            const long long at0 = (static_cast<long long>(sh) * p.M + m0) * p.n + (p.rowwise ? col : col - sh * p.n);
-            float was[kRowsF], acc[kRowsF] = {};
+        const int part = threadIdx.x % LANES;
+        const int rounds = (p.N + WIDTH * col_blocks - 1) / (WIDTH * col_blocks);
+        for (int round = 0; round < rounds; ++round) {  // (whole warps: sums are exchanged between lanes)
+            const int col0 = (round * col_blocks + blockIdx.x % col_blocks) * WIDTH + threadIdx.x / LANES;
+            long long at0[kColsF];
+            bool in[kColsF];
+            float was[kColsF][kRowsF / LANES], acc[kColsF][kRowsF] = {};
 #pragma unroll
-            for (int m = 0; m < kRowsF; ++m)
-                was[m] = in && m0 + m < p.M ? static_cast<const float*>(p.base)[at0 + static_cast<long long>(m) * p.n] : 0.f;
+            for (int c = 0; c < kColsF; ++c) {
+                const int col = col0 + c * (kThreads / LANES);
+                in[c] = col < p.N;
+                const int sh = p.rowwise || !in[c] ? shard : col / p.n;
+                at0[c] = (static_cast<long long>(sh) * p.M + m0) * p.n + (p.rowwise ? col : col - sh * p.n);
+                // this lane's rows: part, part + LANES ..
+#pragma unroll
+                for (int e = 0; e < kRowsF / LANES; ++e) {
+                    const int m = e * LANES + part;
+                    was[c][e] = in[c] && m0 + m < p.M ? static_cast<const float*>(p.base)[at0[c] + static_cast<long long>(m) * p.n] : 0.f;
+                }
+            }
             for (uint32_t left = ids.first; left != 0; left &= left - 1) {
                 const int a = ids.of(__ffs(left) - 1);
                 const uint32_t mine = __ballot_sync(0xffffffffu, ids.id == a);
-                if (!in) continue;
                 const float4* row = reinterpret_cast<const float4*>(static_cast<const float*>(p.B) +
-                                                                    (static_cast<long long>(a) * p.N + col) * p.R);
-#pragma unroll 4
-                for (int r = 0; r < p.R / 4; ++r) {
-                    const float4 w = __ldg(row + r);
+                                                                    (static_cast<long long>(a) * p.N + col0) * p.R);
+                const int next = kThreads / LANES * (p.R / 4);  // from a column's row of B to the other's
+#pragma unroll 2
+                for (int r = part; r < p.R / 4; r += LANES) {
+                    float4 w[kColsF];
+#pragma unroll
+                    for (int c = 0; c < kColsF; ++c) w[c] = in[c] ? __ldg(row + c * next + r) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int m = 0; m < kRowsF; ++m) {
                         if (!(mine >> m & 1)) continue;
                         const float4 v = *reinterpret_cast<const float4*>(&st[m][r * 4]);
-                        acc[m] = fmaf(v.x, w.x, fmaf(v.y, w.y, fmaf(v.z, w.z, fmaf(v.w, w.w, acc[m]))));
+#pragma unroll
+                        for (int c = 0; c < kColsF; ++c)
+                            acc[c][m] = fmaf(v.x, w[c].x, fmaf(v.y, w[c].y, fmaf(v.z, w[c].z, fmaf(v.w, w[c].w, acc[c][m]))));
                     }
                 }
             }
 #pragma unroll
-            for (int m = 0; m < kRowsF; ++m)
-                if (in && m0 + m < p.M && (!in_place || (some >> m & 1)))
-                    static_cast<float*>(p.out)[at0 + static_cast<long long>(m) * p.n] = was[m] + acc[m];
+            for (int c = 0; c < kColsF; ++c)
+#pragma unroll
+                for (int m = 0; m < kRowsF; ++m) {
+                    float v = acc[c][m];
+#pragma unroll
+                    for (int off = 1; off < LANES; off *= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+                    if (m % LANES == part && in[c] && m0 + m < p.M && (!in_place || (some >> m & 1)))
+                        static_cast<float*>(p.out)[at0[c] + static_cast<long long>(m) * p.n] = was[c][m / LANES] + v;
+                }
         }
     }
 }
@@ -620,6 +648,15 @@ cudaError_t up(const LoraParams& p, int num_sms, cudaStream_t s) {
     return launch_after(lora_up_bf16<KT, NC>, tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
 }
 
+template <int LANES>
+cudaError_t up_f32(const LoraParams& p, int row_tiles, int num_sms, cudaStream_t s) {
+    constexpr int WIDTH = kThreads / LANES * kColsF;
+    int col_blocks = (4 * num_sms + row_tiles - 1) / row_tiles;
+    const int most_cols = (p.N + WIDTH - 1) / WIDTH;
+    if (col_blocks > most_cols) col_blocks = most_cols;
+    return launch_after(lora_up_f32<LANES>, row_tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
+}
+
 }  // namespace
 
 cudaError_t launch_lora(LoraParams& p, bool bf16, int num_sms, cudaStream_t s) {
@@ -629,10 +666,7 @@ cudaError_t launch_lora(LoraParams& p, bool bf16, int num_sms, cudaStream_t s) {
         const long long units = static_cast<long long>(row_tiles) * (p.R / 8) * p.splits * (p.rowwise ? p.P : 1);
         e = launch_after(lora_down_f32, static_cast<int>((units + kDownWarps - 1) / kDownWarps), 32 * kDownWarps, 0, s, p);
         if (e != cudaSuccess) return e;
-        int col_blocks = (4 * num_sms + row_tiles - 1) / row_tiles;
-        const int most_cols = (p.N + kThreads - 1) / kThreads;
-        if (col_blocks > most_cols) col_blocks = most_cols;
-        return launch_after(lora_up_f32, row_tiles * col_blocks + 1, kThreads, 0, s, p, col_blocks);
+        return p.R <= 16 ? up_f32<1>(p, row_tiles, num_sms, s) : up_f32<4>(p, row_tiles, num_sms, s);
     }
     e = p.R <= 16 ? down<2>(p, s) : p.R <= 32 ? down<4>(p, s) : down<8>(p, s);
     if (e != cudaSuccess) return e;

@@ -14,14 +14,16 @@ namespace {
 // m = max m_k,  out = sum e^(m_k - m) o_k / sum e^(m_k - m) l_k  over the parts
 // k of a row, in their order.
 //
-// Blocks kJoinBlocks c .. are CTA c's counterparts; an item of n parts is joined
-// by those of its n CTAs, which take its rows in turn, so that one long item
-// (many parts) and many short ones spread over the SMs.  A warp joins a row, or,
-// since the loads of what other SMs have just written take about a microsecond
-// each, the eight warps of a block share one of more than kAlone parts, their
-// sums added in order.  The last block sums up the CTAs' status words.
+// Every part has an entry (its CTA and the slot there) and an entry kJoinBlocks
+// blocks, which all join the entry's item and take its rows in turn, so that one long
+// item (many parts) and many short ones spread over the SMs.  The loads of what other
+// SMs have just written take about a microsecond each: a warp has the parts of two
+// rows of up to kFew parts under way at once; a row of more is a warp's, or, of more
+// than kAlone, the eight warps' of a block, their sums added in order.  The last block
+// sums up the CTAs' status words.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBlocks = 8;
+constexpr int kJoinBlocks = 4;
+constexpr int kFew = 4;
 constexpr int kAlone = 16;
 constexpr int kBatch = 4;  // parts whose loads a lane has in flight
 
@@ -33,12 +35,23 @@ __device__ __forceinline__ void add_scaled(float4& a, float f, const float4& v) 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join(const __grid_constant__ PromptParams p, int ctas) {
+__device__ __forceinline__ void store4(T* out, const float4& v) {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+        *reinterpret_cast<float4*>(out) = v;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) prompt_join(const __grid_constant__ PromptParams p, int ctas) {
     __shared__ float4 sums[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     admit_next();
     await_previous();
-    if (blockIdx.x == ctas * kJoinBlocks) {
+    if (blockIdx.x == ctas * 2 * kJoinBlocks) {
         // the first CTA that failed; if none did, the first that met an index outside its range
         __shared__ int first_bad, first_failed;
         if (threadIdx.x == 0) first_bad = first_failed = ctas;
@@ -62,83 +75,116 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join(const __grid_cons
         }
         return;
     }
-    const int c = blockIdx.x / kJoinBlocks;
+    const int entry = blockIdx.x / kJoinBlocks, c = entry / 2;
+    const PromptItem it = p.parts[c].items[entry % 2];
+    const int n = it.parts;
+    if (n < 2 || it.first < 0 || it.first + n > ctas) return;
+    const int rows = it.tokens * it.heads;
+    const int first = (c - it.first) * kJoinBlocks + blockIdx.x % kJoinBlocks, step = n * kJoinBlocks;
+    // part k of a row: slot 0 of share first + k; the first: slot 1
+    auto slot = [&](int row, int k) {
+        return (2ll * it.first + max(2 * k, 1)) * p.part_rows + row;
+    };
+    auto out_row = [&](int row) { return (it.token0 + row / it.heads) * p.Hq + it.head0 + row % it.heads; };
+    auto lse = [&](float top, float sum) { return sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum); };
+    // in two factors: a part far below the top may have values that are as much larger
+    auto add_part = [](float4& acc, float m, float top, const float4& v) {
+        const float f = pow2_approx(0.5f * (m - top));
+        add_scaled(acc, f, make_float4(f * v.x, f * v.y, f * v.z, f * v.w));
+    };
+    if (n <= kFew) {
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const PromptItem it = p.parts[c].items[which];
-        const int n = it.parts;
-        if (n < 2 || it.first < 0 || it.first + n > ctas) continue;
-        const int rows = it.tokens * it.heads;
-        const bool shared = n > kAlone;
-        const int sub = shared ? warp : 0, ways = shared ? kJoinWarps : 1;
-        const int first = (c - it.first) * kJoinBlocks + blockIdx.x % kJoinBlocks, step = n * kJoinBlocks;
+        for (int r0 = first + warp * step; r0 < rows; r0 += 2 * step * kJoinWarps) {
 #pragma unroll 1
-        for (int r0 = first; r0 < rows; r0 += shared ? step : step * kJoinWarps) {
-            const int row = shared ? r0 : r0 + warp * step;
-            const bool mine = row < rows;
-            // part k: slot 0 of share first + k; the first: slot 1
-            const long long base = 2ll * it.first * p.part_rows + row;
-            auto slot = [&](int k) { return base + max(2 * k, 1) * static_cast<long long>(p.part_rows); };
-            float top = -INFINITY, sum = 0.f;
-            if (mine) {
-                for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[slot(k)].x);
+            for (int d = lane * 4; d < p.D; d += 128) {
+                float2 ml[2][kFew];
+                float4 v[2][kFew];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int k = 0; k < kFew; ++k) {
+                        const int row = r0 + e * step * kJoinWarps;
+                        const bool is = row < rows && k < n;
+                        ml[e][k] = is ? p.part_ml[slot(row, k)] : make_float2(-INFINITY, 0.f);
+                        v[e][k] = is ? *reinterpret_cast<const float4*>(p.part_o + slot(row, k) * p.D + d)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = r0 + e * step * kJoinWarps;
+                    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kFew; ++k) top = fmaxf(top, ml[e][k].x);
+                    if (top == -INFINITY) top = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kFew; ++k) {
+                        sum = fmaf(pow2_approx(ml[e][k].x - top), ml[e][k].y, sum);
+                        add_part(acc, ml[e][k].x, top, v[e][k]);
+                    }
+                    if (row >= rows) continue;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    store4(static_cast<T*>(p.out) + out_row(row) * p.D + d,
+                           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                    if (p.lse != nullptr && d == 0) p.lse[out_row(row)] = lse(top, sum);
+                }
+            }
+        }
+        return;
+    }
+    const bool shared = n > kAlone;
+    const int sub = shared ? warp : 0, ways = shared ? kJoinWarps : 1;
+#pragma unroll 1
+    for (int r0 = first; r0 < rows; r0 += shared ? step : step * kJoinWarps) {
+        const int row = shared ? r0 : r0 + warp * step;
+        const bool mine = row < rows;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int d0 = 0; d0 < p.D; d0 += 128) {
+            const int d = d0 + lane * 4;
+            const bool in = mine && d < p.D;
+            float4 v[kBatch];
+            float m[kBatch];
+            auto load = [&](int k0) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int k = k0 + u * ways;
+                    const bool is = in && k < n;
+                    m[u] = is ? p.part_ml[slot(row, k)].x : -INFINITY;
+                    v[u] = is ? *reinterpret_cast<const float4*>(p.part_o + slot(row, k) * p.D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            };
+            load(sub);  // on its way while the maximum is found
+            if (mine && d0 == 0) {
+                for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[slot(row, k)].x);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                 if (top == -INFINITY) top = 0.f;
                 for (int k = lane; k < n; k += 32) {
-                    const float2 r = p.part_ml[slot(k)];
+                    const float2 r = p.part_ml[slot(row, k)];
                     sum = fmaf(pow2_approx(r.x - top), r.y, sum);
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (p.lse != nullptr && lane == 0 && sub == 0) p.lse[out_row(row)] = lse(top, sum);
             }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int k0 = sub; k0 < n; k0 += kBatch * ways) {
+                if (k0 != sub) load(k0);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) add_part(acc, m[u], top, v[u]);
+            }
+            if (shared) {
+                sums[warp][lane] = acc;
+                __syncthreads();
+                if (warp == 0)
+                    for (int w = 1; w < kJoinWarps; ++w) add_scaled(acc, 1.f, sums[w][lane]);
+                __syncthreads();
+            }
+            if (!in || sub != 0) continue;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const long long orow = (it.token0 + row / it.heads) * p.Hq + it.head0 + row % it.heads;
-            if (p.lse != nullptr && mine && lane == 0 && sub == 0)
-                p.lse[orow] = sum == 0.f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
-#pragma unroll 1
-            for (int d0 = 0; d0 < p.D; d0 += 128) {
-                const int d = d0 + lane * 4;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (mine && d < p.D) {
-#pragma unroll 1
-                    for (int k0 = sub; k0 < n; k0 += kBatch * ways) {
-                        float4 v[kBatch];
-                        float m[kBatch];
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            const int k = k0 + u * ways;
-                            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            m[u] = -INFINITY;
-                            if (k < n) {
-                                m[u] = p.part_ml[slot(k)].x;
-                                v[u] = *reinterpret_cast<const float4*>(p.part_o + slot(k) * p.D + d);
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            // in two factors: a part far below the top may have values that are as much larger
-                            const float f = pow2_approx(0.5f * (m[u] - top));
-                            add_scaled(acc, f, make_float4(f * v[u].x, f * v[u].y, f * v[u].z, f * v[u].w));
-                        }
-                    }
-                }
-                if (shared) {
-                    sums[warp][lane] = acc;
-                    __syncthreads();
-                    if (warp == 0)
-                        for (int w = 1; w < kJoinWarps; ++w) add_scaled(acc, 1.f, sums[w][lane]);
-                    __syncthreads();
-                }
-                if (!mine || sub != 0 || d >= p.D) continue;
-                T* out = static_cast<T*>(p.out) + orow * p.D + d;
-                if constexpr (sizeof(T) == 2) {
-                    reinterpret_cast<__nv_bfloat162*>(out)[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-                    reinterpret_cast<__nv_bfloat162*>(out)[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                } else {
-                    *reinterpret_cast<float4*>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                }
-            }
+            store4(static_cast<T*>(p.out) + out_row(row) * p.D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         }
     }
 }
@@ -180,7 +226,7 @@ cudaError_t launch_prompt_attn(PromptParams& p, bool bf16, bool e4m3, int num_sm
     cudaError_t e = p.withhold_full >= 0 ? launch_prompt_test(p, e4m3, &ctas, s)
                                          : (bf16 ? kernels[e4m3][cap][bias] : launch_prompt_f32)(p, num_sms, &ctas, s);
     if (e != cudaSuccess) return e;
-    const int grid = ctas * kJoinBlocks + 1;
+    const int grid = ctas * 2 * kJoinBlocks + 1;
     return bf16 ? launch_after(prompt_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, s, p, ctas)
                 : launch_after(prompt_join<float>, grid, kJoinWarps * 32, 0, s, p, ctas);
 }

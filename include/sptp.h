@@ -507,8 +507,9 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
  *   cap     0: none (s_j = scale q . k_j - ..); else 1e-30 <= cap <= 1e30
  *   slopes  fp32 [P][Hq], one per query head of every shard, finite, any sign;
  *           NULL: none
- * Numerics: tanh to 2^-22 of the cap, or of the score below an eighth of it;
- * distances exact below 2^24, a bias to 2^-23 of itself.
+ * Numerics: tanh to 2^-22 of the cap, or of the score below an eighth of it
+ * (prompts' attention in bf16, caps up to 128: of the cap); distances exact below
+ * 2^24, a bias to 2^-23 of itself.
  */
 
 /* Workspace bytes needed by sptp_paged_attn_prompt (0 on bad args). */
@@ -556,9 +557,10 @@ typedef struct sptp_paged_attn_prompt_args_s {
  * among the keys that are seen (zero keys and values).  workspace: at least
  * sptp_paged_attn_prompt_workspace_size(...), 256-byte aligned.
  * Numerics: scores, softmax statistics and sums in fp32, out rounded once.  bf16
- * and E4M3 caches: products on the tensor cores, weights rounded to bf16 (2^-8),
- * E4M3 keys and values (code times a power of two) exact in bf16.  fp32: nothing
- * rounded.
+ * and E4M3 caches: products on the tensor cores, weights rounded to bf16 (2^-8) and
+ * taken relative to a base within 2^16 of the largest (2^-110 of it and less: 0; values
+ * of v have to be below 2^111 over a row's keys), E4M3 keys and values (code times a
+ * power of two) exact in bf16.  fp32: nothing rounded.
  */
 int sptp_paged_attn_prompt(const sptp_paged_attn_prompt_args* args);
 

@@ -829,8 +829,8 @@ def sptp_paged_attn_prompt(q, cache, page_table, seq_lens, row_starts, scale=Non
     the rows of B sequences packed, sequence b's from row_starts[b] to
     row_starts[b+1] (int32 [B+1]); page_table int32 [B,max_pages]; seq_lens int32
     [B], the new rows' keys included.  A row at position pos sees its sequence's
-    keys up to pos, the last `window` of them if that is not 0, and the first
-    prefix_lens[b] (int32 [B]) whole.  Scores: cap tanh(scale q.k / cap) (cap 0:
+    keys up to pos, or up to prefix_lens[b] (int32 [B]) where that is more, from
+    pos + 1 - window on if window is not 0.  Scores: cap tanh(scale q.k / cap) (cap 0:
     none) - slopes[head] |pos - key| (slopes fp32 [P,Hq]); scale defaults to
     D^-1/2.  Rows of no sequence are left as they are (undefined in an output
     that is left out).  Returns (out [P,M,Hq*D], lse fp32 [P,M,Hq] or None)."""

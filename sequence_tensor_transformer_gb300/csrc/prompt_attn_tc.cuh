@@ -445,7 +445,6 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     __shared__ Cursor<TK, kItemCost> share_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    admit_next();
     if (tid == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&bars.full[s], C::CODES ? 4 : 1);
@@ -492,6 +491,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     tc_fence_before();
     bool bad = false;
     __syncthreads();
+    // Not before the tensor memory is this CTA's: a CTA of the next call's launch that came
+    // earlier could hold it while it waits for this launch to end.
+    admit_next();
     const Share share = find_share<kThreads>(p, warp_cost, &share_at, &bad);
     tc_fence_after();
     if (bad) bars.out_of_range = 1;

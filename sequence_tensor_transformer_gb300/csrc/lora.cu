@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
     extern __shared__ __align__(16) uint4 down_ring[];  // [STAGES][ITEMS][threads]: a thread's loads under way
     __shared__ __align__(16) float sums[kWarps / 2][16 * NT * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, i = lane & 3;
-    admit_next();
     await_previous();
     const int tiles = (p.M + 15) / 16;
     const int m0 = blockIdx.x % tiles * 16;
@@ -176,6 +175,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_bf16(const __grid_const
                     if (++slot == STAGES) slot = 0;
                 }
             }
+            // (the second launch's blocks only wait until this one is over, in room that its
+            // blocks could have: 3001 rows of rank 64 66 us when admitted first, and 63)
+            admit_next();
             for (int half = ways / 2; half > 0; half /= 2) {  // warps [half, 2 half) of a group to [0, half)
                 float* at = &sums[group * half + (sub < half ? sub : sub - half)][0] + lane * 2;
                 if (sub >= half && sub < 2 * half)
@@ -469,7 +471,6 @@ constexpr int kRowsF = 8;
 constexpr int kDownWarps = 2;  // of a block: few rows spread over the SMs
 __global__ void __launch_bounds__(32 * kDownWarps) lora_down_f32(const __grid_constant__ LoraParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    admit_next();
     await_previous();
     const int tiles = (p.M + kRowsF - 1) / kRowsF, parts = p.R / 8;
     long long unit = static_cast<long long>(blockIdx.x) * kDownWarps + warp;
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_f32(const __grid_co
     const int split = static_cast<int>(unit % p.splits), shard = static_cast<int>(unit / p.splits);
     if (shard >= (p.rowwise ? p.P : 1)) return;
     const Ids ids(p, m0, kRowsF);
+    admit_next();
     const int k0 = split * p.split_k, k1 = min(p.f, k0 + p.split_k);
     const float* x = static_cast<const float*>(p.x) + (static_cast<long long>(shard) * p.M + m0) * p.f;
     float* t = p.t + ((static_cast<long long>(split) * (p.rowwise ? p.P : 1) + shard) * p.M + m0) * p.R + r0;

@@ -3,6 +3,8 @@
 // (prompt_plan.cuh has the split, prompt_attn_{tc,f32} the main kernels).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "attn_scores.cuh"
 #include "prompt_attn.h"
 #include "sptp.h"
@@ -17,8 +19,8 @@ namespace {
 // Every part has an entry (its CTA and the slot there) and an entry kJoinBlocks
 // blocks, which all join the entry's item and take its rows in turn, so that one long
 // item (many parts) and many short ones spread over the SMs.  The loads of what other
-// SMs have just written take about a microsecond each: a warp has the parts of two
-// rows of up to kFew parts under way at once; a row of more is a warp's, or, of more
+// SMs have just written take about a microsecond each: a warp has the parts of four
+// rows of two parts under way at once, or of two of up to kFew; a row of more is a warp's, or, of more
 // than kAlone, the eight warps' of a block, their sums added in order.  The last block
 // sums up the CTAs' status words.
 constexpr int kJoinWarps = 8;
@@ -92,44 +94,56 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) prompt_join(const __grid_c
         const float f = pow2_approx(0.5f * (m - top));
         add_scaled(acc, f, make_float4(f * v.x, f * v.y, f * v.z, f * v.w));
     };
-    if (n <= kFew) {
+    // ROWS rows of up to PARTS parts, all their loads first
+    auto few = [&](auto parts, auto at_once) {
+        constexpr int PARTS = decltype(parts)::value, ROWS = decltype(at_once)::value;
 #pragma unroll 1
-        for (int r0 = first + warp * step; r0 < rows; r0 += 2 * step * kJoinWarps) {
+        for (int r0 = first + warp * step; r0 < rows; r0 += ROWS * step * kJoinWarps) {
 #pragma unroll 1
             for (int d = lane * 4; d < p.D; d += 128) {
-                float2 ml[2][kFew];
-                float4 v[2][kFew];
+                float2 ml[ROWS][PARTS];
+                float4 v[ROWS][PARTS];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int k = 0; k < kFew; ++k) {
-                        const int row = r0 + e * step * kJoinWarps;
-                        const bool is = row < rows && k < n;
-                        ml[e][k] = is ? p.part_ml[slot(row, k)] : make_float2(-INFINITY, 0.f);
-                        v[e][k] = is ? *reinterpret_cast<const float4*>(p.part_o + slot(row, k) * p.D + d)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < ROWS; ++e) {
                     const int row = r0 + e * step * kJoinWarps;
+                    const long long at = 2ll * it.first * p.part_rows + row;
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) {
+                        const bool is = row < rows && k < n;
+                        const long long s = at + max(2 * k, 1) * static_cast<long long>(p.part_rows);
+                        ml[e][k] = is ? p.part_ml[s] : make_float2(-INFINITY, 0.f);
+                        v[e][k] = is ? *reinterpret_cast<const float4*>(p.part_o + s * p.D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < ROWS; ++e) {
+                    const int row = r0 + e * step * kJoinWarps;
+                    if (row >= rows) break;
                     float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                    for (int k = 0; k < kFew; ++k) top = fmaxf(top, ml[e][k].x);
+                    for (int k = 0; k < PARTS; ++k) top = fmaxf(top, ml[e][k].x);
                     if (top == -INFINITY) top = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int k = 0; k < kFew; ++k) {
+                    for (int k = 0; k < PARTS; ++k) {
                         sum = fmaf(pow2_approx(ml[e][k].x - top), ml[e][k].y, sum);
                         add_part(acc, ml[e][k].x, top, v[e][k]);
                     }
-                    if (row >= rows) continue;
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    store4(static_cast<T*>(p.out) + out_row(row) * p.D + d,
+                    const long long orow = out_row(row);
+                    store4(static_cast<T*>(p.out) + orow * p.D + d,
                            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-                    if (p.lse != nullptr && d == 0) p.lse[out_row(row)] = lse(top, sum);
+                    if (p.lse != nullptr && d == 0) p.lse[orow] = lse(top, sum);
                 }
             }
         }
+    };
+    if (n <= 2) {
+        few(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+        return;
+    }
+    if (n <= kFew) {
+        few(std::integral_constant<int, kFew>(), std::integral_constant<int, 2>());
         return;
     }
     const bool shared = n > kAlone;

@@ -159,8 +159,9 @@ def set_library(handle):
         warnings.warn(f"{BINDING_PATH} cannot be loaded ({e}): build it anew (build.build()); until then a decoding "
                       "step's calls cost some microseconds more", RuntimeWarning, stacklevel=2)
         return
-    _decode_binding.use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
-        "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")))
+    for use, names in ((_decode_binding.use, ("sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")),
+                       (_decode_binding.use_batch, ("sptp_paged_attn_decode_ex", "sptp_paged_attn_prompt", "sptp_lora"))):
+        use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in names))
     _fast = _decode_binding
 
 
@@ -784,8 +785,11 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
     scores as in sptp_paged_attn_prompt.  Returns (out [P,B,Hq*D], lse fp32
     [P,B,Hq] or None).  Costs the host less with a workspace given and stream
     left out."""
-    if _fast is not None and stream is None and cap == 0.0 and slopes is None:
-        done = _fast.decode(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
+    if _fast is not None and stream is None:
+        if slopes is None and isinstance(cap, (int, float)) and cap == 0:
+            done = _fast.decode(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
+        else:
+            done = _fast.decode_ex(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse, cap, slopes)
         if done is not NotImplemented:
             return done
     P, B, Hq, D = q.shape
@@ -833,7 +837,13 @@ def sptp_paged_attn_prompt(q, cache, page_table, seq_lens, row_starts, scale=Non
     pos + 1 - window on if window is not 0.  Scores: cap tanh(scale q.k / cap) (cap 0:
     none) - slopes[head] |pos - key| (slopes fp32 [P,Hq]); scale defaults to
     D^-1/2.  Rows of no sequence are left as they are (undefined in an output
-    that is left out).  Returns (out [P,M,Hq*D], lse fp32 [P,M,Hq] or None)."""
+    that is left out).  Returns (out [P,M,Hq*D], lse fp32 [P,M,Hq] or None).
+    Costs the host less with a workspace given and stream left out."""
+    if _fast is not None and stream is None:
+        done = _fast.prompt(q, cache, page_table, seq_lens, row_starts, scale, window, cap, slopes, prefix_lens, out, lse,
+                            workspace, write_lse)
+        if done is not NotImplemented:
+            return done
     args, out, lse, workspace = _prompt_call(q, cache, page_table, seq_lens, row_starts, scale, window, cap, slopes, prefix_lens,
                                              out, lse, workspace, stream, write_lse)
     _check("sptp_paged_attn_prompt", lib().sptp_paged_attn_prompt(args))
@@ -922,7 +932,11 @@ def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=N
     none).  A [adapters,R,K], B [adapters,N,R], gains fp32 [adapters] or None.
     x [M,K] with base [P,M,N/P]: beside a column-parallel projection; x [P,M,K/P]
     with base [P,M,N]: beside a row-parallel one.  out may be base (in place).
-    Returns out."""
+    Returns out.  Costs the host less with a workspace given and stream left out."""
+    if _fast is not None and stream is None:
+        done = _fast.lora(x, A, B, ids, base, gains, out, workspace)
+        if done is not NotImplemented:
+            return done
     n, R, K = A.shape
     N, dtype = B.shape[1], x.dtype
     dt = _dtype_code(x)

@@ -1,5 +1,6 @@
 // Python entries of the calls of a decoding step: sptp_rope,
-// sptp_rope_append_kv and sptp_paged_attn_decode.
+// sptp_rope_append_kv, sptp_paged_attn_decode (with and without a cap or slopes),
+// sptp_paged_attn_prompt and sptp_lora.
 //
 // Those calls last 2 to 8 us on the device, and reading the shapes, types and
 // addresses of their 4 to 12 tensors one attribute at a time from Python takes
@@ -32,6 +33,9 @@ namespace {
 int (*rope_call)(const sptp_rope_args*) = nullptr;
 int (*append_call)(const sptp_rope_append_kv_args*) = nullptr;
 int (*decode_call)(const sptp_paged_attn_decode_args*) = nullptr;
+int (*decode_ex_call)(const sptp_paged_attn_decode_args*, float, const float*) = nullptr;
+int (*prompt_call)(const sptp_paged_attn_prompt_args*) = nullptr;
+decltype(&sptp_lora) lora_call = nullptr;
 
 struct Unfit {};  // thrown: not a call for these entries
 
@@ -150,13 +154,47 @@ struct Cache {
 };
 
 // Makes the call without the interpreter's lock: a full launch queue waits here.
-template <typename Args>
-void make(int (*call)(const Args*), Args& a) {
+template <typename F, typename... Args>
+void make(F call, Args... args) {
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = call(&a);
+    rc = call(args...);
     Py_END_ALLOW_THREADS;
     need(rc == SPTP_OK);
+}
+
+// The out and lse of an attention: (out, lse, write_lse) at o[0], o[1], o[2].
+struct Outs {
+    Out out;
+    PyObject* lse = nullptr;
+    float* lse_at = nullptr;
+
+    Outs(PyObject* o_out, PyObject* o_lse, PyObject* write, const at::Tensor& q, int P, int rows, int Hq, int D, int dev)
+        : out(o_out, q, q.scalar_type(), {P, rows, static_cast<int64_t>(Hq) * D}, dev) {
+        if (o_lse == Py_None && write == Py_False) {
+            lse = Py_NewRef(Py_None);
+        } else {
+            need(o_lse != Py_None || write == Py_True);
+            Out l(o_lse, q, at::kFloat, {P, rows, Hq}, dev);
+            lse_at = static_cast<float*>(l.at);
+            lse = l.object();
+        }
+    }
+    ~Outs() { Py_XDECREF(lse); }
+    PyObject* object() {
+        PyObject* l = lse;
+        lse = nullptr;
+        return Py_BuildValue("(NN)", out.object(), l);
+    }
+};
+
+// fp32 slopes [P][Hq], or none
+const float* slopes_of(PyObject* o, int P, int Hq, int dev) {
+    const at::Tensor* t = tensor_or_none(o);
+    if (t == nullptr) return nullptr;
+    need(t->scalar_type() == at::kFloat);
+    has_shape(*t, {P, Hq});
+    return data<const float>(*t, dev);
 }
 
 // (x, positions, turns, Hr, interleaved, transpose, gain, out)
@@ -182,7 +220,7 @@ PyObject* rope(PyObject* const* o) {
     Out out(o[7], x, x.scalar_type(), {a.P, a.M, a.H, a.D}, dev);
     a.out = out.at;
     a.cuda_stream = c10::cuda::getCurrentCUDAStream(dev).stream();
-    make(rope_call, a);
+    make(rope_call, &a);
     return out.object();
 }
 
@@ -228,11 +266,12 @@ PyObject* append(PyObject* const* o) {
     Out q(o[9], qkv, qkv.scalar_type(), {a.P, a.M, a.Hq, a.D}, dev);
     a.q_out = q.at;
     a.cuda_stream = c10::cuda::getCurrentCUDAStream(dev).stream();
-    make(append_call, a);
+    make(append_call, &a);
     return q.object();
 }
 
-// (q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse)
+// (q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse), and with EX (.., cap, slopes)
+template <bool EX>
 PyObject* decode(PyObject* const* o) {
     const at::Tensor &q = tensor(o[0]), &table = tensor(o[2]), &lens = tensor(o[3]), &ws = tensor(o[8]);
     const int dev = device_for(q);
@@ -262,26 +301,104 @@ PyObject* decode(PyObject* const* o) {
     a.seq_lens = data(lens, dev);
     a.workspace = data(ws, dev);
     a.ws_bytes = ws.nbytes();
-    Out out(o[6], q, q.scalar_type(), {a.P, a.B, static_cast<int64_t>(a.Hq) * a.D}, dev);
-    a.out = out.at;
-    PyObject* lse_object;
-    if (o[7] == Py_None && o[9] == Py_False) {
-        a.lse = nullptr;
-        lse_object = Py_NewRef(Py_None);
-    } else {
-        need(o[7] != Py_None || o[9] == Py_True);
-        Out lse(o[7], q, at::kFloat, {a.P, a.B, a.Hq}, dev);
-        a.lse = lse.at;
-        lse_object = lse.object();
-    }
+    const float cap = EX ? real(o[10]) : 0.f;
+    const float* slopes = EX ? slopes_of(o[11], a.P, a.Hq, dev) : nullptr;
+    Outs outs(o[6], o[7], o[9], q, a.P, a.B, a.Hq, a.D, dev);
+    a.out = outs.out.at;
+    a.lse = outs.lse_at;
     a.cuda_stream = c10::cuda::getCurrentCUDAStream(dev).stream();
-    try {
-        make(decode_call, a);
-    } catch (...) {
-        Py_DECREF(lse_object);
-        throw;
+    if constexpr (EX) {
+        need(decode_ex_call != nullptr);
+        make(decode_ex_call, &a, cap, slopes);
+    } else {
+        make(decode_call, &a);
     }
-    return Py_BuildValue("(NN)", out.object(), lse_object);
+    return outs.object();
+}
+
+// (q, cache, page_table, seq_lens, row_starts, scale, window, cap, slopes, prefix_lens, out, lse, workspace, write_lse)
+PyObject* prompt(PyObject* const* o) {
+    const at::Tensor &q = tensor(o[0]), &table = tensor(o[2]), &lens = tensor(o[3]), &starts = tensor(o[4]), &ws = tensor(o[12]);
+    const at::Tensor* prefixes = tensor_or_none(o[9]);
+    const int dev = device_for(q);
+    need(q.dim() == 4 && table.dim() == 2 && table.scalar_type() == at::kInt && lens.scalar_type() == at::kInt &&
+         starts.scalar_type() == at::kInt && prompt_call != nullptr);
+    sptp_paged_attn_prompt_args a;
+    a.P = size(q.size(0));
+    a.M = size(q.size(1));
+    a.Hq = size(q.size(2));
+    a.D = size(q.size(3));
+    a.B = size(table.size(0));
+    const Cache c(o[1], a.P, q.scalar_type(), dev);
+    need(c.D == a.D);
+    has_shape(lens, {a.B});
+    has_shape(starts, {a.B + 1ll});
+    if (prefixes != nullptr) {
+        need(prefixes->scalar_type() == at::kInt);
+        has_shape(*prefixes, {a.B});
+    }
+    a.Hkv = c.heads;
+    a.max_pages = size(table.size(1));
+    a.num_pages = c.num_pages;
+    a.page_size = c.page_size;
+    a.scale = o[5] == Py_None ? static_cast<float>(std::pow(a.D, -0.5)) : real(o[5]);
+    a.window = integer(o[6]);
+    a.cap = real(o[7]);
+    a.dtype = dtype_code(q);
+    a.kv_type = c.kv_type;
+    a.q = data(q, dev);
+    a.k_cache = c.k;
+    a.v_cache = c.v;
+    a.k_scale = c.k_scale;
+    a.v_scale = c.v_scale;
+    a.page_table = data(table, dev);
+    a.seq_lens = data(lens, dev);
+    a.row_starts = data(starts, dev);
+    a.prefix_lens = prefixes ? data(*prefixes, dev) : nullptr;
+    a.slopes = slopes_of(o[8], a.P, a.Hq, dev);
+    a.workspace = data(ws, dev);
+    a.ws_bytes = ws.nbytes();
+    Outs outs(o[10], o[11], o[13], q, a.P, a.M, a.Hq, a.D, dev);
+    a.out = outs.out.at;
+    a.lse = outs.lse_at;
+    a.cuda_stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+    make(prompt_call, &a);
+    return outs.object();
+}
+
+// (x, A, B, ids, base, gains, out, workspace)
+PyObject* lora(PyObject* const* o) {
+    const at::Tensor &x = tensor(o[0]), &A = tensor(o[1]), &B = tensor(o[2]), &ids = tensor(o[3]), &base = tensor(o[4]),
+                     &ws = tensor(o[7]);
+    const at::Tensor* gains = tensor_or_none(o[5]);
+    const int dev = device_for(x);
+    const at::ScalarType type = x.scalar_type();
+    need((x.dim() == 2 || x.dim() == 3) && A.dim() == 3 && B.dim() == 3 && base.dim() == 3 && lora_call != nullptr);
+    need(A.scalar_type() == type && B.scalar_type() == type && base.scalar_type() == type && ids.scalar_type() == at::kInt);
+    const bool rowwise = x.dim() == 3;
+    const int adapters = size(A.size(0)), R = size(A.size(1)), K = size(A.size(2)), N = size(B.size(1));
+    const int P = size(base.size(0)), M = size(x.size(x.dim() - 2));
+    need(P >= 1 && (rowwise ? K : N) % P == 0);
+    const int n = rowwise ? N : N / P;
+    has_shape(B, {adapters, N, R});
+    has_shape(ids, {M});
+    has_shape(base, {P, M, n});
+    if (rowwise)
+        has_shape(x, {P, M, K / P});
+    else
+        has_shape(x, {M, K});
+    if (gains != nullptr) {
+        need(gains->scalar_type() == at::kFloat);
+        has_shape(*gains, {adapters});
+    }
+    const sptp_dtype dtype = static_cast<sptp_dtype>(dtype_code(x));
+    void *xp = data(x, dev), *Ap = data(A, dev), *Bp = data(B, dev), *bp = data(base, dev), *wp = data(ws, dev);
+    const int* ip = data<const int>(ids, dev);
+    const float* gp = gains ? data<const float>(*gains, dev) : nullptr;
+    Out out(o[6], x, type, {P, M, n}, dev);
+    make(lora_call, xp, Ap, Bp, ip, gp, P, M, K, N, R, adapters, rowwise ? 1 : 0, dtype, bp, out.at, wp, ws.nbytes(),
+         static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+    return out.object();
 }
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -296,21 +413,36 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NOTIMPLEMENTED;
 }
 
-// Addresses of the library's calls: (sptp_rope_packed, sptp_rope_append_kv_packed, sptp_paged_attn_decode_packed).
-PyObject* use(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    void* p[3];
+bool addresses(PyObject* const* args, Py_ssize_t n, void* (&p)[3]) {
     if (n != 3) {
         PyErr_SetString(PyExc_TypeError, "three addresses expected");
-        return nullptr;
+        return false;
     }
     for (int i = 0; i < 3; ++i)
         if ((p[i] = PyLong_AsVoidPtr(args[i])) == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address of 0");
-            return nullptr;
+            return false;
         }
+    return true;
+}
+
+// Addresses of the library's calls: (sptp_rope_packed, sptp_rope_append_kv_packed, sptp_paged_attn_decode_packed).
+PyObject* use(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    void* p[3];
+    if (!addresses(args, n, p)) return nullptr;
     rope_call = reinterpret_cast<decltype(rope_call)>(p[0]);
     append_call = reinterpret_cast<decltype(append_call)>(p[1]);
     decode_call = reinterpret_cast<decltype(decode_call)>(p[2]);
+    Py_RETURN_NONE;
+}
+
+// And of (sptp_paged_attn_decode_ex, sptp_paged_attn_prompt, sptp_lora).
+PyObject* use_batch(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    void* p[3];
+    if (!addresses(args, n, p)) return nullptr;
+    decode_ex_call = reinterpret_cast<decltype(decode_ex_call)>(p[0]);
+    prompt_call = reinterpret_cast<decltype(prompt_call)>(p[1]);
+    lora_call = reinterpret_cast<decltype(lora_call)>(p[2]);
     Py_RETURN_NONE;
 }
 
@@ -326,7 +458,11 @@ extern "C" PyMODINIT_FUNC PyInit__decode_binding() {
         {"use", method(use), METH_FASTCALL, nullptr},
         {"rope", method(entry<rope, 8>), METH_FASTCALL, nullptr},
         {"append", method(entry<append, 11>), METH_FASTCALL, nullptr},
-        {"decode", method(entry<decode, 10>), METH_FASTCALL, nullptr},
+        {"decode", method(entry<decode<false>, 10>), METH_FASTCALL, nullptr},
+        {"use_batch", method(use_batch), METH_FASTCALL, nullptr},
+        {"decode_ex", method(entry<decode<true>, 12>), METH_FASTCALL, nullptr},
+        {"prompt", method(entry<prompt, 14>), METH_FASTCALL, nullptr},
+        {"lora", method(entry<lora, 8>), METH_FASTCALL, nullptr},
         {nullptr, nullptr, 0, nullptr},
     };
     static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode_binding", nullptr, -1, methods};

@@ -194,3 +194,27 @@ def test_lora_binding_names_what_is_wrong(kw, error, text):
     a.update(kw)
     with pytest.raises(error, match=text):
         st.sptp_lora(**a)
+
+
+# ---------------------------------------------------------------- the extension module
+
+def test_the_extension_module_leaves_the_calls():
+    """Tensors on the host, wrong numbers of arguments, and addresses that are none."""
+    fast = st._fast
+    assert fast is not None
+    P, B, Hq, D = 2, 3, 4, 64
+    cache = (torch.zeros(P, 4, 2, 16, D, dtype=BF), torch.zeros(P, 4, 2, 16, D, dtype=BF), None, None)
+    q, ws = torch.zeros(P, B, Hq, D, dtype=BF), torch.zeros(4096, dtype=torch.uint8)
+    table, lens, starts = torch.zeros(B, 2, dtype=torch.int32), torch.zeros(B, dtype=torch.int32), torch.zeros(B + 1, dtype=torch.int32)
+    x, base = torch.zeros(5, 32), torch.zeros(2, 5, 8)
+    a, b, ids = torch.zeros(3, 8, 32), torch.zeros(3, 16, 8), torch.zeros(5, dtype=torch.int32)
+    assert fast.decode_ex(q, cache, table, lens, None, 0, None, None, ws, True, 1.0, None) is NotImplemented
+    assert fast.prompt(q, cache, table, lens, starts, None, 0, 0.0, None, None, None, None, ws, True) is NotImplemented
+    assert fast.lora(x, a, b, ids, base, None, None, ws) is NotImplemented
+    for call in (fast.decode_ex, fast.prompt, fast.lora):
+        for n in (0, 1, 8, 12, 14, 15):
+            assert call(*[None] * n) is NotImplemented
+    for addresses in ((), (1, 2), (0, 1, 2), ("a", 1, 2)):
+        with pytest.raises((TypeError, ValueError)):
+            fast.use_batch(*addresses)
+    st.set_library(st.lib())

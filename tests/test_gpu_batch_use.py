@@ -268,3 +268,114 @@ def test_another_sequences_nan_stays_there(kind):
         t[:, torch.from_numpy(c["table"][1]).cuda()] = 0xFF if kind == "e4m3" else float("nan")
     got, gl, _ = bc.call(c)
     assert torch.equal(got[:, :30], want[:, :30]) and torch.equal(gl[:, :30], wl[:, :30])
+
+
+# ---------------------------------------------------------------- the extension module
+
+def ways(name, call):
+    """The results of a call through the extension module, which has to take it, and without it."""
+    fast, results = st._fast, []
+    took = []
+
+    class Watch:
+        def __getattr__(self, n):
+            def made(*args):
+                done = getattr(fast, n)(*args)
+                took.append((n, done is not NotImplemented))
+                return done
+            return made
+
+    for module in (Watch(), None):
+        st._fast = module
+        try:
+            results.append([None if t is None else t.clone() for t in call()])
+        finally:
+            st._fast = fast
+    torch.cuda.synchronize()
+    assert took == [(name, True)]
+    for a, b in zip(*results):
+        assert (a is None) == (b is None)
+        assert a is None or (a.shape == b.shape and a.dtype == b.dtype and torch.equal(a.view(torch.uint8), b.view(torch.uint8)))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("given", [False, True])
+def test_the_extension_module_makes_the_same_calls(kind, given):
+    assert st._fast is not None
+    g = torch.Generator(device="cuda").manual_seed(3)
+    P, B, Hq, Hkv, D, page = 2, 3, 4, 2, 64, 16
+    dt = torch.float32 if kind == "fp32" else torch.bfloat16
+    cache = st.paged_kv_cache(P, 12, Hkv, page, D, dt, kind == "e4m3")
+    randn = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(dt)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for t in cache[:2]:
+        t.copy_(torch.randint(0, 100, t.shape, generator=g, device="cuda") if kind == "e4m3" else randn(*t.shape))
+    for t in cache[2:]:
+        if t is not None:
+            t.fill_(0.125)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(B, 4)
+    lens, starts, prefixes = ints(40, 5, 64), ints(0, 7, 9, 10), ints(0, 5, 12)
+    slopes = torch.rand(P, Hq, generator=g, device="cuda")
+    q1, q = randn(P, B, Hq, D), randn(P, 10, Hq, D)
+    ws = torch.empty(max(st.sptp_paged_attn_workspace_size(P, B, Hq, Hkv, D),
+                         st.sptp_paged_attn_prompt_workspace_size(P, 10, B, Hq, Hkv, D)), dtype=torch.uint8, device="cuda")
+    new = lambda *shape, dtype=dt: torch.empty(shape, dtype=dtype, device="cuda") if given else None
+    out1, lse1 = new(P, B, Hq * D), new(P, B, Hq, dtype=torch.float32)
+    out, lse = new(P, 10, Hq * D), new(P, 10, Hq, dtype=torch.float32)
+    for cap, bias, prefix in ((0.0, None, None), (20.0, None, prefixes), (0, slopes, prefixes), (20.0, slopes, None)):
+        for write in (True, False):
+            how = dict(scale=None if given else 0.2, window=0 if prefix is None else 17, cap=cap, slopes=bias, workspace=ws, write_lse=write)
+            ways("decode" if not cap and bias is None else "decode_ex",
+                 lambda: st.sptp_paged_attn_decode(q1, cache, table, lens, out=out1, lse=lse1, **how))
+            ways("prompt", lambda: st.sptp_paged_attn_prompt(q, cache, table, lens, starts, prefix_lens=prefix, out=out, lse=lse, **how))
+            assert st.sptp_read_device_status(ws) == 0
+    if kind == "e4m3":
+        return
+    a, b, ids, gains = randn(3, 8, 64), randn(3, 32, 8), ints(0, 2, -1, 1, 1, 2, 0, 0, 1, 2), torch.rand(3, generator=g, device="cuda")
+    for x, base in ((randn(10, 64), randn(P, 10, 16)), (randn(P, 10, 32), randn(P, 10, 32))):
+        lws = torch.empty(st.sptp_lora_workspace_size(P, 10, 64, 32, 8, x.dim() == 3), dtype=torch.uint8, device="cuda")
+        for gain in (None, gains):
+            ways("lora", lambda: [st.sptp_lora(x, a, b, ids, base, gain, torch.empty_like(base) if given else None, lws)])
+
+
+def test_the_extension_module_leaves_what_is_wrong():
+    P, M, Hq, D = 1, 4, 2, 64
+    cache = st.paged_kv_cache(P, 2, 1, 16, D, torch.bfloat16)
+    q = torch.zeros(P, M, Hq, D, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), torch.full((1,), 4, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    ws = torch.empty(st.sptp_paged_attn_prompt_workspace_size(P, M, 1, Hq, 1, D), dtype=torch.uint8, device="cuda")
+    prompt = lambda *a, **kw: st.sptp_paged_attn_prompt(*a, **{"workspace": ws, **kw})
+    x, base = torch.zeros(M, 64, device="cuda"), torch.zeros(1, M, 16, device="cuda")
+    a, b, ids = torch.zeros(1, 8, 64, device="cuda"), torch.zeros(1, 16, 8, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
+    lws = torch.empty(st.sptp_lora_workspace_size(1, M, 64, 16, 8), dtype=torch.uint8, device="cuda")
+    calls = [
+        lambda: prompt(q, cache, table, lens, starts[:1]),
+        lambda: prompt(q, cache, table, lens.long(), starts),
+        lambda: prompt(q, cache, table, lens, starts, cap=-1.0),
+        lambda: prompt(q, cache, table, lens, starts, cap=float("nan")),
+        lambda: prompt(q, cache, table, lens, starts, window=-1),
+        lambda: prompt(q, cache, table, lens, starts, slopes=torch.zeros(2, 1, device="cuda")),
+        lambda: prompt(q, cache, table, lens, starts, prefix_lens=lens.cpu()),
+        lambda: prompt(q, cache, table, lens, starts, out=q.view(P, M, Hq * D)),
+        lambda: prompt(q, cache, table, lens, starts, workspace=ws[:4096]),
+        lambda: prompt(q.transpose(1, 2), cache, table, lens, starts),
+        lambda: st.sptp_paged_attn_decode(q[:, :1].contiguous(), cache, table, lens, cap=-1.0, workspace=ws),
+        lambda: st.sptp_lora(x, a, b.bfloat16(), ids, base, workspace=lws),
+        lambda: st.sptp_lora(x, a, b, ids.long(), base, workspace=lws),
+        lambda: st.sptp_lora(x, a, b, ids, base, workspace=lws[:100]),
+        lambda: st.sptp_lora(x[:, :32], a, b, ids, base, workspace=lws),
+        lambda: st.sptp_lora(x, a, b, ids, base, out=base[:, :, :8], workspace=lws),
+    ]
+    for call in calls:
+        errors = []
+        fast = st._fast
+        for module in (fast, None):
+            st._fast = module
+            try:
+                with pytest.raises(Exception) as e:
+                    call()
+                errors.append((type(e.value), str(e.value)))
+            finally:
+                st._fast = fast
+        assert errors[0] == errors[1]

@@ -6,7 +6,7 @@
 // addresses of their 4 to 12 tensors one attribute at a time from Python takes
 // longer than that: rotation, append and attention cost 5.3, 7.5 and 9.4 us a
 // call that way and 2.5, 2.7 and 4.4 us this way, of which 1.4, 1.4 and 2.9 are
-// the launches.
+// the launches; prompts' attention 10.1 and 4.6, adapters 10.9 and 3.7.
 //
 // The entries here take only calls that are right as they stand: tensors of the
 // expected shapes and types, dense, on the current device.  Anything else, an

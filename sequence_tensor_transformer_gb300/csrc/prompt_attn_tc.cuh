@@ -560,22 +560,21 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                         p.lse[orow] = sm.l == 0.f ? -INFINITY : sm.m * 0.6931471805599453f + logf(sm.l);
                 }
 #pragma unroll 1
-                for (int c0 = 0; c0 < o_cols; c0 += 16) {
-                    uint32_t o[16];
+                for (int c0 = 0; c0 < o_cols; c0 += 32) {
+                    const int halves = c0 + 16 < o_cols ? 2 : 1;  // of 16 columns
+                    uint32_t o[2][16] = {};
                     if (a < b) {
-                        tmem_ld_16cols(o_at + c0, o);
+                        tmem_ld_16cols(o_at + c0, o[0]);
+                        if (halves == 2) tmem_ld_16cols(o_at + c0 + 16, o[1]);
                         tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0;
                     }
                     if (!in) continue;
 #pragma unroll
-                    for (int h = 0; h < 16; h += 8) {
+                    for (int h = 0; h < 32; h += 8) {
                         if (c0 + h >= p.D) break;
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[h + i]) * f;
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[h / 16][h % 16 + i]) * f;
                         if (whole) {
                             uint4 u = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                                  pack_bf16(v[6], v[7]));

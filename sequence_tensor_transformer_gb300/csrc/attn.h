@@ -44,6 +44,7 @@ enum : int {
     kWherePromptScores = 29,
     kWherePromptWeights = 30,
     kWherePromptOutputs = 31,
+    kWherePromptChecked = 32,
 };
 
 // ---------------------------------------------------------------- rotary positions, paged cache

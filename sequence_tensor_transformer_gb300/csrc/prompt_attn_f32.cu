@@ -13,6 +13,7 @@
 // wait for one another: 319 us instead of 305 for 2500 causal capped rows of 2 shards,
 // 8 heads of 64 on 2, and 4.29 ms instead of 4.33 behind 20000 cached keys (36 TFLOP/s).
 #include <atomic>
+#include <type_traits>
 
 #include "attn_scores.cuh"
 #include "prompt_plan.cuh"
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
 #pragma unroll
             for (int n = 0; n < NV; ++n) o[i][n][0] = o[i][n][1] = 0;
         }
+        const int all_lo = first_key(p, c.k.pos0 + c.k.n - 1), all_hi = end_key(c.k.pos0, c.k.prefix);  // every row sees
         // keys and values of tile t, zeros where no row sees one
         auto load = [&](int t) {
             const int key0 = c.key0() + t * kKeys;
@@ -205,28 +207,37 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
                 }
             }
             __syncwarp();  // the weights of a warp's rows are its own
-            for (int k = from & ~3; k < to; k += 4) {
-                ulonglong2 v[4][NV];
+            auto add_values = [&](auto masked) {
+                constexpr bool MASKED = decltype(masked)::value;
+                for (int k = from & ~3; k < to; k += 4) {
+                    ulonglong2 v[4][NV];
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int n = 0; n < NV; ++n)
-                        v[kk][n] = *reinterpret_cast<const ulonglong2*>(sv + (k + kk) * L::VS + n * 64 + tx * 4);
+                        for (int n = 0; n < NV; ++n)
+                            v[kk][n] = *reinterpret_cast<const ulonglong2*>(sv + (k + kk) * L::VS + n * 64 + tx * 4);
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float4 w = *reinterpret_cast<const float4*>(sw + (ty + STEP * i) * L::WS + k);
+                    for (int i = 0; i < R; ++i) {
+                        const float4 w = *reinterpret_cast<const float4*>(sw + (ty + STEP * i) * L::WS + k);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const float f = kk == 0 ? w.x : kk == 1 ? w.y : kk == 2 ? w.z : w.w;
-                        const uint64_t ff = pack2(f, f);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const float f = kk == 0 ? w.x : kk == 1 ? w.y : kk == 2 ? w.z : w.w;
+                            const uint64_t ff = pack2(f, f);
 #pragma unroll
-                        for (int n = 0; n < NV; ++n) {
-                            o[i][n][0] = fma2(ff, v[kk][n].x, o[i][n][0]);
-                            o[i][n][1] = fma2(ff, v[kk][n].y, o[i][n][1]);
+                            for (int n = 0; n < NV; ++n) {
+                                // (0 times what a row does not see need not be 0)
+                                if (MASKED && f == 0.f) continue;
+                                o[i][n][0] = fma2(ff, v[kk][n].x, o[i][n][0]);
+                                o[i][n][1] = fma2(ff, v[kk][n].y, o[i][n][1]);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (key0 < all_lo || key0 + kKeys > all_hi)
+                add_values(std::true_type());
+            else
+                add_values(std::false_type());
             __syncthreads();
             if (L::BUFFERS == 1 && t + 1 < r.here) load(t + 1);
         }

@@ -7,6 +7,7 @@ import torch
 import sequence_tensor_transformer_gb300 as st
 
 from batch_cases import arguments, call, check, ints, make, workspace
+from helpers import host_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -248,3 +249,46 @@ def test_a_tile_beyond_the_share_is_not_missed():
     st.sptp_paged_attn_prompt_wait_selftest(*args, out, ws, 1000)
     assert st.sptp_read_device_status(ws) == 0
     assert torch.equal(out, st.sptp_paged_attn_prompt(*args)[0])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 72, 128, 256])
+@pytest.mark.parametrize("rows,lens,window,prefix", [
+    ((300,), (300,), 0, None),            # every tile on the diagonal
+    ((40, 1, 33), (1500, 9, 9000), 0, None),  # masked tiles at the end only, parts to join
+    ((150, 20), (700, 64), 200, None),    # a window's lower edge too
+    ((90,), (400,), 16, None),            # windows smaller than a tile
+    ((120, 60), (500, 60), 0, (450, 30)),  # a prefix that reaches beyond some rows
+    ((50,), (20,), 0, None),              # rows that see nothing
+])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(kind, D, rows, lens, window, prefix):
+    """Infinities and NaN at keys that some rows of a sequence see and others do not: a
+    row's other elements, and other rows, keep their bits."""
+    P, Hq, Hkv, page = 2, 4, 2, 16
+    c = make(P, rows, lens, Hq, Hkv, D, page, kind, window=window, prefix=prefix)
+    out, lse, ws = call(c)
+    status = SHAPE if any(r > n for r, n in zip(rows, lens)) else 0
+    assert st.sptp_read_device_status(ws) == status
+    rng = np.random.default_rng(1)
+    want = host_f64(out).reshape(P, c["M"], Hq, D).copy()
+    v = c["cache"][1]
+    for b, n in enumerate(lens):
+        near = np.arange(max(0, n - rows[b]), n)  # keys of the new rows, of which some are not seen by all
+        keys = np.unique(np.concatenate([rng.choice(near, min(6, near.size), replace=False), [n - 1], rng.integers(0, n, 2)]))
+        for i, key in enumerate(keys):
+            for p in range(P):
+                h, d = int(rng.integers(Hkv)), int(rng.integers(D))
+                x = (np.inf, -np.inf, np.nan)[i % 3]
+                v[p, int(c["table"][b][key // page]), h, key % page, d] = x
+                for r in range(rows[b]):
+                    pos = n - rows[b] + r
+                    hi = 0 if pos < 0 else max(pos + 1, 0 if prefix is None else min(prefix[b], n))
+                    lo = max(0, pos + 1 - window) if window else 0
+                    if lo <= key < hi:
+                        with np.errstate(invalid="ignore"):
+                            want[p, int(c["starts"][b]) + r, h * 2: h * 2 + 2, d] += x
+    again, lse2, ws = call(c)
+    assert st.sptp_read_device_status(ws) == status
+    got = host_f64(again).reshape(want.shape)
+    assert np.array_equal(got, want, equal_nan=True), np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))[:5]
+    assert torch.equal(lse, lse2)

@@ -548,9 +548,8 @@ typedef struct sptp_paged_attn_prompt_args_s {
  * The work is split over rows, heads and keys, evenly over the SMs whatever the
  * lengths; the parts of a row are joined in a fixed order: equal inputs give
  * equal bits.  What the cache holds outside the keys that a sequence's rows see
- * does not matter, and in bf16 and fp32 neither does, for a row, what lies at keys
- * that it does not see.  E4M3: codes and scales of keys that some rows of a sequence
- * see and others do not have to be finite.
+ * does not matter, and neither does, for a row, what lies at keys that it does not
+ * see.  (E4M3: a code that is no number counts as 480.)
  * Recorded as SPTP_ERR_SHAPE in the workspace status words: a row start outside
  * [0, M] or below the one before it (the rows concerned are undefined); a length
  * outside [0, max_pages * page_size] (cut to it); more rows than keys (the rows

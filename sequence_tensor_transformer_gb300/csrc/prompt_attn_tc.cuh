@@ -95,7 +95,7 @@ struct Shape {
     static constexpr int BYTES = SCALES_AT + (CODES ? STAGES * TK * 4 : 0) + 1024;
     // warps: softmax, four for the others, four that convert codes
     static constexpr int PRODUCER = 4 * NQ, ISSUER = 4 * NQ + 1, CONVERTER = 4 * NQ + 4;
-    static constexpr int CHECKER = 4 * NQ + 2, CHECKERS = 2;  // bf16
+    static constexpr int SIFTER = 4 * NQ + 2, SIFTERS = 2;  // bf16
     static constexpr int WARPS = CONVERTER + (CODES ? 4 : 0);
     // tensor memory columns
     static constexpr int S = 128;                       // between the tiles' scores
@@ -444,9 +444,9 @@ struct Softmax {
 };
 
 // Adds, to a row of out (whole) or of the parts' outputs that this thread has written,
-// what is infinite or NaN among the values of keys [lo, hi) in masked tiles, which is
-// missing from its products.  Rare, so from global memory, key by key.
-template <int TK>
+// what is infinite or NaN among the values of keys [lo, hi) in masked tiles (E4M3: by
+// their scale), which is missing from its products.  Rare, so from global memory, key by key.
+template <int TK, bool CODES>
 __device__ __noinline__ void add_unfinite(const PromptParams& p, const Work& d, int lo, int hi, bool whole, long long row) {
     const int end = min(hi, d.key0 + d.here * TK);
     for (int key = max(lo, d.key0); key < end; ++key) {
@@ -457,9 +457,17 @@ __device__ __noinline__ void add_unfinite(const PromptParams& p, const Work& d, 
         }
         const long long from = pool_row(p, d.seq, d.shard, d.kvh, key);
         if (from < 0) continue;
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + from * p.D;
+        const float scale = CODES ? p.v_scale[from] : 1.f;
+        if (CODES && fabsf(scale) <= 3.4e38f) continue;
         for (int c = 0; c < p.D; ++c) {
-            const float x = __bfloat162float(v[c]);
+            float x;
+            if (CODES) {
+                const int code = static_cast<const uint8_t*>(p.v)[from * p.D + c];
+                x = (code & 0x7f) == 0 ? 0.f : code & 0x80 ? -1.f : 1.f;
+                x *= scale;
+            } else {
+                x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[from * p.D + c]);
+            }
             if (fabsf(x) <= 3.4e38f) continue;
             if (whole) {
                 __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * p.D + c;
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&bars.full[s], C::CODES ? 4 : 1);
             mbar_init(&bars.empty[s], 1);
-            mbar_init(&bars.checked[s], C::CHECKERS);
+            mbar_init(&bars.checked[s], C::SIFTERS);
         }
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars.c_full[s], 1 + 32);
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         mbar_init(&bars.drain, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bars.w_full[i], 1);
-            mbar_init(&bars.w_empty[i], 4 * NQ + 1 + (C::CODES ? 4 : C::CHECKERS));
+            mbar_init(&bars.w_empty[i], 4 * NQ + 1 + (C::CODES ? 4 : C::SIFTERS));
         }
         fence_mbar_init();
         bars.abort_flag = 0;
@@ -626,8 +634,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                         }
                     }
                 }
-                if (!C::CODES && in && *const_cast<const volatile int*>(&d.unfinite))
-                    add_unfinite<TK>(p, d, sm.lo, sm.hi, whole, whole ? orow : at);
+                if (in && *const_cast<const volatile int*>(&d.unfinite))
+                    add_unfinite<TK, C::CODES>(p, d, sm.lo, sm.hi, whole, whole ? orow : at);
                 // the outputs are read before the next item's products (issued behind
                 // this warp's next arrival) write there
                 tc_fence_before();
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         bool ok = true;
         while (ok) {
             if (!warp_sleep(&bars.w_full[w], w_phase, wc, kWherePromptItem, -2)) break;
-            const Work& d = bars.work[w];
+            Work& d = bars.work[w];
             if (d.flags & kStop) break;
             const int tiles = 2 * d.here;
             for (int i = 0; i < tiles; ++i) {
@@ -666,7 +674,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 uint8_t* out = slots + slot * C::SLOT + row * 128;
                 const float f = scales[stage * TK + row];
                 const __nv_bfloat162 f2 = __floats2bfloat162_rn(f, f);
-                const bool seen = row >= from && row < to;
+                bool seen = row >= from && row < to;
+                if ((i & 1) && seen && !(fabsf(f) <= 3.4e38f) && d.masked(key0, TK)) {
+                    d.unfinite = 1;  // (see the warps that look through bf16 tiles)
+                    seen = false;
+                }
 #pragma unroll 4
                 for (int c = first; c < chunks; c += PARTS) {
                     const uint4 u = *reinterpret_cast<const uint4*>(in + c / PER * (TK * C::SPAN) + (((c % PER) ^ swizzle) << 4));
@@ -952,13 +964,13 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             WaitCtx drain{&bars.status, &local_abort, p.wait_limit_ns};
             issue_commit(&bars.drain);
             warp_sleep(&bars.drain, 0, drain, kWhereDrain, -1);
-        } else if (!C::CODES && warp >= C::CHECKER) {
+        } else if (!C::CODES && warp >= C::SIFTER) {
             // -------------------------------------------------- masked tiles of V
             // A weight is 0 where a row does not see a key, and 0 times what lies there may
             // not be: values that no row of the item sees become zeros, and so does what is
             // infinite or NaN among those that some rows see; the softmax warps then give it
-            // to those rows.  (E4M3: the converters clear the former; codes and scales are
-            // finite.)  All of a batch's loads go before their use: with a load and a branch
+            // to those rows.  (E4M3: the converters do the same by a row's scale.)  All of a
+            // batch's loads go before their use: with a load and a branch
             // at a time, by one warp, 16384 plain rows took 1.68 ms instead of 1.43.
             int slot = 0, w = 0;
             uint32_t phase = 0, w_phase = 0;
@@ -983,11 +995,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                         // the sign bit of each half whose exponent is all ones
                         auto ones = [](uint32_t v) { return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
                         auto odd = [&](const uint4& u) { return ones(u.x) | ones(u.y) | ones(u.z) | ones(u.w); };
-                        constexpr int BATCH = 8, STRIDE = 32 * C::CHECKERS;
+                        constexpr int BATCH = 8, STRIDE = 32 * C::SIFTERS;
                         static_assert(TK * C::CB * 8 % (BATCH * STRIDE) == 0, "whole batches");
                         uint4* tile = reinterpret_cast<uint4*>(slots + slot * C::SLOT);
 #pragma unroll 1
-                        for (int i = (warp - C::CHECKER) * 32 + lane; i < TK * C::CB * 8; i += BATCH * STRIDE) {
+                        for (int i = (warp - C::SIFTER) * 32 + lane; i < TK * C::CB * 8; i += BATCH * STRIDE) {
                             uint4 u[BATCH];
 #pragma unroll
                             for (int e = 0; e < BATCH; ++e) u[e] = tile[i + e * STRIDE];

@@ -292,3 +292,31 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(kind, D, ro
     got = host_f64(again).reshape(want.shape)
     assert np.array_equal(got, want, equal_nan=True), np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))[:5]
     assert torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows,lens,window", [((300,), (300,), 0), ((40, 33), (1500, 9000), 0), ((150, 20), (700, 64), 200)])
+def test_scales_that_are_not_finite_stay_with_the_rows_that_see_them(D, rows, lens, window):
+    """The same for the scales of an E4M3 cache's values, and of its keys beyond a row's position."""
+    P, Hq, Hkv, page = 2, 4, 2, 16
+    c = make(P, rows, lens, Hq, Hkv, D, page, "e4m3", window=window)
+    out, lse, ws = call(c)
+    assert st.sptp_read_device_status(ws) == 0
+    rng = np.random.default_rng(2)
+    want = host_f64(out).reshape(P, c["M"], Hq, D).copy()
+    for b, n in enumerate(lens):
+        keys = np.unique(np.concatenate([rng.integers(n - rows[b], n, 3), [n - 1], rng.integers(0, n, 1)]))
+        for i, key in enumerate(keys):
+            h, at = int(rng.integers(Hkv)), (int(c["table"][b][key // page]), int(key % page))
+            bad = (np.inf, np.nan)[i % 2]
+            c["cache"][3][1, at[0], h, at[1]] = bad
+            for r in range(rows[b]):
+                pos = n - rows[b] + r
+                if max(0, pos + 1 - window if window else 0) <= key <= pos:
+                    with np.errstate(invalid="ignore"):
+                        want[1, int(c["starts"][b]) + r, h * 2: h * 2 + 2] += c["v64"][1, at[0], h, at[1]] * bad
+    again, lse2, ws = call(c)
+    assert st.sptp_read_device_status(ws) == 0
+    got = host_f64(again).reshape(want.shape)
+    assert np.array_equal(got, want, equal_nan=True), np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))[:5]
+    assert torch.equal(lse, lse2)

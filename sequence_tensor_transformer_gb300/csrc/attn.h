@@ -45,6 +45,7 @@ enum : int {
     kWherePromptWeights = 30,
     kWherePromptOutputs = 31,
     kWherePromptChecked = 32,
+    kWherePromptMasked = 33,
 };
 
 // ---------------------------------------------------------------- rotary positions, paged cache

@@ -228,7 +228,8 @@ template <class C>
 struct Bars {
     uint64_t c_full[C::STAGES], c_empty[C::STAGES];  // E4M3: tiles of codes
     uint64_t full[C::SLOTS], empty[C::SLOTS];  // K and V tiles
-    uint64_t checked[C::SLOTS];                // bf16: masked tiles of V
+    uint64_t masked[C::SLOTS];                 // bf16: a masked tile of V is on its way there
+    uint64_t checked[C::SLOTS];                // and has been looked through
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];                        // scores in tensor memory (and all products before them done)
     uint64_t p_ready[2];                       // weights there, outputs rescaled (a warp each)
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&bars.full[s], C::CODES ? 4 : 1);
             mbar_init(&bars.empty[s], 1);
+            mbar_init(&bars.masked[s], 1);
             mbar_init(&bars.checked[s], C::SIFTERS);
         }
         for (int s = 0; s < C::STAGES; ++s) {
@@ -793,8 +795,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                     }
                     return pool + page * pages_rows + key - index * p.page_size;
                 };
-                // a tile's boxes, and an E4M3 tile's scales
-                auto load = [&](const CUtensorMap* map, const float* scale, int row) {
+                // a tile's boxes, and an E4M3 tile's scales; sift: a masked tile of V
+                auto load = [&](const CUtensorMap* map, const float* scale, int row, bool sift) {
                     constexpr int kSlots = C::CODES ? C::STAGES : C::SLOTS;
                     uint64_t* full = C::CODES ? &bars.c_full[slot] : &bars.full[slot];
                     if (!warp_sleep(C::CODES ? &bars.c_empty[slot] : &bars.empty[slot], phase, wc, kWhereKvEmpty, issued)) return false;
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                     const bool skip = TEST && blockIdx.x == 0 && issued == p.withhold_full;
                     constexpr int kBoxes = C::CODES ? C::CODE_BOXES : C::CB, kSpan = C::CODES ? C::SPAN : 128;
                     if (lane == 0 && !skip) mbar_arrive_expect_tx(full, __popc(loads) * R * kSpan * kBoxes);
+                    if (!C::CODES && lane == 0 && sift) mbar_arrive(&bars.masked[slot]);
                     __syncwarp();
                     // lane: box lane % nb of column lane / nb
                     const int box = lane % nb, cb = lane / nb;
@@ -830,7 +833,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                 int row = row_of(d.here - 1), next;
                 for (int j = d.here - 1; j >= 0; --j) {
                     next = row_of(j - 1);
-                    if (!(ok = load(&p.map_k, p.k_scale, row))) break;
+                    if (!(ok = load(&p.map_k, p.k_scale, row, false))) break;
                     if (j == d.here - 1) {
                         for (int t = 0; t < NQ && ok; ++t) {
                             if (d.a[t] == d.b[t]) continue;
@@ -848,7 +851,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                         }
                         if (!ok) break;
                     }
-                    if (!(ok = load(&p.map_v, p.v_scale, row))) break;
+                    if (!(ok = load(&p.map_v, p.v_scale, row, d.masked(d.key0 + j * TK, TK)))) break;
                     row = next;
                 }
                 if (ok) more = c.next_item(p, numbers);
@@ -972,8 +975,13 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             // to those rows.  (E4M3: the converters do the same by a row's scale.)  All of a
             // batch's loads go before their use: with a load and a branch
             // at a time, by one warp, 16384 plain rows took 1.68 ms instead of 1.43.
+            // These warps pass over the tiles that every row sees, up to a whole item of them,
+            // and a wait tells a phase of a barrier from the next one only.  So the wait for
+            // a tile comes behind one for the producer's word that it is on its way, which it
+            // gives once the slot's last tile is used up; a slot has no other such word until this
+            // tile is checked.
             int slot = 0, w = 0;
-            uint32_t phase = 0, w_phase = 0;
+            uint32_t phase = 0, w_phase = 0, sifted = 0;  // sifted: bit s, phase of masked[s]
             bool ok = true;
             auto next_slot = [&] {
                 if (++slot == C::SLOTS) {
@@ -990,6 +998,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
                     next_slot();  // K
                     const int key = d.key0 + j * TK;
                     if (d.masked(key, TK)) {
+                        if (!(ok = warp_sleep(&bars.masked[slot], sifted >> slot & 1u, wc, kWherePromptMasked, j))) break;
+                        sifted ^= 1u << slot;
                         if (!(ok = warp_sleep(&bars.full[slot], phase, wc, kWhereKvFull, j))) break;
                         const int from = d.lo - key, to = d.hi - key;
                         // the sign bit of each half whose exponent is all ones

@@ -4,7 +4,7 @@
 namespace sptp {
 
 cudaError_t launch_prompt_e4m3(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
-    return prompt::launch_width<true, false, false>(p, num_sms, ctas, s);
+    return prompt::launch_width<true, prompt::kNoCap, false>(p, num_sms, ctas, s);
 }
 
 }  // namespace sptp

@@ -4,7 +4,7 @@
 namespace sptp {
 
 cudaError_t launch_prompt_e4m3_bias(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
-    return prompt::launch_width<true, false, true>(p, num_sms, ctas, s);
+    return prompt::launch_width<true, prompt::kNoCap, true>(p, num_sms, ctas, s);
 }
 
 }  // namespace sptp

@@ -7,8 +7,8 @@ namespace sptp {
 
 cudaError_t launch_prompt_test(PromptParams& p, bool e4m3, int* ctas, cudaStream_t s) {
     using namespace prompt;
-    return e4m3 ? launch_tc<Shape<128, true>, false, false, true>(p, kSelftestCtas, ctas, s)
-                : launch_tc<Shape<128, false>, false, false, true>(p, kSelftestCtas, ctas, s);
+    return e4m3 ? launch_tc<Shape<128, true>, kNoCap, false, true>(p, kSelftestCtas, ctas, s)
+                : launch_tc<Shape<128, false>, kNoCap, false, true>(p, kSelftestCtas, ctas, s);
 }
 
 }  // namespace sptp

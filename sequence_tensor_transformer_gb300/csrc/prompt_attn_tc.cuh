@@ -57,6 +57,8 @@ constexpr int kItems = 4;      // descriptions under way
 // 1.435 and 1.437 ms with costs of 2, 2.5 and 3; pieces of nine prompts 400, 402 and 406 us).
 constexpr int kItemCost = 5 * kTileCost / 2;
 constexpr float kPlainCap = 128.f;  // up to here 2^-22 of the cap is no more than a score is off by itself
+// No cap; one up to kPlainCap; one above it, or so far from the scale that scale / cap is no normal number
+enum CapForm : int { kNoCap, kCap, kWideCap };
 
 enum : int { kBegins = 1, kEnds = 2, kStop = 4 };
 
@@ -250,7 +252,7 @@ __host__ __device__ constexpr float tanh_term(int i) {
     return i == 0 ? 0.999999986872f : i == 1 ? -0.333330693943f : i == 2 ? 0.133247793204f : i == 3 ? -0.0529860754004f : 0.0171350067528f;
 }
 
-template <class C, bool CAP, bool BIAS>
+template <class C, CapForm CAP, bool BIAS>
 struct Softmax {
     static constexpr int TK = C::TK;
 
@@ -270,12 +272,17 @@ struct Softmax {
         s[j + 1] = f.y;
     }
 
-    // The cap, cap tanh(s / cap), of 32 scores that also still lie at s_at.  Where no
-    // |score| of the warp's rows passes half the cap, three of four by a series on the
-    // fused multiply-adds (7 of them each), the rest on the function unit (an
-    // exponential and a reciprocal), so that both units have their share.
+    // The cap, cap tanh(s / cap), of 32 scores that also still lie at s_at.
+    // kCap: where no |score| of the warp's rows passes half the cap, three of four by a
+    // series on the fused multiply-adds (7 of them each), the rest on the function unit (an
+    // exponential and a reciprocal), so that both units have their share; else all of them
+    // there.  The function unit's are off by 2^-22 of the cap.
+    // kWideCap: up to half the cap the series for all of them, as a factor of the score, so
+    // that they are off by 2^-22 of the score however large the cap is.  (In one kernel
+    // with the other, 16384 rows with a cap of 50 took 2.46 ms instead of 2.34: more
+    // instructions to fetch.)
     __device__ __forceinline__ void apply_cap(const PromptParams& p, const ScoreCap& cap, float (&s)[N], uint32_t s_at) {
-        const float to_u = to_log2 * cap.inv;
+        const float to_u = to_log2 * cap.inv;  // (kWideCap: may be 0 or infinite)
         // cap - 2 cap / (1 + e^(2 s / cap)): off by 2^-22 of the cap
         auto by_units = [&](int j) {
             const float2 x = split2(mul2(at(s, j), both(to_log2 * cap.twice)));
@@ -283,11 +290,14 @@ struct Softmax {
             put(s, j, fma2(pair2(reciprocal_approx(d.x), reciprocal_approx(d.y)), both(-2.f * cap.cap), both(cap.cap)));
         };
         auto by_series = [&](int j) {
-            const uint64_t u = mul2(at(s, j), both(to_u)), v = mul2(u, u);
-            uint64_t y = both(tanh_term(4) * cap.cap);
+            // kCap: u = s / cap times the series times the cap; kWideCap: s times the series
+            const uint64_t x = mul2(at(s, j), both(CAP == kWideCap ? to_log2 : to_u));
+            const uint64_t u = CAP == kWideCap ? mul2(x, both(cap.inv)) : x, v = mul2(u, u);
+            const float unit = CAP == kWideCap ? 1.f : cap.cap;
+            uint64_t y = both(tanh_term(4) * unit);
 #pragma unroll
-            for (int i = 3; i >= 0; --i) y = fma2(y, v, both(tanh_term(i) * cap.cap));
-            put(s, j, mul2(u, y));
+            for (int i = 3; i >= 0; --i) y = fma2(y, v, both(tanh_term(i) * unit));
+            put(s, j, mul2(x, y));
         };
         float most[4];
 #pragma unroll
@@ -300,16 +310,16 @@ struct Softmax {
         for (int i = 0; i < 4; ++i) most[i] = fmaxf(most[i], fabsf(s[28 + i]));
         const float all = max3(most[0], most[1], fmaxf(most[2], most[3]));
         // (of rows that a token has: what the others hold must not choose the arithmetic)
-        const bool far = __any_sync(0xffffffffu, in && all * fabsf(to_u) > 0.5f);
+        const bool far = __any_sync(0xffffffffu, in && !(all * fabsf(to_u) <= 0.5f));
         if (!far) {
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
-                if (j % 8 == 2 && N == 32)
+                if (CAP == kCap && j % 8 == 2)
                     by_units(j);
                 else
                     by_series(j);
             }
-        } else if (p.cap <= kPlainCap) {
+        } else if constexpr (CAP == kCap) {
 #pragma unroll
             for (int j = 0; j < N; j += 2) by_units(j);
         } else {
@@ -390,7 +400,7 @@ struct Softmax {
             // bit j: key j of the 32 is seen
             const int from = max(lo - key, 0), to = min(max(hi - key, 0), N);
             const uint32_t seen = from >= to ? 0u : (0xffffffffu >> (32 - (to - from))) << from;
-            if constexpr (CAP) {
+            if constexpr (CAP != kNoCap) {
                 if (masked) {  // (nor must what lies where no key is)
 #pragma unroll
                     for (int j = 0; j < N; ++j) s[j] = seen >> j & 1u ? s[j] : 0.f;
@@ -480,7 +490,7 @@ __device__ __noinline__ void add_unfinite(const PromptParams& p, const Work& d, 
     }
 }
 
-template <class C, bool CAP, bool BIAS, bool TEST = false>
+template <class C, CapForm CAP, bool BIAS, bool TEST = false>
 __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __grid_constant__ PromptParams p) {
     constexpr int TK = C::TK, NQ = C::NQ, kThreads = 32 * C::WARPS;
     extern __shared__ uint8_t smem_raw[];
@@ -1068,7 +1078,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
 
 namespace {  // internal: a process may load the library and its checked build, each with `done` of its own
 
-template <class C, bool CAP, bool BIAS, bool TEST = false>
+template <class C, CapForm CAP, bool BIAS, bool TEST = false>
 cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     plan_prompt(p, C::NQ * kTileRows, kTileRows);
     // the largest boxes that never cross a page
@@ -1095,12 +1105,19 @@ cudaError_t launch_tc(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     return launch_after(prompt_tc_kernel<C, CAP, BIAS, TEST>, *ctas, 32 * C::WARPS, C::BYTES, s, p);
 }
 
-// By row width.
-template <bool CODES, bool CAP, bool BIAS>
+// By row width, and the form of the cap.
+template <bool CODES, CapForm CAP, bool BIAS>
 cudaError_t launch_width(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
     if (p.D <= 64) return launch_tc<Shape<64, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
     if (p.D <= 128) return launch_tc<Shape<128, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
     return launch_tc<Shape<256, CODES>, CAP, BIAS>(p, num_sms, ctas, s);
+}
+
+template <bool CODES, bool BIAS>
+cudaError_t launch_cap(PromptParams& p, int num_sms, int* ctas, cudaStream_t s) {
+    const float to_u = fabsf(p.scale / p.cap);
+    return p.cap <= kPlainCap && to_u > 1e-30f && to_u < 1e30f ? launch_width<CODES, kCap, BIAS>(p, num_sms, ctas, s)
+                                                                : launch_width<CODES, kWideCap, BIAS>(p, num_sms, ctas, s);
 }
 
 }  // namespace

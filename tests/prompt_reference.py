@@ -45,8 +45,9 @@ def reference(c, rows_at_once=1024):
                     yield p, h, m, w @ V, lse, w @ V.abs(), sizes
 
 
-def compare(c, out, lse):
-    """batch_cases.check against `reference`."""
+def compare(c, out, lse, cap_error=None):
+    """batch_cases.check against `reference`.  cap_error: how far the cap may put a score off,
+    from the largest sum of |scale q_i k_ji|, instead of score_error's part of the cap."""
     P, M, Hq, D = c["P"], c["M"], c["Hq"], c["D"]
     out, untouched = out.view(P, M, Hq, D), torch.ones(M, dtype=torch.bool, device="cuda")
     for p, h, m, ref, rl, mean, (dots, far, keys) in reference(c):
@@ -54,7 +55,9 @@ def compare(c, out, lse):
         untouched[rows] = False
         got, gl = out[p, rows, h].double(), lse[p, rows, h].double()
         assert not got.isnan().any() and not gl.isnan().any()
-        es = score_error(D, dots, far, c["cap"]) + keys * 2.0 ** -24
+        es = score_error(D, dots, far, 0.0 if cap_error else c["cap"]) + keys * 2.0 ** -24
+        if cap_error:
+            es += cap_error(dots)
         rounded = 0.0 if c["kind"] == "fp32" else 2.0 ** -8
         tol = (rounded + 2 * es)[:, None] * mean + HALF[c["dtype"]] * ref.abs() * (1 + 2.0 ** -7)
         off = (got - ref).abs()

@@ -22,7 +22,7 @@ namespace {
 // SMs have just written take about a microsecond each: a warp has the parts of four
 // rows of two parts under way at once, or of two of up to kFew; a row of more is a warp's, or, of more
 // than kAlone, the eight warps' of a block, their sums added in order.  The last block
-// sums up the CTAs' status words.
+// looks through the sequences' rows and lengths and sums up the CTAs' status words.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinBlocks = 4;
 constexpr int kFew = 4;
@@ -54,10 +54,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) prompt_join(const __grid_c
     admit_next();
     await_previous();
     if (blockIdx.x == ctas * 2 * kJoinBlocks) {
-        // the first CTA that failed; if none did, the first that met an index outside its range
-        __shared__ int first_bad, first_failed;
-        if (threadIdx.x == 0) first_bad = first_failed = ctas;
+        // the first CTA that failed; if none did, the first sequence whose rows or length are outside
+        // their range (every one is looked at: the main kernel's numbers of blocks pass over
+        // some where row starts descend), or the first CTA that met a page outside
+        __shared__ int first_bad, first_failed, first_sequence;
+        if (threadIdx.x == 0) {
+            first_bad = first_failed = ctas;
+            first_sequence = p.B;
+        }
         __syncthreads();
+        const int most = p.max_pages * p.page_size;
+        for (int b = threadIdx.x; b < p.B; b += kJoinWarps * 32) {
+            const int s = __ldg(p.row_starts + b), e = __ldg(p.row_starts + b + 1), len = __ldg(p.seq_lens + b);
+            if (s < 0 || e > p.M || e < s || len < 0 || len > most || e - s > len) atomicMin(&first_sequence, b);
+        }
         for (int c = threadIdx.x; c < ctas; c += kJoinWarps * 32) {
             const int status = p.parts[c].status;
             if (status != 0) atomicMin(&first_bad, c);
@@ -67,7 +77,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) prompt_join(const __grid_c
         if (threadIdx.x == 0) {
             DeviceStatus st = {0, 0, 0, 0, 0};
             const int at = first_failed < ctas ? first_failed : first_bad;
-            if (at < ctas) {
+            if (first_failed == ctas && first_sequence < p.B) {
+                st.code = SPTP_ERR_SHAPE;
+                st.where = kWhereKvPage;
+                st.info = first_sequence;
+            } else if (at < ctas) {
                 st.code = p.parts[at].status;
                 st.where = p.parts[at].where;
                 st.block = at;

@@ -73,9 +73,7 @@ __global__ void __launch_bounds__(kThreads, F32Smem<DP>::CTAS) prompt_f32_kernel
     admit_next();
     if (tid == 0) bad_at = bad_any = 0;
     await_previous();
-    bool bad = false;
-    const Share share = find_share<kThreads>(p, warp_cost, &share_at, &bad);
-    if (bad) bad_any = 1;
+    const Share share = find_share<kThreads>(p, warp_cost, &share_at);
     PromptPart* part = p.parts + blockIdx.x;
     if (tid == 0) part->items[0].parts = part->items[1].parts = 0;
     const long long numbers = block_numbers(p);

@@ -549,14 +549,12 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
     }
     await_previous();
     tc_fence_before();
-    bool bad = false;
     __syncthreads();
     // Not before the tensor memory is this CTA's: a CTA of the next call's launch that came
     // earlier could hold it while it waits for this launch to end.
     admit_next();
-    const Share share = find_share<kThreads>(p, warp_cost, &share_at, &bad);
+    const Share share = find_share<kThreads>(p, warp_cost, &share_at);
     tc_fence_after();
-    if (bad) bars.out_of_range = 1;
     const uint32_t tmem = bars.tmem;
     WaitCtx wc{&bars.status, &bars.abort_flag, p.wait_limit_ns};
     PromptPart* part = p.parts + blockIdx.x;

@@ -49,14 +49,12 @@ __device__ __forceinline__ int first_key(const PromptParams& p, int pos) {
 __device__ __forceinline__ int end_key(int pos, int prefix) { return pos < 0 ? 0 : max(pos + 1, prefix); }
 
 template <int TK>
-__device__ __forceinline__ Block block_of(const PromptParams& p, long long number, int b, bool* bad) {
+__device__ __forceinline__ Block block_of(const PromptParams& p, long long number, int b) {
     Block k;
     k.b = b;
-    const int raw0 = __ldg(p.row_starts + b), raw1 = __ldg(p.row_starts + b + 1), raw_len = __ldg(p.seq_lens + b);
-    const int s = max(0, min(p.M, raw0)), e = max(s, min(p.M, raw1));
-    const int most = p.max_pages * p.page_size;
-    if (raw0 < 0 || raw1 > p.M || raw1 < raw0 || raw_len < 0 || raw_len > most || raw1 - raw0 > raw_len) *bad = true;
-    k.len = max(0, min(raw_len, most));
+    // (what is outside its range is cut to it here, and reported by the join)
+    const int s = row_start(p, b), e = max(s, row_start(p, b + 1));
+    k.len = max(0, min(p.max_pages * p.page_size, __ldg(p.seq_lens + b)));
     k.prefix = p.prefix_lens != nullptr ? max(0, min(k.len, __ldg(p.prefix_lens + b))) : 0;
     const long long i = number - (s / p.tokens + b);
     k.tiles = 0;
@@ -103,11 +101,10 @@ struct Cursor {
         t = 0;
         if (++j < p.items_per_block) return true;
         j = 0;
-        bool bad = false;
         for (++number; number < numbers; ++number) {
             int b = k.b;
             while (b + 1 < p.B && row_start(p, b + 1) / p.tokens + b + 1 <= number) ++b;
-            k = block_of<TK>(p, number, b, &bad);
+            k = block_of<TK>(p, number, b);
             if (k.tiles != 0) return true;
         }
         return false;
@@ -119,10 +116,9 @@ struct Share {
 };
 
 // This CTA's share, by all its THREADS threads; `warp_cost` [THREADS / 32] and
-// `at` are shared memory.  at->k.tiles == 0 afterwards: an empty share.  bad: a
-// length or a row number outside its range was met.
+// `at` are shared memory.  at->k.tiles == 0 afterwards: an empty share.
 template <int THREADS, int TK, int ITEM_COST>
-__device__ __forceinline__ Share find_share(const PromptParams& p, long long* warp_cost, Cursor<TK, ITEM_COST>* at, bool* bad) {
+__device__ __forceinline__ Share find_share(const PromptParams& p, long long* warp_cost, Cursor<TK, ITEM_COST>* at) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long numbers = block_numbers(p);
     const long long run = (numbers + THREADS - 1) / THREADS;
@@ -132,7 +128,7 @@ __device__ __forceinline__ Share find_share(const PromptParams& p, long long* wa
     const int b0 = b;
     for (long long n = n0; n < n1; ++n) {
         while (b + 1 < p.B && row_start(p, b + 1) / p.tokens + b + 1 <= n) ++b;
-        const Block k = block_of<TK>(p, n, b, bad);
+        const Block k = block_of<TK>(p, n, b);
         if (k.tiles != 0) mine += static_cast<long long>(k.tiles) * kTileCost + ITEM_COST;
     }
     mine *= p.items_per_block;
@@ -160,11 +156,10 @@ __device__ __forceinline__ Share find_share(const PromptParams& p, long long* wa
     if (s.begin >= before && s.begin < before + mine) {
         Cursor<TK, ITEM_COST> c;
         c.at = before;
-        bool unused = false;
         int q = b0;
         for (c.number = n0;; ++c.number) {
             while (q + 1 < p.B && row_start(p, q + 1) / p.tokens + q + 1 <= c.number) ++q;
-            c.k = block_of<TK>(p, c.number, q, &unused);
+            c.k = block_of<TK>(p, c.number, q);
             if (c.k.tiles == 0) continue;
             const long long n = c.item_cost() * p.items_per_block;
             if (s.begin < c.at + n) break;

@@ -505,11 +505,11 @@ int sptp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cac
  *     s_j = cap tanh(scale q . k_j / cap) - slope |pos - j|
  *   for a row at position pos of its sequence and key j.
  *   cap     0: none (s_j = scale q . k_j - ..); else 1e-30 <= cap <= 1e30
- *   slopes  fp32 [P][Hq], one per query head of every shard, finite, any sign;
+ *   slopes  fp32 [P][Hq], one per query head of every shard, any sign, |slope| < 2e38;
  *           NULL: none
  * Numerics: tanh to 2^-22 of the cap, or of the score below an eighth of it
  * (prompts' attention in bf16, caps up to 128: of the cap); distances exact below
- * 2^24, a bias to 2^-23 of itself.
+ * 2^24, a bias to 2^-23 of itself (prompts' attention in bf16, slopes up to 1: or 2^-17).
  */
 
 /* Workspace bytes needed by sptp_paged_attn_prompt (0 on bad args). */

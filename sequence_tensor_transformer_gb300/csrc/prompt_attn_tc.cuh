@@ -260,6 +260,7 @@ struct Softmax {
     float to_log2, slope;
     int lo, hi, pos;  // keys that this row sees; its position
     bool in;          // a token has it
+    int simple;       // BIAS: keys before it lie behind all of the warp's rows; 0 if one has a slope above 1
 
     static constexpr int N = 32;      // scores at a time
     static constexpr int P = TK / 2;  // column of the weights, in the place of scores that are read before
@@ -410,8 +411,10 @@ struct Softmax {
             }
             if constexpr (BIAS) {
                 const float far = static_cast<float>(pos - key);
-                if (p.prefix_lens == nullptr || !__any_sync(0xffffffffu, key + N > pos + 1)) {
-                    // slope (j - pos), of which the part without j can wait
+                if (key + N <= simple) {
+                    // slope (j - pos), of which the part without j can wait: off by the roundings
+                    // of 31 slope and of the whole bias, 2^-17 for slopes up to 1.  (Each
+                    // key's distance times the slope: 16384 rows 1.84 ms instead of 1.60.)
 #pragma unroll
                     for (int j = 0; j < N; j += 2) put(s, j, fma2(at(s, j), both(unit), pair2(slope * j, slope * (j + 1))));
                     bias = -slope * far;
@@ -587,6 +590,10 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) prompt_tc_kernel(const __gri
             sm.lo = in ? first_key(p, sm.pos) : 0;
             sm.hi = in ? min(d.len, end_key(sm.pos, d.prefix)) : 0x7fffffff;
             sm.slope = BIAS && p.slopes != nullptr && in ? __ldg(p.slopes + d.slope0 + head) * kLog2e : 0.f;
+            if constexpr (BIAS)
+                sm.simple = __reduce_min_sync(0xffffffffu, fabsf(sm.slope) > kLog2e               ? 0
+                                                           : in && p.prefix_lens != nullptr ? max(0, sm.pos + 1)
+                                                                                             : 0x7fffffff);
             const int a = d.a[t], b = d.b[t], key0 = d.key0;
             bool ok = true;
             for (int j = b - 1; j >= a; --j) {

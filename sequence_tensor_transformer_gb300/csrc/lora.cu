@@ -42,13 +42,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
-// v = hi + lo up to 2^-16 of it
-__device__ __forceinline__ void split2bf(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = pack2(x, y);
-    const float2 h = unpack2(hi);
-    lo = pack2(x - h.x, y - h.y);
+// The bf16 next below x in magnitude (0: 0): of x's sign and finite unless x is NaN.
+__device__ __forceinline__ uint32_t below(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u << 1 == 0 ? 0u : (u - 1) & 0xffff0000u;
 }
-
+// v = hi + lo up to 2^-16 of it, both of its sign and neither 0 unless it is: so an infinite
+// v (lo is infinite, hi is not) and a finite one times an infinity give the infinity that v
+// itself does, where hi rounded to the nearest would leave infinity - infinity or 0 times infinity.
+__device__ __forceinline__ void split2bf(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const uint32_t hx = below(x), hy = below(y);
+    hi = hx >> 16 | hy;
+    lo = pack2(x - __uint_as_float(hx), y - __uint_as_float(hy));
+}
 
 // The adapters of 16 rows: lane r < 16 has row r's (-1: none or no row), and `first`
 // the lanes whose row is the first with its adapter.

@@ -639,6 +639,19 @@ int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const
               size_t ws_bytes, void* cuda_stream);
 
 /*
+ * sptp_lora_ex -- sptp_lora next to the projection's own call.
+ *   status_workspace  the workspace whose status words record an id >= adapters,
+ *                     unless they hold an error already (a row without one
+ *                     writes nothing there); NULL: workspace
+ *   check_only        nonzero: the status of the call's arguments, nothing
+ *                     enqueued (needs no GPU), so that a projection need not
+ *                     be started whose adapters are refused
+ */
+int sptp_lora_ex(const void* x, const void* A, const void* B, const int* ids, const float* gains, int P, int M, int K, int N,
+                 int R, int adapters, int rowwise, sptp_dtype dtype, const void* base, void* out, void* workspace,
+                 size_t ws_bytes, void* cuda_stream, void* status_workspace, int check_only);
+
+/*
  * sptp_read_device_status -- synchronises `cuda_stream` and returns the
  * status the kernels recorded in the workspace header since the last call
  * that reset it (every entry point above resets it when it starts, unless it

@@ -63,7 +63,7 @@ EXPORTED_SYMBOLS = (
     "sptp_rope_turns", "sptp_rope", "sptp_rope_append_kv", "sptp_paged_attn_workspace_size",
     "sptp_paged_attn_decode", "sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed",
     "sptp_paged_attn_wait_selftest", "sptp_paged_attn_prompt_workspace_size", "sptp_paged_attn_prompt",
-    "sptp_paged_attn_decode_ex", "sptp_lora_workspace_size", "sptp_lora",
+    "sptp_paged_attn_decode_ex", "sptp_lora_workspace_size", "sptp_lora", "sptp_lora_ex",
     "sptp_paged_attn_prompt_wait_selftest",
 )
 
@@ -109,6 +109,7 @@ _SIGS = {
     "sptp_paged_attn_decode_ex": (_I, [ctypes.c_char_p, _F, _P]),
     "sptp_lora_workspace_size": (_Z, [_I] * 6),
     "sptp_lora": (_I, [_P] * 5 + [_I] * 8 + [_P] * 3 + [_Z, _P]),
+    "sptp_lora_ex": (_I, [_P] * 5 + [_I] * 8 + [_P] * 3 + [_Z, _P, _P, _I]),
     "sptp_paged_attn_prompt_workspace_size": (_Z, [_I] * 6),
     "sptp_paged_attn_prompt": (_I, [ctypes.c_char_p]),
     "sptp_paged_attn_prompt_wait_selftest": (_I, [ctypes.c_char_p, _I, _U64]),
@@ -363,8 +364,8 @@ def sptp_gateup_swiglu(y, W1g, W1u, P, s_out=None, workspace=None, stream=None):
 
 def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None, adapters=None, adapter_workspace=None):
     """Row-parallel projection of every shard: out [P,M,d] from s [P,M,F/P].  adapters:
-    (A, B, ids, gains) as in sptp_lora, added to out in place (adapter_workspace: that
-    call's)."""
+    (A, B, ids, gains) as in sptp_lora, added to out in place.  adapter_workspace: that
+    call's, with its status; left out, an id outside its range is recorded in workspace."""
     _, M, f = s.shape
     d, F = W2.shape
     _expect("s", s, (P, M, F // P), s.dtype)
@@ -375,12 +376,12 @@ def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None, adapters=Non
     if workspace is None:
         workspace = _workspace(SPTP_WS_HEADER_BYTES, s.device)
     _same_device(s, W2, out, workspace)
+    beside = None if adapters is None else _adapters_beside(s, adapters, out, workspace, adapter_workspace, stream)
     code = lib().sptp_down_proj(_ptr(s), _ptr(W2), M, d, F, P, _dtype_code(s), _ptr(out), _ptr(workspace),
                                 _nbytes(workspace), _stream(stream))
     _check("sptp_down_proj", code)
-    if adapters is not None and M != 0:
-        A, B, ids, gains = adapters
-        sptp_lora(s, A, B, ids, out, gains, out=out, workspace=adapter_workspace, stream=stream)
+    if beside is not None:
+        _add_adapters(beside)
     return out
 
 
@@ -418,7 +419,8 @@ def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None
     """Boundary in front of attention: returns (qkv [P,M,N/P], resid_out).
     variant: "auto" (the library's default), "pair" or "fused".  adapters: (A, B,
     ids, gains) as in sptp_lora, added to qkv in place (sptp_lora on the normed rows
-    in the workspace; adapter_workspace: that call's)."""
+    in the workspace).  adapter_workspace: that call's, with its status; left out, an
+    id outside its range is recorded in workspace."""
     M, d = x.shape
     N = Wqkv.shape[0]
     dt = _dtype_code(x)
@@ -434,14 +436,19 @@ def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None
         resid_out = torch.empty_like(x)
     if workspace is None:
         workspace = _workspace(sptp_attn_qkv_workspace_size(M, d, N, P, chunks, dt), x.device)
+    beside = None
+    if adapters is not None:
+        # the normed rows, behind the workspace's header
+        rows = workspace.view(-1).view(torch.uint8)[SPTP_WS_HEADER_BYTES:SPTP_WS_HEADER_BYTES + x.nbytes]
+        if rows.nbytes < x.nbytes:
+            raise SptpError("sptp_attn_qkv_forward", STATUS["workspace"])
+        beside = _adapters_beside(rows.view(x.dtype).view(M, d), adapters, qkv_out, workspace, adapter_workspace, stream)
     code = lib().sptp_attn_qkv_forward_ex(_ptr(x), _ptr(partials), _ptr(gamma), _ptr(Wqkv), M, d, N, P, chunks,
                                           float(eps), dt, _ptr(qkv_out), _ptr(resid_out), _ptr(workspace),
                                           _nbytes(workspace), _stream(stream), _variant(variant))
     _check("sptp_attn_qkv_forward", code)
-    if adapters is not None and M != 0:
-        A, B, ids, gains = adapters
-        y = workspace[SPTP_WS_HEADER_BYTES:SPTP_WS_HEADER_BYTES + x.nbytes].view(x.dtype).view(M, d)
-        sptp_lora(y, A, B, ids, qkv_out, gains, out=qkv_out, workspace=adapter_workspace, stream=stream)
+    if beside is not None:
+        _add_adapters(beside)
     return qkv_out, resid_out
 
 
@@ -937,6 +944,29 @@ def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=N
         done = _fast.lora(x, A, B, ids, base, gains, out, workspace)
         if done is not NotImplemented:
             return done
+    args, out, workspace = _lora_call(x, A, B, ids, base, gains, out, workspace, stream)
+    _check("sptp_lora", lib().sptp_lora(*args))
+    return out
+
+
+def _adapters_beside(x, adapters, out, workspace, adapter_workspace, stream):
+    """The adapters of a projection that is about to be enqueued into `out`: their call, for
+    _add_adapters behind it.  What is wrong with it is raised here, before anything is enqueued."""
+    A, B, ids, gains = adapters
+    status = None if adapter_workspace is not None else workspace.data_ptr()
+    args, _, adapter_workspace = _lora_call(x, A, B, ids, out, gains, out, adapter_workspace, stream)
+    _check("sptp_lora", lib().sptp_lora_ex(*args, status, 1))
+    return args, status, adapter_workspace
+
+
+def _add_adapters(beside):
+    args, status, _ = beside
+    _check("sptp_lora", lib().sptp_lora_ex(*args, status, 0))
+
+
+def _lora_call(x, A, B, ids, base, gains, out, workspace, stream):
+    """The checked arguments of a call, its out, and the workspace (to be kept until the
+    call is made)."""
     n, R, K = A.shape
     N, dtype = B.shape[1], x.dtype
     dt = _dtype_code(x)
@@ -958,8 +988,6 @@ def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=N
     if workspace is None:
         workspace = _new((max(sptp_lora_workspace_size(P, M, K, N, R, rowwise), SPTP_WS_HEADER_BYTES),), torch.uint8, x.device,
                          stream)
-    code = lib().sptp_lora(x.data_ptr(), A.data_ptr(), B.data_ptr(), ids.data_ptr(), None if gains is None else gains.data_ptr(),
-                           P, M, K, N, R, n, int(rowwise), dt, base.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                           workspace.nbytes, _raw_stream(stream, cur))
-    _check("sptp_lora", code)
-    return out
+    args = (x.data_ptr(), A.data_ptr(), B.data_ptr(), ids.data_ptr(), None if gains is None else gains.data_ptr(), P, M, K, N, R, n,
+            int(rowwise), dt, base.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, cur))
+    return args, out, workspace

@@ -72,8 +72,9 @@ struct Ids {
     __device__ __forceinline__ int of(int row) const { return __shfl_sync(0xffffffffu, id, row); }
 };
 
-// The status words: the first row whose adapter is outside its range.  By the
-// last block of the second launch.
+// The status words: the first row whose adapter is outside its range (beside another
+// call's: only if there is one, and the other call recorded nothing).  By the last block
+// of the second launch.
 __device__ __forceinline__ void report_rows(const LoraParams& p) {
     __shared__ int first;
     if (threadIdx.x == 0) first = p.M;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void report_rows(const LoraParams& p) {
             st.where = kWhereAdapter;
             st.info = first;
         }
-        *p.status = st;
+        if (!p.beside || (st.code != 0 && p.status->code == 0)) *p.status = st;
     }
 }
 

@@ -19,6 +19,7 @@ struct LoraParams {
     int n;                // columns of a row of out
     int splits, split_k;  // of a row of x: split s has elements [s * split_k, (s + 1) * split_k)
     DeviceStatus* status;
+    int beside;           // the status is another call's too: only an id outside its range is recorded, where there is none yet
 };
 
 constexpr int kLoraMaxRank = 128;

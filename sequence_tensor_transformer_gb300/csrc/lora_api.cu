@@ -39,6 +39,13 @@ size_t sptp_lora_workspace_size(int P, int M, int K, int N, int R, int rowwise) 
 int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const float* gains, int P, int M, int K, int N,
               int R, int adapters, int rowwise, sptp_dtype dtype, const void* base, void* out, void* workspace,
               size_t ws_bytes, void* cuda_stream) {
+    return sptp_lora_ex(x, A, B, ids, gains, P, M, K, N, R, adapters, rowwise, dtype, base, out, workspace, ws_bytes, cuda_stream,
+                        nullptr, 0);
+}
+
+int sptp_lora_ex(const void* x, const void* A, const void* B, const int* ids, const float* gains, int P, int M, int K, int N,
+                 int R, int adapters, int rowwise, sptp_dtype dtype, const void* base, void* out, void* workspace,
+                 size_t ws_bytes, void* cuda_stream, void* status_workspace, int check_only) {
     if (!workspace || (M != 0 && (!x || !ids || !base || !out || (adapters != 0 && (!A || !B))))) return SPTP_ERR_NULL;
     if (!dtype_ok(dtype)) return SPTP_ERR_DTYPE;
     int rc = check_lora(P, M, K, N, R, adapters, rowwise);
@@ -48,12 +55,13 @@ int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const
     const size_t out_bytes = (rowwise ? static_cast<size_t>(P) : 1) * m * N * es;
     const Buf ins[] = {{base, out_bytes, 16}, {x, m * K * es, 16}, {A, n * R * K * es, 16}, {B, n * N * R * es, 16},
                        {ids, m * 4, 4}, {gains, n * 4, 4}};
-    const Buf outs[] = {{out, out_bytes, 16}, {workspace, need, kAlign}};
-    if ((rc = check_aligned(ins, 6)) != SPTP_OK || (rc = check_aligned(outs, 2)) != SPTP_OK) return rc;
+    const Buf outs[] = {{out, out_bytes, 16}, {workspace, need, kAlign}, {status_workspace, sizeof(DeviceStatus), kAlign}};
+    const int n_outs = status_workspace ? 3 : 2;
+    if ((rc = check_aligned(ins, 6)) != SPTP_OK || (rc = check_aligned(outs, n_outs)) != SPTP_OK) return rc;
     if (ws_bytes < need) return SPTP_ERR_WORKSPACE;
     const int skip = out == base ? 1 : 0;
-    if ((rc = check_alias(outs, 2, ins + skip, 6 - skip)) != SPTP_OK) return rc;
-    if (M == 0) return SPTP_OK;
+    if ((rc = check_alias(outs, n_outs, ins + skip, 6 - skip)) != SPTP_OK) return rc;
+    if (M == 0 || check_only) return SPTP_OK;
     DevInfo di;
     if ((rc = device_info(&di)) != SPTP_OK) return rc;
     LoraParams p;
@@ -76,7 +84,8 @@ int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const
     p.f = rowwise ? K / P : K;
     p.n = rowwise ? N : N / P;
     p.splits = lora_splits(M, p.f, R, rowwise ? P : 1, dtype == SPTP_BF16, &p.split_k);
-    p.status = ws_status(workspace);
+    p.status = ws_status(status_workspace ? status_workspace : workspace);
+    p.beside = status_workspace != nullptr;
     return cuda_status(launch_lora(p, dtype == SPTP_BF16, di.sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 

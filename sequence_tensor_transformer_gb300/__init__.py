@@ -799,6 +799,7 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
             done = _fast.decode_ex(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, write_lse, cap, slopes)
         if done is not NotImplemented:
             return done
+    _check_cap("sptp_paged_attn_decode", cap)
     P, B, Hq, D = q.shape
     k, v, ks, vs = cache
     dtype, i32 = q.dtype, torch.int32
@@ -828,6 +829,12 @@ def sptp_paged_attn_decode(q, cache, page_table, seq_lens, scale=None, window=0,
         page_size, window, dt, kv_type, D ** -0.5 if scale is None else scale), cap, None if slopes is None else slopes.data_ptr())
     _check("sptp_paged_attn_decode", code)
     return out, lse
+
+
+def _check_cap(fn, cap):
+    """A cap too small for fp32 is refused like any below 1e-30 (it would be passed as 0: none)."""
+    if cap != 0 and abs(cap) < 1e-30:
+        raise SptpError(fn, STATUS["shape"])
 
 
 def sptp_paged_attn_prompt_workspace_size(P, M, B, Hq, Hkv, D) -> int:
@@ -872,6 +879,7 @@ def _prompt_call(q, cache, page_table, seq_lens, row_starts, scale, window, cap,
                  stream, write_lse):
     """The checked arguments of a call as one block, its out and its lse, and the
     workspace (to be kept until the call is made)."""
+    _check_cap("sptp_paged_attn_prompt", cap)
     P, M, Hq, D = q.shape
     k, v, ks, vs = cache
     dtype, i32 = q.dtype, torch.int32

@@ -70,8 +70,9 @@ float real(PyObject* o) {
         PyErr_Clear();
         throw Unfit{};
     }
-    need(std::fabs(v) <= FLT_MAX);
-    return static_cast<float>(v);
+    const float f = static_cast<float>(v);
+    need(std::fabs(v) <= FLT_MAX && (f != 0.f) == (v != 0.0));
+    return f;
 }
 
 int size(int64_t n) {

@@ -532,8 +532,8 @@ typedef struct sptp_paged_attn_prompt_args_s {
  *     lse = ln sum_j e^s_j,  out = sum_j e^(s_j - lse) v_j
  *   over lo <= j < hi:  pos = seq_lens[b] - n_b + r for row r of the sequence's
  *   n_b rows;  hi = pos + 1, or prefix_lens[b] where that is more (a prefix that
- *   every row of the sequence sees whole);  lo = pos + 1 - window if window > 0
- *   and that is positive, else 0.
+ *   rows see beyond their own position);  lo = pos + 1 - window if window > 0
+ *   and that is positive, else 0 (a window cuts the prefix, too).
  *   q           [P][M][Hq][D] (sptp_rope_append_kv's q_out)
  *   row_starts  [B + 1] int32: sequence b's rows are row_starts[b] ..
  *               row_starts[b+1] - 1, ascending, 0 <= .. <= M.  Other rows of out
@@ -550,7 +550,7 @@ typedef struct sptp_paged_attn_prompt_args_s {
  * equal bits.  What the cache holds outside the keys that a sequence's rows see
  * does not matter, and neither does, for a row, what lies at keys that it does not
  * see.  (E4M3: a code that is no number counts as 480.)
- * Recorded as SPTP_ERR_SHAPE in the workspace status words: a row start outside
+ * Recorded as SPTP_ERR_SHAPE in the workspace status words, for any sequence: a row start outside
  * [0, M] or below the one before it (the rows concerned are undefined); a length
  * outside [0, max_pages * page_size] (cut to it); more rows than keys (the rows
  * before position 0 see nothing: zeros, lse -inf); a page outside [0, num_pages)
@@ -632,7 +632,8 @@ size_t sptp_lora_workspace_size(int P, int M, int K, int N, int R, int rowwise);
  * M == 0 enqueues nothing.  workspace: at least
  * sptp_lora_workspace_size(...), 256-byte aligned.
  * Numerics: A_a x summed in fp32, and kept to 2^-16 of itself for its product
- * with B_a (bf16; in fp32 not rounded), sums in fp32, out rounded once.
+ * with B_a (bf16; in fp32 not rounded), sums in fp32, out rounded once.  Infinities are
+ * those of the formula.
  */
 int sptp_lora(const void* x, const void* A, const void* B, const int* ids, const float* gains, int P, int M, int K, int N,
               int R, int adapters, int rowwise, sptp_dtype dtype, const void* base, void* out, void* workspace,

@@ -23,7 +23,9 @@ struct LoraParams {
 };
 
 constexpr int kLoraMaxRank = 128;
-// Rows below which the second launch has a block per row instead of one per 16.
+// Rows below which the second launch has a block per row instead of one per 16 (measured at rank
+// 16 with an adapter of its own for most rows; with one adapter for all of 16 rows, and at
+// higher ranks, the block per row reads B more often than it need be).
 constexpr int kLoraFew = 160;
 
 // How the product with A is split along a row of f elements: pieces of *split_k,

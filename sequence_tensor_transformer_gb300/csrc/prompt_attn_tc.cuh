@@ -28,9 +28,9 @@
 //    lies above the largest score so far and moves only when one is 2^16 above it, so
 //    that the outputs in tensor memory are rarely rescaled.
 //
-// Measured, causal, heads of 128: 4 shards of 16384 rows and 7 heads on one, 1.44 ms
-// (1340 TFLOP/s), 1.60 with a bias, 2.35 with a cap (there the softmax is what lasts:
-// 8 multiply-adds a score for the cap beside an exponential and its sum).
+// Measured, causal, heads of 128: 4 shards of 16384 rows and 7 heads on one, 1.45 ms
+// (1330 TFLOP/s), 1.62 with a bias, 2.36 with a cap (there the softmax is what lasts:
+// 8 multiply-adds a score for the cap beside an exponential and its sum), 2.53 with both.
 #pragma once
 
 #include <atomic>
@@ -48,7 +48,7 @@ constexpr int kTileRows = 128;
 // moves, which rescales the row's outputs in tensor memory and makes its warp's other
 // rows wait, when a score is kSlack above it.  Weights are thus within 2^16 of the
 // largest score's, which costs no bits (both their types have eight bits of exponent):
-// scores 2^-110 of the largest vanish, and values up to 2^112 over a row's keys stay
+// scores 2^-110 of the largest vanish, and values whose sum over a row's keys is below 2^111 stay
 // finite.  16384 capped rows of scores of deviation 6: 2.35 ms, with 16 and 8 2.40, with
 // 16 and 0 2.57, with 8 and 0 2.77.
 constexpr float kSlack = 16.f, kHead = 16.f;

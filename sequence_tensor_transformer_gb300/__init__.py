@@ -161,7 +161,7 @@ def set_library(handle):
                       "step's calls cost some microseconds more", RuntimeWarning, stacklevel=2)
         return
     for use, names in ((_decode_binding.use, ("sptp_rope_packed", "sptp_rope_append_kv_packed", "sptp_paged_attn_decode_packed")),
-                       (_decode_binding.use_batch, ("sptp_paged_attn_decode_ex", "sptp_paged_attn_prompt", "sptp_lora"))):
+                       (_decode_binding.use_batch, ("sptp_paged_attn_decode_ex", "sptp_paged_attn_prompt", "sptp_lora_ex"))):
         use(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in names))
     _fast = _decode_binding
 
@@ -381,7 +381,7 @@ def sptp_down_proj(s, W2, P, out=None, workspace=None, stream=None, adapters=Non
                                 _nbytes(workspace), _stream(stream))
     _check("sptp_down_proj", code)
     if beside is not None:
-        _add_adapters(beside)
+        _lora_beside(beside, stream)
     return out
 
 
@@ -439,6 +439,7 @@ def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None
     beside = None
     if adapters is not None:
         # the normed rows, behind the workspace's header
+        _ptr(workspace)  # (dense)
         rows = workspace.view(-1).view(torch.uint8)[SPTP_WS_HEADER_BYTES:SPTP_WS_HEADER_BYTES + x.nbytes]
         if rows.nbytes < x.nbytes:
             raise SptpError("sptp_attn_qkv_forward", STATUS["workspace"])
@@ -448,7 +449,7 @@ def sptp_attn_qkv_forward(x, partials, gamma, Wqkv, P, chunks, eps, qkv_out=None
                                           _nbytes(workspace), _stream(stream), _variant(variant))
     _check("sptp_attn_qkv_forward", code)
     if beside is not None:
-        _add_adapters(beside)
+        _lora_beside(beside, stream)
     return qkv_out, resid_out
 
 
@@ -949,7 +950,7 @@ def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=N
     with base [P,M,N]: beside a row-parallel one.  out may be base (in place).
     Returns out.  Costs the host less with a workspace given and stream left out."""
     if _fast is not None and stream is None:
-        done = _fast.lora(x, A, B, ids, base, gains, out, workspace)
+        done = _fast.lora(x, A, B, ids, base, gains, out, workspace, None, False)
         if done is not NotImplemented:
             return done
     args, out, workspace = _lora_call(x, A, B, ids, base, gains, out, workspace, stream)
@@ -958,18 +959,25 @@ def sptp_lora(x, A, B, ids, base, gains=None, out=None, workspace=None, stream=N
 
 
 def _adapters_beside(x, adapters, out, workspace, adapter_workspace, stream):
-    """The adapters of a projection that is about to be enqueued into `out`: their call, for
-    _add_adapters behind it.  What is wrong with it is raised here, before anything is enqueued."""
+    """The adapters of a projection that is about to be enqueued into `out`: their call, to be
+    made by _lora_beside behind it.  What is wrong with it is raised here, before anything is
+    enqueued."""
     A, B, ids, gains = adapters
-    status = None if adapter_workspace is not None else workspace.data_ptr()
-    args, _, adapter_workspace = _lora_call(x, A, B, ids, out, gains, out, adapter_workspace, stream)
-    _check("sptp_lora", lib().sptp_lora_ex(*args, status, 1))
-    return args, status, adapter_workspace
+    status = None if adapter_workspace is not None else workspace
+    if adapter_workspace is None and A.dim() == 3 and B.dim() == 3:
+        n = sptp_lora_workspace_size(out.shape[0], x.shape[-2], A.shape[2], B.shape[1], A.shape[1], x.dim() == 3)
+        adapter_workspace = _new((max(n, SPTP_WS_HEADER_BYTES),), torch.uint8, x.device, stream)
+    call = (x, A, B, ids, out, gains, out, adapter_workspace, status)
+    _lora_beside(call, stream, check_only=True)
+    return call
 
 
-def _add_adapters(beside):
-    args, status, _ = beside
-    _check("sptp_lora", lib().sptp_lora_ex(*args, status, 0))
+def _lora_beside(call, stream, check_only=False):
+    if _fast is not None and stream is None and _fast.lora(*call, check_only) is not NotImplemented:
+        return
+    *arguments, status = call
+    args = _lora_call(*arguments, stream)[0]
+    _check("sptp_lora", lib().sptp_lora_ex(*args, None if status is None else status.data_ptr(), int(check_only)))
 
 
 def _lora_call(x, A, B, ids, base, gains, out, workspace, stream):

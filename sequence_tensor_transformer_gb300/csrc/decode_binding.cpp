@@ -35,7 +35,7 @@ int (*append_call)(const sptp_rope_append_kv_args*) = nullptr;
 int (*decode_call)(const sptp_paged_attn_decode_args*) = nullptr;
 int (*decode_ex_call)(const sptp_paged_attn_decode_args*, float, const float*) = nullptr;
 int (*prompt_call)(const sptp_paged_attn_prompt_args*) = nullptr;
-decltype(&sptp_lora) lora_call = nullptr;
+decltype(&sptp_lora_ex) lora_call = nullptr;
 
 struct Unfit {};  // thrown: not a call for these entries
 
@@ -367,11 +367,12 @@ PyObject* prompt(PyObject* const* o) {
     return outs.object();
 }
 
-// (x, A, B, ids, base, gains, out, workspace)
+// (x, A, B, ids, base, gains, out, workspace, status_workspace, check_only)
 PyObject* lora(PyObject* const* o) {
     const at::Tensor &x = tensor(o[0]), &A = tensor(o[1]), &B = tensor(o[2]), &ids = tensor(o[3]), &base = tensor(o[4]),
                      &ws = tensor(o[7]);
-    const at::Tensor* gains = tensor_or_none(o[5]);
+    const at::Tensor *gains = tensor_or_none(o[5]), *status = tensor_or_none(o[8]);
+    need(o[9] == Py_False || o[9] == Py_True);
     const int dev = device_for(x);
     const at::ScalarType type = x.scalar_type();
     need((x.dim() == 2 || x.dim() == 3) && A.dim() == 3 && B.dim() == 3 && base.dim() == 3 && lora_call != nullptr);
@@ -396,9 +397,10 @@ PyObject* lora(PyObject* const* o) {
     void *xp = data(x, dev), *Ap = data(A, dev), *Bp = data(B, dev), *bp = data(base, dev), *wp = data(ws, dev);
     const int* ip = data<const int>(ids, dev);
     const float* gp = gains ? data<const float>(*gains, dev) : nullptr;
+    void* sp = status ? data(*status, dev) : nullptr;
     Out out(o[6], x, type, {P, M, n}, dev);
     make(lora_call, xp, Ap, Bp, ip, gp, P, M, K, N, R, adapters, rowwise ? 1 : 0, dtype, bp, out.at, wp, ws.nbytes(),
-         static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+         static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev).stream()), sp, o[9] == Py_True ? 1 : 0);
     return out.object();
 }
 
@@ -437,7 +439,7 @@ PyObject* use(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// And of (sptp_paged_attn_decode_ex, sptp_paged_attn_prompt, sptp_lora).
+// And of (sptp_paged_attn_decode_ex, sptp_paged_attn_prompt, sptp_lora_ex).
 PyObject* use_batch(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* p[3];
     if (!addresses(args, n, p)) return nullptr;
@@ -463,7 +465,7 @@ extern "C" PyMODINIT_FUNC PyInit__decode_binding() {
         {"use_batch", method(use_batch), METH_FASTCALL, nullptr},
         {"decode_ex", method(entry<decode<true>, 12>), METH_FASTCALL, nullptr},
         {"prompt", method(entry<prompt, 14>), METH_FASTCALL, nullptr},
-        {"lora", method(entry<lora, 8>), METH_FASTCALL, nullptr},
+        {"lora", method(entry<lora, 10>), METH_FASTCALL, nullptr},
         {nullptr, nullptr, 0, nullptr},
     };
     static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode_binding", nullptr, -1, methods};
